@@ -1,0 +1,654 @@
+// Embedding lookup with scaling and its gradient by sorted tokens (sm_103a).
+//
+//   y_i = s W[t_i],   dW_r (+)= s sum_{i: t_i = r} dy_i
+//
+// Bound: HBM.  The lookup reads each named row and writes each output row once.
+// The gradient reads dy once and writes the table once (or reads and writes the
+// named rows, when accumulating); no atomic addition touches a value, so the
+// result depends on the tokens alone.
+//
+// Gradient, four launches:
+//   1. sort_tokens_kernel: one cluster sorts (token, position) pairs by token,
+//      stably (radix sort), and marks the tokens that occur in a bitmap;
+//   2. zero_rows_kernel (not when accumulating): zeros into every other row;
+//   3. sum_rows_kernel: the sorted pairs in chunks of kChunk; each thread owns
+//      a few columns of a chunk and adds its rows in fp32 in sorted order.  A
+//      token whose pairs lie within one chunk is finished there; the parts of
+//      one that spans chunks go to the workspace, so a token that fills half of
+//      a batch is spread over as many CTAs as any other half;
+//   4. join_rows_kernel: adds such a token's parts in chunk order.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "fsp_host.h"
+#include "fsp_internal.h"
+#include "fsp_ops.h"
+
+namespace fsp {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr unsigned kErrToken = 16u;   // a token outside [0, vocab)
+__device__ unsigned int g_token_error = 0;
+
+// ---- element access -----------------------------------------------------------
+
+template <typename T, int V>
+struct Vec {   // V consecutive elements
+  T x[V];
+};
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// V elements from p, 4 * V or 2 * V bytes, aligned to min(that, 16).
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float* f) {
+  constexpr int kBytes = int(sizeof(T)) * V;
+  if constexpr (kBytes >= 16) {
+#pragma unroll
+    for (int k = 0; k < kBytes / 16; ++k) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + k);
+      const T* t = reinterpret_cast<const T*>(&b);
+#pragma unroll
+      for (int j = 0; j < 16 / int(sizeof(T)); ++j) f[k * (16 / int(sizeof(T))) + j] = widen(t[j]);
+    }
+  } else if constexpr (kBytes == 8) {
+    const uint2 b = __ldg(reinterpret_cast<const uint2*>(p));
+    const T* t = reinterpret_cast<const T*>(&b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = widen(t[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = widen(p[j]);
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float* f) {
+  constexpr int kBytes = int(sizeof(T)) * V;
+  alignas(16) T t[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) t[j] = narrow<T>(f[j]);
+  if constexpr (kBytes >= 16) {
+#pragma unroll
+    for (int k = 0; k < kBytes / 16; ++k) __stcs(reinterpret_cast<uint4*>(p) + k, reinterpret_cast<uint4*>(t)[k]);
+  } else if constexpr (kBytes == 8) {
+    __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<uint2*>(t));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[j] = t[j];
+  }
+}
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int index_bytes, int64_t i) {
+  return index_bytes == 8 ? static_cast<const int64_t*>(tokens)[i] : int64_t(static_cast<const int32_t*>(tokens)[i]);
+}
+
+// ---- lookup ---------------------------------------------------------------------
+
+constexpr int kLookupThreads = 256;
+
+struct LookupArgs {
+  const void* weight;
+  const void* tokens;
+  void* out;
+  int64_t vocab, dim, weight_stride, out_stride, n_tokens;
+  float scale;
+  int index_bytes;
+};
+
+// A warp per token: the row in steps of 32 x V elements.
+template <typename W, typename O, int V>
+__global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const __grid_constant__ LookupArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = int64_t(blockIdx.x) * (kLookupThreads / 32) + (threadIdx.x >> 5);
+  if (i >= a.n_tokens) return;
+  const int64_t t = token_at(a.tokens, a.index_bytes, i);
+  const bool ok = t >= 0 && t < a.vocab;
+  if (!ok && lane == 0) atomicOr(&g_token_error, kErrToken);
+  const W* row = static_cast<const W*>(a.weight) + (ok ? t : 0) * a.weight_stride;
+  O* out = static_cast<O*>(a.out) + i * a.out_stride;
+#pragma unroll 4
+  for (int64_t c = int64_t(lane) * V; c < a.dim; c += 32 * V) {
+    float f[V];
+    load_vec<W, V>(row + c, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = ok ? f[j] * a.scale : 0.f;
+    store_vec<O, V>(out + c, f);
+  }
+}
+
+// ---- gradient: sort ----------------------------------------------------------------
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9;
+constexpr int kBins = 1 << kDigitBits;
+constexpr int kSortCluster = 8;             // CTAs of a large sort
+constexpr int64_t kSortOneCta = 4096;       // tokens that one CTA sorts alone
+constexpr int kSortSmem = kSortWarps * kBins * 4 + 2 * kBins * 4 + kSortWarps * 4;
+
+struct SortArgs {
+  const void* tokens;
+  uint2* a;             // (key, position) after an odd number of passes
+  uint2* b;             // ... an even number
+  uint32_t* present;    // bitmap of the tokens that occur
+  uint32_t* totals;     // [kSortCluster][kBins]
+  int64_t vocab;
+  int64_t padding_idx;
+  int n;
+  int index_bytes;
+  int n_words;          // of the bitmap
+  int passes, bits;     // passes of `bits` bits
+};
+
+// The sort key: the token, or `vocab` (which sorts last) for one whose gradient
+// is dropped.
+__device__ __forceinline__ uint32_t token_key(const SortArgs& s, int i) {
+  const int64_t t = token_at(s.tokens, s.index_bytes, i);
+  if (t < 0 || t >= s.vocab) {
+    atomicOr(&g_token_error, kErrToken);
+    return uint32_t(s.vocab);
+  }
+  return t == s.padding_idx ? uint32_t(s.vocab) : uint32_t(t);
+}
+
+// The lanes of the warp whose digit equals this one's (kDigitBits ballots).
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, bool valid) {
+  uint32_t mask = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+  for (int b = 0; b < kDigitBits; ++b) {
+    const uint32_t v = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+    mask &= (d >> b) & 1u ? v : ~v;
+  }
+  return mask;
+}
+
+// Least significant digit first.  CTA c of the cluster holds a contiguous run
+// of the items and each of its warps a contiguous run of that, so "earlier
+// CTA, earlier warp, earlier round, lower lane" is the input's order and every
+// pass is stable.  Per pass: each warp counts its digits in shared memory; the
+// counts become each warp's first output slot per digit (a scan over digits,
+// CTAs and warps); each warp then walks its items again and places them.
+__global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const __grid_constant__ SortArgs s) {
+  extern __shared__ uint32_t smem[];
+  uint32_t* hist = smem;                            // [kSortWarps][kBins]
+  uint32_t* total = hist + kSortWarps * kBins;      // [kBins]: this CTA's, then its first slot
+  uint32_t* sums = total + 2 * kBins;               // [kSortWarps]
+  cg::cluster_group cluster = cg::this_cluster();
+  const int n_ctas = int(gridDim.x), cta = int(blockIdx.x);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = cta * kSortThreads + tid; i < s.n_words; i += n_ctas * kSortThreads) s.present[i] = 0;
+  cluster.sync();
+  const int per_warp = ((s.n + n_ctas * kSortWarps - 1) / (n_ctas * kSortWarps) + 31) / 32 * 32;
+  const int64_t first = int64_t(cta * kSortWarps + warp) * per_warp;
+  const int begin = int(min(first, int64_t(s.n))), end = int(min(first + per_warp, int64_t(s.n)));
+  for (int pass = 0; pass < s.passes; ++pass) {
+    const int shift = pass * s.bits;
+    const uint32_t digit_mask = (1u << s.bits) - 1u;
+    const uint2* src = pass & 1 ? s.a : s.b;
+    uint2* dst = pass & 1 ? s.b : s.a;
+    for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = begin + lane; i < end; i += 32) {
+      uint32_t key;
+      if (pass == 0) {
+        key = token_key(s, i);
+        if (key < uint32_t(s.vocab)) atomicOr(&s.present[key >> 5], 1u << (key & 31));
+      } else {
+        key = __ldcg(&src[i]).x;
+      }
+      atomicAdd(&hist[warp * kBins + ((key >> shift) & digit_mask)], 1u);
+    }
+    __syncthreads();
+    if (tid < kBins) {   // counts -> each warp's offset within this CTA's items of the digit
+      uint32_t run = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = hist[w * kBins + tid];
+        hist[w * kBins + tid] = run;
+        run += c;
+      }
+      total[tid] = run;
+      s.totals[cta * kBins + tid] = run;
+    }
+    cluster.sync();
+    // first slot of each digit (over all CTAs), then of this CTA's items of it
+    uint32_t all = 0, before = 0;
+    if (tid < kBins) {
+      for (int c = 0; c < n_ctas; ++c) {
+        const uint32_t x = __ldcg(&s.totals[c * kBins + tid]);
+        if (c < cta) before += x;
+        all += x;
+      }
+    }
+    uint32_t scan = all;   // inclusive over the warp's digits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += x;
+    }
+    if (lane == 31) sums[warp] = scan;
+    __syncthreads();
+    if (tid < kBins) {
+      uint32_t base = 0;
+      for (int w = 0; w < warp; ++w) base += sums[w];
+      total[tid] = base + scan - all + before;
+    }
+    __syncthreads();
+    for (int i0 = begin; i0 < end; i0 += 32) {
+      const int i = i0 + lane;
+      const bool valid = i < end;
+      uint2 item = make_uint2(0, 0);
+      if (valid) item = pass == 0 ? make_uint2(token_key(s, i), uint32_t(i)) : __ldcg(&src[i]);
+      const uint32_t d = (item.x >> shift) & digit_mask;
+      const uint32_t peers = same_digit(d, valid);
+      uint32_t at = 0;
+      if (valid) at = hist[warp * kBins + d];
+      __syncwarp();
+      if (valid) {
+        const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
+        if (rank == 0) hist[warp * kBins + d] = at + __popc(peers);
+        dst[total[d] + at + rank] = item;
+      }
+      __syncwarp();
+    }
+    cluster.sync();   // the pass's items, and totals[] before it is written again
+  }
+}
+
+// ---- gradient: rows ------------------------------------------------------------------
+
+constexpr int kRowThreads = 128;
+constexpr int kChunk = 32;   // sorted pairs of one thread's walk
+constexpr int kAhead = 8;    // rows in flight per thread
+
+struct RowArgs {
+  const uint2* items;        // sorted (key, position)
+  const uint32_t* present;
+  const void* grad;
+  void* weight;
+  float* parts;              // [chunk][2][dim]: of a token begun before / going on after the chunk
+  int64_t vocab, dim, grad_stride, weight_stride;
+  float scale;
+  int n;
+  int accumulate;
+  int cols;                  // threads along the columns (a power of two)
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void finish_row(const RowArgs& a, uint32_t row, int64_t col, const float* acc) {
+  T* p = static_cast<T*>(a.weight) + int64_t(row) * a.weight_stride + col;
+  float f[V], old[V];
+  if (a.accumulate) {
+    load_vec<T, V>(p, old);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = __fmaf_rn(acc[j], a.scale, old[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = acc[j] * a.scale;
+  }
+  store_vec<T, V>(p, f);
+}
+
+// A thread: V columns of one chunk.
+template <typename G, typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) sum_rows_kernel(const __grid_constant__ RowArgs a) {
+  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
+  const int64_t chunk = int64_t(blockIdx.x) * (kRowThreads / a.cols) + cy;
+  const int64_t col = (int64_t(blockIdx.y) * a.cols + cx) * V;
+  const int64_t begin = chunk * kChunk;
+  if (begin >= a.n || col >= a.dim) return;
+  const int end = int(min(begin + kChunk, int64_t(a.n)));
+  const uint32_t none = uint32_t(a.vocab);
+  uint32_t row = a.items[begin].x;
+  bool head = begin > 0 && a.items[begin - 1].x == row;
+  const G* grad = static_cast<const G*>(a.grad) + col;
+  float acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] = 0.f;
+  for (int i0 = int(begin); i0 < end && row < none; i0 += kAhead) {
+    uint2 it[kAhead];
+    float f[kAhead][V];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      it[k] = i0 + k < end ? a.items[i0 + k] : make_uint2(none, 0);
+      if (it[k].x < none) load_vec<G, V>(grad + int64_t(it[k].y) * a.grad_stride, f[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i0 + k >= end) break;
+      if (it[k].x != row) {   // the token before is complete (its end lies in this chunk)
+        if (head)
+          store_vec<float, V>(a.parts + (chunk * 2) * a.dim + col, acc);
+        else
+          finish_row<T, V>(a, row, col, acc);
+        head = false;
+        row = it[k].x;
+        if (row >= none) return;   // dropped tokens sort last
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] += f[k][j];
+    }
+  }
+  if (row >= none) return;
+  const bool tail = end < a.n && a.items[end].x == row;
+  if (head || tail)
+    store_vec<float, V>(a.parts + (chunk * 2 + (head ? 0 : 1)) * a.dim + col, acc);
+  else
+    finish_row<T, V>(a, row, col, acc);
+}
+
+// A thread: V columns of the token that begins in a chunk and goes on after it.
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) join_rows_kernel(const __grid_constant__ RowArgs a) {
+  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
+  int64_t chunk = int64_t(blockIdx.x) * (kRowThreads / a.cols) + cy;
+  const int64_t col = (int64_t(blockIdx.y) * a.cols + cx) * V;
+  const int64_t begin = chunk * kChunk, end = begin + kChunk;
+  if (end >= a.n || col >= a.dim) return;
+  const uint32_t row = a.items[end - 1].x;
+  if (row >= uint32_t(a.vocab) || a.items[end].x != row) return;
+  if (a.items[begin].x == row && begin > 0 && a.items[begin - 1].x == row) return;   // begun before
+  float acc[V];
+  load_vec<float, V>(a.parts + (chunk * 2 + 1) * a.dim + col, acc);
+  for (int64_t c = chunk + 1; c * kChunk < a.n && a.items[c * kChunk].x == row; ++c) {
+    float f[V];
+    load_vec<float, V>(a.parts + (c * 2) * a.dim + col, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] += f[j];
+  }
+  finish_row<T, V>(a, row, col, acc);
+}
+
+// Zeros into the rows that no token names: a warp per row.
+template <typename T, int V>
+__global__ void __launch_bounds__(kLookupThreads) zero_rows_kernel(const __grid_constant__ RowArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * (kLookupThreads / 32) + (threadIdx.x >> 5);
+  if (row >= a.vocab || (a.present[row >> 5] >> (row & 31) & 1u)) return;
+  T* p = static_cast<T*>(a.weight) + row * a.weight_stride;
+  const float zero[V] = {};
+#pragma unroll 4
+  for (int64_t c = int64_t(lane) * V; c < a.dim; c += 32 * V) store_vec<T, V>(p + c, zero);
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+size_t size_of(int32_t dtype) { return dtype == FSP_DTYPE_F32 ? 4 : 2; }
+bool known(int32_t dtype) { return dtype == FSP_DTYPE_F32 || dtype == FSP_DTYPE_BF16; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Bytes from a matrix's first to past its last element.
+size_t span_bytes(int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
+  return rows > 0 && cols > 0 ? (size_t(rows - 1) * size_t(stride) + size_t(cols)) * size_of(dtype) : 0;
+}
+
+fsp_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype, const char* name) {
+  if (!known(dtype)) return fail(FSP_EINVAL, std::string("unknown dtype of ") + name);
+  if (stride < cols || (rows > 0 && stride > (int64_t(1) << 58) / rows))
+    return fail(FSP_EINVAL, std::string(name) + "'s rows overlap or their stride is out of range");
+  const size_t bytes = span_bytes(rows, cols, stride, dtype);
+  if (!bytes) return FSP_OK;
+  if (!p) return fail(FSP_EINVAL, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % size_of(dtype)) return fail(FSP_EINVAL, std::string(name) + " is not aligned to its elements");
+  return check_allocation(p, bytes, name);
+}
+
+fsp_status check_tokens(const void* tokens, int32_t index_bytes, int64_t n) {
+  if (index_bytes != 4 && index_bytes != 8) return fail(FSP_EINVAL, "index_bytes must be 4 or 8");
+  if (n < 0 || n > (int64_t(1) << 58)) return fail(FSP_EINVAL, "n_tokens is out of range");
+  if (n == 0) return FSP_OK;
+  if (!tokens) return fail(FSP_EINVAL, "tokens is NULL");
+  if (reinterpret_cast<uintptr_t>(tokens) % size_t(index_bytes)) return fail(FSP_EINVAL, "tokens is not aligned to its elements");
+  return check_allocation(tokens, size_t(n) * size_t(index_bytes), "tokens");
+}
+
+bool overlap(const void* p, size_t pb, const void* q, size_t qb) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return pb && qb && a < b + qb && b < a + pb;
+}
+
+// Whether rows of V elements may be accessed as vectors.
+bool rows_fit(const void* p, int64_t stride, int32_t dtype, int v) {
+  const size_t bytes = std::min<size_t>(16, size_t(v) * size_of(dtype));
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && size_t(stride) * size_of(dtype) % bytes == 0;
+}
+
+fsp_status launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
+}
+
+template <typename W, typename O>
+void launch_lookup(const LookupArgs& a, bool vec, cudaStream_t st) {
+  const unsigned ctas = unsigned((a.n_tokens + kLookupThreads / 32 - 1) / (kLookupThreads / 32));
+  if (vec)
+    lookup_kernel<W, O, 8><<<ctas, kLookupThreads, 0, st>>>(a);
+  else
+    lookup_kernel<W, O, 1><<<ctas, kLookupThreads, 0, st>>>(a);
+}
+
+fsp_status lookup(const void* weight, int32_t wd, int64_t vocab, int64_t dim, int64_t ws, const void* tokens,
+                  int32_t index_bytes, int64_t n, float scale, void* out, int32_t od, int64_t os, void* stream) {
+  if (vocab < 0 || dim < 0) return fail(FSP_EINVAL, "vocab and dim must be >= 0");
+  fsp_status s = check_tokens(tokens, index_bytes, n);
+  if (s == FSP_OK) s = check_matrix(weight, vocab, dim, ws, wd, "weight");
+  if (s == FSP_OK) s = check_matrix(out, n, dim, os, od, "out");
+  if (s != FSP_OK) return s;
+  const size_t ob = span_bytes(n, dim, os, od);
+  if (overlap(out, ob, weight, span_bytes(vocab, dim, ws, wd)) || overlap(out, ob, tokens, size_t(n) * size_t(index_bytes)))
+    return fail(FSP_EINVAL, "out overlaps an input");
+  if (n == 0 || dim == 0) return FSP_OK;
+  if (vocab == 0) return fail(FSP_EINVAL, "tokens look up an empty table");
+  if (n > int64_t(INT32_MAX) * (kLookupThreads / 32)) return fail(FSP_EUNSUPPORTED, "too many tokens");
+  const LookupArgs a{weight, tokens, out, vocab, dim, ws, os, n, scale, index_bytes};
+  const bool vec = dim % 8 == 0 && rows_fit(weight, ws, wd, 8) && rows_fit(out, os, od, 8);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  using B = __nv_bfloat16;
+  if (wd == FSP_DTYPE_F32)
+    od == FSP_DTYPE_F32 ? launch_lookup<float, float>(a, vec, st) : launch_lookup<float, B>(a, vec, st);
+  else
+    od == FSP_DTYPE_F32 ? launch_lookup<B, float>(a, vec, st) : launch_lookup<B, B>(a, vec, st);
+  return launched("embedding kernel launch");
+}
+
+struct Workspace {   // byte offsets
+  size_t a, b, present, totals, parts, bytes;
+};
+Workspace workspace_of(int64_t vocab, int64_t dim, int64_t n) {
+  Workspace w{};
+  const size_t items = round256(size_t(n) * sizeof(uint2));
+  const size_t chunks = size_t((n + kChunk - 1) / kChunk);
+  w.a = 0;
+  w.b = w.a + items;
+  w.present = w.b + items;
+  w.totals = w.present + round256(size_t((vocab + 31) / 32) * 4);
+  w.parts = w.totals + size_t(kSortCluster) * kBins * 4;
+  w.bytes = w.parts + round256(chunks * 2 * size_t(dim) * 4);
+  return w;
+}
+
+fsp_status check_sizes(int64_t vocab, int64_t dim, int64_t n) {
+  if (vocab < 0 || dim < 0 || n < 0) return fail(FSP_EINVAL, "vocab, dim and n_tokens must be >= 0");
+  if (vocab >= INT32_MAX || n >= INT32_MAX - 4096) return fail(FSP_EUNSUPPORTED, "vocab and n_tokens must be below 2^31");
+  if (dim > (int64_t(1) << 24)) return fail(FSP_EUNSUPPORTED, "dim must be at most 2^24");
+  return FSP_OK;
+}
+
+template <typename G, typename T, int V>
+fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
+  if (!a.accumulate && a.vocab > 0) {
+    zero_rows_kernel<T, V><<<unsigned((a.vocab + kLookupThreads / 32 - 1) / (kLookupThreads / 32)), kLookupThreads, 0, st>>>(a);
+    const fsp_status s = launched("embedding gradient (zero) kernel launch");
+    if (s != FSP_OK) return s;
+  }
+  if (a.n == 0) return FSP_OK;
+  a.cols = 1;
+  while (a.cols < kRowThreads && int64_t(a.cols) * V < a.dim) a.cols *= 2;
+  const int64_t chunks = (int64_t(a.n) + kChunk - 1) / kChunk;
+  const int per_cta = kRowThreads / a.cols;
+  const dim3 grid(unsigned((chunks + per_cta - 1) / per_cta), unsigned((a.dim + int64_t(a.cols) * V - 1) / (int64_t(a.cols) * V)));
+  if (grid.y > 65535u) return fail(FSP_EUNSUPPORTED, "dim is too large for this alignment");
+  sum_rows_kernel<G, T, V><<<grid, kRowThreads, 0, st>>>(a);
+  fsp_status s = launched("embedding gradient (sum) kernel launch");
+  if (s != FSP_OK || chunks == 1) return s;
+  join_rows_kernel<T, V><<<grid, kRowThreads, 0, st>>>(a);
+  return launched("embedding gradient (join) kernel launch");
+}
+
+template <typename G, typename T>
+fsp_status launch_rows_v(RowArgs& a, int v, cudaStream_t st) {
+  return v == 8 ? launch_rows<G, T, 8>(a, st) : v == 4 ? launch_rows<G, T, 4>(a, st) : launch_rows<G, T, 1>(a, st);
+}
+
+fsp_status launch_sort(const SortArgs& s, cudaStream_t st) {
+  static const cudaError_t allowed =
+      cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (token sort)", allowed));
+  const int ctas = s.n > kSortOneCta ? kSortCluster : 1;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_tokens_kernel, s);
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("token sort kernel launch", e));
+}
+
+fsp_status backward(const void* tokens, int32_t index_bytes, int64_t n, const void* grad, int32_t gd, int64_t dim,
+                    int64_t gs, void* weight, int32_t wd, int64_t vocab, int64_t ws, float scale, int64_t padding_idx,
+                    int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  fsp_status s = check_sizes(vocab, dim, n);
+  if (s == FSP_OK) s = check_tokens(tokens, index_bytes, n);
+  if (s == FSP_OK) s = check_matrix(grad, n, dim, gs, gd, "grad_out");
+  if (s == FSP_OK) s = check_matrix(weight, vocab, dim, ws, wd, "grad_weight");
+  if (s != FSP_OK) return s;
+  if (vocab == 0 || dim == 0 || (n == 0 && accumulate)) return FSP_OK;
+  const Workspace w = workspace_of(vocab, dim, n);
+  if (!workspace) return fail(FSP_EINVAL, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 16) return fail(FSP_EINVAL, "workspace is not 16-byte aligned");
+  if (workspace_bytes < w.bytes) return fail(FSP_EINVAL, "workspace is smaller than fsp_embedding_backward_workspace_bytes");
+  s = check_allocation(workspace, w.bytes, "workspace");
+  if (s != FSP_OK) return s;
+  const struct {
+    const void* p;
+    size_t bytes;
+    const char* name;
+  } bufs[] = {{weight, span_bytes(vocab, dim, ws, wd), "grad_weight"},
+              {workspace, w.bytes, "workspace"},
+              {grad, span_bytes(n, dim, gs, gd), "grad_out"},
+              {tokens, size_t(n) * size_t(index_bytes), "tokens"}};
+  for (int i = 0; i < 2; ++i)   // what is written
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+        return fail(FSP_EINVAL, std::string(bufs[i].name) + " overlaps " + bufs[j].name);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(workspace);
+  SortArgs sa{};
+  sa.tokens = tokens;
+  sa.a = reinterpret_cast<uint2*>(base + w.a);
+  sa.b = reinterpret_cast<uint2*>(base + w.b);
+  sa.present = reinterpret_cast<uint32_t*>(base + w.present);
+  sa.totals = reinterpret_cast<uint32_t*>(base + w.totals);
+  sa.vocab = vocab;
+  sa.padding_idx = padding_idx;
+  sa.n = int(n);
+  sa.index_bytes = index_bytes;
+  sa.n_words = int((vocab + 31) / 32);
+  int bits = 1;   // of the largest key, vocab
+  while ((vocab >> bits) != 0) ++bits;
+  sa.passes = (bits + kDigitBits - 1) / kDigitBits;
+  sa.bits = (bits + sa.passes - 1) / sa.passes;
+  s = launch_sort(sa, st);
+  if (s != FSP_OK) return s;
+  RowArgs a{};
+  a.items = sa.passes & 1 ? sa.a : sa.b;
+  a.present = sa.present;
+  a.grad = grad;
+  a.weight = weight;
+  a.parts = reinterpret_cast<float*>(base + w.parts);
+  a.vocab = vocab;
+  a.dim = dim;
+  a.grad_stride = gs;
+  a.weight_stride = ws;
+  a.scale = scale;
+  a.n = int(n);
+  a.accumulate = accumulate != 0;
+  int v = 1;
+  for (int k : {8, 4})
+    if (v == 1 && dim % k == 0 && rows_fit(grad, gs, gd, k) && rows_fit(weight, ws, wd, k)) v = k;
+  using B = __nv_bfloat16;
+  if (gd == FSP_DTYPE_F32)
+    return wd == FSP_DTYPE_F32 ? launch_rows_v<float, float>(a, v, st) : launch_rows_v<float, B>(a, v, st);
+  return wd == FSP_DTYPE_F32 ? launch_rows_v<B, float>(a, v, st) : launch_rows_v<B, B>(a, v, st);
+}
+
+}  // namespace
+
+cudaError_t take_token_error(unsigned* bits) {
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_token_error, sizeof(*bits));
+  const unsigned zero = 0;
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_token_error, &zero, sizeof(zero));
+  return e;
+}
+
+}  // namespace fsp
+
+extern "C" fsp_status fsp_embedding(const void* weight, int32_t weight_dtype, int64_t vocab, int64_t dim,
+                                    int64_t weight_stride, const void* tokens, int32_t index_bytes, int64_t n_tokens,
+                                    float scale, void* out, int32_t out_dtype, int64_t out_stride, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::lookup(weight, weight_dtype, vocab, dim, weight_stride, tokens, index_bytes, n_tokens, scale, out,
+                       out_dtype, out_stride, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_embedding_backward_workspace_bytes(int64_t vocab, int64_t dim, int64_t n_tokens,
+                                                             size_t* bytes) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    if (!bytes) return fsp::fail(FSP_EINVAL, "bytes is NULL");
+    const fsp_status s = fsp::check_sizes(vocab, dim, n_tokens);
+    if (s == FSP_OK) *bytes = fsp::workspace_of(vocab, dim, n_tokens).bytes;
+    return s;
+  });
+}
+
+extern "C" fsp_status fsp_embedding_backward(const void* tokens, int32_t index_bytes, int64_t n_tokens,
+                                             const void* grad_out, int32_t grad_dtype, int64_t dim,
+                                             int64_t grad_stride, void* grad_weight, int32_t weight_dtype,
+                                             int64_t vocab, int64_t weight_stride, float scale, int64_t padding_idx,
+                                             int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                             void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::backward(tokens, index_bytes, n_tokens, grad_out, grad_dtype, dim, grad_stride, grad_weight,
+                         weight_dtype, vocab, weight_stride, scale, padding_idx, accumulate, workspace,
+                         workspace_bytes, cuda_stream);
+  });
+}

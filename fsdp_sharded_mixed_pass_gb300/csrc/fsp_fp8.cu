@@ -1,0 +1,416 @@
+// Matrices in 8-bit floating point with a scale per block of 128 along the
+// summed axis, and their product (sm_103a).
+//
+//   s = 2^e, e = min{e: 448 s >= max|x|};  code = e4m3(x / s)
+//   C = sum_k (code_a s_a) (code_b s_b), summed in fp32
+//
+// A power of two loses no bit of a value, so the codes and the sum are those
+// that exact arithmetic on the inputs gives, up to the order of the fp32 sum.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "fsp_host.h"
+#include "fsp_internal.h"
+#include "fsp_ops.h"
+
+namespace fsp {
+namespace {
+
+constexpr int kBlock = 128;                        // elements that share a scale
+constexpr int kTileBytes = 128 * 128;              // 128 rows x one block of codes
+constexpr int kScaleBytes = 128 * 4;               // 128 rows x four blocks' scales
+
+// Where a matrix's parts lie (the layout fsp_ops.h states).
+struct Fp8Layout {
+  int64_t row_tiles, blocks, pieces;   // rows / 128, cols / 128, cols / 512, rounded up
+  int64_t scale_offset, bytes;
+};
+__host__ __device__ __forceinline__ Fp8Layout layout_of(int64_t rows, int64_t cols) {
+  Fp8Layout l;
+  l.row_tiles = (rows + 127) / 128;
+  l.blocks = (cols + 127) / 128;
+  l.pieces = (cols + 511) / 512;
+  l.scale_offset = l.row_tiles * l.blocks * kTileBytes;
+  l.bytes = l.scale_offset + l.row_tiles * l.pieces * kScaleBytes;
+  return l;
+}
+// Row r's 16-byte piece p (of 8) within a tile; row r's scale of block k within a piece.
+__host__ __device__ __forceinline__ int code_at(int r, int p) { return r * 128 + ((p ^ (r & 7)) << 4); }
+__host__ __device__ __forceinline__ int scale_at(int r, int k) { return (r & 31) * 16 + (r >> 5) * 4 + k; }
+
+// ---- quantisation ------------------------------------------------------------------
+
+constexpr int kQuantThreads = 256;
+
+struct QuantArgs {
+  const void* x;
+  uint8_t* out;
+  int64_t rows, cols, stride;
+  Fp8Layout l;
+};
+
+// The biased exponent of a block's scale from the bits of its largest
+// magnitude: p - 8 for f 2^p with f <= 1.75 (448 = 1.75 x 2^8), else p - 7.
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+  if (top >= 0x7f800000u) return 255;
+  const int b = int(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(b, 0);   // 2^-127 at least (a zero or subnormal largest value too)
+}
+// 1 / s of a scale byte below 255: 2^(127 - byte), a normal number.
+__device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float(uint32_t(254 - min(byte, 253)) << 23); }
+
+__device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+__device__ __forceinline__ uint4 codes16(const float* x, float inv) {
+  return make_uint4(codes4(x, inv), codes4(x + 4, inv), codes4(x + 8, inv), codes4(x + 12, inv));
+}
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// 16 elements of a row from column c, zeros past the last one.
+template <typename T>
+__device__ __forceinline__ void load16(const T* row, int64_t c, int64_t cols, bool vec, float* x) {
+  if (vec && c + 16 <= cols) {
+#pragma unroll
+    for (int k = 0; k < int(sizeof(T)); ++k) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(row + c) + k);
+      const T* t = reinterpret_cast<const T*>(&b);
+#pragma unroll
+      for (int j = 0; j < 16 / int(sizeof(T)); ++j) x[k * (16 / int(sizeof(T))) + j] = widen(t[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = c + j < cols ? widen(row[c + j]) : 0.f;
+  }
+}
+
+// Blocks along the rows of x: a warp per row and four blocks, eight lanes of
+// 16 elements per block.
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __grid_constant__ QuantArgs a, bool vec) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = int64_t(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
+  const int64_t row = w / a.l.pieces, piece = w % a.l.pieces;
+  if (row >= a.rows) return;
+  const int64_t block = piece * 4 + (lane >> 3);
+  float x[16];
+  load16(static_cast<const T*>(a.x) + row * a.stride, piece * 512 + lane * 16, a.cols, vec, x);
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int s = scale_byte(top);
+  const int r = int(row & 127);
+  const int64_t tile = row >> 7;
+  if (block < a.l.blocks)
+    *reinterpret_cast<uint4*>(a.out + (tile * a.l.blocks + block) * kTileBytes + code_at(r, lane & 7)) =
+        codes16(x, inverse_scale(s));
+  uint32_t word = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) word |= uint32_t(__shfl_sync(0xffffffffu, s, k * 8)) << (8 * k);
+  if (lane == 0)
+    *reinterpret_cast<uint32_t*>(a.out + a.l.scale_offset + (tile * a.l.pieces + piece) * kScaleBytes + scale_at(r, 0)) =
+        word;
+}
+
+// Blocks along the columns of x (the transpose's rows): a CTA per 128 rows x 64
+// columns, through shared memory; a.l is the transpose's layout.
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ float tile[128][65];
+  __shared__ uint32_t tops[4][64];
+  const int64_t c0 = int64_t(blockIdx.x) * 64, block = blockIdx.y, r0 = block * 128;
+  for (int i = threadIdx.x; i < 128 * 64; i += kQuantThreads) {
+    const int r = i >> 6, c = i & 63;
+    const bool in = r0 + r < a.rows && c0 + c < a.cols;
+    tile[r][c] = in ? widen(static_cast<const T*>(a.x)[(r0 + r) * a.stride + c0 + c]) : 0.f;
+  }
+  __syncthreads();
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;   // a column, a quarter of its block
+  float x[32];
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    x[j] = tile[q * 32 + j][c];
+    top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+  }
+  tops[q][c] = top;
+  __syncthreads();
+  top = max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c]));
+  const int s = scale_byte(top);
+  const int64_t row = c0 + c;   // of the transpose
+  if (row >= a.cols) return;
+  const int r = int(row & 127);
+  uint8_t* out = a.out + ((row >> 7) * a.l.blocks + block) * kTileBytes;
+  const float inv = inverse_scale(s);
+  *reinterpret_cast<uint4*>(out + code_at(r, 2 * q)) = codes16(x, inv);
+  *reinterpret_cast<uint4*>(out + code_at(r, 2 * q + 1)) = codes16(x + 16, inv);
+  if (q == 0)
+    a.out[a.l.scale_offset + ((row >> 7) * a.l.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))] =
+        uint8_t(s);
+}
+
+__device__ __forceinline__ float scale_value(uint8_t b) {
+  return __uint_as_float(b == 255 ? 0x7fffffffu : b ? uint32_t(b) << 23 : 0x00400000u);
+}
+__device__ __forceinline__ float code_value(uint8_t c) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+__global__ void __launch_bounds__(kQuantThreads) values_kernel(const uint8_t* q, int64_t rows, int64_t cols,
+                                                               Fp8Layout l, float* out) {
+  const int64_t i = int64_t(blockIdx.x) * kQuantThreads + threadIdx.x;
+  if (i >= rows * cols) return;
+  const int64_t row = i / cols, col = i % cols;
+  const int r = int(row & 127), k = int(col & 127);
+  const int64_t tile = row >> 7, block = col >> 7;
+  const uint8_t code = q[(tile * l.blocks + block) * kTileBytes + code_at(r, k >> 4) + (k & 15)];
+  const uint8_t s = q[l.scale_offset + (tile * l.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))];
+  out[i] = code_value(code) * scale_value(s);
+}
+
+// ---- product -------------------------------------------------------------------------
+
+constexpr int kMmThreads = 256;
+
+struct MmArgs {
+  const uint8_t* a;
+  const uint8_t* b;
+  void* c;
+  int64_t m, n, k, c_stride;
+  Fp8Layout la, lb;
+  int accumulate;
+};
+
+// 64 x 64 of C per CTA, 4 x 4 per thread, 32 of k at a time through shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kMmThreads) matmul_kernel(const __grid_constant__ MmArgs g) {
+  __shared__ float as[32][65], bs[32][65];
+  const int64_t m0 = int64_t(blockIdx.y) * 64, n0 = int64_t(blockIdx.x) * 64;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float acc[4][4] = {};
+  for (int64_t k0 = 0; k0 < g.la.blocks * kBlock; k0 += 32) {
+    const int64_t block = k0 >> 7;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * 32; i += kMmThreads) {
+      const int k = i & 31, j = i >> 5, kk = int(k0 & 127) + k;
+      const int64_t ra = m0 + j, rb = n0 + j;
+      float x = 0.f, y = 0.f;
+      if (ra < g.m) {
+        const int r = int(ra & 127);
+        x = code_value(g.a[((ra >> 7) * g.la.blocks + block) * kTileBytes + code_at(r, kk >> 4) + (kk & 15)]) *
+            scale_value(g.a[g.la.scale_offset + ((ra >> 7) * g.la.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))]);
+      }
+      if (rb < g.n) {
+        const int r = int(rb & 127);
+        y = code_value(g.b[((rb >> 7) * g.lb.blocks + block) * kTileBytes + code_at(r, kk >> 4) + (kk & 15)]) *
+            scale_value(g.b[g.lb.scale_offset + ((rb >> 7) * g.lb.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))]);
+      }
+      as[k][j] = x;
+      bs[k][j] = y;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
+      if (r >= g.m || c >= g.n) continue;
+      T* p = static_cast<T*>(g.c) + r * g.c_stride + c;
+      if constexpr (sizeof(T) == 4)
+        *p = g.accumulate ? *p + acc[i][j] : acc[i][j];
+      else
+        *p = __float2bfloat16_rn(acc[i][j]);
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+size_t size_of(int32_t dtype) { return dtype == FSP_DTYPE_F32 ? 4 : 2; }
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+
+fsp_status launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
+}
+
+fsp_status check_dims(std::initializer_list<int64_t> dims) {
+  for (int64_t d : dims)
+    if (d < 0 || d > kMaxDim) return fail(FSP_EINVAL, "a size is out of range");
+  return FSP_OK;
+}
+
+fsp_status check_codes(const void* p, const Fp8Layout& l, const char* name) {
+  if (!p) return fail(FSP_EINVAL, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % 16) return fail(FSP_EINVAL, std::string(name) + " is not 16-byte aligned");
+  return check_allocation(p, size_t(l.bytes), name);
+}
+
+bool overlap(const void* p, int64_t pb, const void* q, int64_t qb) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + uintptr_t(qb) && b < a + uintptr_t(pb);
+}
+
+template <typename T>
+fsp_status run_quantize(const QuantArgs& in, void* out, void* out_t, bool vec, cudaStream_t st) {
+  QuantArgs a = in;
+  if (out) {
+    a.out = static_cast<uint8_t*>(out);
+    a.l = layout_of(a.rows, a.cols);
+    const int64_t ctas = (a.rows * a.l.pieces + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+    if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
+    quantize_rows_kernel<T><<<unsigned(ctas), kQuantThreads, 0, st>>>(a, vec);
+    const fsp_status s = launched("quantisation kernel launch");
+    if (s != FSP_OK) return s;
+  }
+  if (out_t) {
+    a.out = static_cast<uint8_t*>(out_t);
+    a.l = layout_of(a.cols, a.rows);
+    if (a.l.blocks > 65535) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
+    quantize_cols_kernel<T><<<dim3(unsigned((a.cols + 63) / 64), unsigned(a.l.blocks)), kQuantThreads, 0, st>>>(a);
+    return launched("transposing quantisation kernel launch");
+  }
+  return FSP_OK;
+}
+
+fsp_status quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, void* out, void* out_t,
+                    void* stream) {
+  fsp_status s = check_dims({rows, cols});
+  if (s != FSP_OK) return s;
+  if (dtype != FSP_DTYPE_F32 && dtype != FSP_DTYPE_BF16) return fail(FSP_EINVAL, "unknown dtype of x");
+  if (stride < cols || (rows > 0 && stride > (int64_t(1) << 58) / rows)) return fail(FSP_EINVAL, "x's rows overlap or their stride is out of range");
+  if (rows == 0 || cols == 0) return FSP_OK;
+  if (!out && !out_t) return fail(FSP_EINVAL, "out and out_t are both NULL");
+  if (!x) return fail(FSP_EINVAL, "x is NULL");
+  if (reinterpret_cast<uintptr_t>(x) % size_of(dtype)) return fail(FSP_EINVAL, "x is not aligned to its elements");
+  const int64_t xb = ((rows - 1) * stride + cols) * int64_t(size_of(dtype));
+  s = check_allocation(x, size_t(xb), "x");
+  const Fp8Layout l = layout_of(rows, cols), lt = layout_of(cols, rows);
+  if (s == FSP_OK && out) s = check_codes(out, l, "out");
+  if (s == FSP_OK && out_t) s = check_codes(out_t, lt, "out_t");
+  if (s != FSP_OK) return s;
+  if (overlap(out, l.bytes, x, xb) || overlap(out_t, lt.bytes, x, xb) || overlap(out, l.bytes, out_t, lt.bytes))
+    return fail(FSP_EINVAL, "an output overlaps another buffer");
+  QuantArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.stride = stride;
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && size_t(stride) * size_of(dtype) % 16 == 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dtype == FSP_DTYPE_F32 ? run_quantize<float>(a, out, out_t, vec, st)
+                                : run_quantize<__nv_bfloat16>(a, out, out_t, vec, st);
+}
+
+fsp_status values(const void* q, int64_t rows, int64_t cols, float* out, void* stream) {
+  fsp_status s = check_dims({rows, cols});
+  if (s != FSP_OK || rows == 0 || cols == 0) return s;
+  const Fp8Layout l = layout_of(rows, cols);
+  s = check_codes(q, l, "q");
+  if (s != FSP_OK) return s;
+  if (!out) return fail(FSP_EINVAL, "out is NULL");
+  if (reinterpret_cast<uintptr_t>(out) % 4) return fail(FSP_EINVAL, "out is not aligned to its elements");
+  s = check_allocation(out, size_t(rows) * size_t(cols) * 4, "out");
+  if (s != FSP_OK) return s;
+  if (overlap(q, l.bytes, out, rows * cols * 4)) return fail(FSP_EINVAL, "out overlaps q");
+  const int64_t ctas = (rows * cols + kQuantThreads - 1) / kQuantThreads;
+  if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
+  values_kernel<<<unsigned(ctas), kQuantThreads, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint8_t*>(q), rows,
+                                                                                          cols, l, out);
+  return launched("8-bit values kernel launch");
+}
+
+fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
+                  int64_t c_stride, int32_t accumulate, void* stream) {
+  fsp_status s = check_dims({m, n, k});
+  if (s != FSP_OK) return s;
+  if (dtype != FSP_DTYPE_F32 && dtype != FSP_DTYPE_BF16) return fail(FSP_EINVAL, "unknown dtype of c");
+  if (accumulate && dtype != FSP_DTYPE_F32) return fail(FSP_EUNSUPPORTED, "accumulate adds to fp32 only");
+  if (c_stride < n || (m > 0 && c_stride > (int64_t(1) << 58) / m)) return fail(FSP_EINVAL, "c's rows overlap or their stride is out of range");
+  if (m == 0 || n == 0) return FSP_OK;
+  if (!c) return fail(FSP_EINVAL, "c is NULL");
+  if (reinterpret_cast<uintptr_t>(c) % size_of(dtype)) return fail(FSP_EINVAL, "c is not aligned to its elements");
+  const int64_t cb = ((m - 1) * c_stride + n) * int64_t(size_of(dtype));
+  s = check_allocation(c, size_t(cb), "c");
+  if (s != FSP_OK) return s;
+  MmArgs g{};
+  g.la = layout_of(m, k);
+  g.lb = layout_of(n, k);
+  if (k > 0) {
+    s = check_codes(a, g.la, "a");
+    if (s == FSP_OK) s = check_codes(b, g.lb, "b");
+    if (s != FSP_OK) return s;
+    if (overlap(c, cb, a, g.la.bytes) || overlap(c, cb, b, g.lb.bytes)) return fail(FSP_EINVAL, "c overlaps an operand");
+  }
+  g.a = static_cast<const uint8_t*>(a);
+  g.b = static_cast<const uint8_t*>(b);
+  g.c = c;
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  g.c_stride = c_stride;
+  g.accumulate = accumulate != 0;
+  const dim3 grid(unsigned((n + 63) / 64), unsigned((m + 63) / 64));
+  if (grid.y > 65535u) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == FSP_DTYPE_F32)
+    matmul_kernel<float><<<grid, kMmThreads, 0, st>>>(g);
+  else
+    matmul_kernel<__nv_bfloat16><<<grid, kMmThreads, 0, st>>>(g);
+  return launched("8-bit product kernel launch");
+}
+
+}  // namespace
+}  // namespace fsp
+
+extern "C" fsp_status fsp_fp8_bytes(int64_t rows, int64_t cols, size_t* bytes, size_t* scale_offset) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    if (!bytes || !scale_offset) return fsp::fail(FSP_EINVAL, "bytes or scale_offset is NULL");
+    const fsp_status s = fsp::check_dims({rows, cols});
+    if (s != FSP_OK) return s;
+    const fsp::Fp8Layout l = fsp::layout_of(rows, cols);
+    *bytes = size_t(l.bytes);
+    *scale_offset = size_t(l.scale_offset);
+    return FSP_OK;
+  });
+}
+
+extern "C" fsp_status fsp_fp8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride,
+                                       void* out, void* out_t, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::quantize(x, dtype, rows, cols, stride, out, out_t, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_fp8_values(const void* q, int64_t rows, int64_t cols, float* out, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::values(q, rows, cols, out, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_fp8_matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c,
+                                     int32_t dtype, int64_t c_stride, int32_t accumulate, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::matmul(a, b, m, n, k, c, dtype, c_stride, accumulate, cuda_stream);
+  });
+}

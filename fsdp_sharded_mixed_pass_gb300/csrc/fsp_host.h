@@ -57,5 +57,8 @@ fsp_status run_clipped_passes(const fsp_plan* p, StepArgs& a, float max_norm, fl
 fsp_status clipped_empty(float* norm_out, void* stream);
 // *step_dev += 1 on `stream` (one thread).
 fsp_status advance_step(int64_t* step_dev, void* stream);
+// Reads and clears the error bits of the embedding kernels (their part of the
+// device error word).
+cudaError_t take_token_error(unsigned* bits);
 
 }  // namespace fsp

@@ -13,6 +13,7 @@
 #include <string>
 #include <vector>
 
+#include "fsp_adamw_kernels.cuh"
 #include "fsp_host.h"
 #include "fsp_internal.h"
 #include "fsp_kernels.cuh"
@@ -920,7 +921,10 @@ extern "C" fsp_status fsp_device_error(uint32_t* bits) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(fsp::g_fsp_device_error, &zero, sizeof(zero));
     if (e != cudaSuccess) return fsp::fail(FSP_ECUDA, fsp::cuda_msg("clearing the device error word", e));
-    *bits = v;
+    unsigned int token = 0;
+    e = fsp::take_token_error(&token);
+    if (e != cudaSuccess) return fsp::fail(FSP_ECUDA, fsp::cuda_msg("reading the embedding's error word", e));
+    *bits = v | token;
     return FSP_OK;
   });
 }

@@ -17,7 +17,7 @@ FSP_OK, FSP_EINVAL, FSP_ENOMEM, FSP_ECUDA, FSP_EUNSUPPORTED = range(5)
 MODES = {"fsdp2": 0, "distopt": 1, "hsdp": 2}
 DTYPES = {"f32": 0, "bf16": 1}
 
-# Every symbol include/fsp.h declares.
+# Every symbol include/fsp.h declares (ops.EXPORTS: include/fsp_ops.h's).
 EXPORTS = ("fsp_plan_layout", "fsp_plan_layout_hsdp", "fsp_plan_layout_params", "fsp_plan_param", "fsp_plan_info_get",
            "fsp_plan_segment", "fsp_plan_ledger", "fsp_plan_tiles", "fsp_plan_round_order", "fsp_plan_destroy",
            "fsp_sharded_step", "fsp_sharded_step_device_t", "fsp_sharded_step_clipped", "fsp_sharded_step_debug",
@@ -133,6 +133,8 @@ def lib():
     L.fsp_status_string.restype = ctypes.c_char_p
     L.fsp_last_error.argtypes = []
     L.fsp_last_error.restype = ctypes.c_char_p
+    from . import ops
+    ops.bind(L)
     _lib = L
     return L
 
