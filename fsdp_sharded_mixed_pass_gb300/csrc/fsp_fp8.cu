@@ -24,6 +24,14 @@ constexpr int kBlock = 128;                        // elements that share a scal
 constexpr int kTileBytes = 128 * 128;              // 128 rows x one block of codes
 constexpr int kScaleBytes = 128 * 4;               // 128 rows x four blocks' scales
 
+}  // namespace
+}  // namespace fsp
+
+#include "fsp_fp8_mma.cuh"
+
+namespace fsp {
+namespace {
+
 // Where a matrix's parts lie (the layout fsp_ops.h states).
 struct Fp8Layout {
   int64_t row_tiles, blocks, pieces;   // rows / 128, cols / 128, cols / 512, rounded up
@@ -178,68 +186,6 @@ __global__ void __launch_bounds__(kQuantThreads) values_kernel(const uint8_t* q,
   out[i] = code_value(code) * scale_value(s);
 }
 
-// ---- product -------------------------------------------------------------------------
-
-constexpr int kMmThreads = 256;
-
-struct MmArgs {
-  const uint8_t* a;
-  const uint8_t* b;
-  void* c;
-  int64_t m, n, k, c_stride;
-  Fp8Layout la, lb;
-  int accumulate;
-};
-
-// 64 x 64 of C per CTA, 4 x 4 per thread, 32 of k at a time through shared memory.
-template <typename T>
-__global__ void __launch_bounds__(kMmThreads) matmul_kernel(const __grid_constant__ MmArgs g) {
-  __shared__ float as[32][65], bs[32][65];
-  const int64_t m0 = int64_t(blockIdx.y) * 64, n0 = int64_t(blockIdx.x) * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < g.la.blocks * kBlock; k0 += 32) {
-    const int64_t block = k0 >> 7;
-    __syncthreads();
-    for (int i = threadIdx.x; i < 64 * 32; i += kMmThreads) {
-      const int k = i & 31, j = i >> 5, kk = int(k0 & 127) + k;
-      const int64_t ra = m0 + j, rb = n0 + j;
-      float x = 0.f, y = 0.f;
-      if (ra < g.m) {
-        const int r = int(ra & 127);
-        x = code_value(g.a[((ra >> 7) * g.la.blocks + block) * kTileBytes + code_at(r, kk >> 4) + (kk & 15)]) *
-            scale_value(g.a[g.la.scale_offset + ((ra >> 7) * g.la.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))]);
-      }
-      if (rb < g.n) {
-        const int r = int(rb & 127);
-        y = code_value(g.b[((rb >> 7) * g.lb.blocks + block) * kTileBytes + code_at(r, kk >> 4) + (kk & 15)]) *
-            scale_value(g.b[g.lb.scale_offset + ((rb >> 7) * g.lb.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))]);
-      }
-      as[k][j] = x;
-      bs[k][j] = y;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
-      if (r >= g.m || c >= g.n) continue;
-      T* p = static_cast<T*>(g.c) + r * g.c_stride + c;
-      if constexpr (sizeof(T) == 4)
-        *p = g.accumulate ? *p + acc[i][j] : acc[i][j];
-      else
-        *p = __float2bfloat16_rn(acc[i][j]);
-    }
-}
-
 // ---- host ----------------------------------------------------------------------------
 
 size_t size_of(int32_t dtype) { return dtype == FSP_DTYPE_F32 ? 4 : 2; }
@@ -336,6 +282,37 @@ fsp_status values(const void* q, int64_t rows, int64_t cols, float* out, void* s
   return launched("8-bit values kernel launch");
 }
 
+int sm_count() {
+  static const int n = [] {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 0;
+    return sms;
+  }();
+  return n;
+}
+
+template <int BN, bool kSwap, typename T>
+fsp_status launch_product_of(const MmArgs& g, cudaStream_t st) {
+  constexpr int kSmem = MmCfg<BN>::kSmem;
+  static const cudaError_t allowed =
+      cudaFuncSetAttribute(fp8_product_kernel<BN, kSwap, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (8-bit product)", allowed));
+  const int sms = sm_count();
+  if (sms <= 0) return fail(FSP_ECUDA, "cannot read the number of SMs");
+  const unsigned grid = unsigned(std::min<int64_t>(sms, g.tiles_p * g.tiles_q));
+  fp8_product_kernel<BN, kSwap, T><<<grid, kMmThreads, kSmem, st>>>(g);
+  return launched("8-bit product kernel launch");
+}
+
+template <int BN, bool kSwap>
+fsp_status launch_product(MmArgs& g, int32_t dtype, cudaStream_t st) {
+  g.tiles_q = (g.nq + BN - 1) / BN;
+  return dtype == FSP_DTYPE_F32 ? launch_product_of<BN, kSwap, float>(g, st)
+                                : launch_product_of<BN, kSwap, __nv_bfloat16>(g, st);
+}
+
 fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
                   int64_t c_stride, int32_t accumulate, void* stream) {
   fsp_status s = check_dims({m, n, k});
@@ -349,34 +326,47 @@ fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k,
   const int64_t cb = ((m - 1) * c_stride + n) * int64_t(size_of(dtype));
   s = check_allocation(c, size_t(cb), "c");
   if (s != FSP_OK) return s;
-  MmArgs g{};
-  g.la = layout_of(m, k);
-  g.lb = layout_of(n, k);
-  if (k > 0) {
-    s = check_codes(a, g.la, "a");
-    if (s == FSP_OK) s = check_codes(b, g.lb, "b");
-    if (s != FSP_OK) return s;
-    if (overlap(c, cb, a, g.la.bytes) || overlap(c, cb, b, g.lb.bytes)) return fail(FSP_EINVAL, "c overlaps an operand");
+  const Fp8Layout la = layout_of(m, k), lb = layout_of(n, k);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (k == 0) {   // the sum of nothing
+    if (accumulate) return FSP_OK;
+    const cudaError_t e = cudaMemset2DAsync(c, size_t(c_stride) * size_of(dtype), 0, size_t(n) * size_of(dtype), size_t(m), st);
+    return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("cudaMemset2DAsync", e));
   }
-  g.a = static_cast<const uint8_t*>(a);
-  g.b = static_cast<const uint8_t*>(b);
+  s = check_codes(a, la, "a");
+  if (s == FSP_OK) s = check_codes(b, lb, "b");
+  if (s != FSP_OK) return s;
+  if (overlap(c, cb, a, la.bytes) || overlap(c, cb, b, lb.bytes)) return fail(FSP_EINVAL, "c overlaps an operand");
+  // Up to 64 rows of a: b's rows fill the 128 rows of the tiles, a's their columns.
+  const bool swap = m <= 64;
+  MmArgs g{};
+  g.p = static_cast<const uint8_t*>(swap ? b : a);
+  g.q = static_cast<const uint8_t*>(swap ? a : b);
   g.c = c;
-  g.m = m;
-  g.n = n;
-  g.k = k;
+  g.np = swap ? n : m;
+  g.nq = swap ? m : n;
+  g.blocks = la.blocks;
+  g.pieces = la.pieces;
+  g.p_scales = (swap ? lb : la).scale_offset;
+  g.q_scales = (swap ? la : lb).scale_offset;
   g.c_stride = c_stride;
   g.accumulate = accumulate != 0;
-  const dim3 grid(unsigned((n + 63) / 64), unsigned((m + 63) / 64));
-  if (grid.y > 65535u) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == FSP_DTYPE_F32)
-    matmul_kernel<float><<<grid, kMmThreads, 0, st>>>(g);
-  else
-    matmul_kernel<__nv_bfloat16><<<grid, kMmThreads, 0, st>>>(g);
-  return launched("8-bit product kernel launch");
+  g.vec = reinterpret_cast<uintptr_t>(c) % 16 == 0 && size_t(c_stride) * size_of(dtype) % 16 == 0;
+  g.tiles_p = (g.np + kTileP - 1) / kTileP;
+  if (!swap) return launch_product<192, false>(g, dtype, st);
+  if (m <= 16) return launch_product<16, true>(g, dtype, st);
+  return m <= 32 ? launch_product<32, true>(g, dtype, st) : launch_product<64, true>(g, dtype, st);
 }
 
 }  // namespace
+
+cudaError_t take_fp8_error(unsigned* bits) {
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_fp8_error, sizeof(*bits));
+  const unsigned zero = 0;
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof(zero));
+  return e;
+}
+
 }  // namespace fsp
 
 extern "C" fsp_status fsp_fp8_bytes(int64_t rows, int64_t cols, size_t* bytes, size_t* scale_offset) {

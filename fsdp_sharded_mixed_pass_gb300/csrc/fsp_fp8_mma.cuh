@@ -1,0 +1,401 @@
+// The product of two 8-bit block-scaled matrices on the tensor cores (sm_103a):
+//
+//   D[p][q] = sum_k (P[p][k] s_P[p][k / 128]) (Q[q][k] s_Q[q][k / 128])
+//
+// tcgen05.mma kind::mxf8f6f4 multiplies e4m3 codes and applies an 8-bit
+// exponent per row and 32 elements of k inside the tensor core, so a scale per
+// 128 costs nothing: its byte is named for all four instructions of a block.
+//
+// A persistent CTA per SM, six warps:
+//   warp 0     producer: bulk copies of the operands' tiles (stored in the order
+//              that shared memory wants them, so each is one run of bytes) and
+//              of their scales into a ring of stages, a block of 128 of k each;
+//   warp 1     issues the copies of a stage's scales to tensor memory and its
+//              four MMAs; owns the tensor memory;
+//   warps 2-5  read a finished accumulator (32 lanes of tensor memory each),
+//              round it and write C, while the next tile is being summed in the
+//              other accumulator.
+// Every mbarrier wait gives up after about 2 s, records a bit in the error word
+// and ends its role; the CTA then lets its copies land and frees its memory.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fsp {
+namespace {
+
+constexpr unsigned kErrProduct = 32u;   // a wait of the product kernel ran out
+__device__ unsigned int g_fp8_error = 0;
+
+// ---- PTX ----------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// False once about 2 s have passed.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t - t0 > 2000000000ull) break;
+    }
+  }
+  atomicOr(&g_fp8_error, kErrProduct);
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add))
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptors.  Operands: rows of 128 bytes in the 128-byte
+// swizzle, eight rows (1024 bytes) apart from the next eight.  Scales: 32 rows of
+// 16 bytes, no swizzle, eight rows (128 bytes) apart from the next eight.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(1) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+         uint64_t(2) << 61;
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(128 >> 4) << 32 | uint64_t(1) << 46;
+}
+
+// ---- the kernel ----------------------------------------------------------------------
+
+constexpr int kMmThreads = 192;
+constexpr int kTileP = 128;
+constexpr int kGroupP = 32;   // tiles of P walked before the next tile of Q
+
+struct MmArgs {
+  const uint8_t* p;
+  const uint8_t* q;
+  void* c;
+  int64_t np, nq;             // rows of P and Q
+  int64_t blocks;             // of 128 along k
+  int64_t pieces;             // of 512 along k (scales)
+  int64_t p_scales, q_scales; // byte offsets of the scales
+  int64_t c_stride;
+  int64_t tiles_p, tiles_q;
+  int accumulate;
+  int vec;                    // C's rows are 16-byte aligned
+};
+
+// BN: rows of Q per tile.  kSwap: C is written transposed (C[q][p]).
+template <int BN>
+struct MmCfg {
+  static constexpr int kScaleChunks = BN > 128 ? 2 : 1;            // 128-row scale pieces a tile of Q touches
+  static constexpr int kScaleCols = 4 + 4 * kScaleChunks;          // tensor memory columns of a stage's scales
+  static constexpr int kStageBytes = kTileP * 128 + BN * 128 + 512 + 512 * kScaleChunks;
+  static constexpr int kEpilogue = 4 * 32 * 144;                   // four warps, 32 rows of up to 128 bytes (+ 16)
+  static constexpr int kFixed = 1024 + 256 + kEpilogue;            // alignment, barriers, epilogue
+  static constexpr int kFit = (232448 - kFixed) / kStageBytes;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kAccCols = BN < 32 ? 32 : BN;
+  static constexpr int kScaleBase = 2 * kAccCols;
+  static constexpr int kColsUsed = kScaleBase + kStages * kScaleCols;
+  static constexpr int kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
+  static constexpr int kSmem = kFixed + kStages * kStageBytes;
+  static_assert(kColsUsed <= 512, "tensor memory");
+  static_assert(BN % 16 == 0 && BN <= 256 && (BN * 128) % 1024 == 0, "tile of Q");
+};
+
+struct TileAt {
+  int64_t p, q;
+};
+// Tiles of P in groups, all of a group before the next tile of Q: the CTAs that
+// run at one time share few tiles of each operand.
+__device__ __forceinline__ TileAt tile_at(const MmArgs& g, int64_t t) {
+  const int64_t per_group = kGroupP * g.tiles_q;
+  const int64_t group = t / per_group, rest = t - group * per_group;
+  const int64_t size = min(int64_t(kGroupP), g.tiles_p - group * kGroupP);
+  return {group * kGroupP + rest % size, rest / size};
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Rows p0 .. p0 + 31 (a lane each), columns q0 .. q0 + 31 of C from registers,
+// through this warp's part of shared memory so that rows are written in runs.
+template <typename T>
+__device__ __forceinline__ void write_block(const MmArgs& g, const uint32_t* acc, unsigned char* stage, int lane, int64_t p0,
+                                            int64_t q0) {
+  constexpr int kPitch = int(sizeof(T)) * 32 + 16;
+  constexpr int kVecs = int(sizeof(T)) * 2;   // 16-byte vectors of a row
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPitch);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    if constexpr (sizeof(T) == 4)
+      mine[j] = make_uint4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+    else
+      mine[j] = make_uint4(pack_bf16(acc[8 * j], acc[8 * j + 1]), pack_bf16(acc[8 * j + 2], acc[8 * j + 3]),
+                           pack_bf16(acc[8 * j + 4], acc[8 * j + 5]), pack_bf16(acc[8 * j + 6], acc[8 * j + 7]));
+  }
+  __syncwarp();
+  T* c = static_cast<T*>(g.c);
+  if (g.vec && q0 + 32 <= g.nq) {
+    constexpr int kRows = 32 / kVecs;   // rows of one pass of the warp
+    const int r = lane / kVecs, v = lane % kVecs;
+#pragma unroll
+    for (int i = 0; i < 32; i += kRows) {
+      if (p0 + i + r >= g.np) continue;
+      uint4 x = *reinterpret_cast<const uint4*>(stage + (i + r) * kPitch + v * 16);
+      uint4* dst = reinterpret_cast<uint4*>(c + (p0 + i + r) * g.c_stride + q0) + v;
+      if constexpr (sizeof(T) == 4) {
+        if (g.accumulate) {
+          const float4 o = *reinterpret_cast<const float4*>(dst);
+          x = make_uint4(__float_as_uint(__uint_as_float(x.x) + o.x), __float_as_uint(__uint_as_float(x.y) + o.y),
+                         __float_as_uint(__uint_as_float(x.z) + o.z), __float_as_uint(__uint_as_float(x.w) + o.w));
+        }
+      }
+      *dst = x;
+    }
+  } else if (q0 + lane < g.nq) {
+    const int rows = int(min(int64_t(32), g.np - p0));
+    for (int i = 0; i < rows; ++i) {
+      T x = *reinterpret_cast<const T*>(stage + i * kPitch + lane * int(sizeof(T)));
+      T* dst = c + (p0 + i) * g.c_stride + q0 + lane;
+      if constexpr (sizeof(T) == 4) {
+        if (g.accumulate) x += *dst;
+      }
+      *dst = x;
+    }
+  }
+  __syncwarp();
+}
+
+template <int BN, bool kSwap, typename T>
+__global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid_constant__ MmArgs g) {
+  using Cfg = MmCfg<BN>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ unsigned char raw[];
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  unsigned char* smem = raw + (base - smem_addr(raw));
+  const uint32_t at_p = base, at_q = at_p + S * kTileP * 128, at_sp = at_q + S * BN * 128;
+  const uint32_t at_sq = at_sp + S * 512, at_epi = at_sq + S * 512 * Cfg::kScaleChunks;
+  const uint32_t bars = at_epi + Cfg::kEpilogue;
+  const uint32_t full = bars, empty = full + 8 * S, acc_full = empty + 8 * S, acc_empty = acc_full + 16;
+  const uint32_t drained = acc_empty + 16, slot = drained + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_empty + 8 * b, 4);
+    }
+    mbar_init(drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  if (warp == 1) tmem_alloc(slot, Cfg::kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - base));
+  const int64_t tiles = g.tiles_p * g.tiles_q;
+  const int blocks = int(g.blocks);
+
+  if (warp == 0 && lane == 0) {
+    // ---- producer ----
+    int s = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const TileAt tile = tile_at(g, t);
+      const int64_t q0 = tile.q * BN, q_tile = q0 >> 7;
+      const int64_t q_tiles = (g.nq + 127) >> 7;
+      // rows of Q: from q_tile's row (q0 mod 128), and the next 128-row tile's first ones
+      const int first = min(BN, 128 - int(q0 & 127));
+      const int second = q_tile + 1 < q_tiles ? BN - first : 0;
+      const int sq_chunks = min(Cfg::kScaleChunks, int(q_tiles - q_tile));
+      const uint32_t bytes = uint32_t(kTileP + first + second) * 128u + 512u * uint32_t(1 + sq_chunks);
+      const uint8_t* src_p = g.p + tile.p * g.blocks * kTileBytes;
+      const uint8_t* src_q = g.q + q_tile * g.blocks * kTileBytes + (q0 & 127) * 128;
+      const uint8_t* src_q2 = g.q + (q_tile + 1) * g.blocks * kTileBytes;
+      const uint8_t* src_sp = g.p + g.p_scales + tile.p * g.pieces * kScaleBytes;
+      const uint8_t* src_sq = g.q + g.q_scales + q_tile * g.pieces * kScaleBytes;
+      for (int k = 0; k < blocks; ++k) {
+        if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1u))) break;
+        const uint32_t bar = full + 8 * s;
+        mbar_expect(bar, bytes);
+        bulk_load(at_p + s * kTileP * 128, src_p + int64_t(k) * kTileBytes, kTileP * 128, bar);
+        bulk_load(at_q + s * BN * 128, src_q + int64_t(k) * kTileBytes, first * 128, bar);
+        if (second) bulk_load(at_q + s * BN * 128 + first * 128, src_q2 + int64_t(k) * kTileBytes, second * 128, bar);
+        const int64_t piece = int64_t(k >> 2) * kScaleBytes;
+        bulk_load(at_sp + s * 512, src_sp + piece, 512, bar);
+        for (int j = 0; j < sq_chunks; ++j)
+          bulk_load(at_sq + (s * Cfg::kScaleChunks + j) * 512, src_sq + j * g.pieces * kScaleBytes + piece, 512, bar);
+        ++issued;
+        if (++s == S) s = 0, phase ^= 1u;
+      }
+    }
+    // the copies in flight land before the CTA's memory is given back
+    for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
+      if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
+  } else if (warp == 1 && lane == 0) {
+    // ---- scales and MMAs ----
+    const uint32_t idesc = uint32_t(BN >> 3) << 17 | 1u << 23 | uint32_t(kTileP >> 4) << 24;
+    int s = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const uint32_t sq_shift = uint32_t((tile_at(g, t).q * BN) & 127) / 32;   // columns of the scale pieces before q0
+      if (!(ok = mbar_wait(acc_empty + 8 * buf, acc_phase ^ 1u))) break;
+      fence_after();
+      const uint32_t d = tmem + buf * Cfg::kAccCols;
+      for (int k = 0; k < blocks; ++k) {
+        if (!(ok = mbar_wait(full + 8 * s, phase))) break;
+        fence_after();
+        const uint32_t sp = tmem + Cfg::kScaleBase + s * Cfg::kScaleCols, sq = sp + 4;
+        scale_copy(sp, scale_desc(at_sp + s * 512));
+#pragma unroll
+        for (int j = 0; j < Cfg::kScaleChunks; ++j)
+          scale_copy(sq + 4 * j, scale_desc(at_sq + (s * Cfg::kScaleChunks + j) * 512));
+        const uint32_t id = idesc | uint32_t(k & 3) << 4 | uint32_t(k & 3) << 29;   // which byte of a row's four
+        const uint64_t dp = operand_desc(at_p + s * kTileP * 128), dq = operand_desc(at_q + s * BN * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_scaled(d, dp + 2 * i, dq + 2 * i, id, sp, sq + sq_shift, (k | i) != 0);
+        mma_commit(empty + 8 * s);
+        if (++s == S) s = 0, phase ^= 1u;
+      }
+      mma_commit(acc_full + 8 * buf);   // (on a wait that ran out too: what was issued completes)
+      buf ^= 1;
+      if (buf == 0) acc_phase ^= 1u;
+    }
+    mma_commit(drained);   // nothing of this thread runs on when the tensor memory is given back
+    mbar_wait(drained, 0);
+  } else if (warp >= 2) {
+    // ---- epilogue ----
+    const int quarter = warp & 3;   // the tensor memory lanes this warp may read
+    unsigned char* stage = smem + (at_epi - base) + (warp - 2) * (Cfg::kEpilogue / 4);
+    int buf = 0;
+    uint32_t phase = 0;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const TileAt tile = tile_at(g, t);
+      if (!mbar_wait(acc_full + 8 * buf, phase)) break;
+      fence_after();
+      const uint32_t d = tmem + buf * Cfg::kAccCols + (uint32_t(quarter * 32) << 16);
+      const int64_t p0 = tile.p * kTileP + quarter * 32, q0 = tile.q * BN;
+      if constexpr (kSwap) {
+        // a lane holds one row of P: 32 lanes are 32 neighbours of a row of C
+        T* c = static_cast<T*>(g.c) + p0 + lane;
+#pragma unroll
+        for (int j0 = 0; j0 < BN; j0 += 16) {
+          uint32_t acc[16];
+          tmem_load16(d + j0, acc);
+          tmem_wait_loads();
+          if (p0 + lane < g.np) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (q0 + j0 + j >= g.nq) break;
+              T* dst = c + (q0 + j0 + j) * g.c_stride;
+              if constexpr (sizeof(T) == 4)
+                *dst = g.accumulate ? *dst + __uint_as_float(acc[j]) : __uint_as_float(acc[j]);
+              else
+                *dst = __float2bfloat16_rn(__uint_as_float(acc[j]));
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        for (int j0 = 0; j0 < BN; j0 += 32) {
+          uint32_t acc[32];
+          tmem_load32(d + j0, acc);
+          tmem_wait_loads();
+          if (p0 < g.np && q0 + j0 < g.nq) write_block<T>(g, acc, stage, lane, p0, q0 + j0);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+      buf ^= 1;
+      if (buf == 0) phase ^= 1u;
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free(tmem, Cfg::kCols);
+}
+
+}  // namespace
+}  // namespace fsp

@@ -60,5 +60,7 @@ fsp_status advance_step(int64_t* step_dev, void* stream);
 // Reads and clears the error bits of the embedding kernels (their part of the
 // device error word).
 cudaError_t take_token_error(unsigned* bits);
+// The same for the 8-bit product's kernels.
+cudaError_t take_fp8_error(unsigned* bits);
 
 }  // namespace fsp

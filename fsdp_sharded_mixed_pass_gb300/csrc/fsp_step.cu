@@ -924,7 +924,10 @@ extern "C" fsp_status fsp_device_error(uint32_t* bits) {
     unsigned int token = 0;
     e = fsp::take_token_error(&token);
     if (e != cudaSuccess) return fsp::fail(FSP_ECUDA, fsp::cuda_msg("reading the embedding's error word", e));
-    *bits = v | token;
+    unsigned int product = 0;
+    e = fsp::take_fp8_error(&product);
+    if (e != cudaSuccess) return fsp::fail(FSP_ECUDA, fsp::cuda_msg("reading the 8-bit product's error word", e));
+    *bits = v | token | product;
     return FSP_OK;
   });
 }

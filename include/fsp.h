@@ -507,7 +507,7 @@ fsp_status fsp_sharded_step_noalloc(const fsp_plan* plan, const void* const* gra
  * are bounded (about 2 s); one that runs out sets a bit here (1: the storer
  * waited for the consumers' results, 2: the producer waited for a free
  * stage; 4: the self-test below; 8: a device-resident update index below 1; 16: a token
- * outside an embedding's table, fsp_ops.h),
+ * outside an embedding's table, 32: a wait of the 8-bit product's kernel, both fsp_ops.h),
  * lets its copies land and ends the kernel,
  * leaving that step's results incomplete.  0 means every step since the last
  * read completed normally. */
