@@ -20,7 +20,6 @@
 namespace fsp {
 namespace {
 
-constexpr int kBlock = 128;                        // elements that share a scale
 constexpr int kTileBytes = 128 * 128;              // 128 rows x one block of codes
 constexpr int kScaleBytes = 128 * 4;               // 128 rows x four blocks' scales
 
@@ -313,6 +312,54 @@ fsp_status launch_product(MmArgs& g, int32_t dtype, cudaStream_t st) {
                                 : launch_product_of<BN, kSwap, __nv_bfloat16>(g, st);
 }
 
+// Pairs of CTAs that can run at one time: a pair's SMs share a GPC, so this can be
+// fewer than half of the SMs, and a pair that had to wait for others to finish
+// would double a launch's time.
+template <typename T>
+fsp_status resident_pairs(int* pairs) {
+  struct Got {
+    cudaError_t e;
+    int pairs;
+  };
+  static const Got got = [] {
+    cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::kSmem);
+    int n = 0;
+    if (e == cudaSuccess) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(unsigned(2 * std::max(1, sm_count() / 2)));
+      cfg.blockDim = dim3(kMmThreads);
+      cfg.dynamicSmemBytes = PairCfg::kSmem;
+      cudaLaunchAttribute attr{};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel<T>, &cfg);
+    }
+    return Got{e, n};
+  }();
+  if (got.e != cudaSuccess || got.pairs < 1) return fail(FSP_ECUDA, cuda_msg("8-bit product set-up", got.e));
+  *pairs = got.pairs;
+  return FSP_OK;
+}
+
+template <typename T>
+fsp_status launch_pairs_of(const MmArgs& g, cudaStream_t st) {
+  int pairs = 0;
+  const fsp_status s = resident_pairs<T>(&pairs);
+  if (s != FSP_OK) return s;
+  const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, g.tiles_p * g.tiles_q));
+  fp8_pair_kernel<T><<<grid, kMmThreads, PairCfg::kSmem, st>>>(g);
+  return launched("8-bit product kernel launch");
+}
+
+fsp_status launch_pairs(MmArgs& g, int32_t dtype, cudaStream_t st) {
+  g.tiles_p = (g.np + PairCfg::kTile - 1) / PairCfg::kTile;
+  g.tiles_q = (g.nq + PairCfg::kTile - 1) / PairCfg::kTile;
+  return dtype == FSP_DTYPE_F32 ? launch_pairs_of<float>(g, st) : launch_pairs_of<__nv_bfloat16>(g, st);
+}
+
 fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
                   int64_t c_stride, int32_t accumulate, void* stream) {
   fsp_status s = check_dims({m, n, k});
@@ -353,6 +400,7 @@ fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k,
   g.accumulate = accumulate != 0;
   g.vec = reinterpret_cast<uintptr_t>(c) % 16 == 0 && size_t(c_stride) * size_of(dtype) % 16 == 0;
   g.tiles_p = (g.np + kTileP - 1) / kTileP;
+  if (!swap && m > 128) return launch_pairs(g, dtype, st);
   if (!swap) return launch_product<192, false>(g, dtype, st);
   if (m <= 16) return launch_product<16, true>(g, dtype, st);
   return m <= 32 ? launch_product<32, true>(g, dtype, st) : launch_product<64, true>(g, dtype, st);

@@ -68,12 +68,26 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   return false;
 }
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity);
+  for (int i = 0; i < 4; ++i)
+    if (mbar_try(bar, parity)) return true;
+  return mbar_wait_slow(bar, parity);
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+
+// One lane of a converged warp.  The warps that issue MMAs and copies run their
+// loops whole, so that addresses and descriptors live in uniform registers, and
+// elect a lane for the instructions themselves (with the whole loop inside a
+// single-lane branch a block of k took 717 cycles to issue, above its MMAs' 512).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
@@ -310,9 +324,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     // the copies in flight land before the CTA's memory is given back
     for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
       if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---- scales and MMAs ----
     const uint32_t idesc = uint32_t(BN >> 3) << 17 | 1u << 23 | uint32_t(kTileP >> 4) << 24;
+    const uint64_t desc_p = operand_desc(at_p), desc_q = operand_desc(at_q);
+    const uint64_t desc_sp = scale_desc(at_sp), desc_sq = scale_desc(at_sq);
     int s = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
@@ -325,22 +341,26 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
         if (!(ok = mbar_wait(full + 8 * s, phase))) break;
         fence_after();
         const uint32_t sp = tmem + Cfg::kScaleBase + s * Cfg::kScaleCols, sq = sp + 4;
-        scale_copy(sp, scale_desc(at_sp + s * 512));
-#pragma unroll
-        for (int j = 0; j < Cfg::kScaleChunks; ++j)
-          scale_copy(sq + 4 * j, scale_desc(at_sq + (s * Cfg::kScaleChunks + j) * 512));
         const uint32_t id = idesc | uint32_t(k & 3) << 4 | uint32_t(k & 3) << 29;   // which byte of a row's four
-        const uint64_t dp = operand_desc(at_p + s * kTileP * 128), dq = operand_desc(at_q + s * BN * 128);
+        const uint64_t dp = desc_p + uint64_t(s * (kTileP * 128 / 16)), dq = desc_q + uint64_t(s * (BN * 128 / 16));
+        if (elect_one()) {
+          scale_copy(sp, desc_sp + uint64_t(s * 32));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_scaled(d, dp + 2 * i, dq + 2 * i, id, sp, sq + sq_shift, (k | i) != 0);
-        mma_commit(empty + 8 * s);
+          for (int j = 0; j < Cfg::kScaleChunks; ++j) scale_copy(sq + 4 * j, desc_sq + uint64_t((s * Cfg::kScaleChunks + j) * 32));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_scaled(d, dp + 2 * i, dq + 2 * i, id, sp, sq + sq_shift, (k | i) != 0);
+          mma_commit(empty + 8 * s);
+        }
+        __syncwarp();
         if (++s == S) s = 0, phase ^= 1u;
       }
-      mma_commit(acc_full + 8 * buf);   // (on a wait that ran out too: what was issued completes)
+      if (elect_one()) mma_commit(acc_full + 8 * buf);   // (on a wait that ran out too: what was issued completes)
+      __syncwarp();
       buf ^= 1;
       if (buf == 0) acc_phase ^= 1u;
     }
-    mma_commit(drained);   // nothing of this thread runs on when the tensor memory is given back
+    if (elect_one()) mma_commit(drained);   // nothing issued here runs on when the tensor memory is given back
+    __syncwarp();
     mbar_wait(drained, 0);
   } else if (warp >= 2) {
     // ---- epilogue ----
@@ -395,6 +415,250 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
   __syncthreads();
   fence_after();
   if (warp == 1) tmem_free(tmem, Cfg::kCols);
+}
+
+
+// ---- pairs of CTAs ---------------------------------------------------------------------
+//
+// Large products: two SMs work on one 256 x 256 tile (cta_group::2).  Each CTA
+// loads 128 rows of P and 128 rows of Q, and the tensor cores of both read both
+// halves of Q, so a byte loaded is used for twice as many products.  The leader
+// (rank 0 of the cluster) issues the MMAs of both.
+//
+// Tensor memory: two accumulators of 256 columns and the scales do not fit into
+// 512 columns, so the accumulators overlap by the scales' 24 columns.  The
+// epilogue reads the overlapping block of an accumulator first and gives it
+// back; the next tile's sum starts then, into the other accumulator.  Scales are
+// copied once per four blocks of k into one of two slots.
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+// Arrives at a barrier of the other CTA.  Relaxed: what it reports is done by the
+// asynchronous proxy (copies that an mbarrier has counted) or ordered by tcgen05
+// fences (reads of tensor memory); no ordinary access has to become visible
+// across the pair, and a release at cluster scope, a fence of every earlier
+// access of the thread, slowed each block of k down (8192^3: 631 us, 429 without).
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_commit(uint32_t bar) {   // arrives at `bar` of both CTAs
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"(uint16_t(3))
+               : "memory");
+}
+__device__ __forceinline__ void pair_scale_copy(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add))
+      : "memory");
+}
+
+struct PairCfg {
+  static constexpr int kTile = 256;                     // of P and of Q
+  static constexpr int kOperand = 128 * 128;            // bytes of one operand's stage in one CTA
+  static constexpr int kScales = 3 * 512;               // a stage's scales: 128 rows of P, 256 of Q
+  static constexpr int kEpilogue = 4 * 32 * 144;
+  static constexpr int kStages = 6;
+  static constexpr int kSmem = 1024 + 256 + kEpilogue + kStages * (2 * kOperand + kScales);
+  static constexpr int kScaleCols = 12;
+  static constexpr int kScaleBase = 512 - 2 * kScaleCols;
+  static constexpr int kSecond = kScaleBase - 256;      // first column of the second accumulator
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(256 - kSecond <= 32, "the overlap lies within one block of 32 columns of either accumulator");
+};
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ MmArgs g) {
+  using Cfg = PairCfg;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ unsigned char raw[];
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  unsigned char* smem = raw + (base - smem_addr(raw));
+  const uint32_t at_p = base, at_q = at_p + S * Cfg::kOperand, at_s = at_q + S * Cfg::kOperand;
+  const uint32_t at_epi = at_s + S * Cfg::kScales;
+  const uint32_t bars = at_epi + Cfg::kEpilogue;
+  const uint32_t full = bars, empty = full + 8 * S, acc_full = empty + 8 * S, acc_part = acc_full + 16;
+  const uint32_t drained = acc_part + 16, slot = drained + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, rank == 0 ? 2 : 1);   // the leader's: its own copies, and word of the other CTA's
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_part + 8 * b, 8);
+    }
+    mbar_init(drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  if (warp == 1) asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(slot) : "memory");
+  fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - base));
+  const int64_t tiles = g.tiles_p * g.tiles_q;
+  const int64_t step = gridDim.x >> 1;
+  const int blocks = int(g.blocks);
+
+  if (warp == 0 && lane == 0) {
+    // ---- producer: this CTA's 128 rows of each operand ----
+    int s = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    const int64_t p_tiles = (g.np + 127) >> 7, q_tiles = (g.nq + 127) >> 7;
+    for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step) {
+      const TileAt tile = tile_at(g, t);
+      const int64_t p_tile = tile.p * 2 + rank, q_first = tile.q * 2, q_tile = q_first + rank;
+      const bool has_p = p_tile < p_tiles, has_q = q_tile < q_tiles;   // rows past the matrices are not loaded
+      const int q_scales = q_first + 1 < q_tiles ? 2 : 1;
+      const uint32_t bytes = uint32_t(has_p ? Cfg::kOperand : 0) + uint32_t(has_q ? Cfg::kOperand : 0);
+      const uint32_t scale_bytes = 512u * uint32_t(q_scales + (has_p ? 1 : 0));
+      const uint8_t* src_p = g.p + p_tile * g.blocks * kTileBytes;
+      const uint8_t* src_q = g.q + q_tile * g.blocks * kTileBytes;
+      const uint8_t* src_sp = g.p + g.p_scales + p_tile * g.pieces * kScaleBytes;
+      const uint8_t* src_sq = g.q + g.q_scales + q_first * g.pieces * kScaleBytes;
+      for (int k = 0; k < blocks; ++k) {
+        if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1u))) break;
+        const uint32_t bar = full + 8 * s;
+        const bool scales = (k & 3) == 0;
+        mbar_expect(bar, bytes + (scales ? scale_bytes : 0u));
+        if (has_p) bulk_load(at_p + s * Cfg::kOperand, src_p + int64_t(k) * kTileBytes, Cfg::kOperand, bar);
+        if (has_q) bulk_load(at_q + s * Cfg::kOperand, src_q + int64_t(k) * kTileBytes, Cfg::kOperand, bar);
+        if (scales) {
+          const int64_t piece = int64_t(k >> 2) * kScaleBytes;
+          const uint32_t dst = at_s + s * Cfg::kScales;
+          if (has_p) bulk_load(dst, src_sp + piece, 512, bar);
+          for (int j = 0; j < q_scales; ++j)
+            bulk_load(dst + 512 * (1 + j), src_sq + j * g.pieces * kScaleBytes + piece, 512, bar);
+        }
+        ++issued;
+        if (++s == S) s = 0, phase ^= 1u;
+      }
+    }
+    for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
+      if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
+  } else if (warp == 1 && lane == 0 && rank != 0) {
+    // ---- the other CTA: tells the leader what has landed here ----
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step)
+      for (int k = 0; k < blocks; ++k) {
+        if (!(ok = mbar_wait(full + 8 * s, phase))) break;
+        mbar_arrive_at(in_cta(full + 8 * s, 0));
+        if (++s == S) s = 0, phase ^= 1u;
+      }
+  } else if (warp == 1 && rank == 0) {
+    // ---- leader: scales and MMAs of both CTAs ----
+    const uint32_t idesc = uint32_t(Cfg::kTile >> 3) << 17 | 1u << 23 | uint32_t(Cfg::kTile >> 4) << 24;
+    const uint64_t desc_p = operand_desc(at_p), desc_q = operand_desc(at_q), desc_s = scale_desc(at_s);
+    int s = 0, n = 0;   // n: tiles so far
+    uint32_t phase = 0, group = 0;
+    // the barrier and parity that show the last block reading each slot of scales complete
+    uint32_t bar0 = 0, par0 = 0, bar1 = 0, par1 = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step, ++n) {
+      // the columns that this tile's accumulator shares with the one before it have been read
+      if (n > 0 && !(ok = mbar_wait(acc_part + 8 * ((n - 1) & 1), uint32_t((n - 1) >> 1) & 1u))) break;
+      fence_after();
+      const uint32_t d = tmem + (n & 1 ? Cfg::kSecond : 0);
+      uint32_t sp = 0;
+      for (int k = 0; k < blocks; ++k) {
+        if (!(ok = mbar_wait(full + 8 * s, phase))) break;
+        if ((k & 3) == 0) {
+          if (group >= 2 && !(ok = mbar_wait(group & 1 ? bar1 : bar0, group & 1 ? par1 : par0))) break;
+          sp = tmem + Cfg::kScaleBase + (group & 1) * Cfg::kScaleCols;
+        }
+        fence_after();
+        const uint32_t id = idesc | uint32_t(k & 3) << 4 | uint32_t(k & 3) << 29;
+        const uint64_t dp = desc_p + uint64_t(s * (Cfg::kOperand / 16)), dq = desc_q + uint64_t(s * (Cfg::kOperand / 16));
+        const uint64_t ds = desc_s + uint64_t(s * (Cfg::kScales / 16));
+        if (elect_one()) {
+          if ((k & 3) == 0) {
+            pair_scale_copy(sp, ds);
+            pair_scale_copy(sp + 4, ds + 32);
+            pair_scale_copy(sp + 8, ds + 64);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pair_mma(d, dp + 2 * i, dq + 2 * i, id, sp, sp + 4, (k | i) != 0);
+          pair_commit(empty + 8 * s);
+        }
+        __syncwarp();
+        if ((k & 3) == 3 || k + 1 == blocks) {   // the slot's last block
+          if (group & 1)
+            bar1 = empty + 8 * s, par1 = phase;
+          else
+            bar0 = empty + 8 * s, par0 = phase;
+          ++group;
+        }
+        if (++s == S) s = 0, phase ^= 1u;
+      }
+      if (elect_one()) pair_commit(acc_full + 8 * (n & 1));
+      __syncwarp();
+    }
+    if (elect_one()) pair_commit(drained);
+    __syncwarp();
+    mbar_wait(drained, 0);
+  } else if (warp >= 2) {
+    // ---- epilogue: this CTA's 128 rows ----
+    const int quarter = warp & 3;
+    unsigned char* stage = smem + (at_epi - base) + (warp - 2) * (Cfg::kEpilogue / 4);
+    int n = 0;
+    for (int64_t t = blockIdx.x >> 1; t < tiles; t += step, ++n) {
+      const TileAt tile = tile_at(g, t);
+      const int buf = n & 1;
+      if (!mbar_wait(acc_full + 8 * buf, uint32_t(n >> 1) & 1u)) break;
+      fence_after();
+      const uint32_t d = tmem + (buf ? Cfg::kSecond : 0) + (uint32_t(quarter * 32) << 16);
+      const int64_t p0 = tile.p * Cfg::kTile + rank * 128 + quarter * 32, q0 = tile.q * Cfg::kTile;
+      for (int j = 0; j < Cfg::kTile; j += 32) {
+        // the first accumulator's last block, the second one's first, are what the other needs next
+        const int j0 = buf ? j : (j + 224) & 255;
+        uint32_t acc[32];
+        tmem_load32(d + j0, acc);
+        tmem_wait_loads();
+        if (j == 0) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(in_cta(acc_part + 8 * buf, 0));
+        }
+        if (p0 < g.np && q0 + j0 < g.nq) write_block<T>(g, acc, stage, lane, p0, q0 + j0);
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA's memory is read or signalled by the other any more
+  fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
 }
 
 }  // namespace
