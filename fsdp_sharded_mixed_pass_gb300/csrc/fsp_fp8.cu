@@ -58,6 +58,7 @@ struct QuantArgs {
   uint8_t* out;
   int64_t rows, cols, stride;
   Fp8Layout l;
+  int64_t row_tile;   // of 128 rows, that x's first row begins
 };
 
 // The biased exponent of a block's scale from the bits of its largest
@@ -82,88 +83,167 @@ __device__ __forceinline__ uint4 codes16(const float* x, float inv) {
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// 16 elements of a row from column c, zeros past the last one.
-template <typename T>
-__device__ __forceinline__ void load16(const T* row, int64_t c, int64_t cols, bool vec, float* x) {
-  if (vec && c + 16 <= cols) {
+// V elements of a row from column c, as they are stored; zeros past the last one.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int64_t c, int64_t cols, bool vec, T* x) {
+  if (vec && c + V <= cols) {
 #pragma unroll
-    for (int k = 0; k < int(sizeof(T)); ++k) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(row + c) + k);
-      const T* t = reinterpret_cast<const T*>(&b);
-#pragma unroll
-      for (int j = 0; j < 16 / int(sizeof(T)); ++j) x[k * (16 / int(sizeof(T))) + j] = widen(t[j]);
-    }
+    for (int k = 0; k < V * int(sizeof(T)) / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldg(reinterpret_cast<const uint4*>(row + c) + k);
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = c + j < cols ? widen(row[c + j]) : 0.f;
+    for (int j = 0; j < V; ++j) x[j] = c + j < cols ? row[c + j] : T(0.f);
   }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ uint32_t largest(const T* x) {   // the bits of the largest magnitude, NaN above all
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(widen(x[j])) & 0x7fffffffu);
+  return top;
 }
 
 // Blocks along the rows of x: a warp per row and four blocks, eight lanes of
-// 16 elements per block.
+// 16 elements per block, two rows at a time; the rows of a CTA follow each other,
+// so that each of the four tiles that it writes gets one run of bytes.
+constexpr int kRowsPerWarp = 2;
+constexpr int kRowsPerCta = kRowsPerWarp * kQuantThreads / 32;
+
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __grid_constant__ QuantArgs a, bool vec) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = int64_t(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
-  const int64_t row = w / a.l.pieces, piece = w % a.l.pieces;
-  if (row >= a.rows) return;
+  const int64_t piece = blockIdx.x;
+  const int64_t row0 = int64_t(blockIdx.y) * kRowsPerCta + (threadIdx.x >> 5) * kRowsPerWarp;
   const int64_t block = piece * 4 + (lane >> 3);
-  float x[16];
-  load16(static_cast<const T*>(a.x) + row * a.stride, piece * 512 + lane * 16, a.cols, vec, x);
-  uint32_t top = 0;
+  alignas(16) T x[kRowsPerWarp][16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+  for (int i = 0; i < kRowsPerWarp; ++i)
+    if (row0 + i < a.rows)
+      load_row<T, 16>(static_cast<const T*>(a.x) + (row0 + i) * a.stride, piece * 512 + lane * 16, a.cols, vec, x[i]);
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const int s = scale_byte(top);
-  const int r = int(row & 127);
-  const int64_t tile = row >> 7;
-  if (block < a.l.blocks)
-    *reinterpret_cast<uint4*>(a.out + (tile * a.l.blocks + block) * kTileBytes + code_at(r, lane & 7)) =
-        codes16(x, inverse_scale(s));
-  uint32_t word = 0;
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    const int64_t row = row0 + i;
+    if (row >= a.rows) return;   // the whole warp
+    uint32_t top = largest<T, 16>(x[i]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) word |= uint32_t(__shfl_sync(0xffffffffu, s, k * 8)) << (8 * k);
-  if (lane == 0)
-    *reinterpret_cast<uint32_t*>(a.out + a.l.scale_offset + (tile * a.l.pieces + piece) * kScaleBytes + scale_at(r, 0)) =
-        word;
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int s = scale_byte(top);
+    const int r = int(row & 127);
+    const int64_t tile = a.row_tile + (row >> 7);
+    float f[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j] = widen(x[i][j]);
+    if (block < a.l.blocks)
+      *reinterpret_cast<uint4*>(a.out + (tile * a.l.blocks + block) * kTileBytes + code_at(r, lane & 7)) =
+          codes16(f, inverse_scale(s));
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) word |= uint32_t(__shfl_sync(0xffffffffu, s, k * 8)) << (8 * k);
+    if (lane == 0)
+      *reinterpret_cast<uint32_t*>(a.out + a.l.scale_offset + (tile * a.l.pieces + piece) * kScaleBytes +
+                                   scale_at(r, 0)) = word;
+  }
 }
 
-// Blocks along the columns of x (the transpose's rows): a CTA per 128 rows x 64
-// columns, through shared memory; a.l is the transpose's layout.
+// Blocks along the columns of x (the transpose's rows), and where `out` is given
+// those along its rows too: a CTA per 128 x 128 tile, read once into shared
+// memory.  Rows: 16 lanes of eight elements each, on the way in.  Columns: a
+// thread takes two neighbouring columns and a quarter of their block; its codes
+// go back through shared memory, laid out as the transpose's tile, so that the
+// tile is written as one run of 16 KB.
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
-  __shared__ float tile[128][65];
-  __shared__ uint32_t tops[4][64];
-  const int64_t c0 = int64_t(blockIdx.x) * 64, block = blockIdx.y, r0 = block * 128;
-  for (int i = threadIdx.x; i < 128 * 64; i += kQuantThreads) {
-    const int r = i >> 6, c = i & 63;
-    const bool in = r0 + r < a.rows && c0 + c < a.cols;
-    tile[r][c] = in ? widen(static_cast<const T*>(a.x)[(r0 + r) * a.stride + c0 + c]) : 0.f;
+struct ColsSmem {
+  static constexpr int kPitch = 128 + 16 / int(sizeof(T));   // elements
+  T x[128][kPitch];
+  uint32_t tops[4][128];
+};
+static_assert(sizeof(ColsSmem<__nv_bfloat16>) >= kTileBytes, "the codes take the tile's place");
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_cols_kernel(const __grid_constant__ QuantArgs a, uint8_t* out, Fp8Layout l, bool vec) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  ColsSmem<T>& sm = *reinterpret_cast<ColsSmem<T>*>(raw);
+  const int tid = threadIdx.x;
+  const int64_t c0 = int64_t(blockIdx.x) * 128, r0 = int64_t(blockIdx.y) * 128;
+  {
+    const int c = (tid & 15) * 8, first = tid >> 4;
+    const bool rows = out != nullptr;
+    alignas(16) T x[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = r0 + first + 16 * i;
+      if (row < a.rows) {
+        load_row<T, 8>(static_cast<const T*>(a.x) + row * a.stride, c0 + c, a.cols, vec, x[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = T(0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = first + 16 * i;
+#pragma unroll
+      for (int k = 0; k < int(sizeof(T)) / 2; ++k)
+        reinterpret_cast<uint4*>(&sm.x[r][c])[k] = reinterpret_cast<const uint4*>(x[i])[k];
+      if (rows) {
+        uint32_t top = largest<T, 8>(x[i]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (r0 + r < a.rows) {
+          const int s = scale_byte(top);
+          const float inv = inverse_scale(s);
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = widen(x[i][j]);
+          *reinterpret_cast<uint2*>(out + (int64_t(blockIdx.y) * l.blocks + blockIdx.x) * kTileBytes + code_at(r, c >> 4) +
+                                    (c & 8)) = make_uint2(codes4(f, inv), codes4(f + 4, inv));
+          if (c == 0)
+            out[l.scale_offset + (int64_t(blockIdx.y) * l.pieces + (blockIdx.x >> 2)) * kScaleBytes +
+                scale_at(r, int(blockIdx.x & 3))] = uint8_t(s);
+        }
+      }
+    }
   }
   __syncthreads();
-  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;   // a column, a quarter of its block
-  float x[32];
-  uint32_t top = 0;
+  const int c = (tid & 63) * 2, q = tid >> 6;   // two columns, a quarter of their block
+  float x[2][32];
+  uint32_t top[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    x[j] = tile[q * 32 + j][c];
-    top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    alignas(8) T two[2];
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<uint2*>(two) = *reinterpret_cast<const uint2*>(&sm.x[q * 32 + j][c]);
+    else
+      *reinterpret_cast<uint32_t*>(two) = *reinterpret_cast<const uint32_t*>(&sm.x[q * 32 + j][c]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x[k][j] = widen(two[k]);
+      top[k] = max(top[k], __float_as_uint(x[k][j]) & 0x7fffffffu);
+    }
   }
-  tops[q][c] = top;
+  sm.tops[q][c] = top[0];
+  sm.tops[q][c + 1] = top[1];
+  __syncthreads();   // (every value of the tile is in registers: the codes may take its place)
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = c + k;   // of the transpose's tile
+    const int s = scale_byte(max(max(sm.tops[0][r], sm.tops[1][r]), max(sm.tops[2][r], sm.tops[3][r])));
+    const float inv = inverse_scale(s);
+    *reinterpret_cast<uint4*>(raw + code_at(r, 2 * q)) = codes16(x[k], inv);
+    *reinterpret_cast<uint4*>(raw + code_at(r, 2 * q + 1)) = codes16(x[k] + 16, inv);
+    if (q == 0 && c0 + r < a.cols)
+      a.out[a.l.scale_offset + (int64_t(blockIdx.x) * a.l.pieces + (blockIdx.y >> 2)) * kScaleBytes +
+            scale_at(r, int(blockIdx.y & 3))] = uint8_t(s);
+  }
   __syncthreads();
-  top = max(max(tops[0][c], tops[1][c]), max(tops[2][c], tops[3][c]));
-  const int s = scale_byte(top);
-  const int64_t row = c0 + c;   // of the transpose
-  if (row >= a.cols) return;
-  const int r = int(row & 127);
-  uint8_t* out = a.out + ((row >> 7) * a.l.blocks + block) * kTileBytes;
-  const float inv = inverse_scale(s);
-  *reinterpret_cast<uint4*>(out + code_at(r, 2 * q)) = codes16(x, inv);
-  *reinterpret_cast<uint4*>(out + code_at(r, 2 * q + 1)) = codes16(x + 16, inv);
-  if (q == 0)
-    a.out[a.l.scale_offset + ((row >> 7) * a.l.pieces + (block >> 2)) * kScaleBytes + scale_at(r, int(block & 3))] =
-        uint8_t(s);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t(blockIdx.x) * a.l.blocks + blockIdx.y) * kTileBytes);
+  const int n = int(min(int64_t(128), a.cols - c0)) * 8;   // 16-byte pieces of the rows that exist
+#pragma unroll
+  for (int i = 0; i < kTileBytes / 16 / kQuantThreads; ++i) {
+    const int at = i * kQuantThreads + tid;
+    if (at < n) dst[at] = reinterpret_cast<const uint4*>(raw)[at];
+  }
 }
 
 __device__ __forceinline__ float scale_value(uint8_t b) {
@@ -215,21 +295,32 @@ bool overlap(const void* p, int64_t pb, const void* q, int64_t qb) {
 template <typename T>
 fsp_status run_quantize(const QuantArgs& in, void* out, void* out_t, bool vec, cudaStream_t st) {
   QuantArgs a = in;
-  if (out) {
-    a.out = static_cast<uint8_t*>(out);
-    a.l = layout_of(a.rows, a.cols);
-    const int64_t ctas = (a.rows * a.l.pieces + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-    if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
-    quantize_rows_kernel<T><<<unsigned(ctas), kQuantThreads, 0, st>>>(a, vec);
-    const fsp_status s = launched("quantisation kernel launch");
-    if (s != FSP_OK) return s;
-  }
+  const Fp8Layout l = layout_of(a.rows, a.cols);
   if (out_t) {
+    constexpr int kSmem = int(sizeof(ColsSmem<T>));
+    static const cudaError_t allowed =
+        cudaFuncSetAttribute(quantize_cols_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (quantisation)", allowed));
     a.out = static_cast<uint8_t*>(out_t);
     a.l = layout_of(a.cols, a.rows);
     if (a.l.blocks > 65535) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
-    quantize_cols_kernel<T><<<dim3(unsigned((a.cols + 63) / 64), unsigned(a.l.blocks)), kQuantThreads, 0, st>>>(a);
+    quantize_cols_kernel<T><<<dim3(unsigned(a.l.row_tiles), unsigned(a.l.blocks)), kQuantThreads, kSmem, st>>>(
+        a, static_cast<uint8_t*>(out), l, vec);
     return launched("transposing quantisation kernel launch");
+  }
+  a.out = static_cast<uint8_t*>(out);
+  a.l = l;
+  const int64_t ctas = (a.rows + kRowsPerCta - 1) / kRowsPerCta;
+  // (the grid's second dimension holds 65535: taller matrices in several launches)
+  constexpr int64_t kMost = 65535 / 8 * 8;
+  for (int64_t done = 0; done < ctas; done += kMost) {
+    QuantArgs part = a;
+    part.x = static_cast<const T*>(a.x) + done * kRowsPerCta * a.stride;
+    part.rows = std::min(a.rows - done * kRowsPerCta, kMost * kRowsPerCta);
+    part.row_tile = done * kRowsPerCta / 128;
+    quantize_rows_kernel<T><<<dim3(unsigned(a.l.pieces), unsigned(std::min(kMost, ctas - done))), kQuantThreads, 0, st>>>(part, vec);
+    const fsp_status s = launched("quantisation kernel launch");
+    if (s != FSP_OK) return s;
   }
   return FSP_OK;
 }
@@ -327,7 +418,7 @@ fsp_status resident_pairs(int* pairs) {
     if (e == cudaSuccess) {
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(unsigned(2 * std::max(1, sm_count() / 2)));
-      cfg.blockDim = dim3(kMmThreads);
+      cfg.blockDim = dim3(PairCfg::kThreads);
       cfg.dynamicSmemBytes = PairCfg::kSmem;
       cudaLaunchAttribute attr{};
       attr.id = cudaLaunchAttributeClusterDimension;
@@ -350,7 +441,7 @@ fsp_status launch_pairs_of(const MmArgs& g, cudaStream_t st) {
   const fsp_status s = resident_pairs<T>(&pairs);
   if (s != FSP_OK) return s;
   const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, g.tiles_p * g.tiles_q));
-  fp8_pair_kernel<T><<<grid, kMmThreads, PairCfg::kSmem, st>>>(g);
+  fp8_pair_kernel<T><<<grid, PairCfg::kThreads, PairCfg::kSmem, st>>>(g);
   return launched("8-bit product kernel launch");
 }
 

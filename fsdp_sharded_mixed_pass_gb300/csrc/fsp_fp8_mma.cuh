@@ -166,13 +166,17 @@ struct MmArgs {
   int vec;                    // C's rows are 16-byte aligned
 };
 
+// The epilogue's part of shared memory, per warp: 32 rows of 64 bytes.
+constexpr int kStagePitch = 64 + 16;              // bytes of a row: eight lanes' 16-byte stores meet no bank twice
+constexpr int kWarpStage = 32 * kStagePitch;
+
 // BN: rows of Q per tile.  kSwap: C is written transposed (C[q][p]).
 template <int BN>
 struct MmCfg {
   static constexpr int kScaleChunks = BN > 128 ? 2 : 1;            // 128-row scale pieces a tile of Q touches
   static constexpr int kScaleCols = 4 + 4 * kScaleChunks;          // tensor memory columns of a stage's scales
   static constexpr int kStageBytes = kTileP * 128 + BN * 128 + 512 + 512 * kScaleChunks;
-  static constexpr int kEpilogue = 4 * 32 * 144;                   // four warps, 32 rows of up to 128 bytes (+ 16)
+  static constexpr int kEpilogue = 4 * kWarpStage;
   static constexpr int kFixed = 1024 + 256 + kEpilogue;            // alignment, barriers, epilogue
   static constexpr int kFit = (232448 - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -203,52 +207,62 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
 }
 
 // Rows p0 .. p0 + 31 (a lane each), columns q0 .. q0 + 31 of C from registers,
-// through this warp's part of shared memory so that rows are written in runs.
+// through this warp's part of shared memory so that rows are written in runs of
+// 64 bytes: 32 columns of bf16, or 16 of fp32 at a time.
+
 template <typename T>
 __device__ __forceinline__ void write_block(const MmArgs& g, const uint32_t* acc, unsigned char* stage, int lane, int64_t p0,
                                             int64_t q0) {
-  constexpr int kPitch = int(sizeof(T)) * 32 + 16;
-  constexpr int kVecs = int(sizeof(T)) * 2;   // 16-byte vectors of a row
-  uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPitch);
+  constexpr int kCols = 64 / int(sizeof(T));
+  T* const c = static_cast<T*>(g.c) + p0 * g.c_stride + q0;
+  const int rows = int(min(int64_t(32), g.np - p0));
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    if constexpr (sizeof(T) == 4)
-      mine[j] = make_uint4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-    else
-      mine[j] = make_uint4(pack_bf16(acc[8 * j], acc[8 * j + 1]), pack_bf16(acc[8 * j + 2], acc[8 * j + 3]),
-                           pack_bf16(acc[8 * j + 4], acc[8 * j + 5]), pack_bf16(acc[8 * j + 6], acc[8 * j + 7]));
-  }
-  __syncwarp();
-  T* c = static_cast<T*>(g.c);
-  if (g.vec && q0 + 32 <= g.nq) {
-    constexpr int kRows = 32 / kVecs;   // rows of one pass of the warp
-    const int r = lane / kVecs, v = lane % kVecs;
+  for (int h = 0; h < 32 / kCols; ++h) {
+    const uint32_t* x = acc + h * kCols;
+    const int cols = int(min(int64_t(kCols), g.nq - q0 - h * kCols));
+    if (cols <= 0) break;
+    uint4* mine = reinterpret_cast<uint4*>(stage + lane * kStagePitch);
 #pragma unroll
-    for (int i = 0; i < 32; i += kRows) {
-      if (p0 + i + r >= g.np) continue;
-      uint4 x = *reinterpret_cast<const uint4*>(stage + (i + r) * kPitch + v * 16);
-      uint4* dst = reinterpret_cast<uint4*>(c + (p0 + i + r) * g.c_stride + q0) + v;
-      if constexpr (sizeof(T) == 4) {
-        if (g.accumulate) {
-          const float4 o = *reinterpret_cast<const float4*>(dst);
-          x = make_uint4(__float_as_uint(__uint_as_float(x.x) + o.x), __float_as_uint(__uint_as_float(x.y) + o.y),
-                         __float_as_uint(__uint_as_float(x.z) + o.z), __float_as_uint(__uint_as_float(x.w) + o.w));
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4)
+        mine[j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      else
+        mine[j] = make_uint4(pack_bf16(x[8 * j], x[8 * j + 1]), pack_bf16(x[8 * j + 2], x[8 * j + 3]),
+                             pack_bf16(x[8 * j + 4], x[8 * j + 5]), pack_bf16(x[8 * j + 6], x[8 * j + 7]));
+    }
+    __syncwarp();
+    if (g.vec && cols == kCols) {
+      const int r = lane >> 2, v = lane & 3;   // eight rows of four 16-byte vectors at a time
+      uint4* dst = reinterpret_cast<uint4*>(c + r * g.c_stride + h * kCols) + v;
+      const int64_t step = g.c_stride * int(sizeof(T)) / 2;   // eight rows, in vectors
+#pragma unroll
+      for (int i = 0; i < 32; i += 8, dst += step) {
+        if (i + r >= rows) break;
+        uint4 y = *reinterpret_cast<const uint4*>(stage + (i + r) * kStagePitch + v * 16);
+        if constexpr (sizeof(T) == 4) {
+          if (g.accumulate) {
+            const float4 o = *reinterpret_cast<const float4*>(dst);
+            y = make_uint4(__float_as_uint(__uint_as_float(y.x) + o.x), __float_as_uint(__uint_as_float(y.y) + o.y),
+                           __float_as_uint(__uint_as_float(y.z) + o.z), __float_as_uint(__uint_as_float(y.w) + o.w));
+          }
         }
+        *dst = y;
       }
-      *dst = x;
+    } else {
+      // 32 / kCols rows at a time, a lane per element
+      const int r = lane / kCols, v = lane % kCols;
+      if (v < cols)
+        for (int i = r; i < rows; i += 32 / kCols) {
+          T y = *reinterpret_cast<const T*>(stage + i * kStagePitch + v * int(sizeof(T)));
+          T* dst = c + i * g.c_stride + h * kCols + v;
+          if constexpr (sizeof(T) == 4) {
+            if (g.accumulate) y += *dst;
+          }
+          *dst = y;
+        }
     }
-  } else if (q0 + lane < g.nq) {
-    const int rows = int(min(int64_t(32), g.np - p0));
-    for (int i = 0; i < rows; ++i) {
-      T x = *reinterpret_cast<const T*>(stage + i * kPitch + lane * int(sizeof(T)));
-      T* dst = c + (p0 + i) * g.c_stride + q0 + lane;
-      if constexpr (sizeof(T) == 4) {
-        if (g.accumulate) x += *dst;
-      }
-      *dst = x;
-    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 template <int BN, bool kSwap, typename T>
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
   } else if (warp >= 2) {
     // ---- epilogue ----
     const int quarter = warp & 3;   // the tensor memory lanes this warp may read
-    unsigned char* stage = smem + (at_epi - base) + (warp - 2) * (Cfg::kEpilogue / 4);
+    unsigned char* stage = smem + (at_epi - base) + (warp - 2) * kWarpStage;
     int buf = 0;
     uint32_t phase = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -474,7 +488,9 @@ struct PairCfg {
   static constexpr int kTile = 256;                     // of P and of Q
   static constexpr int kOperand = 128 * 128;            // bytes of one operand's stage in one CTA
   static constexpr int kScales = 3 * 512;               // a stage's scales: 128 rows of P, 256 of Q
-  static constexpr int kEpilogue = 4 * 32 * 144;
+  static constexpr int kWarps = 8;                      // of the epilogue, two per quarter of the rows
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kEpilogue = kWarps * kWarpStage;
   static constexpr int kStages = 6;
   static constexpr int kSmem = 1024 + 256 + kEpilogue + kStages * (2 * kOperand + kScales);
   static constexpr int kScaleCols = 12;
@@ -485,7 +501,7 @@ struct PairCfg {
 };
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ MmArgs g) {
   using Cfg = PairCfg;
   constexpr int S = Cfg::kStages;
@@ -507,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_part + 8 * b, 8);
+      mbar_init(acc_part + 8 * b, 2 * Cfg::kWarps);
     }
     mbar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -625,8 +641,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     mbar_wait(drained, 0);
   } else if (warp >= 2) {
     // ---- epilogue: this CTA's 128 rows ----
-    const int quarter = warp & 3;
-    unsigned char* stage = smem + (at_epi - base) + (warp - 2) * (Cfg::kEpilogue / 4);
+    const int quarter = warp & 3, half = (warp - 2) >> 2;   // rows; alternate blocks of 32 columns
+    unsigned char* stage = smem + (at_epi - base) + (warp - 2) * kWarpStage;
     int n = 0;
     for (int64_t t = blockIdx.x >> 1; t < tiles; t += step, ++n) {
       const TileAt tile = tile_at(g, t);
@@ -635,13 +651,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       fence_after();
       const uint32_t d = tmem + (buf ? Cfg::kSecond : 0) + (uint32_t(quarter * 32) << 16);
       const int64_t p0 = tile.p * Cfg::kTile + rank * 128 + quarter * 32, q0 = tile.q * Cfg::kTile;
-      for (int j = 0; j < Cfg::kTile; j += 32) {
+#pragma unroll 1
+      for (int j = 32 * half; j < Cfg::kTile; j += 64) {
         // the first accumulator's last block, the second one's first, are what the other needs next
         const int j0 = buf ? j : (j + 224) & 255;
         uint32_t acc[32];
         tmem_load32(d + j0, acc);
         tmem_wait_loads();
-        if (j == 0) {
+        if (j < 64) {
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(in_cta(acc_part + 8 * buf, 0));
