@@ -265,6 +265,128 @@ __global__ void __launch_bounds__(kQuantThreads) values_kernel(const uint8_t* q,
   out[i] = code_value(code) * scale_value(s);
 }
 
+// ---- few rows times a matrix ----------------------------------------------------------
+//
+// Up to four rows of x: the product is bound by the bytes of w, read once, and a
+// tensor-core tile would be mostly empty.  A CTA quantises x for itself (its codes'
+// values go to shared memory as fp32) and takes 16 rows of w at a time; its eight
+// warps share out the blocks of k.  A lane holds one 16-byte piece of a block
+// for four rows of w (rows r, r + 4, ...), so that a warp's load is 512 bytes of
+// a tile in a run, and x's 16 values serve four rows.  The eight lanes of a row,
+// then the eight warps, are added in a fixed order.
+constexpr int kFewThreads = 256;
+constexpr int kFewRows = 16;             // of w, per CTA and turn
+constexpr int64_t kFewSmem = 64 * 1024;  // of x's values, at most
+
+struct FewArgs {
+  const void* x;
+  const uint8_t* w;
+  void* y;
+  int64_t cols, x_stride, n, y_stride;
+  Fp8Layout l;   // of w
+  int rows;
+};
+
+__device__ __forceinline__ void values16(uint4 c, float* f) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+    const float2 v = __half22float2(__half2(h));
+    f[2 * j] = v.x;
+    f[2 * j + 1] = v.y;
+  }
+}
+
+template <int M, typename T, typename O>
+__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_constant__ FewArgs a) {
+  extern __shared__ float xv[];   // [M][blocks * 128], then [8 warps][16][M]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t width = a.l.blocks * 128;
+  for (int64_t b = warp; b < a.l.blocks * M; b += kFewThreads / 32) {
+    const int64_t m = b / a.l.blocks, block = b % a.l.blocks, c = block * 128 + lane * 4;
+    const T* row = static_cast<const T*>(a.x) + m * a.x_stride;
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = m < a.rows && c + j < a.cols ? widen(row[c + j]) : 0.f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    const int s = scale_byte(__reduce_max_sync(0xffffffffu, top));
+    const uint32_t codes = codes4(f, inverse_scale(s));
+    const float scale = scale_value(uint8_t(s));
+    float4 v;
+    v.x = code_value(uint8_t(codes)) * scale;
+    v.y = code_value(uint8_t(codes >> 8)) * scale;
+    v.z = code_value(uint8_t(codes >> 16)) * scale;
+    v.w = code_value(uint8_t(codes >> 24)) * scale;
+    *reinterpret_cast<float4*>(xv + m * width + c) = v;
+  }
+  __syncthreads();
+  float* part = xv + M * width;
+  const int sub = lane >> 3, p = lane & 7;
+  for (int64_t n0 = int64_t(blockIdx.x) * kFewRows; n0 < a.n; n0 += int64_t(gridDim.x) * kFewRows) {
+    const int64_t tile = n0 >> 7;
+    const int r0 = int(n0 & 127) + sub;
+    float acc[4][M];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < M; ++m) acc[i][m] = 0.f;
+    for (int64_t block = warp; block < a.l.blocks; block += kFewThreads / 32) {
+      const uint8_t* src = a.w + (tile * a.l.blocks + block) * kTileBytes;
+      const uint8_t* scales = a.w + a.l.scale_offset + (tile * a.l.pieces + (block >> 2)) * kScaleBytes;
+      uint4 c[4];
+      float s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = __ldcs(reinterpret_cast<const uint4*>(src + code_at(r0 + 4 * i, p)));
+        s[i] = scale_value(__ldg(scales + scale_at(r0 + 4 * i, int(block & 3))));
+      }
+      float x[M][16];
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(&x[m][4 * j]) = *reinterpret_cast<const float4*>(xv + m * width + block * 128 + p * 16 + 4 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[16], sum[M];
+        values16(c[i], f);
+#pragma unroll
+        for (int m = 0; m < M; ++m) sum[m] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int m = 0; m < M; ++m) sum[m] = fmaf(f[j], x[m][j], sum[m]);
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[i][m] = fmaf(sum[m], s[i], acc[i][m]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) acc[i][m] += __shfl_xor_sync(0xffffffffu, acc[i][m], o);
+        if (p == 0) part[(warp * kFewRows + sub + 4 * i) * M + m] = acc[i][m];
+      }
+    __syncthreads();
+    const int r = threadIdx.x / M, m = threadIdx.x % M;
+    if (r < kFewRows && n0 + r < a.n && m < a.rows) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewThreads / 32; ++w) sum += part[(w * kFewRows + r) * M + m];
+      O* y = static_cast<O*>(a.y) + m * a.y_stride + n0 + r;
+      if constexpr (sizeof(O) == 4)
+        *y = sum;
+      else
+        *y = __float2bfloat16_rn(sum);
+    }
+    __syncthreads();
+  }
+}
+
 // ---- host ----------------------------------------------------------------------------
 
 size_t size_of(int32_t dtype) { return dtype == FSP_DTYPE_F32 ? 4 : 2; }
@@ -325,33 +447,47 @@ fsp_status run_quantize(const QuantArgs& in, void* out, void* out_t, bool vec, c
   return FSP_OK;
 }
 
-fsp_status quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, void* out, void* out_t,
-                    void* stream) {
-  fsp_status s = check_dims({rows, cols});
-  if (s != FSP_OK) return s;
-  if (dtype != FSP_DTYPE_F32 && dtype != FSP_DTYPE_BF16) return fail(FSP_EINVAL, "unknown dtype of x");
-  if (stride < cols || (rows > 0 && stride > (int64_t(1) << 58) / rows)) return fail(FSP_EINVAL, "x's rows overlap or their stride is out of range");
+fsp_status check_matrix(const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, const char* name) {
+  if (dtype != FSP_DTYPE_F32 && dtype != FSP_DTYPE_BF16) return fail(FSP_EINVAL, std::string("unknown dtype of ") + name);
+  if (stride < cols || (rows > 0 && stride > (int64_t(1) << 58) / rows))
+    return fail(FSP_EINVAL, std::string(name) + "'s rows overlap or their stride is out of range");
   if (rows == 0 || cols == 0) return FSP_OK;
-  if (!out && !out_t) return fail(FSP_EINVAL, "out and out_t are both NULL");
-  if (!x) return fail(FSP_EINVAL, "x is NULL");
-  if (reinterpret_cast<uintptr_t>(x) % size_of(dtype)) return fail(FSP_EINVAL, "x is not aligned to its elements");
-  const int64_t xb = ((rows - 1) * stride + cols) * int64_t(size_of(dtype));
-  s = check_allocation(x, size_t(xb), "x");
-  const Fp8Layout l = layout_of(rows, cols), lt = layout_of(cols, rows);
-  if (s == FSP_OK && out) s = check_codes(out, l, "out");
-  if (s == FSP_OK && out_t) s = check_codes(out_t, lt, "out_t");
-  if (s != FSP_OK) return s;
-  if (overlap(out, l.bytes, x, xb) || overlap(out_t, lt.bytes, x, xb) || overlap(out, l.bytes, out_t, lt.bytes))
-    return fail(FSP_EINVAL, "an output overlaps another buffer");
+  if (!p) return fail(FSP_EINVAL, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % size_of(dtype))
+    return fail(FSP_EINVAL, std::string(name) + " is not aligned to its elements");
+  return check_allocation(p, size_t((rows - 1) * stride + cols) * size_of(dtype), name);
+}
+int64_t span(int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
+  return rows > 0 && cols > 0 ? ((rows - 1) * stride + cols) * int64_t(size_of(dtype)) : 0;
+}
+
+// On checked arguments: rows and cols above 0.
+fsp_status quantize_checked(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, void* out, void* out_t,
+                            cudaStream_t st) {
   QuantArgs a{};
   a.x = x;
   a.rows = rows;
   a.cols = cols;
   a.stride = stride;
   const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && size_t(stride) * size_of(dtype) % 16 == 0;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == FSP_DTYPE_F32 ? run_quantize<float>(a, out, out_t, vec, st)
                                 : run_quantize<__nv_bfloat16>(a, out, out_t, vec, st);
+}
+
+fsp_status quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, void* out, void* out_t,
+                    void* stream) {
+  fsp_status s = check_dims({rows, cols});
+  if (s == FSP_OK && rows > 0 && cols > 0 && !out && !out_t) return fail(FSP_EINVAL, "out and out_t are both NULL");
+  if (s == FSP_OK) s = check_matrix(x, dtype, rows, cols, stride, "x");
+  if (s != FSP_OK || rows == 0 || cols == 0) return s;
+  const Fp8Layout l = layout_of(rows, cols), lt = layout_of(cols, rows);
+  if (out) s = check_codes(out, l, "out");
+  if (s == FSP_OK && out_t) s = check_codes(out_t, lt, "out_t");
+  if (s != FSP_OK) return s;
+  const int64_t xb = span(rows, cols, stride, dtype);
+  if (overlap(out, l.bytes, x, xb) || overlap(out_t, lt.bytes, x, xb) || overlap(out, l.bytes, out_t, lt.bytes))
+    return fail(FSP_EINVAL, "an output overlaps another buffer");
+  return quantize_checked(x, dtype, rows, cols, stride, out, out_t, static_cast<cudaStream_t>(stream));
 }
 
 fsp_status values(const void* q, int64_t rows, int64_t cols, float* out, void* stream) {
@@ -381,6 +517,27 @@ int sm_count() {
     return sms;
   }();
   return n;
+}
+
+// Whether `rows` rows of `cols` values go through few_rows_kernel.
+constexpr int64_t kFewMost = 4;
+bool few(int64_t rows, int64_t cols) { return rows <= kFewMost && rows * ((cols + 127) / 128 * 128) * 4 <= kFewSmem; }
+
+template <int M, typename T, typename O>
+fsp_status launch_few_of(const FewArgs& a, cudaStream_t st) {
+  constexpr int kMost = int(kFewSmem) * 2 + 8 * kFewRows * 4 * M;   // (three rows run in the kernel of four)
+  static const cudaError_t allowed =
+      cudaFuncSetAttribute(few_rows_kernel<M, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (few rows)", allowed));
+  const size_t smem = size_t(M) * size_t(a.l.blocks) * 512 + 8 * kFewRows * 4 * M;
+  // x is quantised once per CTA: at most eight CTAs per SM, which then take turns
+  const int64_t ctas = std::min<int64_t>((a.n + kFewRows - 1) / kFewRows, int64_t(sm_count()) * 8);
+  few_rows_kernel<M, T, O><<<unsigned(ctas), kFewThreads, smem, st>>>(a);
+  return launched("8-bit linear (few rows) kernel launch");
+}
+template <typename T, typename O>
+fsp_status launch_few(const FewArgs& a, cudaStream_t st) {
+  return a.rows == 1 ? launch_few_of<1, T, O>(a, st) : a.rows == 2 ? launch_few_of<2, T, O>(a, st) : launch_few_of<4, T, O>(a, st);
 }
 
 template <int BN, bool kSwap, typename T>
@@ -451,30 +608,10 @@ fsp_status launch_pairs(MmArgs& g, int32_t dtype, cudaStream_t st) {
   return dtype == FSP_DTYPE_F32 ? launch_pairs_of<float>(g, st) : launch_pairs_of<__nv_bfloat16>(g, st);
 }
 
-fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
-                  int64_t c_stride, int32_t accumulate, void* stream) {
-  fsp_status s = check_dims({m, n, k});
-  if (s != FSP_OK) return s;
-  if (dtype != FSP_DTYPE_F32 && dtype != FSP_DTYPE_BF16) return fail(FSP_EINVAL, "unknown dtype of c");
-  if (accumulate && dtype != FSP_DTYPE_F32) return fail(FSP_EUNSUPPORTED, "accumulate adds to fp32 only");
-  if (c_stride < n || (m > 0 && c_stride > (int64_t(1) << 58) / m)) return fail(FSP_EINVAL, "c's rows overlap or their stride is out of range");
-  if (m == 0 || n == 0) return FSP_OK;
-  if (!c) return fail(FSP_EINVAL, "c is NULL");
-  if (reinterpret_cast<uintptr_t>(c) % size_of(dtype)) return fail(FSP_EINVAL, "c is not aligned to its elements");
-  const int64_t cb = ((m - 1) * c_stride + n) * int64_t(size_of(dtype));
-  s = check_allocation(c, size_t(cb), "c");
-  if (s != FSP_OK) return s;
+// On checked arguments: m, n and k above 0.
+fsp_status matmul_checked(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
+                          int64_t c_stride, bool accumulate, cudaStream_t st) {
   const Fp8Layout la = layout_of(m, k), lb = layout_of(n, k);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (k == 0) {   // the sum of nothing
-    if (accumulate) return FSP_OK;
-    const cudaError_t e = cudaMemset2DAsync(c, size_t(c_stride) * size_of(dtype), 0, size_t(n) * size_of(dtype), size_t(m), st);
-    return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("cudaMemset2DAsync", e));
-  }
-  s = check_codes(a, la, "a");
-  if (s == FSP_OK) s = check_codes(b, lb, "b");
-  if (s != FSP_OK) return s;
-  if (overlap(c, cb, a, la.bytes) || overlap(c, cb, b, lb.bytes)) return fail(FSP_EINVAL, "c overlaps an operand");
   // Up to 64 rows of a: b's rows fill the 128 rows of the tiles, a's their columns.
   const bool swap = m <= 64;
   MmArgs g{};
@@ -488,13 +625,138 @@ fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k,
   g.p_scales = (swap ? lb : la).scale_offset;
   g.q_scales = (swap ? la : lb).scale_offset;
   g.c_stride = c_stride;
-  g.accumulate = accumulate != 0;
+  g.accumulate = accumulate;
   g.vec = reinterpret_cast<uintptr_t>(c) % 16 == 0 && size_t(c_stride) * size_of(dtype) % 16 == 0;
   g.tiles_p = (g.np + kTileP - 1) / kTileP;
   if (!swap && m > 128) return launch_pairs(g, dtype, st);
   if (!swap) return launch_product<192, false>(g, dtype, st);
   if (m <= 16) return launch_product<16, true>(g, dtype, st);
   return m <= 32 ? launch_product<32, true>(g, dtype, st) : launch_product<64, true>(g, dtype, st);
+}
+
+fsp_status sum_of_nothing(int64_t m, int64_t n, void* c, int32_t dtype, int64_t c_stride, cudaStream_t st) {
+  const cudaError_t e = cudaMemset2DAsync(c, size_t(c_stride) * size_of(dtype), 0, size_t(n) * size_of(dtype), size_t(m), st);
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("cudaMemset2DAsync", e));
+}
+
+fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
+                  int64_t c_stride, int32_t accumulate, void* stream) {
+  fsp_status s = check_dims({m, n, k});
+  if (s != FSP_OK) return s;
+  if (accumulate && dtype == FSP_DTYPE_BF16) return fail(FSP_EUNSUPPORTED, "accumulate adds to fp32 only");
+  s = check_matrix(c, dtype, m, n, c_stride, "c");
+  if (s != FSP_OK || m == 0 || n == 0) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (k == 0) return accumulate ? FSP_OK : sum_of_nothing(m, n, c, dtype, c_stride, st);
+  const Fp8Layout la = layout_of(m, k), lb = layout_of(n, k);
+  s = check_codes(a, la, "a");
+  if (s == FSP_OK) s = check_codes(b, lb, "b");
+  if (s != FSP_OK) return s;
+  const int64_t cb = span(m, n, c_stride, dtype);
+  if (overlap(c, cb, a, la.bytes) || overlap(c, cb, b, lb.bytes)) return fail(FSP_EINVAL, "c overlaps an operand");
+  return matmul_checked(a, b, m, n, k, c, dtype, c_stride, accumulate != 0, st);
+}
+
+// ---- the linear layer ---------------------------------------------------------------
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+int64_t forward_workspace(int64_t rows, int64_t in, int64_t out) {
+  return rows == 0 || in == 0 || out == 0 || few(rows, in) ? 0 : round256(layout_of(rows, in).bytes);
+}
+int64_t backward_workspace(int64_t rows, int64_t in, int64_t out) {
+  if (rows == 0 || in == 0 || out == 0) return 0;
+  return round256(layout_of(rows, out).bytes) + round256(layout_of(out, rows).bytes) + round256(layout_of(in, rows).bytes);
+}
+
+fsp_status check_workspace(const void* p, size_t bytes, int64_t want) {
+  if (want == 0) return FSP_OK;
+  if (!p) return fail(FSP_EINVAL, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % 16) return fail(FSP_EINVAL, "workspace is not 16-byte aligned");
+  if (bytes < size_t(want)) return fail(FSP_EINVAL, "workspace is smaller than fsp_fp8_linear_workspace_bytes");
+  return check_allocation(p, size_t(want), "workspace");
+}
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+// The first `written` of the ranges against each other and all the others.
+fsp_status check_disjoint(const Range* r, int n, int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
+        return fail(FSP_EINVAL, std::string(r[i].name) + " overlaps " + r[j].name);
+  return FSP_OK;
+}
+
+fsp_status linear(const void* x, int32_t xd, int64_t rows, int64_t in, int64_t xs, const void* w, int64_t out, void* y,
+                  int32_t yd, int64_t ys, void* workspace, size_t workspace_bytes, void* stream) {
+  fsp_status s = check_dims({rows, in, out});
+  if (s == FSP_OK) s = check_matrix(x, xd, rows, in, xs, "x");
+  if (s == FSP_OK) s = check_matrix(y, yd, rows, out, ys, "y");
+  if (s != FSP_OK || rows == 0 || out == 0) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (in == 0) return sum_of_nothing(rows, out, y, yd, ys, st);
+  const Fp8Layout lw = layout_of(out, in);
+  const int64_t want = forward_workspace(rows, in, out);
+  s = check_codes(w, lw, "w");
+  if (s == FSP_OK) s = check_workspace(workspace, workspace_bytes, want);
+  if (s != FSP_OK) return s;
+  const Range ranges[] = {{y, span(rows, out, ys, yd), "y"},
+                          {workspace, want, "workspace"},
+                          {x, span(rows, in, xs, xd), "x"},
+                          {w, lw.bytes, "w"}};
+  s = check_disjoint(ranges, 4, 2);
+  if (s != FSP_OK) return s;
+  if (few(rows, in)) {
+    const FewArgs a{x, static_cast<const uint8_t*>(w), y, in, xs, out, ys, lw, int(rows)};
+    using B = __nv_bfloat16;
+    if (xd == FSP_DTYPE_F32) return yd == FSP_DTYPE_F32 ? launch_few<float, float>(a, st) : launch_few<float, B>(a, st);
+    return yd == FSP_DTYPE_F32 ? launch_few<B, float>(a, st) : launch_few<B, B>(a, st);
+  }
+  s = quantize_checked(x, xd, rows, in, xs, workspace, nullptr, st);
+  return s != FSP_OK ? s : matmul_checked(workspace, w, rows, out, in, y, yd, ys, false, st);
+}
+
+fsp_status linear_backward(const void* x, int32_t xd, int64_t xs, const void* dy, int32_t dyd, int64_t dys, int64_t rows,
+                           int64_t in, int64_t out, const void* wt, void* dx, int32_t dxd, int64_t dxs, float* dw,
+                           int64_t dws, bool accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  fsp_status s = check_dims({rows, in, out});
+  if (s == FSP_OK) s = check_matrix(dy, dyd, rows, out, dys, "grad_y");
+  if (s == FSP_OK && dw) s = check_matrix(x, xd, rows, in, xs, "x");
+  if (s == FSP_OK && dx) s = check_matrix(dx, dxd, rows, in, dxs, "grad_x");
+  if (s == FSP_OK && dw) s = check_matrix(dw, FSP_DTYPE_F32, out, in, dws, "grad_w");
+  if (s != FSP_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0 || in == 0 || out == 0) {   // one of the products may still be a sum of nothing
+    if (dx && rows > 0 && in > 0) s = sum_of_nothing(rows, in, dx, dxd, dxs, st);
+    if (s == FSP_OK && dw && !accumulate && out > 0 && in > 0) s = sum_of_nothing(out, in, dw, FSP_DTYPE_F32, dws, st);
+    return s;
+  }
+  if (!dx && !dw) return FSP_OK;
+  const Fp8Layout lw = layout_of(in, out);
+  const int64_t want = backward_workspace(rows, in, out);
+  if (dx) s = check_codes(wt, lw, "wt");
+  if (s == FSP_OK) s = check_workspace(workspace, workspace_bytes, want);
+  if (s != FSP_OK) return s;
+  const Range ranges[] = {{dx, dx ? span(rows, in, dxs, dxd) : 0, "grad_x"},
+                          {dw, dw ? span(out, in, dws, FSP_DTYPE_F32) : 0, "grad_w"},
+                          {workspace, want, "workspace"},
+                          {dy, span(rows, out, dys, dyd), "grad_y"},
+                          {x, dw ? span(rows, in, xs, xd) : 0, "x"},
+                          {wt, dx ? lw.bytes : 0, "wt"}};
+  s = check_disjoint(ranges, 6, 3);
+  if (s != FSP_OK) return s;
+  char* q = static_cast<char*>(workspace);
+  char* qt = q + round256(layout_of(rows, out).bytes);
+  char* xt = qt + round256(layout_of(out, rows).bytes);
+  s = quantize_checked(dy, dyd, rows, out, dys, dx ? q : nullptr, dw ? qt : nullptr, st);
+  if (s == FSP_OK && dx) s = matmul_checked(q, wt, rows, in, out, dx, dxd, dxs, false, st);
+  if (s == FSP_OK && dw) s = quantize_checked(x, xd, rows, in, xs, nullptr, xt, st);
+  if (s == FSP_OK && dw) s = matmul_checked(qt, xt, out, in, rows, dw, FSP_DTYPE_F32, dws, accumulate, st);
+  return s;
 }
 
 }  // namespace
@@ -541,5 +803,42 @@ extern "C" fsp_status fsp_fp8_matmul(const void* a, const void* b, int64_t m, in
   return fsp::guard([&]() -> fsp_status {
     fsp::clear_error();
     return fsp::matmul(a, b, m, n, k, c, dtype, c_stride, accumulate, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_fp8_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t in_features, int64_t x_stride,
+                                     const void* w, int64_t out_features, void* y, int32_t y_dtype, int64_t y_stride,
+                                     void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::linear(x, x_dtype, rows, in_features, x_stride, w, out_features, y, y_dtype, y_stride, workspace,
+                       workspace_bytes, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_fp8_linear_backward(const void* x, int32_t x_dtype, int64_t x_stride, const void* grad_y,
+                                              int32_t grad_y_dtype, int64_t grad_y_stride, int64_t rows,
+                                              int64_t in_features, int64_t out_features, const void* wt, void* grad_x,
+                                              int32_t grad_x_dtype, int64_t grad_x_stride, float* grad_w,
+                                              int64_t grad_w_stride, int32_t accumulate, void* workspace,
+                                              size_t workspace_bytes, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::linear_backward(x, x_dtype, x_stride, grad_y, grad_y_dtype, grad_y_stride, rows, in_features,
+                                out_features, wt, grad_x, grad_x_dtype, grad_x_stride, grad_w, grad_w_stride,
+                                accumulate != 0, workspace, workspace_bytes, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features,
+                                                     int32_t backward, size_t* bytes) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    if (!bytes) return fsp::fail(FSP_EINVAL, "bytes is NULL");
+    const fsp_status s = fsp::check_dims({rows, in_features, out_features});
+    if (s == FSP_OK)
+      *bytes = size_t(backward ? fsp::backward_workspace(rows, in_features, out_features)
+                               : fsp::forward_workspace(rows, in_features, out_features));
+    return s;
   });
 }

@@ -107,10 +107,15 @@ fsp_status check_allocation(const void* ptr, size_t bytes, const char* name) {
   // The driver call needs a current context on this thread; a thread that has
   // made no runtime call yet has none, so bind the current device's primary
   // context (cudaSetDevice does that, and nothing else, when it is current).
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaSetDevice(dev);
-  if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("binding the device context", e));
+  // Once per thread: a later change of device binds that device's context itself.
+  static thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("binding the device context", e));
+    bound = true;
+  }
   CUdeviceptr base = 0;
   size_t size = 0;
   if (get_range(&base, &size, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS)

@@ -15,7 +15,8 @@ STATE_BLOCK = 256   # elements of a tensor that share a scale in 8-bit AdamW sta
 EXPORTS = ("fsp_adamw_list_create", "fsp_adamw_list_info", "fsp_adamw_list_destroy", "fsp_adamw_list_step",
            "fsp_adamw_list_state_values", "fsp_adamw_list_state_load", "fsp_embedding",
            "fsp_embedding_backward_workspace_bytes", "fsp_embedding_backward", "fsp_fp8_bytes", "fsp_fp8_quantize",
-           "fsp_fp8_values", "fsp_fp8_matmul")
+           "fsp_fp8_values", "fsp_fp8_matmul", "fsp_fp8_linear", "fsp_fp8_linear_backward",
+           "fsp_fp8_linear_workspace_bytes")
 
 
 def bind(L) -> None:
@@ -36,22 +37,46 @@ def bind(L) -> None:
         "fsp_fp8_quantize": [vp, i32, i64, i64, i64, vp, vp, vp],
         "fsp_fp8_values": [vp, i64, i64, vp, vp],
         "fsp_fp8_matmul": [vp, vp, i64, i64, i64, vp, i32, i64, i32, vp],
+        "fsp_fp8_linear": [vp, i32, i64, i64, i64, vp, i64, vp, i32, i64, vp, size, vp],
+        "fsp_fp8_linear_backward": [vp, i32, i64, vp, i32, i64, i64, i64, i64, vp, vp, i32, i64, vp, i64, i32, vp, size,
+                                    vp],
+        "fsp_fp8_linear_workspace_bytes": [i64, i64, i64, i32, P(size)],
     }.items():
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = None if name == "fsp_adamw_list_destroy" else ctypes.c_int
 
 
-_dtype_codes = None
+# What every call needs, looked up once: a call on one token is a few microseconds
+# of the GPU's time, so the host's share is kept as small.
+_torch = _lib = _raw_stream = _device = None
+_CODES, _INDEX = {}, {}   # dtype -> the library's code; index dtype -> bytes
+
+
+def _ready():
+    global _torch, _lib, _raw_stream, _device
+    import torch
+    _lib = _fsp.lib()
+    _CODES.update({torch.float32: _fsp.DTYPES["f32"], torch.bfloat16: _fsp.DTYPES["bf16"]})
+    _INDEX.update({torch.int64: 8, torch.int32: 4})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _device = getattr(torch._C, "_cuda_getDevice", None)
+    _torch = torch
+    return _lib
+
+
+def _handle(stream):
+    """The cudaStream_t of a stream argument (None: the current stream)."""
+    if stream is None and _raw_stream is not None and _device is not None:
+        return _raw_stream(_device())
+    return _fsp._stream_handle(stream)
 
 
 def _dtype(x, what: str) -> int:
     """The library's code of a CUDA tensor's dtype (fp32 or bf16)."""
-    global _dtype_codes
-    if _dtype_codes is None:
-        import torch
-        _dtype_codes = {torch.float32: _fsp.DTYPES["f32"], torch.bfloat16: _fsp.DTYPES["bf16"]}
-    code = _dtype_codes.get(x.dtype)
+    if _torch is None:
+        _ready()
+    code = _CODES.get(x.dtype)
     if code is None:
         raise TypeError(f"{what}: unsupported dtype {x.dtype}")
     if not x.is_cuda:
@@ -64,35 +89,52 @@ def _rows(x, what: str):
     if x.dim() != 2:
         raise ValueError(f"{what} must have 2 dimensions")
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    stride, step = x.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be adjacent")
-    return rows, cols, x.stride(0) if rows > 1 else max(1, cols)
+    return rows, cols, stride if rows > 1 and cols > 0 else max(1, cols)
 
 
-def _tokens(tokens):
-    """A token tensor's (pointer, bytes per index, count)."""
-    import torch
-    if tokens.dtype == torch.int64:
-        size = 8
-    elif tokens.dtype == torch.int32:
-        size = 4
-    else:
+def _flat(x, features: int, what: str):
+    """(rows, row stride) of a tensor of any leading dimensions as rows x features."""
+    if x.dim() == 2:
+        rows, cols, stride = _rows(x, what)
+        if cols != features:
+            raise ValueError(f"{what}'s last dimension must be {features}")
+        return rows, stride
+    if x.dim() < 1 or x.shape[-1] != features:
+        raise ValueError(f"{what}'s last dimension must be {features}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous unless it has 2 dimensions")
+    rows = 1
+    for d in x.shape[:-1]:
+        rows *= d
+    return rows, max(1, features)
+
+
+def _tokens(tokens) -> int:
+    """Bytes per index of a token tensor."""
+    if _torch is None:
+        _ready()
+    size = _INDEX.get(tokens.dtype)
+    if size is None:
         raise TypeError(f"tokens: unsupported dtype {tokens.dtype}")
     if not tokens.is_cuda:
         raise ValueError("tokens is not on a CUDA device")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
-    return tokens.data_ptr(), size, tokens.numel()
+    return size
 
 
 def _empty(shape, dtype, device, stream):
     """A buffer whose memory is handed out (and later taken back) in the order
     of the stream the call runs on."""
-    import torch
+    if _torch is None:
+        _ready()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
     with _on_stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 # ---- AdamW over a list of tensors ----------------------------------------------
@@ -183,16 +225,20 @@ class TensorAdamW:
             self._t = int(value)
 
     def _states(self):
-        return [None if x is None else x.data_ptr()
-                for x in (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)]
+        if self.state_bits == 32:
+            return self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), None, None
+        return (self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), self.exp_avg_scale.data_ptr(),
+                self.exp_avg_sq_scale.data_ptr())
 
     def step(self, grad_scale=None, stream=None) -> None:
         if grad_scale is not None and (_dtype(grad_scale, "grad_scale") != 0 or grad_scale.numel() != 1):
             raise ValueError("grad_scale must be one fp32 element")
-        _fsp._check(_fsp.lib().fsp_adamw_list_step(
+        status = (_lib or _ready()).fsp_adamw_list_step(
             self._h, 0 if self.state_bits == 32 else 1, *self._states(), ctypes.byref(_fsp._hp(self.hparams)),
             self._t + 1, None if self._next_t is None else self._next_t.data_ptr(), 1,
-            None if grad_scale is None else grad_scale.data_ptr(), _fsp._stream_handle(stream)), "fsp_adamw_list_step")
+            None if grad_scale is None else grad_scale.data_ptr(), _handle(stream))
+        if status:
+            _fsp._check(status, "fsp_adamw_list_step")
         if self._next_t is None:
             self._t += 1   # only once the step was accepted
 
@@ -211,7 +257,7 @@ class TensorAdamW:
         m, v = out if out is not None else [_empty((self.state_len,), torch.float32, self.exp_avg.device, stream)
                                             for _ in range(2)]
         _fsp._check(_fsp.lib().fsp_adamw_list_state_values(self._h, *self._states(), *self._fp32_states(m, v),
-                                                           _fsp._stream_handle(stream)), "fsp_adamw_list_state_values")
+                                                           _handle(stream)), "fsp_adamw_list_state_values")
         return m, v
 
     def load_state(self, exp_avg, exp_avg_sq, stream=None) -> None:
@@ -223,7 +269,7 @@ class TensorAdamW:
                 self.exp_avg_sq.copy_(exp_avg_sq)
             return
         _fsp._check(_fsp.lib().fsp_adamw_list_state_load(self._h, pm, pv, *self._states(),
-                                                         _fsp._stream_handle(stream)), "fsp_adamw_list_state_load")
+                                                         _handle(stream)), "fsp_adamw_list_state_load")
 
     def close(self):
         if self._h is not None and self._h.value:
@@ -243,28 +289,27 @@ def embedding(weight, tokens, scale: float = 1.0, out=None, out_dtype=None, stre
     """``out[..., :] = scale * weight[tokens[...], :]``, multiplied in fp32 and
     rounded once to ``out_dtype`` (default: the weight's).  A token outside the
     table gives zeros and sets bit 16 of ``device_error()``."""
+    size = _tokens(tokens)
+    code = _dtype(weight, "weight")
     vocab, dim, stride = _rows(weight, "weight")
-    ptr, size, n = _tokens(tokens)
     if out is None:
         out = _empty((*tokens.shape, dim), out_dtype or weight.dtype, weight.device, stream)
-        out_stride = dim
+        out_stride = max(1, dim)
     else:
         if tuple(out.shape) != (*tokens.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError("out has another shape or dtype")
-        if out.dim() != 2 and not out.is_contiguous():
-            raise ValueError("out must be contiguous unless it has 2 dimensions")
-        out_stride = _rows(out, "out")[2] if out.dim() == 2 else dim
-    _fsp._check(_fsp.lib().fsp_embedding(weight.data_ptr(), _dtype(weight, "weight"), vocab, dim, stride, ptr, size, n,
-                                         scale, out.data_ptr(), _dtype(out, "out"), max(out_stride, dim),
-                                         _fsp._stream_handle(stream)), "fsp_embedding")
+        out_stride = _flat(out, dim, "out")[1]
+    status = _lib.fsp_embedding(weight.data_ptr(), code, vocab, dim, stride, tokens.data_ptr(), size, tokens.numel(),
+                                scale, out.data_ptr(), _dtype(out, "out"), out_stride, _handle(stream))
+    if status:
+        _fsp._check(status, "fsp_embedding")
     return out
 
 
 def embedding_backward_workspace_bytes(vocab: int, dim: int, n_tokens: int) -> int:
     """Device workspace bytes ``embedding_backward`` needs."""
     out = ctypes.c_size_t(0)
-    _fsp._check(_fsp.lib().fsp_embedding_backward_workspace_bytes(int(vocab), int(dim), int(n_tokens),
-                                                                  ctypes.byref(out)),
+    _fsp._check((_lib or _ready()).fsp_embedding_backward_workspace_bytes(vocab, dim, n_tokens, ctypes.byref(out)),
                 "fsp_embedding_backward_workspace_bytes")
     return out.value
 
@@ -276,23 +321,22 @@ def embedding_backward(tokens, grad_out, grad_weight, scale: float = 1.0, paddin
     embedding's slice of a rank's main-grad buffer.  ``padding_idx`` gets no
     gradient.  ``workspace``: a device tensor of at least
     ``embedding_backward_workspace_bytes`` bytes (None: allocated here)."""
-    import torch
+    size, n = _tokens(tokens), tokens.numel()
     vocab, dim, stride = _rows(grad_weight, "grad_weight")
-    ptr, size, n = _tokens(tokens)
     if tuple(grad_out.shape) != (*tokens.shape, dim):
         raise ValueError(f"grad_out must have shape {(*tokens.shape, dim)}")
-    if grad_out.dim() != 2 and not grad_out.is_contiguous():
-        raise ValueError("grad_out must be contiguous unless it has 2 dimensions")
-    grad_stride = _rows(grad_out, "grad_out")[2] if grad_out.dim() == 2 else dim
+    grad_stride = _flat(grad_out, dim, "grad_out")[1]
     if padding_idx is not None and not 0 <= padding_idx < vocab:
         raise ValueError("padding_idx is not a row of grad_weight")
     if workspace is None:
-        workspace = _empty((embedding_backward_workspace_bytes(vocab, dim, n),), torch.uint8, grad_weight.device, stream)
-    _fsp._check(_fsp.lib().fsp_embedding_backward(
-        ptr, size, n, grad_out.data_ptr(), _dtype(grad_out, "grad_out"), dim, max(grad_stride, dim),
-        grad_weight.data_ptr(), _dtype(grad_weight, "grad_weight"), vocab, max(stride, dim), scale,
+        workspace = _empty(embedding_backward_workspace_bytes(vocab, dim, n), _torch.uint8, grad_weight.device, stream)
+    status = _lib.fsp_embedding_backward(
+        tokens.data_ptr(), size, n, grad_out.data_ptr(), _dtype(grad_out, "grad_out"), dim, grad_stride,
+        grad_weight.data_ptr(), _dtype(grad_weight, "grad_weight"), vocab, stride, scale,
         -1 if padding_idx is None else padding_idx, 1 if accumulate else 0, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _fsp._stream_handle(stream)), "fsp_embedding_backward")
+        workspace.numel() * workspace.element_size(), _handle(stream))
+    if status:
+        _fsp._check(status, "fsp_embedding_backward")
     return grad_weight
 
 
@@ -303,18 +347,17 @@ class Fp8Matrix:
     block of 128 of a row, in the library's tile layout (``fsp_fp8_bytes``)."""
 
     def __init__(self, rows: int, cols: int, device="cuda", stream=None):
-        import torch
         nbytes, off = ctypes.c_size_t(), ctypes.c_size_t()
-        _fsp._check(_fsp.lib().fsp_fp8_bytes(rows, cols, ctypes.byref(nbytes), ctypes.byref(off)), "fsp_fp8_bytes")
+        _fsp._check((_lib or _ready()).fsp_fp8_bytes(rows, cols, ctypes.byref(nbytes), ctypes.byref(off)),
+                    "fsp_fp8_bytes")
         self.rows, self.cols, self.scale_offset = rows, cols, off.value
-        self.data = _empty((nbytes.value,), torch.uint8, device, stream)
+        self.data = _empty(nbytes.value, _torch.uint8, device, stream)
 
     def values(self, stream=None):
         """What the codes stand for, as an fp32 tensor."""
-        import torch
-        out = _empty((self.rows, self.cols), torch.float32, self.data.device, stream)
-        _fsp._check(_fsp.lib().fsp_fp8_values(self.data.data_ptr(), self.rows, self.cols, out.data_ptr(),
-                                              _fsp._stream_handle(stream)), "fsp_fp8_values")
+        out = _empty((self.rows, self.cols), _torch.float32, self.data.device, stream)
+        _fsp._check(_lib.fsp_fp8_values(self.data.data_ptr(), self.rows, self.cols, out.data_ptr(), _handle(stream)),
+                    "fsp_fp8_values")
         return out
 
 
@@ -323,20 +366,20 @@ def quantize_fp8(x, rows=True, transposed=None, stream=None):
     in one pass: ``rows`` and ``transposed`` are each True (a new ``Fp8Matrix``), an
     ``Fp8Matrix`` to fill, or None / False (not wanted).  Returns the wanted one, or
     the pair."""
-    r, c, stride = _rows(x, "x")
     code = _dtype(x, "x")
+    r, c, stride = _rows(x, "x")
     got = []
     for want, shape in ((rows, (r, c)), (transposed, (c, r))):
         if want is True:
             want = Fp8Matrix(*shape, device=x.device, stream=stream)
-        elif not want and want is not None and not isinstance(want, Fp8Matrix):
+        elif want is False:
             want = None
         if want is not None and (want.rows, want.cols) != shape:
             raise ValueError(f"the matrix to fill is {want.rows} x {want.cols}, not {shape[0]} x {shape[1]}")
         got.append(want)
-    _fsp._check(_fsp.lib().fsp_fp8_quantize(x.data_ptr(), code, r, c, stride,
-                                            *[None if q is None else q.data.data_ptr() for q in got],
-                                            _fsp._stream_handle(stream)), "fsp_fp8_quantize")
+    _fsp._check(_lib.fsp_fp8_quantize(x.data_ptr(), code, r, c, stride,
+                                      *[None if q is None else q.data.data_ptr() for q in got], _handle(stream)),
+                "fsp_fp8_quantize")
     if got[0] is None:
         return got[1]
     return got[0] if got[1] is None else tuple(got)
@@ -345,19 +388,18 @@ def quantize_fp8(x, rows=True, transposed=None, stream=None):
 def matmul_fp8(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """``out[m, n] = sum_k a[m, k] b[n, k]`` in fp32, rounded once to bf16 (the
     default) or fp32; ``accumulate`` adds to an fp32 ``out``."""
-    import torch
     if a.cols != b.cols:
         raise ValueError(f"the operands sum over {a.cols} and {b.cols} elements")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _empty((a.rows, b.rows), out_dtype or torch.bfloat16, a.data.device, stream)
+        out = _empty((a.rows, b.rows), out_dtype or _torch.bfloat16, a.data.device, stream)
     elif tuple(out.shape) != (a.rows, b.rows) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out has another shape or dtype")
     m, n, stride = _rows(out, "out")
-    _fsp._check(_fsp.lib().fsp_fp8_matmul(a.data.data_ptr(), b.data.data_ptr(), m, n, a.cols, out.data_ptr(),
-                                          _dtype(out, "out"), stride, 1 if accumulate else 0,
-                                          _fsp._stream_handle(stream)), "fsp_fp8_matmul")
+    _fsp._check(_lib.fsp_fp8_matmul(a.data.data_ptr(), b.data.data_ptr(), m, n, a.cols, out.data_ptr(),
+                                    _dtype(out, "out"), stride, 1 if accumulate else 0, _handle(stream)),
+                "fsp_fp8_matmul")
     return out
 
 
@@ -382,22 +424,32 @@ class Fp8Linear:
         """Lays out a new weight of the same shape."""
         quantize_fp8(weight, self.codes, self.codes_t, stream=stream)
 
-    def _flat(self, x, features, what):
-        if x.dim() < 1 or x.shape[-1] != features:
-            raise ValueError(f"{what}'s last dimension must be {features}")
-        if x.dim() == 2:
-            return x
-        if not x.is_contiguous():
-            raise ValueError(f"{what} must be contiguous unless it has 2 dimensions")
-        return x.view(-1, features)
+    def _workspace(self, rows: int, backward: int, device, stream):
+        size = ctypes.c_size_t(0)
+        _fsp._check(_lib.fsp_fp8_linear_workspace_bytes(rows, self.in_features, self.out_features, backward,
+                                                        ctypes.byref(size)), "fsp_fp8_linear_workspace_bytes")
+        return _empty(size.value, _torch.uint8, device, stream) if size.value else None
 
     def forward(self, x, out=None, out_dtype=None, stream=None):
         """``x W^T`` (bf16 unless ``out`` or ``out_dtype`` says fp32)."""
-        flat = self._flat(x, self.in_features, "x")
-        y = matmul_fp8(quantize_fp8(flat, stream=stream), self.codes,
-                       out=None if out is None else self._flat(out, self.out_features, "out"), out_dtype=out_dtype,
-                       stream=stream)
-        return y if x.dim() == 2 else y.view(*x.shape[:-1], self.out_features)
+        code = _dtype(x, "x")
+        rows, stride = _flat(x, self.in_features, "x")
+        n = self.out_features
+        if out is None:
+            out = _empty((*x.shape[:-1], n), out_dtype or _torch.bfloat16, x.device, stream)
+            out_stride = max(1, n)
+        else:
+            if out.shape[:-1] != x.shape[:-1] or (out_dtype is not None and out.dtype != out_dtype):
+                raise ValueError("out has another shape or dtype")
+            out_stride = _flat(out, n, "out")[1]
+        work = self._workspace(rows, 0, x.device, stream)
+        status = _lib.fsp_fp8_linear(x.data_ptr(), code, rows, self.in_features, stride, self.codes.data.data_ptr(), n,
+                                     out.data_ptr(), _dtype(out, "out"), out_stride,
+                                     None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
+                                     _handle(stream))
+        if status:
+            _fsp._check(status, "fsp_fp8_linear")
+        return out
 
     def backward(self, x, grad_out, grad_weight=None, accumulate: bool = False, need_grad_x: bool = True, out=None,
                  stream=None):
@@ -406,20 +458,32 @@ class Fp8Linear:
         to it, as micro-batches add to a main gradient)."""
         if not self.train:
             raise ValueError("this layer was laid out for forward only (train=False)")
-        flat, dy = self._flat(x, self.in_features, "x"), self._flat(grad_out, self.out_features, "grad_out")
-        if flat.shape[0] != dy.shape[0]:
+        k, n = self.in_features, self.out_features
+        rows, stride = _flat(x, k, "x")
+        dy_rows, dy_stride = _flat(grad_out, n, "grad_out")
+        if rows != dy_rows:
             raise ValueError("x and grad_out must have as many rows")
         if not need_grad_x and grad_weight is None:
             return None
-        got = quantize_fp8(dy, need_grad_x, grad_weight is not None, stream=stream)
-        q, qt = got if need_grad_x and grad_weight is not None else (got, None) if need_grad_x else (None, got)
-        grad_x = None
+        dx = dw = None
+        dx_stride = dw_stride = max(1, k)
+        dx_code = 1
         if need_grad_x:
-            grad_x = matmul_fp8(q, self.codes_t, out=None if out is None else self._flat(out, self.in_features, "out"),
-                                stream=stream)
-            if x.dim() != 2:
-                grad_x = grad_x.view(x.shape)
+            dx = out if out is not None else _empty(x.shape, _torch.bfloat16, x.device, stream)
+            if dx.shape != x.shape:
+                raise ValueError("out must have x's shape")
+            dx_stride, dx_code = _flat(dx, k, "out")[1], _dtype(dx, "out")
         if grad_weight is not None:
-            xt = quantize_fp8(flat, None, True, stream=stream)
-            matmul_fp8(qt, xt, out=grad_weight, accumulate=accumulate, stream=stream)
-        return grad_x
+            if _dtype(grad_weight, "grad_weight") != 0:
+                raise TypeError("grad_weight must be fp32")
+            if tuple(grad_weight.shape) != (n, k):
+                raise ValueError(f"grad_weight must have shape {(n, k)}")
+            dw, dw_stride = grad_weight, _rows(grad_weight, "grad_weight")[2]
+        work = self._workspace(rows, 1, x.device, stream)
+        _fsp._check(_lib.fsp_fp8_linear_backward(
+            x.data_ptr(), _dtype(x, "x"), stride, grad_out.data_ptr(), _dtype(grad_out, "grad_out"), dy_stride, rows, k,
+            n, self.codes_t.data.data_ptr(), None if dx is None else dx.data_ptr(), dx_code, dx_stride,
+            None if dw is None else dw.data_ptr(), dw_stride, 1 if accumulate else 0,
+            None if work is None else work.data_ptr(), 0 if work is None else work.numel(), _handle(stream)),
+            "fsp_fp8_linear_backward")
+        return dx

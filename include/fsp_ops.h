@@ -167,6 +167,31 @@ fsp_status fsp_fp8_values(const void* q, int64_t rows, int64_t cols, float* out,
 fsp_status fsp_fp8_matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
                           int64_t c_stride, int32_t accumulate, void* cuda_stream);
 
+/* A linear layer's forward pass on 8-bit operands: y = q(x) w^T, with x (rows x
+ * in_features of x_dtype, rows x_stride apart) quantised along its rows here and
+ * w (out_features x in_features) as fsp_fp8_quantize's `out` laid it out.
+ *   y: rows x out_features of y_dtype, rows y_stride apart.
+ *   workspace: 16-byte aligned, at least fsp_fp8_linear_workspace_bytes (NULL
+ *   where that is 0: up to four rows are quantised on chip). */
+fsp_status fsp_fp8_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t in_features, int64_t x_stride,
+                          const void* w, int64_t out_features, void* y, int32_t y_dtype, int64_t y_stride,
+                          void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Its gradients: grad_x = q(grad_y) wt^T (NULL: not wanted), wt being w's
+ * transpose as `out_t` laid it out, and grad_w (+)= q(grad_y^T) q(x^T)^T (fp32;
+ * NULL: not wanted; accumulate: added to it).  x and wt are read only where
+ * grad_w and grad_x are wanted. */
+fsp_status fsp_fp8_linear_backward(const void* x, int32_t x_dtype, int64_t x_stride, const void* grad_y,
+                                   int32_t grad_y_dtype, int64_t grad_y_stride, int64_t rows, int64_t in_features,
+                                   int64_t out_features, const void* wt, void* grad_x, int32_t grad_x_dtype,
+                                   int64_t grad_x_stride, float* grad_w, int64_t grad_w_stride, int32_t accumulate,
+                                   void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Device workspace, in bytes, of fsp_fp8_linear (backward 0) and of
+ * fsp_fp8_linear_backward (backward 1). */
+fsp_status fsp_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features, int32_t backward,
+                                          size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

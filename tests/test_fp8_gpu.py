@@ -166,6 +166,50 @@ def test_linear_layer(m, n, k):
     assert z.shape == (1, m, n) and torch.equal(z[0], 2 * y)
 
 
+@pytest.mark.parametrize("x,y", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,n,k,pad,shift", [(1, 1, 1, 0, 0), (1, 15, 128, 0, 0), (1, 2048, 1024, 0, 0), (2, 129, 777, 3, 1),
+                                                (3, 1000, 5632, 0, 0), (4, 17, 130, 8, 8), (4, 33, 4096, 0, 0), (3, 40, 5461, 1, 1),
+                                                (1, 30, 16384, 0, 0), (1, 30, 16385, 0, 0), (4, 30, 4097, 0, 0), (1, 20000, 96, 0, 0)])
+def test_few_rows(rows, n, k, pad, shift, x, y):
+    rng = np.random.default_rng(rows * n + k)
+    buf = torch.zeros(rows * (k + pad) + shift, dtype=DT[x], device="cuda")
+    xd = buf[shift:].view(rows, k + pad)[:, :k]
+    xd.copy_(torch.from_numpy(_wide(rng, rows, k)))
+    w = torch.from_numpy(rng.normal(0, 1, (n, k)).astype(np.float32)).cuda()
+    g = Guarded(rows * (n + pad) + shift, DT[y], 0)
+    out = g.t[shift:].view(rows, n + pad)[:, :n]
+    assert fsp.Fp8Linear(w).forward(xd, out=out) is out
+    want, mag = _product(_values(xd), _values(w))
+    tol = _tolerance(k, mag)
+    if y == "bf16":
+        assert rounds_to(_values(out), want, tol).all()
+    else:
+        assert (np.abs(_values(out) - want) <= tol).all()
+    if pad:
+        assert float(g.t[shift:].view(rows, n + pad)[:, n:].abs().sum()) == 0
+    assert g.guards_intact()
+
+
+def test_few_rows_with_a_non_finite_value():
+    x = torch.ones(2, 300, device="cuda")
+    x[1, 200] = float("inf")
+    y = _values(fsp.Fp8Linear(torch.ones(40, 300, device="cuda")).forward(x, out_dtype=torch.float32))
+    assert (y[0] == 300).all() and np.isnan(y[1]).all()
+
+
+def test_empty_layers():
+    w = torch.ones(6, 5, device="cuda")
+    layer = fsp.Fp8Linear(w, train=True)
+    assert layer.forward(torch.ones(0, 5, device="cuda")).shape == (0, 6)
+    dw = torch.ones(6, 5, device="cuda")
+    e = torch.zeros(0, 5, device="cuda")
+    assert layer.backward(e, torch.zeros(0, 6, device="cuda"), dw, accumulate=True).shape == (0, 5) and float(dw.sum()) == 30
+    layer.backward(e, torch.zeros(0, 6, device="cuda"), dw)
+    assert float(dw.abs().sum()) == 0
+    none = fsp.Fp8Linear(torch.ones(6, 0, device="cuda"))
+    assert float(none.forward(torch.ones(3, 0, device="cuda")).abs().sum()) == 0
+
+
 def test_gradients_against_differences():
     """On values that 8 bits hold exactly the layer is linear, and so the
     difference quotients of L = sum(dy * y) are exact."""

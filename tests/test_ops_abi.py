@@ -129,6 +129,24 @@ def test_fp8_sizes_and_refusals(lib):
     assert lib.fsp_fp8_values(None, 4, 4, None, None) == B.FSP_EINVAL and lib.fsp_fp8_values(None, 0, 4, None, None) == B.FSP_OK
 
 
+def test_fp8_linear_refusals(lib):
+    size = ctypes.c_size_t()
+    bytes_of = lambda r, i, o, b: (lib.fsp_fp8_linear_workspace_bytes(r, i, o, b, ctypes.byref(size)), size.value)  # noqa: E731
+    assert bytes_of(1, 1024, 2048, 0) == (B.FSP_OK, 0) and bytes_of(0, 5, 5, 1) == (B.FSP_OK, 0)
+    assert bytes_of(5, 1024, 2048, 0)[1] >= 5 * 1024 and bytes_of(300, 500, 700, 1)[1] >= 300 * (2 * 700 + 500)
+    assert bytes_of(-1, 5, 5, 0)[0] == B.FSP_EINVAL and lib.fsp_fp8_linear_workspace_bytes(1, 1, 1, 0, None) == B.FSP_EINVAL
+    f = lib.fsp_fp8_linear
+    assert f(None, 0, 0, 8, 8, None, 8, None, 0, 8, None, 0, None) == B.FSP_OK
+    for args in ((None, 0, 4, 8, 8, FAKE, 8, FAKE, 0, 8), (FAKE, 3, 4, 8, 8, FAKE, 8, FAKE, 0, 8),
+                 (FAKE, 0, 4, 8, 7, FAKE, 8, FAKE, 0, 8), (FAKE, 0, 4, 8, 8, FAKE, 8, FAKE, 0, 7),
+                 (FAKE, 0, -4, 8, 8, FAKE, 8, FAKE, 0, 8), (FAKE + 2, 0, 4, 8, 8, FAKE, 8, FAKE, 0, 8)):
+        assert f(*args, None, 0, None) == B.FSP_EINVAL, args
+    g = lib.fsp_fp8_linear_backward
+    assert g(None, 0, 8, None, 0, 8, 0, 8, 8, None, None, 0, 8, None, 8, 0, None, 0, None) == B.FSP_OK
+    assert g(FAKE, 0, 8, None, 0, 8, 4, 8, 8, FAKE, FAKE, 0, 8, None, 8, 0, None, 0, None) == B.FSP_EINVAL
+    assert g(FAKE, 0, 8, FAKE, 0, 7, 4, 8, 8, FAKE, FAKE, 0, 8, None, 8, 0, None, 0, None) == B.FSP_EINVAL
+
+
 # ---- the references themselves ---------------------------------------------------------
 
 def test_reference_e4m3_against_torch():
