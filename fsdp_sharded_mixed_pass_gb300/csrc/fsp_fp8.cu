@@ -403,15 +403,36 @@ fsp_status check_dims(std::initializer_list<int64_t> dims) {
   return FSP_OK;
 }
 
-fsp_status check_codes(const void* p, const Fp8Layout& l, const char* name) {
+fsp_status check_codes(const void* p, const char* name) {
   if (!p) return fail(FSP_EINVAL, std::string(name) + " is NULL");
   if (reinterpret_cast<uintptr_t>(p) % 16) return fail(FSP_EINVAL, std::string(name) + " is not 16-byte aligned");
-  return check_allocation(p, size_t(l.bytes), name);
+  return FSP_OK;
 }
 
 bool overlap(const void* p, int64_t pb, const void* q, int64_t qb) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return p && q && a < b + uintptr_t(qb) && b < a + uintptr_t(pb);
+}
+
+// A buffer of a call: NULL or 0 bytes where the call has none.
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+// The first `written` of the ranges against each other and all the others, then
+// that each lies in a live allocation.
+fsp_status check_ranges(const Range* r, int n, int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
+        return fail(FSP_EINVAL, std::string(r[i].name) + " overlaps " + r[j].name);
+  for (int i = 0; i < n; ++i)
+    if (r[i].p && r[i].bytes > 0) {
+      const fsp_status s = check_allocation(r[i].p, size_t(r[i].bytes), r[i].name);
+      if (s != FSP_OK) return s;
+    }
+  return FSP_OK;
 }
 
 template <typename T>
@@ -455,7 +476,7 @@ fsp_status check_matrix(const void* p, int32_t dtype, int64_t rows, int64_t cols
   if (!p) return fail(FSP_EINVAL, std::string(name) + " is NULL");
   if (reinterpret_cast<uintptr_t>(p) % size_of(dtype))
     return fail(FSP_EINVAL, std::string(name) + " is not aligned to its elements");
-  return check_allocation(p, size_t((rows - 1) * stride + cols) * size_of(dtype), name);
+  return FSP_OK;
 }
 int64_t span(int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
   return rows > 0 && cols > 0 ? ((rows - 1) * stride + cols) * int64_t(size_of(dtype)) : 0;
@@ -481,12 +502,12 @@ fsp_status quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, in
   if (s == FSP_OK) s = check_matrix(x, dtype, rows, cols, stride, "x");
   if (s != FSP_OK || rows == 0 || cols == 0) return s;
   const Fp8Layout l = layout_of(rows, cols), lt = layout_of(cols, rows);
-  if (out) s = check_codes(out, l, "out");
-  if (s == FSP_OK && out_t) s = check_codes(out_t, lt, "out_t");
+  if (out) s = check_codes(out, "out");
+  if (s == FSP_OK && out_t) s = check_codes(out_t, "out_t");
   if (s != FSP_OK) return s;
-  const int64_t xb = span(rows, cols, stride, dtype);
-  if (overlap(out, l.bytes, x, xb) || overlap(out_t, lt.bytes, x, xb) || overlap(out, l.bytes, out_t, lt.bytes))
-    return fail(FSP_EINVAL, "an output overlaps another buffer");
+  const Range ranges[] = {{out, l.bytes, "out"}, {out_t, lt.bytes, "out_t"}, {x, span(rows, cols, stride, dtype), "x"}};
+  s = check_ranges(ranges, 3, 2);
+  if (s != FSP_OK) return s;
   return quantize_checked(x, dtype, rows, cols, stride, out, out_t, static_cast<cudaStream_t>(stream));
 }
 
@@ -494,13 +515,12 @@ fsp_status values(const void* q, int64_t rows, int64_t cols, float* out, void* s
   fsp_status s = check_dims({rows, cols});
   if (s != FSP_OK || rows == 0 || cols == 0) return s;
   const Fp8Layout l = layout_of(rows, cols);
-  s = check_codes(q, l, "q");
+  s = check_codes(q, "q");
+  if (s == FSP_OK) s = check_matrix(out, FSP_DTYPE_F32, rows, cols, cols, "out");
   if (s != FSP_OK) return s;
-  if (!out) return fail(FSP_EINVAL, "out is NULL");
-  if (reinterpret_cast<uintptr_t>(out) % 4) return fail(FSP_EINVAL, "out is not aligned to its elements");
-  s = check_allocation(out, size_t(rows) * size_t(cols) * 4, "out");
+  const Range ranges[] = {{out, rows * cols * 4, "out"}, {q, l.bytes, "q"}};
+  s = check_ranges(ranges, 2, 1);
   if (s != FSP_OK) return s;
-  if (overlap(q, l.bytes, out, rows * cols * 4)) return fail(FSP_EINVAL, "out overlaps q");
   const int64_t ctas = (rows * cols + kQuantThreads - 1) / kQuantThreads;
   if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
   values_kernel<<<unsigned(ctas), kQuantThreads, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint8_t*>(q), rows,
@@ -647,13 +667,18 @@ fsp_status matmul(const void* a, const void* b, int64_t m, int64_t n, int64_t k,
   s = check_matrix(c, dtype, m, n, c_stride, "c");
   if (s != FSP_OK || m == 0 || n == 0) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (k == 0) return accumulate ? FSP_OK : sum_of_nothing(m, n, c, dtype, c_stride, st);
+  if (k == 0) {
+    const Range ranges[] = {{c, span(m, n, c_stride, dtype), "c"}};
+    s = check_ranges(ranges, 1, 1);
+    return s != FSP_OK || accumulate ? s : sum_of_nothing(m, n, c, dtype, c_stride, st);
+  }
   const Fp8Layout la = layout_of(m, k), lb = layout_of(n, k);
-  s = check_codes(a, la, "a");
-  if (s == FSP_OK) s = check_codes(b, lb, "b");
+  s = check_codes(a, "a");
+  if (s == FSP_OK) s = check_codes(b, "b");
   if (s != FSP_OK) return s;
-  const int64_t cb = span(m, n, c_stride, dtype);
-  if (overlap(c, cb, a, la.bytes) || overlap(c, cb, b, lb.bytes)) return fail(FSP_EINVAL, "c overlaps an operand");
+  const Range ranges[] = {{c, span(m, n, c_stride, dtype), "c"}, {a, la.bytes, "a"}, {b, lb.bytes, "b"}};
+  s = check_ranges(ranges, 3, 1);
+  if (s != FSP_OK) return s;
   return matmul_checked(a, b, m, n, k, c, dtype, c_stride, accumulate != 0, st);
 }
 
@@ -674,20 +699,6 @@ fsp_status check_workspace(const void* p, size_t bytes, int64_t want) {
   if (!p) return fail(FSP_EINVAL, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(p) % 16) return fail(FSP_EINVAL, "workspace is not 16-byte aligned");
   if (bytes < size_t(want)) return fail(FSP_EINVAL, "workspace is smaller than fsp_fp8_linear_workspace_bytes");
-  return check_allocation(p, size_t(want), "workspace");
-}
-
-struct Range {
-  const void* p;
-  int64_t bytes;
-  const char* name;
-};
-// The first `written` of the ranges against each other and all the others.
-fsp_status check_disjoint(const Range* r, int n, int written) {
-  for (int i = 0; i < written; ++i)
-    for (int j = i + 1; j < n; ++j)
-      if (overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
-        return fail(FSP_EINVAL, std::string(r[i].name) + " overlaps " + r[j].name);
   return FSP_OK;
 }
 
@@ -698,18 +709,18 @@ fsp_status linear(const void* x, int32_t xd, int64_t rows, int64_t in, int64_t x
   if (s == FSP_OK) s = check_matrix(y, yd, rows, out, ys, "y");
   if (s != FSP_OK || rows == 0 || out == 0) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (in == 0) return sum_of_nothing(rows, out, y, yd, ys, st);
   const Fp8Layout lw = layout_of(out, in);
   const int64_t want = forward_workspace(rows, in, out);
-  s = check_codes(w, lw, "w");
+  if (in > 0) s = check_codes(w, "w");
   if (s == FSP_OK) s = check_workspace(workspace, workspace_bytes, want);
   if (s != FSP_OK) return s;
   const Range ranges[] = {{y, span(rows, out, ys, yd), "y"},
                           {workspace, want, "workspace"},
                           {x, span(rows, in, xs, xd), "x"},
                           {w, lw.bytes, "w"}};
-  s = check_disjoint(ranges, 4, 2);
+  s = check_ranges(ranges, 4, 2);
   if (s != FSP_OK) return s;
+  if (in == 0) return sum_of_nothing(rows, out, y, yd, ys, st);
   if (few(rows, in)) {
     const FewArgs a{x, static_cast<const uint8_t*>(w), y, in, xs, out, ys, lw, int(rows)};
     using B = __nv_bfloat16;
@@ -731,14 +742,17 @@ fsp_status linear_backward(const void* x, int32_t xd, int64_t xs, const void* dy
   if (s != FSP_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows == 0 || in == 0 || out == 0) {   // one of the products may still be a sum of nothing
-    if (dx && rows > 0 && in > 0) s = sum_of_nothing(rows, in, dx, dxd, dxs, st);
+    const Range ranges[] = {{dx, dx ? span(rows, in, dxs, dxd) : 0, "grad_x"},
+                            {dw, dw ? span(out, in, dws, FSP_DTYPE_F32) : 0, "grad_w"}};
+    s = check_ranges(ranges, 2, 2);
+    if (s == FSP_OK && dx && rows > 0 && in > 0) s = sum_of_nothing(rows, in, dx, dxd, dxs, st);
     if (s == FSP_OK && dw && !accumulate && out > 0 && in > 0) s = sum_of_nothing(out, in, dw, FSP_DTYPE_F32, dws, st);
     return s;
   }
   if (!dx && !dw) return FSP_OK;
   const Fp8Layout lw = layout_of(in, out);
   const int64_t want = backward_workspace(rows, in, out);
-  if (dx) s = check_codes(wt, lw, "wt");
+  if (dx) s = check_codes(wt, "wt");
   if (s == FSP_OK) s = check_workspace(workspace, workspace_bytes, want);
   if (s != FSP_OK) return s;
   const Range ranges[] = {{dx, dx ? span(rows, in, dxs, dxd) : 0, "grad_x"},
@@ -747,7 +761,7 @@ fsp_status linear_backward(const void* x, int32_t xd, int64_t xs, const void* dy
                           {dy, span(rows, out, dys, dyd), "grad_y"},
                           {x, dw ? span(rows, in, xs, xd) : 0, "x"},
                           {wt, dx ? lw.bytes : 0, "wt"}};
-  s = check_disjoint(ranges, 6, 3);
+  s = check_ranges(ranges, 6, 3);
   if (s != FSP_OK) return s;
   char* q = static_cast<char*>(workspace);
   char* qt = q + round256(layout_of(rows, out).bytes);
