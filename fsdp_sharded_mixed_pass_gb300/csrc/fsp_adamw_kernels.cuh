@@ -31,98 +31,220 @@ namespace fsp {
 constexpr int kListThreads = 256;
 static_assert(kListTile == kListThreads / 32 * kListBlock, "one block per warp");
 
-// Codes and back.  Every step is a separately rounded operation, so that the
-// codes are a function of the values that any IEEE implementation reproduces.
+// ---- 8-bit states, two elements at a time ----------------------------------------
+//
+// The arithmetic runs on pairs of floats (one instruction for two products or
+// sums, each rounded as its own).  Every step of a code is a separately rounded
+// operation, so that codes are a function of the values that any IEEE
+// implementation reproduces.
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 abs2(float2 x) { return make_float2(fabsf(x.x), fabsf(x.y)); }
+
+// Code bytes 2 h, 2 h + 1 of a word as floats: the byte becomes the low bits of
+// 2^23, whose ulp is 1.
+__device__ __forceinline__ float2 bytes2(uint32_t w, int h, float offset) {
+  const float lo = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | unsigned(2 * h)));
+  const float hi = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | unsigned(2 * h + 1)));
+  return __fadd2_rn(make_float2(lo, hi), both(-offset));
+}
 constexpr float kInv127 = float(1.0 / 127.0), kInv255 = float(1.0 / 255.0);
-
-__device__ __forceinline__ float m_of_code(int q, float s) {
-  const float x = __fmul_rn(float(q), kInv127);
-  return __fmul_rn(s, __fmul_rn(x, fabsf(x)));
-}
-__device__ __forceinline__ float v_of_code(unsigned q, float s) {
-  float x = __fmul_rn(float(q), kInv255);
-  x = __fmul_rn(x, x);
-  return __fmul_rn(s, __fmul_rn(x, x));
-}
-__device__ __forceinline__ int code_of_m(float m, float s) {
-  if (!(s > 0.f)) return 0;
-  const int q = __float2int_rn(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m), s)), 127.f));
-  return m < 0.f ? -q : q;
-}
-__device__ __forceinline__ unsigned code_of_v(float v, float s) {
-  if (!(s > 0.f)) return 0u;
-  const unsigned q = __float2uint_rn(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fdiv_rn(v, s))), 255.f));
-  return v > 0.f && q == 0u ? 1u : q;
-}
-
-// The largest |x| of the warp's block: magnitudes order as their bit patterns,
-// NaN above infinity, so a NaN anywhere is what comes back.
-__device__ __forceinline__ float block_largest(const float* x) {
-  unsigned top = 0;
+// What four codes stand for in a block of scale s.
+__device__ __forceinline__ void m_of_codes(uint32_t q, float s, float2* m) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  for (int h = 0; h < 2; ++h) {
+    const float2 x = __fmul2_rn(bytes2(q ^ 0x80808080u, h, 8388608.f + 128.f), both(kInv127));
+    m[h] = __fmul2_rn(both(s), __fmul2_rn(x, abs2(x)));
+  }
 }
+__device__ __forceinline__ void v_of_codes(uint32_t q, float s, float2* v) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float2 x = __fmul2_rn(bytes2(q, h, 8388608.f), both(kInv255));
+    x = __fmul2_rn(x, x);
+    v[h] = __fmul2_rn(both(s), __fmul2_rn(x, x));
+  }
+}
+
+__device__ __forceinline__ int exact_code_of_m(float m, float s) {   // of |m|
+  return __float2int_rn(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m), s)), 127.f));
+}
+__device__ __forceinline__ int exact_code_of_v(float v, float s) {
+  return __float2int_rn(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fdiv_rn(v, s))), 255.f));
+}
+__device__ __forceinline__ float sqrt_approx_ftz(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A block's scale and its reciprocal for the quick evaluation (NaN where that
+// could leave the range of fp32: such a block takes the exact one throughout).
+struct BlockScale {
+  float s, inv;
+};
+__device__ __forceinline__ BlockScale block_scale(float s) {
+  return {s, s > 0x1p-100f && s < 0x1p100f ? rcp_approx(s) : __int_as_float(0x7fffffff)};
+}
+
+// rint(r) for |r| < 2^22 as the low bits of r + 3 2^22, whose ulp is 1.
+constexpr float kRintMagic = 12582912.f;
+// The quick evaluations err by at most 2^-13 codes (below); nearer to a tie than
+// 2^-12 an element takes the exact one, so every code is the exact one's.
+constexpr float kNearTie = 0.5f - 0x1p-12f;
+
+// The rounded value's low bits in t's, and whether no rounding is near a tie.
+__device__ __forceinline__ bool rint2(float2 r, float2& t) {
+  t = __fadd2_rn(r, both(kRintMagic));
+  const float2 f = __fadd2_rn(t, both(-kRintMagic));
+  const float2 e = __fadd2_rn(r, make_float2(-f.x, -f.y));
+  return fabsf(e.x) <= kNearTie && fabsf(e.y) <= kNearTie;
+}
+__device__ __forceinline__ uint32_t low_bytes(const float2* t) {
+  const uint32_t lo = __byte_perm(__float_as_uint(t[0].x), __float_as_uint(t[0].y), 0x0040u);
+  const uint32_t hi = __byte_perm(__float_as_uint(t[1].x), __float_as_uint(t[1].y), 0x0040u);
+  return __byte_perm(lo, hi, 0x5410u);
+}
+
+// The codes of four elements, the first in the low byte.  Approximate roots: with
+// x' = |m| inv (two roundings and rcp_approx: relative error below 2^-21.4) the
+// approximate root errs by 2^-22 and half of that, 127 x' by 2^-24 more: together
+// below 2^-21 of a code of at most 127, or 2^-14.  v: two roots and a quarter of
+// x's error, below 2^-21 of at most 255, or 2^-13.
+__device__ __forceinline__ uint32_t codes_of_m(const float2* m, BlockScale b) {
+  if (!(b.s > 0.f)) return 0u;
+  float2 t[2];
+  bool sure = true;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 x = __fmul2_rn(m[h], both(b.inv));
+    const float2 r = __fmul2_rn(make_float2(copysignf(sqrt_approx_ftz(fabsf(x.x)), x.x), copysignf(sqrt_approx_ftz(fabsf(x.y)), x.y)),
+                                both(127.f));
+    sure = rint2(r, t[h]) && sure;
+  }
+  uint32_t w = low_bytes(t);
+  if (!sure) {
+    w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = j & 1 ? m[j >> 1].y : m[j >> 1].x;
+      const int q = exact_code_of_m(x, b.s);
+      w |= uint32_t((x < 0.f ? -q : q) & 0xff) << (8 * j);
+    }
+  }
+  return w;
+}
+__device__ __forceinline__ uint32_t codes_of_v(const float2* v, BlockScale b) {
+  if (!(b.s > 0.f)) return 0u;
+  float2 t[2];
+  bool sure = true;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 x = __fmul2_rn(v[h], both(b.inv));
+    const float2 r = __fmul2_rn(make_float2(sqrt_approx_ftz(sqrt_approx_ftz(x.x)), sqrt_approx_ftz(sqrt_approx_ftz(x.y))), both(255.f));
+    sure = rint2(r, t[h]) && sure;
+    // above 0 but rounded to 0: code 1
+    sure = sure && !(r.x < 0.5f && v[h].x > 0.f) && !(r.y < 0.5f && v[h].y > 0.f);
+  }
+  uint32_t w = low_bytes(t);
+  if (!sure) {
+    w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = j & 1 ? v[j >> 1].y : v[j >> 1].x;
+      w |= uint32_t(x > 0.f ? max(exact_code_of_v(x, b.s), 1) : 0) << (8 * j);
+    }
+  }
+  return w;
+}
+
+// The largest |x| of the warp's block, NaN where one is: magnitudes order as
+// their bit patterns, NaN above infinity.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float block_largest(const float2* x) {
+  float top = max_nan(fabsf(x[0].x), fabsf(x[0].y));
+#pragma unroll
+  for (int j = 1; j < 4; ++j) top = max_nan(top, max_nan(fabsf(x[j].x), fabsf(x[j].y)));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+}
+
+// ---- element access ---------------------------------------------------------------
 
 // Four consecutive elements at base + i (i counted in elements): one vector
 // access where the tensor's pointers allow it, else element by element with
 // `n` of the four inside the tensor.
-__device__ __forceinline__ void load4(const void* base, bool bf16, bool vec, int64_t i, int n, float* x) {
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
+
+__device__ __forceinline__ void load4(const void* base, bool bf16, bool vec, int64_t i, int n, float2* x) {
   if (bf16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + i;
     if (vec && n == 4) {
       const uint2 b = __ldcs(reinterpret_cast<const uint2*>(p));
-      x[0] = __uint_as_float(b.x << 16);
-      x[1] = __uint_as_float(b.x & 0xffff0000u);
-      x[2] = __uint_as_float(b.y << 16);
-      x[3] = __uint_as_float(b.y & 0xffff0000u);
+      x[0] = make_float2(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u));
+      x[1] = make_float2(__uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = j < n ? __uint_as_float(uint32_t(__ldcs(p + j)) << 16) : 0.f;
+      for (int h = 0; h < 2; ++h)
+        x[h] = make_float2(2 * h < n ? bf16_value(__ldcs(p + 2 * h)) : 0.f, 2 * h + 1 < n ? bf16_value(__ldcs(p + 2 * h + 1)) : 0.f);
     }
   } else {
     const float* p = static_cast<const float*>(base) + i;
     if (vec && n == 4) {
       const float4 f = __ldcs(reinterpret_cast<const float4*>(p));
-      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+      x[0] = make_float2(f.x, f.y);
+      x[1] = make_float2(f.z, f.w);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = j < n ? __ldcs(p + j) : 0.f;
+      for (int h = 0; h < 2; ++h)
+        x[h] = make_float2(2 * h < n ? __ldcs(p + 2 * h) : 0.f, 2 * h + 1 < n ? __ldcs(p + 2 * h + 1) : 0.f);
     }
   }
 }
 
-__device__ __forceinline__ void store4(void* base, bool bf16, bool vec, int64_t i, int n, const float* x) {
+__device__ __forceinline__ void store4(void* base, bool bf16, bool vec, int64_t i, int n, const float2* x) {
   if (bf16) {
     uint16_t* p = static_cast<uint16_t*>(base) + i;
     if (vec && n == 4) {
-      __stcs(reinterpret_cast<uint2*>(p), pack_bf16x4(make_float4(x[0], x[1], x[2], x[3])));
+      __stcs(reinterpret_cast<uint2*>(p), pack_bf16x4(make_float4(x[0].x, x[0].y, x[1].x, x[1].y)));
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) __stcs(p + j, bf16_bits(x[j]));
+      for (int h = 0; h < 2; ++h) {
+        if (2 * h < n) __stcs(p + 2 * h, bf16_bits(x[h].x));
+        if (2 * h + 1 < n) __stcs(p + 2 * h + 1, bf16_bits(x[h].y));
+      }
     }
   } else {
     float* p = static_cast<float*>(base) + i;
     if (vec && n == 4) {
-      __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(reinterpret_cast<float4*>(p), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) __stcs(p + j, x[j]);
+      for (int h = 0; h < 2; ++h) {
+        if (2 * h < n) __stcs(p + 2 * h, x[h].x);
+        if (2 * h + 1 < n) __stcs(p + 2 * h + 1, x[h].y);
+      }
     }
   }
 }
 
-// The update of one element whose states will be rounded to 8 bits: m' and v'
+// The update of two elements whose states will be rounded to 8 bits: m' and v'
 // with every product rounded on its own (their codes are then reproducible),
-// p' as adamw()'s fp32 evaluation (the states' 1.6 % steps leave nothing for
-// its float-pair refinement to keep).
-__device__ __forceinline__ void adamw_coarse(float g, float& p, float& m, float& v, const Coeffs& c) {
-  m = __fadd_rn(__fmul_rn(m, c.beta1), __fmul_rn(g, c.one_minus_beta1_hi));
-  v = __fadd_rn(__fmul_rn(v, c.beta2), __fmul_rn(__fmul_rn(g, g), c.one_minus_beta2_hi));
-  const float r = rcp_approx(__fmaf_rn(sqrt_approx(v), c.isb_hi, c.eps));
-  p = __fsub_rn(__fmul_rn(p, c.decay_hi), __fmul_rn(c.step_hi, __fmul_rn(m, r)));
+// p' in fp32 as adamw()'s first evaluation (the states' 1.6 % steps leave
+// nothing for its float-pair refinement to keep).
+__device__ __forceinline__ void adamw_coarse(float2 g, float2& p, float2& m, float2& v, const Coeffs& c) {
+  m = __fmul2_rn(m, both(c.beta1));
+  v = __fmul2_rn(v, both(c.beta2));
+  const float2 gm = __fmul2_rn(g, both(c.one_minus_beta1_hi));
+  const float2 gv = __fmul2_rn(__fmul2_rn(g, g), both(c.one_minus_beta2_hi));
+  m = make_float2(__fadd_rn(m.x, gm.x), __fadd_rn(m.y, gm.y));   // (a sum of pairs would be fused with its product)
+  v = make_float2(__fadd_rn(v.x, gv.x), __fadd_rn(v.y, gv.y));
+  const float2 d = __ffma2_rn(make_float2(sqrt_approx(v.x), sqrt_approx(v.y)), both(c.isb_hi), both(c.eps));
+  const float2 u = __fmul2_rn(m, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+  p = __ffma2_rn(p, both(c.decay_hi), __fmul2_rn(u, both(-c.step_hi)));
 }
 
 __device__ __forceinline__ Coeffs list_coeffs(const ListArgs& a) {
@@ -137,100 +259,108 @@ __device__ __forceinline__ Coeffs list_coeffs(const ListArgs& a) {
   return c;
 }
 
+// One block as a lane holds it: elements 4 l .. 4 l + 3 of each half.
+struct ListBlock {
+  float2 g[4], p[4];
+  float2 m[4], v[4];          // fp32 states
+  uint32_t qm[2], qv[2];      // 8-bit states
+  float ms, vs;
+};
+
 template <bool k8Bit>
-__global__ void __launch_bounds__(kListThreads) adamw_list_kernel(const __grid_constant__ ListArgs a) {
-  const ListTile tile = a.tiles[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int begin = warp * kListBlock;   // this warp's block in the tile
-  if (begin >= tile.len) return;
-  const bool pb = tile.flags & kListParamBf16, gb = tile.flags & kListGradBf16, vec = tile.flags & kListVec;
-  const int64_t slot = tile.state_off + begin;
-  const int i0 = begin + lane * 4, i1 = i0 + kListBlock / 2;
-  const int n0 = min(4, max(0, tile.len - i0)), n1 = min(4, max(0, tile.len - i1));
-  float g[8], p[8], m[8], v[8];
-  load4(tile.grad, gb, vec, i0, n0, g);
-  load4(tile.grad, gb, vec, i1, n1, g + 4);
-  load4(tile.param, pb, vec, i0, n0, p);
-  load4(tile.param, pb, vec, i1, n1, p + 4);
-  char4* mq = nullptr;
-  uchar4* vq = nullptr;
-  float *mf = nullptr, *vf = nullptr;
+__device__ __forceinline__ void load_block(const ListArgs& a, const ListTile& t, int begin, int lane, ListBlock& b) {
+  const bool pb = t.flags & kListParamBf16, gb = t.flags & kListGradBf16, vec = t.flags & kListVec;
+  const int64_t slot = t.state_off + begin;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = begin + h * (kListBlock / 2) + lane * 4, n = min(4, max(0, t.len - i));
+    load4(t.grad, gb, vec, i, n, b.g + 2 * h);
+    load4(t.param, pb, vec, i, n, b.p + 2 * h);
+    if (k8Bit) {
+      const uint32_t in = n == 4 ? ~0u : (1u << (8 * n)) - 1u;   // nothing past the tensor's end
+      b.qm[h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + slot) + 32 * h + lane) & in;
+      b.qv[h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + slot) + 32 * h + lane) & in;
+    } else {
+      load4(static_cast<const float*>(a.m) + t.state_off, false, true, i, n, b.m + 2 * h);
+      load4(static_cast<const float*>(a.v) + t.state_off, false, true, i, n, b.v + 2 * h);
+    }
+  }
   if (k8Bit) {
-    mq = reinterpret_cast<char4*>(static_cast<int8_t*>(a.m) + slot) + lane;
-    vq = reinterpret_cast<uchar4*>(static_cast<uint8_t*>(a.v) + slot) + lane;
-    const float ms = a.m_scale[slot / kListBlock], vs = a.v_scale[slot / kListBlock];
+    b.ms = a.m_scale[slot / kListBlock];
+    b.vs = a.v_scale[slot / kListBlock];
+  }
+}
+
+template <bool k8Bit>
+__device__ __forceinline__ void update_block(const ListArgs& a, const ListTile& t, const Coeffs& c, float coef, int begin,
+                                             int lane, ListBlock& b) {
+  const bool pb = t.flags & kListParamBf16, vec = t.flags & kListVec;
+  const int64_t slot = t.state_off + begin;
+  if (k8Bit) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const char4 cm = mq[32 * h];
-      const uchar4 cv = vq[32 * h];
-      const int n = h ? n1 : n0;
-      const int qm[4] = {cm.x, cm.y, cm.z, cm.w};
-      const unsigned qv[4] = {cv.x, cv.y, cv.z, cv.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[4 * h + j] = j < n ? m_of_code(qm[j], ms) : 0.f;
-        v[4 * h + j] = j < n ? v_of_code(qv[j], vs) : 0.f;
-      }
+      m_of_codes(b.qm[h], b.ms, b.m + 2 * h);
+      v_of_codes(b.qv[h], b.vs, b.v + 2 * h);
     }
-  } else {
-    mf = static_cast<float*>(a.m) + slot - begin;
-    vf = static_cast<float*>(a.v) + slot - begin;
-    load4(mf, false, true, i0, n0, m);
-    load4(mf, false, true, i1, n1, m + 4);
-    load4(vf, false, true, i0, n0, v);
-    load4(vf, false, true, i1, n1, v + 4);
   }
-  const float coef = a.grad_scale ? *a.grad_scale : 1.f;
-  const Coeffs c = list_coeffs(a);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float gj = __fmul_rn(g[j], coef);
-    if (k8Bit)
-      adamw_coarse(gj, p[j], m[j], v[j], c);
-    else
-      adamw(gj, p[j], m[j], v[j], c);
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = __fmul2_rn(b.g[j], both(coef));
+    if (k8Bit) {
+      adamw_coarse(x, b.p[j], b.m[j], b.v[j], c);
+    } else {
+      adamw(x.x, b.p[j].x, b.m[j].x, b.v[j].x, c);
+      adamw(x.y, b.p[j].y, b.m[j].y, b.v[j].y, c);
+    }
   }
-  store4(tile.param, pb, vec, i0, n0, p);
-  store4(tile.param, pb, vec, i1, n1, p + 4);
-  if (tile.copy) {
-    store4(tile.copy, true, vec, i0, n0, p);
-    store4(tile.copy, true, vec, i1, n1, p + 4);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = begin + h * (kListBlock / 2) + lane * 4, n = min(4, max(0, t.len - i));
+    store4(t.param, pb, vec, i, n, b.p + 2 * h);
+    if (t.copy) store4(t.copy, true, vec, i, n, b.p + 2 * h);
+    if (!k8Bit) {
+      store4(static_cast<float*>(a.m) + t.state_off, false, true, i, n, b.m + 2 * h);
+      store4(static_cast<float*>(a.v) + t.state_off, false, true, i, n, b.v + 2 * h);
+    }
   }
   if (k8Bit) {
     // past the tensor's end g, m and v are 0: they stay out of the largest value
     // (unless coef is not finite, which every element of the block then shows)
-    const float ms = block_largest(m), vs = block_largest(v);
+    const BlockScale ms = block_scale(block_largest(b.m)), vs = block_scale(block_largest(b.v));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float* x = m + 4 * h;
-      const float* y = v + 4 * h;
-      char4 cm = make_char4(code_of_m(x[0], ms), code_of_m(x[1], ms), code_of_m(x[2], ms), code_of_m(x[3], ms));
-      uchar4 cv = make_uchar4(code_of_v(y[0], vs), code_of_v(y[1], vs), code_of_v(y[2], vs), code_of_v(y[3], vs));
-      const int n = h ? n1 : n0;
+      const uint32_t qm = codes_of_m(b.m + 2 * h, ms), qv = codes_of_v(b.v + 2 * h, vs);
+      uint32_t* pm = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + slot) + 32 * h + lane;
+      uint32_t* pv = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + slot) + 32 * h + lane;
+      const int n = min(4, max(0, t.len - (begin + h * (kListBlock / 2) + lane * 4)));
       if (n == 4) {
-        mq[32 * h] = cm;
-        vq[32 * h] = cv;
+        __stcs(pm, qm);
+        __stcs(pv, qv);
       } else {
-        const signed char qm[4] = {cm.x, cm.y, cm.z, cm.w};
-        const unsigned char qv[4] = {cv.x, cv.y, cv.z, cv.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (j < n) {
-            reinterpret_cast<signed char*>(mq + 32 * h)[j] = qm[j];
-            reinterpret_cast<unsigned char*>(vq + 32 * h)[j] = qv[j];
+            reinterpret_cast<uint8_t*>(pm)[j] = uint8_t(qm >> (8 * j));
+            reinterpret_cast<uint8_t*>(pv)[j] = uint8_t(qv >> (8 * j));
           }
       }
     }
     if (lane == 0) {
-      a.m_scale[slot / kListBlock] = ms;
-      a.v_scale[slot / kListBlock] = vs;
+      a.m_scale[slot / kListBlock] = ms.s;
+      a.v_scale[slot / kListBlock] = vs.s;
     }
-  } else {
-    store4(mf, false, true, i0, n0, m);
-    store4(mf, false, true, i1, n1, m + 4);
-    store4(vf, false, true, i0, n0, v);
-    store4(vf, false, true, i1, n1, v + 4);
   }
+}
+
+template <bool k8Bit>
+__global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel(const __grid_constant__ ListArgs a) {
+  const ListTile tile = a.tiles[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int begin = warp * kListBlock;   // this warp's block in the tile
+  if (begin >= tile.len) return;
+  ListBlock b;
+  load_block<k8Bit>(a, tile, begin, lane, b);
+  update_block<k8Bit>(a, tile, list_coeffs(a), a.grad_scale ? *a.grad_scale : 1.f, begin, lane, b);
 }
 
 // fp32 states <-> 8-bit states of whole blocks: a warp per block, grid over
@@ -245,12 +375,11 @@ __global__ void __launch_bounds__(kListThreads) list_state_values_kernel(const i
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t i = b * kListBlock + h * (kListBlock / 2) + lane * 4;
-    const char4 cm = *reinterpret_cast<const char4*>(m8 + i);
-    const uchar4 cv = *reinterpret_cast<const uchar4*>(v8 + i);
-    __stcs(reinterpret_cast<float4*>(m + i),
-           make_float4(m_of_code(cm.x, s), m_of_code(cm.y, s), m_of_code(cm.z, s), m_of_code(cm.w, s)));
-    __stcs(reinterpret_cast<float4*>(v + i),
-           make_float4(v_of_code(cv.x, t), v_of_code(cv.y, t), v_of_code(cv.z, t), v_of_code(cv.w, t)));
+    float2 x[2];
+    m_of_codes(*reinterpret_cast<const uint32_t*>(m8 + i), s, x);
+    store4(m, false, true, i, 4, x);
+    v_of_codes(*reinterpret_cast<const uint32_t*>(v8 + i), t, x);
+    store4(v, false, true, i, 4, x);
   }
 }
 
@@ -260,27 +389,23 @@ __global__ void __launch_bounds__(kListThreads) list_state_load_kernel(const flo
   const int lane = threadIdx.x & 31;
   const int64_t b = int64_t(blockIdx.x) * (kListThreads / 32) + (threadIdx.x >> 5);
   if (b >= n_blocks) return;
-  float x[8], y[8];
+  float2 x[4], y[4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t i = b * kListBlock + h * (kListBlock / 2) + lane * 4;
-    load4(m, false, true, i, 4, x + 4 * h);
-    load4(v, false, true, i, 4, y + 4 * h);
+    load4(m, false, true, i, 4, x + 2 * h);
+    load4(v, false, true, i, 4, y + 2 * h);
   }
-  const float s = block_largest(x), t = block_largest(y);
+  const BlockScale s = block_scale(block_largest(x)), t = block_scale(block_largest(y));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t i = b * kListBlock + h * (kListBlock / 2) + lane * 4;
-    const float* xh = x + 4 * h;
-    const float* yh = y + 4 * h;
-    *reinterpret_cast<char4*>(m8 + i) =
-        make_char4(code_of_m(xh[0], s), code_of_m(xh[1], s), code_of_m(xh[2], s), code_of_m(xh[3], s));
-    *reinterpret_cast<uchar4*>(v8 + i) =
-        make_uchar4(code_of_v(yh[0], t), code_of_v(yh[1], t), code_of_v(yh[2], t), code_of_v(yh[3], t));
+    *reinterpret_cast<uint32_t*>(m8 + i) = codes_of_m(x + 2 * h, s);
+    *reinterpret_cast<uint32_t*>(v8 + i) = codes_of_v(y + 2 * h, t);
   }
   if (lane == 0) {
-    ms[b] = s;
-    vs[b] = t;
+    ms[b] = s.s;
+    vs[b] = t.s;
   }
 }
 
