@@ -7,16 +7,17 @@
 // named rows, when accumulating); no atomic addition touches a value, so the
 // result depends on the tokens alone.
 //
-// Gradient, four launches:
+// Gradient, three launches, the later two with programmatic stream serialisation
+// (their CTAs are there when the launch before them ends):
 //   1. sort_tokens_kernel: one cluster sorts (token, position) pairs by token,
 //      stably (radix sort), and marks the tokens that occur in a bitmap;
-//   2. zero_rows_kernel (not when accumulating): zeros into every other row;
-//   3. sum_rows_kernel: the sorted pairs in chunks of kChunk; each thread owns
-//      a few columns of a chunk and adds its rows in fp32 in sorted order.  A
-//      token whose pairs lie within one chunk is finished there; the parts of
-//      one that spans chunks go to the workspace, so a token that fills half of
-//      a batch is spread over as many CTAs as any other half;
-//   4. join_rows_kernel: adds such a token's parts in chunk order.
+//   2. sum_rows_kernel: the sorted pairs in chunks of 32; a warp owns 32 x V columns
+//      of a chunk and adds its rows in fp32 in sorted order.  A token whose pairs
+//      lie within one chunk is finished there; the parts of one that spans chunks
+//      go to the workspace, so a token that fills half of a batch is spread over as
+//      many CTAs as any other half.  Between them, CTAs that write zeros into the
+//      rows that no token names (not when accumulating);
+//   3. join_rows_kernel: adds such a token's parts, eight warps a share each.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,12 +37,12 @@ namespace cg = cooperative_groups;
 constexpr unsigned kErrToken = 16u;   // a token outside [0, vocab)
 __device__ unsigned int g_token_error = 0;
 
-// ---- element access -----------------------------------------------------------
+// Programmatic dependent launch: let the next launch on the stream that allows
+// it be scheduled; wait until the launches this grid depends on have completed.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-template <typename T, int V>
-struct Vec {   // V consecutive elements
-  T x[V];
-};
+// ---- element access -----------------------------------------------------------
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -76,6 +77,21 @@ __device__ __forceinline__ void load_vec(const T* p, float* f) {
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] = widen(p[j]);
+  }
+}
+
+// As load_vec, without widening.
+template <typename T, int V>
+__device__ __forceinline__ void load_raw(const T* p, T* x) {
+  constexpr int kBytes = int(sizeof(T)) * V;
+  if constexpr (kBytes >= 16) {
+#pragma unroll
+    for (int k = 0; k < kBytes / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+  } else if constexpr (kBytes == 8) {
+    *reinterpret_cast<uint2*>(x) = __ldcs(reinterpret_cast<const uint2*>(p));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = p[j];
   }
 }
 
@@ -140,9 +156,13 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kSortCluster = 8;             // CTAs of a large sort
-constexpr int64_t kSortOneCta = 4096;       // tokens that one CTA sorts alone
-constexpr int kSortSmem = kSortWarps * kBins * 4 + 2 * kBins * 4 + kSortWarps * 4;
+constexpr int kSortCluster = 16;            // most CTAs of a sort (65536 tokens: 23 us, in eight CTAs 36)
+constexpr int kHeld = 8;                    // items of a lane that stay in registers
+constexpr int kSortOne = 4096;              // tokens that one CTA sorts in its shared memory
+constexpr int64_t kSortPerCta = 2048;       // tokens per CTA of a cluster from which twice as many pay
+constexpr int kSortSmem = kSortWarps * kBins * 4 + kBins * 4 + kSortWarps * 4;
+constexpr int kSortSmemOne = kSortSmem + 2 * kSortOne * 8;
+static_assert(kSortOne <= kSortThreads * kHeld, "one CTA holds its items");
 
 struct SortArgs {
   const void* tokens;
@@ -183,58 +203,103 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t d, bool valid) {
 // Least significant digit first.  CTA c of the cluster holds a contiguous run
 // of the items and each of its warps a contiguous run of that, so "earlier
 // CTA, earlier warp, earlier round, lower lane" is the input's order and every
-// pass is stable.  Per pass: each warp counts its digits in shared memory; the
-// counts become each warp's first output slot per digit (a scan over digits,
-// CTAs and warps); each warp then walks its items again and places them.
+// pass is stable.  Per pass: each warp ranks its items within their digit,
+// counting in shared memory; the counts become each warp's first output slot per
+// digit (a scan over digits, CTAs and warps); the items are placed.  Up to
+// kHeld rounds of 32 a warp keeps items and ranks in registers (131072 tokens in
+// 16 CTAs); beyond, it walks them a second time.  kOne: a single CTA, whose passes
+// before the last stay in shared memory.
+template <bool kOne>
 __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const __grid_constant__ SortArgs s) {
-  extern __shared__ uint32_t smem[];
+  extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* hist = smem;                            // [kSortWarps][kBins]
-  uint32_t* total = hist + kSortWarps * kBins;      // [kBins]: this CTA's, then its first slot
-  uint32_t* sums = total + 2 * kBins;               // [kSortWarps]
-  cg::cluster_group cluster = cg::this_cluster();
+  uint32_t* total = hist + kSortWarps * kBins;      // [kBins]: first slot of this CTA's items of the digit
+  uint32_t* sums = total + kBins;                   // [kSortWarps]
+  uint2* local = reinterpret_cast<uint2*>(sums + kSortWarps);   // kOne: two buffers of items
+  auto sync = [] {
+    if constexpr (kOne)
+      __syncthreads();
+    else
+      cg::this_cluster().sync();
+  };
+  auto item_at = [](const uint2* p) {   // written by any CTA of the cluster before its last sync
+    if constexpr (kOne)
+      return *p;
+    else
+      return __ldcg(p);
+  };
+  launch_dependents();
   const int n_ctas = int(gridDim.x), cta = int(blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = cta * kSortThreads + tid; i < s.n_words; i += n_ctas * kSortThreads) s.present[i] = 0;
-  cluster.sync();
   const int per_warp = ((s.n + n_ctas * kSortWarps - 1) / (n_ctas * kSortWarps) + 31) / 32 * 32;
   const int64_t first = int64_t(cta * kSortWarps + warp) * per_warp;
   const int begin = int(min(first, int64_t(s.n))), end = int(min(first + per_warp, int64_t(s.n)));
+  const bool held = per_warp <= 32 * kHeld;
+  const uint32_t digit_mask = (1u << s.bits) - 1u;
+  uint32_t* mine = hist + warp * kBins;
+  uint2 item[kHeld];
+  uint32_t rank[kHeld];
+  uint2* dst = s.b;
   for (int pass = 0; pass < s.passes; ++pass) {
     const int shift = pass * s.bits;
-    const uint32_t digit_mask = (1u << s.bits) - 1u;
-    const uint2* src = pass & 1 ? s.a : s.b;
-    uint2* dst = pass & 1 ? s.b : s.a;
+    const uint2* src = kOne ? local + ((pass + 1) & 1) * kSortOne : pass & 1 ? s.a : s.b;
+    dst = kOne && pass + 1 < s.passes ? local + (pass & 1) * kSortOne : pass & 1 ? s.b : s.a;
+    auto load = [&](int from) {   // kHeld rounds of this warp's items
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int i = from + 32 * k + lane;
+        if (i < end) item[k] = pass == 0 ? make_uint2(token_key(s, i), uint32_t(i)) : item_at(&src[i]);
+      }
+    };
+    auto rank_round = [&](int k, int i) {   // item k's rank among this warp's items of its digit so far
+      const bool valid = i < end;
+      const uint32_t d = valid ? (item[k].x >> shift) & digit_mask : 0u;
+      const uint32_t peers = same_digit(d, valid);
+      const uint32_t at = mine[d];
+      __syncwarp();
+      const uint32_t before = __popc(peers & ((1u << lane) - 1u));
+      if (valid && before == 0) mine[d] = at + __popc(peers);
+      __syncwarp();
+      return at + before;
+    };
+    load(begin);
     for (int i = tid; i < kSortWarps * kBins; i += kSortThreads) hist[i] = 0;
     __syncthreads();
-    for (int i = begin + lane; i < end; i += 32) {
-      uint32_t key;
-      if (pass == 0) {
-        key = token_key(s, i);
-        if (key < uint32_t(s.vocab)) atomicOr(&s.present[key >> 5], 1u << (key & 31));
-      } else {
-        key = __ldcg(&src[i]).x;
+    for (int from = begin; from < end; from += 32 * kHeld) {
+      if (from > begin) load(from);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        if (from + 32 * k >= end) break;
+        rank[k] = rank_round(k, from + 32 * k + lane);
       }
-      atomicAdd(&hist[warp * kBins + ((key >> shift) & digit_mask)], 1u);
     }
     __syncthreads();
     if (tid < kBins) {   // counts -> each warp's offset within this CTA's items of the digit
-      uint32_t run = 0;
+      uint32_t c[kSortWarps], run = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * kBins + tid];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = hist[w * kBins + tid];
         hist[w * kBins + tid] = run;
-        run += c;
+        run += c[w];
       }
       total[tid] = run;
-      s.totals[cta * kBins + tid] = run;
+      if (!kOne) s.totals[cta * kBins + tid] = run;
     }
-    cluster.sync();
+    if (!kOne) sync();
     // first slot of each digit (over all CTAs), then of this CTA's items of it
     uint32_t all = 0, before = 0;
-    if (tid < kBins) {
-      for (int c = 0; c < n_ctas; ++c) {
-        const uint32_t x = __ldcg(&s.totals[c * kBins + tid]);
-        if (c < cta) before += x;
-        all += x;
+    if (kOne && tid < kBins) {
+      all = total[tid];
+    } else if (tid < kBins) {
+      uint32_t t[kSortCluster];
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) t[c] = c < n_ctas ? __ldcg(&s.totals[c * kBins + tid]) : 0u;
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        if (c < cta) before += t[c];
+        all += t[c];
       }
     }
     uint32_t scan = all;   // inclusive over the warp's digits
@@ -251,32 +316,40 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const __grid_
       total[tid] = base + scan - all + before;
     }
     __syncthreads();
-    for (int i0 = begin; i0 < end; i0 += 32) {
-      const int i = i0 + lane;
-      const bool valid = i < end;
-      uint2 item = make_uint2(0, 0);
-      if (valid) item = pass == 0 ? make_uint2(token_key(s, i), uint32_t(i)) : __ldcg(&src[i]);
-      const uint32_t d = (item.x >> shift) & digit_mask;
-      const uint32_t peers = same_digit(d, valid);
-      uint32_t at = 0;
-      if (valid) at = hist[warp * kBins + d];
-      __syncwarp();
-      if (valid) {
-        const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
-        if (rank == 0) hist[warp * kBins + d] = at + __popc(peers);
-        dst[total[d] + at + rank] = item;
+    if (held) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (begin + 32 * k + lane < end) {
+          const uint32_t d = (item[k].x >> shift) & digit_mask;
+          dst[total[d] + mine[d] + rank[k]] = item[k];
+        }
+    } else {
+      for (int from = begin; from < end; from += 32 * kHeld) {
+        load(from);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+          const int i = from + 32 * k + lane;
+          if (from + 32 * k >= end) break;
+          const uint32_t at = rank_round(k, i);   // (from the warp's offset on)
+          if (i < end) dst[total[(item[k].x >> shift) & digit_mask] + at] = item[k];
+        }
       }
-      __syncwarp();
     }
-    cluster.sync();   // the pass's items, and totals[] before it is written again
+    sync();   // the pass's items, and totals[] before it is written again
+  }
+  // the first item of each token marks it
+  const int step = n_ctas * kSortThreads;
+  for (int i = cta * kSortThreads + tid; i < s.n; i += step) {
+    const uint32_t key = item_at(&dst[i]).x;
+    if (key < uint32_t(s.vocab) && (i == 0 || item_at(&dst[i - 1]).x != key)) atomicOr(&s.present[key >> 5], 1u << (key & 31));
   }
 }
 
 // ---- gradient: rows ------------------------------------------------------------------
 
 constexpr int kRowThreads = 128;
-constexpr int kChunk = 32;   // sorted pairs of one thread's walk
-constexpr int kAhead = 8;    // rows in flight per thread
+constexpr int kChunk = 32;       // sorted pairs of one warp's walk
+constexpr int kZeroRows = 32;    // rows of one CTA that writes zeros: a word of the bitmap
 
 struct RowArgs {
   const uint2* items;        // sorted (key, position)
@@ -288,7 +361,9 @@ struct RowArgs {
   float scale;
   int n;
   int accumulate;
-  int cols;                  // threads along the columns (a power of two)
+  int cols;                  // threads along the columns: 32, 64 or 128
+  int col_ctas;              // CTAs along the columns
+  int64_t sum_ctas, zero_ctas;
 };
 
 template <typename T, int V>
@@ -306,88 +381,176 @@ __device__ __forceinline__ void finish_row(const RowArgs& a, uint32_t row, int64
   store_vec<T, V>(p, f);
 }
 
-// A thread: V columns of one chunk.
+// A warp: 32 x V columns of one chunk.
 template <typename G, typename T, int V>
-__global__ void __launch_bounds__(kRowThreads) sum_rows_kernel(const __grid_constant__ RowArgs a) {
-  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
-  const int64_t chunk = int64_t(blockIdx.x) * (kRowThreads / a.cols) + cy;
-  const int64_t col = (int64_t(blockIdx.y) * a.cols + cx) * V;
+__device__ __forceinline__ void sum_chunk(const RowArgs& a, int64_t chunk, int64_t col, int lane) {
+  constexpr int kAhead = int(sizeof(G)) * V <= 16 ? 16 : 8;   // rows in flight
   const int64_t begin = chunk * kChunk;
-  if (begin >= a.n || col >= a.dim) return;
-  const int end = int(min(begin + kChunk, int64_t(a.n)));
+  if (begin >= a.n) return;
   const uint32_t none = uint32_t(a.vocab);
-  uint32_t row = a.items[begin].x;
-  bool head = begin > 0 && a.items[begin - 1].x == row;
+  const uint2 it = begin + lane < a.n ? a.items[begin + lane] : make_uint2(none, 0);
+  const uint32_t prev = begin > 0 ? a.items[begin - 1].x : none;
+  const uint32_t next = begin + kChunk < a.n ? a.items[begin + kChunk].x : none;
+  const int count = __popc(__ballot_sync(0xffffffffu, it.x < none));   // dropped tokens sort last
+  if (count == 0) return;
+  const bool in = col < a.dim;
   const G* grad = static_cast<const G*>(a.grad) + col;
+  uint32_t row = __shfl_sync(0xffffffffu, it.x, 0);
+  bool head = prev == row;
   float acc[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) acc[j] = 0.f;
-  for (int i0 = int(begin); i0 < end && row < none; i0 += kAhead) {
-    uint2 it[kAhead];
-    float f[kAhead][V];
+  for (int k0 = 0; k0 < count; k0 += kAhead) {
+    alignas(16) G x[kAhead][V];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      it[k] = i0 + k < end ? a.items[i0 + k] : make_uint2(none, 0);
-      if (it[k].x < none) load_vec<G, V>(grad + int64_t(it[k].y) * a.grad_stride, f[k]);
+      const uint32_t at = __shfl_sync(0xffffffffu, it.y, (k0 + k) & 31);
+      if (k0 + k < count && in) load_raw<G, V>(grad + int64_t(at) * a.grad_stride, x[k]);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (i0 + k >= end) break;
-      if (it[k].x != row) {   // the token before is complete (its end lies in this chunk)
-        if (head)
-          store_vec<float, V>(a.parts + (chunk * 2) * a.dim + col, acc);
-        else
-          finish_row<T, V>(a, row, col, acc);
+      if (k0 + k >= count) break;
+      const uint32_t key = __shfl_sync(0xffffffffu, it.x, k0 + k);
+      if (key != row) {   // the token before is complete: its end lies in this chunk
+        if (in) {
+          if (head)
+            store_vec<float, V>(a.parts + (chunk * 2) * a.dim + col, acc);
+          else
+            finish_row<T, V>(a, row, col, acc);
+        }
         head = false;
-        row = it[k].x;
-        if (row >= none) return;   // dropped tokens sort last
+        row = key;
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] = 0.f;
       }
+      if (in) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] += f[k][j];
+        for (int j = 0; j < V; ++j) acc[j] += widen(x[k][j]);
+      }
     }
   }
-  if (row >= none) return;
-  const bool tail = end < a.n && a.items[end].x == row;
+  if (!in) return;
+  const bool tail = count == kChunk && next == row;
   if (head || tail)
     store_vec<float, V>(a.parts + (chunk * 2 + (head ? 0 : 1)) * a.dim + col, acc);
   else
     finish_row<T, V>(a, row, col, acc);
 }
 
-// A thread: V columns of the token that begins in a chunk and goes on after it.
-template <typename T, int V>
-__global__ void __launch_bounds__(kRowThreads) join_rows_kernel(const __grid_constant__ RowArgs a) {
-  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
-  int64_t chunk = int64_t(blockIdx.x) * (kRowThreads / a.cols) + cy;
-  const int64_t col = (int64_t(blockIdx.y) * a.cols + cx) * V;
-  const int64_t begin = chunk * kChunk, end = begin + kChunk;
-  if (end >= a.n || col >= a.dim) return;
-  const uint32_t row = a.items[end - 1].x;
-  if (row >= uint32_t(a.vocab) || a.items[end].x != row) return;
-  if (a.items[begin].x == row && begin > 0 && a.items[begin - 1].x == row) return;   // begun before
-  float acc[V];
-  load_vec<float, V>(a.parts + (chunk * 2 + 1) * a.dim + col, acc);
-  for (int64_t c = chunk + 1; c * kChunk < a.n && a.items[c * kChunk].x == row; ++c) {
-    float f[V];
-    load_vec<float, V>(a.parts + (c * 2) * a.dim + col, f);
-#pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] += f[j];
+template <typename G, typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) sum_rows_kernel(const __grid_constant__ RowArgs a) {
+  launch_dependents();
+  grid_dependency_wait();
+  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols, per_cta = kRowThreads / a.cols;
+  // CTAs that sum and CTAs that write zeros, in proportion all along the grid:
+  // reads and writes then share the launch's time
+  const int64_t ctas = a.sum_ctas + a.zero_ctas, i = blockIdx.x;
+  const int64_t sums = i * a.sum_ctas / ctas;
+  if ((i + 1) * a.sum_ctas / ctas > sums) {
+    const int64_t chunk = sums / a.col_ctas * per_cta + cy;
+    sum_chunk<G, T, V>(a, chunk, (sums % a.col_ctas * a.cols + cx) * V, threadIdx.x & 31);
+    return;
   }
-  finish_row<T, V>(a, row, col, acc);
+  const int64_t word = i - sums, row0 = word * kZeroRows;
+  const uint32_t present = a.present[word];
+  const float zero[V] = {};
+  const int rows = int(min(int64_t(kZeroRows), a.vocab - row0));
+  for (int r = cy; r < rows; r += per_cta) {
+    if (present >> r & 1u) continue;
+    T* p = static_cast<T*>(a.weight) + (row0 + r) * a.weight_stride;
+    for (int64_t c = int64_t(cx) * V; c < a.dim; c += a.cols * V) store_vec<T, V>(p + c, zero);
+  }
 }
 
-// Zeros into the rows that no token names: a warp per row.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+
+// A CTA: the tokens that begin in one of eight chunks and go on after it, 32 x V
+// columns.  A token of up to kAlone parts (its chunks') is added by the warp of its
+// first chunk; of a longer one each warp adds parts w, w + 8, ..., and then the
+// eight sums are added in order.  (One token after the other, by the whole CTA,
+// took 40 us on 65536 text-like tokens.)
+constexpr int kAlone = 16;
+
 template <typename T, int V>
-__global__ void __launch_bounds__(kLookupThreads) zero_rows_kernel(const __grid_constant__ RowArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * (kLookupThreads / 32) + (threadIdx.x >> 5);
-  if (row >= a.vocab || (a.present[row >> 5] >> (row & 31) & 1u)) return;
-  T* p = static_cast<T*>(a.weight) + row * a.weight_stride;
-  const float zero[V] = {};
-#pragma unroll 4
-  for (int64_t c = int64_t(lane) * V; c < a.dim; c += 32 * V) store_vec<T, V>(p + c, zero);
+__global__ void __launch_bounds__(kJoinThreads) join_rows_kernel(const __grid_constant__ RowArgs a) {
+  __shared__ float share[kJoinWarps][32 * V];
+  __shared__ int64_t count[kJoinWarps];   // parts of the token that begins in this chunk
+  launch_dependents();
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t first = int64_t(blockIdx.x) * kJoinWarps;
+  const int64_t col = (int64_t(blockIdx.y) * 32 + lane) * V;
+  // parts begin, begin + step, ... of the token that begins in `chunk`
+  float acc[V];
+  auto add_parts = [&](int64_t chunk, int64_t begin, int64_t parts, int step) {
+    constexpr int kAhead = 4;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    for (int64_t p = begin; p < parts && col < a.dim; p += kAhead * step) {
+      float f[kAhead][V];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int64_t at = p + k * step;
+        if (at < parts) load_vec<float, V>(a.parts + ((chunk + at) * 2 + (at == 0 ? 1 : 0)) * a.dim + col, f[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (p + k * step < parts) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[j] += f[k][j];
+        }
+    }
+  };
+  {
+    const int64_t chunk = first + warp, begin = chunk * kChunk, end = begin + kChunk;
+    int64_t parts = 0;
+    uint32_t row = 0;
+    if (end < a.n) {
+      row = a.items[end - 1].x;
+      const uint32_t next = a.items[end].x, head = a.items[begin].x, prev = begin > 0 ? a.items[begin - 1].x : ~0u;
+      if (row < uint32_t(a.vocab) && next == row && !(head == row && prev == row)) {   // goes on, and not begun before
+        // the chunks after this one that begin with it, 128 at a time
+        parts = 1;
+        for (bool more = true; more;) {
+          bool same[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int64_t at = (chunk + parts + 32 * k + lane) * kChunk;
+            same[k] = at < a.n && a.items[at].x == row;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int got = __popc(__ballot_sync(0xffffffffu, same[k]));   // sorted: no gaps
+            parts += more ? got : 0;
+            more = more && got == 32;
+          }
+        }
+      }
+    }
+    if (parts > 0 && parts <= kAlone) {
+      add_parts(chunk, 0, parts, 1);
+      if (col < a.dim) finish_row<T, V>(a, row, col, acc);
+    }
+    if (lane == 0) count[warp] = parts > kAlone ? parts : 0;
+  }
+  __syncthreads();
+  for (int t = 0; t < kJoinWarps; ++t) {
+    const int64_t parts = count[t];
+    if (parts == 0) continue;   // the whole CTA
+    add_parts(first + t, warp, parts, kJoinWarps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) share[warp][j * 32 + lane] = acc[j];
+    __syncthreads();
+    if (warp == 0 && col < a.dim) {
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] += share[w][j * 32 + lane];
+      finish_row<T, V>(a, a.items[(first + t) * kChunk + kChunk - 1].x, col, acc);
+    }
+    __syncthreads();
+  }
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -493,25 +656,40 @@ fsp_status check_sizes(int64_t vocab, int64_t dim, int64_t n) {
   return FSP_OK;
 }
 
+// Launches with programmatic stream serialisation.
+template <typename K>
+fsp_status launch_next(K kernel, dim3 grid, int threads, const RowArgs& a, cudaStream_t st, const char* what) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
+}
+
 template <typename G, typename T, int V>
 fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
-  if (!a.accumulate && a.vocab > 0) {
-    zero_rows_kernel<T, V><<<unsigned((a.vocab + kLookupThreads / 32 - 1) / (kLookupThreads / 32)), kLookupThreads, 0, st>>>(a);
-    const fsp_status s = launched("embedding gradient (zero) kernel launch");
-    if (s != FSP_OK) return s;
-  }
-  if (a.n == 0) return FSP_OK;
-  a.cols = 1;
+  a.cols = 32;
   while (a.cols < kRowThreads && int64_t(a.cols) * V < a.dim) a.cols *= 2;
+  a.col_ctas = int((a.dim + int64_t(a.cols) * V - 1) / (int64_t(a.cols) * V));
   const int64_t chunks = (int64_t(a.n) + kChunk - 1) / kChunk;
   const int per_cta = kRowThreads / a.cols;
-  const dim3 grid(unsigned((chunks + per_cta - 1) / per_cta), unsigned((a.dim + int64_t(a.cols) * V - 1) / (int64_t(a.cols) * V)));
-  if (grid.y > 65535u) return fail(FSP_EUNSUPPORTED, "dim is too large for this alignment");
-  sum_rows_kernel<G, T, V><<<grid, kRowThreads, 0, st>>>(a);
-  fsp_status s = launched("embedding gradient (sum) kernel launch");
-  if (s != FSP_OK || chunks == 1) return s;
-  join_rows_kernel<T, V><<<grid, kRowThreads, 0, st>>>(a);
-  return launched("embedding gradient (join) kernel launch");
+  a.sum_ctas = (chunks + per_cta - 1) / per_cta * a.col_ctas;
+  a.zero_ctas = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
+  const int64_t ctas = a.sum_ctas + a.zero_ctas;
+  constexpr int kJoinV = V > 4 ? 4 : V;
+  const int64_t join_cols = (a.dim + 32 * kJoinV - 1) / (32 * kJoinV);
+  if (ctas > INT32_MAX || join_cols > 65535) return fail(FSP_EUNSUPPORTED, "too many tokens times columns");
+  const fsp_status s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(ctas)), kRowThreads, a, st,
+                                   "embedding gradient (sum) kernel launch");
+  if (s != FSP_OK || chunks <= 1) return s;
+  return launch_next(join_rows_kernel<T, kJoinV>, dim3(unsigned((chunks + kJoinWarps - 1) / kJoinWarps), unsigned(join_cols)),
+                     kJoinThreads, a, st, "embedding gradient (join) kernel launch");
 }
 
 template <typename G, typename T>
@@ -520,10 +698,21 @@ fsp_status launch_rows_v(RowArgs& a, int v, cudaStream_t st) {
 }
 
 fsp_status launch_sort(const SortArgs& s, cudaStream_t st) {
-  static const cudaError_t allowed =
-      cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (s.n <= kSortOne) {
+    static const cudaError_t allowed =
+        cudaFuncSetAttribute(sort_tokens_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemOne);
+    if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (token sort)", allowed));
+    sort_tokens_kernel<true><<<1, kSortThreads, kSortSmemOne, st>>>(s);
+    return launched("token sort kernel launch");
+  }
+  static const cudaError_t allowed = [] {   // clusters of 16 are beyond the size every device has to offer
+    cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(sort_tokens_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+  }();
   if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (token sort)", allowed));
-  const int ctas = s.n > kSortOneCta ? kSortCluster : 1;
+  int ctas = 4;
+  while (ctas < kSortCluster && s.n > ctas * kSortPerCta) ctas *= 2;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = unsigned(ctas);
@@ -535,7 +724,7 @@ fsp_status launch_sort(const SortArgs& s, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_tokens_kernel, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_tokens_kernel<false>, s);
   return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("token sort kernel launch", e));
 }
 
