@@ -16,8 +16,8 @@ struct fsp_adamw_list {
   int device = -1;
   int64_t state_len = 0;
   std::vector<int64_t> offsets;
-  fsp::ListTile* tiles = nullptr;   // device
-  int64_t n_tiles = 0;
+  fsp::ListTile* tiles = nullptr;   // device, with the launches' two counters behind them
+  int64_t n_tiles = 0, bulk_tiles = 0;
   // every registered tensor as [begin, end) device addresses, sorted by begin
   std::vector<std::pair<uintptr_t, uintptr_t>> spans;
 };
@@ -72,7 +72,7 @@ fsp_status create_list(int32_t n, const int64_t* numels, void* const* params, co
     } bufs[] = {{params[i], size_of(pd[i]), "params"},
                 {grads[i], size_of(gd[i]), "grads"},
                 {copies ? copies[i] : nullptr, 2, "copies"}};
-    bool vec = true;
+    bool vec = true, bulk = true;
     for (const auto& b : bufs) {
       if (!b.ptr) {
         if (b.name[0] == 'c') continue;
@@ -81,10 +81,11 @@ fsp_status create_list(int32_t n, const int64_t* numels, void* const* params, co
       const uintptr_t p = reinterpret_cast<uintptr_t>(b.ptr);
       if (p % b.esz != 0) return fail(FSP_EINVAL, b.name + at + " is not aligned to its elements");
       vec = vec && p % (4 * b.esz) == 0;
+      bulk = bulk && p % 16 == 0;
       spans.push_back({p, p + size_t(len) * b.esz, b.name + at});
     }
     const int32_t flags = (pd[i] == FSP_DTYPE_BF16 ? kListParamBf16 : 0) | (gd[i] == FSP_DTYPE_BF16 ? kListGradBf16 : 0) |
-                          (vec ? kListVec : 0);
+                          (vec ? kListVec : 0) | (bulk ? kListBulk : 0);
     for (int64_t k = 0; k < len; k += kListTile) {
       ListTile t{};
       t.param = static_cast<char*>(params[i]) + size_t(k) * size_of(pd[i]);
@@ -94,6 +95,7 @@ fsp_status create_list(int32_t n, const int64_t* numels, void* const* params, co
       t.len = int32_t(std::min<int64_t>(kListTile, len - k));
       t.flags = flags;
       tiles.push_back(t);
+      l->bulk_tiles += bulk ? 1 : 0;
     }
     l->state_len += (len + kListBlock - 1) / kListBlock * kListBlock;
   }
@@ -109,13 +111,15 @@ fsp_status create_list(int32_t n, const int64_t* numels, void* const* params, co
   if (!tiles.empty()) {
     cudaError_t e = cudaGetDevice(&l->device);
     if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaGetDevice", e));
-    e = cudaMalloc(reinterpret_cast<void**>(&l->tiles), tiles.size() * sizeof(ListTile));
+    const size_t bytes = tiles.size() * sizeof(ListTile);
+    e = cudaMalloc(reinterpret_cast<void**>(&l->tiles), bytes + 2 * sizeof(unsigned long long));
     if (e != cudaSuccess) {
       cudaGetLastError();
       l->tiles = nullptr;
       return fail(FSP_ENOMEM, cuda_msg("cudaMalloc (list tiles)", e));
     }
-    e = upload_table(l->tiles, tiles.data(), tiles.size() * sizeof(ListTile));
+    e = cudaMemset(l->tiles + tiles.size(), 0, 2 * sizeof(unsigned long long));
+    if (e == cudaSuccess) e = upload_table(l->tiles, tiles.data(), bytes);
     if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("uploading the list tiles", e));
   }
   own.l = nullptr;
@@ -189,6 +193,9 @@ fsp_status step_list(const fsp_adamw_list* l, int32_t sd, void* m, void* v, floa
     set_coeffs(sa, hp, step_dev ? 1 : step);
     ListArgs a{};
     a.tiles = l->tiles;
+    a.n_tiles = l->n_tiles;
+    a.bulk_tiles = l->bulk_tiles;
+    a.counter = reinterpret_cast<unsigned long long*>(l->tiles + l->n_tiles);
     a.m = m;
     a.v = v;
     a.m_scale = ms;
@@ -197,7 +204,7 @@ fsp_status step_list(const fsp_adamw_list* l, int32_t sd, void* m, void* v, floa
     a.step_dev = step_dev;
     a.lr = sa.lr;
     a.c = sa.c;
-    s = launch_adamw_list(a, eight, l->n_tiles, stream);
+    s = launch_adamw_list(a, eight, stream);
     if (s != FSP_OK) return s;
   } else if (step_dev) {
     const fsp_status s = check_allocation(step_dev, 8, "step_dev");

@@ -363,6 +363,275 @@ __global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel
   update_block<k8Bit>(a, tile, list_coeffs(a), a.grad_scale ? *a.grad_scale : 1.f, begin, lane, b);
 }
 
+// ---- long lists: a ring of stages in shared memory ---------------------------------
+//
+// One CTA per SM.  A producer warp takes tiles in order from a counter and
+// streams each one's gradient, parameter and states into a stage with bulk
+// asynchronous copies (its scales with 4-byte asynchronous copies: they have no
+// 16-byte alignment); two teams of eight consumer warps take the stages in turn, a
+// block per warp, and leave the results in place; a storer thread writes them back
+// with bulk stores and frees the stage.  Warps then wait for shared memory only,
+// and loads are in flight whatever the arithmetic does.  A tile that bulk copies
+// cannot move (a tensor off 16-byte alignment, the last odd elements of one) gets
+// an empty stage, and the team does it from global memory.
+//
+// Against one CTA per tile (same box): see kRingMinTiles.
+
+constexpr int kTeamWarps = kListTile / kListBlock, kTeams = 2;
+constexpr int kRingThreads = 64 + 32 * kTeamWarps * kTeams;
+
+template <bool k8Bit>
+struct Ring {
+  static constexpr int kStateBytes = kListTile * (k8Bit ? 1 : 4);
+  static constexpr int kGrad = 0, kParam = kListTile * 4, kM = 2 * kListTile * 4, kV = kM + kStateBytes;
+  static constexpr int kCopy = kV + kStateBytes, kScale = kCopy + kListTile * 2;   // kScale: [2][kTeamWarps] floats
+  static constexpr int kStage = kScale + (k8Bit ? 128 : 0);
+  static constexpr int kStages = k8Bit ? 8 : 6;
+  static constexpr int kHeaders = 256;                  // after the barriers
+  static constexpr int kBase = kHeaders + kStages * 64; // 64 bytes per header
+  static constexpr int kSmem = (kBase + 127) / 128 * 128 + kStages * kStage;
+  static_assert(kStage % 128 == 0 && kSmem <= 232448, "shared memory of the ring");
+  static_assert(sizeof(ListTile) <= 64, "header");
+};
+
+__device__ __forceinline__ bool bulk_tile(const ListTile& t) { return (t.flags & kListBulk) && t.len % 16 == 0; }
+
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives at `bar` once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Four elements of a stage's array from element i.
+__device__ __forceinline__ void stage_load4(const unsigned char* base, bool bf16, int i, float2* x) {
+  if (bf16) {
+    const uint2 b = *reinterpret_cast<const uint2*>(base + 2 * i);
+    x[0] = make_float2(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u));
+    x[1] = make_float2(__uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+  } else {
+    const float4 f = *reinterpret_cast<const float4*>(base + 4 * i);
+    x[0] = make_float2(f.x, f.y);
+    x[1] = make_float2(f.z, f.w);
+  }
+}
+__device__ __forceinline__ void stage_store4(unsigned char* base, bool bf16, int i, const float2* x) {
+  const float4 f = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  if (bf16)
+    *reinterpret_cast<uint2*>(base + 2 * i) = pack_bf16x4(f);
+  else
+    *reinterpret_cast<float4*>(base + 4 * i) = f;
+}
+
+// One block of a stage, in place.
+template <bool k8Bit>
+__device__ __forceinline__ void update_stage(const ListArgs& a, const ListTile& t, const Coeffs& c, float coef, int begin,
+                                             int lane, unsigned char* stage) {
+  using R = Ring<k8Bit>;
+  const bool pb = t.flags & kListParamBf16, gb = t.flags & kListGradBf16;
+  float2 g[4], p[4], m[4], v[4];
+  const int block = begin / kListBlock;
+  float* scales = reinterpret_cast<float*>(stage + R::kScale);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = begin + h * (kListBlock / 2) + lane * 4;
+    const bool in = i < t.len;   // (a multiple of 16: all four or none)
+    stage_load4(stage + R::kGrad, gb, i, g + 2 * h);
+    stage_load4(stage + R::kParam, pb, i, p + 2 * h);
+    if (k8Bit) {
+      m_of_codes(in ? *reinterpret_cast<const uint32_t*>(stage + R::kM + i) : 0u, scales[block], m + 2 * h);
+      v_of_codes(in ? *reinterpret_cast<const uint32_t*>(stage + R::kV + i) : 0u, scales[kTeamWarps + block], v + 2 * h);
+    } else {
+      stage_load4(stage + R::kM, false, i, m + 2 * h);
+      stage_load4(stage + R::kV, false, i, v + 2 * h);
+    }
+    if (!in) g[2 * h] = g[2 * h + 1] = both(0.f);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = __fmul2_rn(g[j], both(coef));
+    if (k8Bit) {
+      adamw_coarse(x, p[j], m[j], v[j], c);
+    } else {
+      adamw(x.x, p[j].x, m[j].x, v[j].x, c);
+      adamw(x.y, p[j].y, m[j].y, v[j].y, c);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = begin + h * (kListBlock / 2) + lane * 4;
+    stage_store4(stage + R::kParam, pb, i, p + 2 * h);
+    if (t.copy) stage_store4(stage + R::kCopy, true, i, p + 2 * h);
+    if (!k8Bit) {
+      stage_store4(stage + R::kM, false, i, m + 2 * h);
+      stage_store4(stage + R::kV, false, i, v + 2 * h);
+    }
+  }
+  if (k8Bit) {
+    const BlockScale ms = block_scale(block_largest(m)), vs = block_scale(block_largest(v));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = begin + h * (kListBlock / 2) + lane * 4;
+      *reinterpret_cast<uint32_t*>(stage + R::kM + i) = codes_of_m(m + 2 * h, ms);
+      *reinterpret_cast<uint32_t*>(stage + R::kV + i) = codes_of_v(v + 2 * h, vs);
+    }
+    if (lane == 0) {
+      const int64_t at = (t.state_off + begin) / kListBlock;
+      a.m_scale[at] = ms.s;
+      a.v_scale[at] = vs.s;
+    }
+  }
+}
+
+template <bool k8Bit>
+__global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __grid_constant__ ListArgs a) {
+  using R = Ring<k8Bit>;
+  constexpr int S = R::kStages;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t bars = smem_addr(smem);
+  const uint32_t full = bars, computed = full + 8 * S, empty = computed + 8 * S;
+  unsigned char* const stages = smem + (R::kBase + 127) / 128 * 128;
+  auto header = [&](int s) { return reinterpret_cast<ListTile*>(smem + R::kHeaders + 64 * s); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, k8Bit ? 33 : 1);   // the bulk copies, and each lane's copies of scales
+      mbar_init(computed + 8 * s, kTeamWarps);
+      mbar_init(empty + 8 * s, 1);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == 0) {
+    // ---- producer: the whole warp, lane 0 issues the bulk copies ----
+    auto claim = [&] {
+      unsigned long long t = 0;
+      if (lane == 0) t = atomicAdd(a.counter, 1ull);
+      return int64_t(__shfl_sync(0xffffffffu, t, 0));
+    };
+    auto fetch = [&](int64_t i) {
+      ListTile t{};
+      if (i < a.n_tiles)
+        t = a.tiles[i];
+      else
+        t.len = -1;   // no more work
+      return t;
+    };
+    // claims two tiles ahead, descriptors one
+    ListTile tile = fetch(claim());
+    int64_t next = claim(), after = claim();
+    int s = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    int ends = 0;
+    while (true) {
+      const ListTile ahead = fetch(next);
+      next = after;
+      if (ahead.len >= 0) after = claim();
+      if (!mbar_wait(empty + 8 * s, phase ^ 1u)) {
+        if (lane == 0) atomicOr(&g_fsp_device_error, kErrProducerWait);
+        break;
+      }
+      const uint32_t bar = full + 8 * s;
+      unsigned char* stage = stages + s * R::kStage;
+      const uint32_t at = smem_addr(stage);
+      const bool bulk = tile.len > 0 && bulk_tile(tile);
+      if (lane == 0) *header(s) = tile;
+      if (k8Bit && bulk && lane < 2 * kTeamWarps) {
+        const int block = lane % kTeamWarps;
+        const float* src = (lane < kTeamWarps ? a.m_scale : a.v_scale) + tile.state_off / kListBlock + block;
+        if (block * kListBlock < tile.len) copy4_async(at + R::kScale + 4 * lane, src);
+      }
+      if (k8Bit) arrive_after_copies(bar);
+      if (lane == 0) {
+        const uint32_t n = uint32_t(bulk ? tile.len : 0);
+        const uint32_t gb = n * (tile.flags & kListGradBf16 ? 2 : 4), pb = n * (tile.flags & kListParamBf16 ? 2 : 4);
+        const uint32_t sb = n * (k8Bit ? 1 : 4);
+        mbar_arrive_expect_tx(bar, gb + pb + 2 * sb);
+        if (bulk) {
+          const int64_t off = tile.state_off * (k8Bit ? 1 : 4);
+          bulk_load(at + R::kGrad, tile.grad, gb, bar);
+          bulk_load(at + R::kParam, tile.param, pb, bar);
+          bulk_load(at + R::kM, static_cast<const char*>(a.m) + off, sb, bar);
+          bulk_load(at + R::kV, static_cast<const char*>(a.v) + off, sb, bar);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == S) s = 0, phase ^= 1u;
+      if (tile.len < 0 && ++ends == kTeams) break;   // each team gets an end
+      if (tile.len >= 0) tile = ahead;
+    }
+    for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)   // what is in flight lands
+      if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
+  } else if (warp == 1) {
+    // ---- storer ----
+    if (lane == 0) {
+      int s = 0, ends = 0;
+      uint32_t phase = 0;
+      while (ends < kTeams) {
+        if (!mbar_wait(computed + 8 * s, phase)) {
+          atomicOr(&g_fsp_device_error, kErrConsumerWait);
+          break;
+        }
+        const ListTile t = *header(s);
+        if (t.len < 0) ++ends;
+        if (t.len > 0 && bulk_tile(t)) {
+          const uint32_t at = smem_addr(stages + s * R::kStage), n = uint32_t(t.len);
+          const int64_t off = t.state_off * (k8Bit ? 1 : 4);
+          bulk_store(t.param, at + R::kParam, n * (t.flags & kListParamBf16 ? 2 : 4));
+          if (t.copy) bulk_store(t.copy, at + R::kCopy, n * 2);
+          bulk_store(static_cast<char*>(a.m) + off, at + R::kM, n * (k8Bit ? 1 : 4));
+          bulk_store(static_cast<char*>(a.v) + off, at + R::kV, n * (k8Bit ? 1 : 4));
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+        mbar_arrive(empty + 8 * s);
+        if (++s == S) s = 0, phase ^= 1u;
+      }
+      bulk_wait_all();
+    }
+  } else {
+    // ---- consumers: team k takes stages k, k + kTeams, ... ----
+    const int team = (warp - 2) / kTeamWarps, begin = (warp - 2) % kTeamWarps * kListBlock;
+    const float coef = a.grad_scale ? *a.grad_scale : 1.f;
+    const Coeffs c = list_coeffs(a);
+    int s = team;
+    uint32_t phase = 0;
+    while (true) {
+      if (!mbar_wait(full + 8 * s, phase)) {
+        if (lane == 0) atomicOr(&g_fsp_device_error, kErrConsumerWait);
+        break;
+      }
+      const ListTile t = *header(s);
+      if (begin < t.len) {
+        if (bulk_tile(t)) {
+          update_stage<k8Bit>(a, t, c, coef, begin, lane, stages + s * R::kStage);
+        } else {
+          ListBlock b;
+          load_block<k8Bit>(a, t, begin, lane, b);
+          update_block<k8Bit>(a, t, c, coef, begin, lane, b);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(computed + 8 * s);
+      if (t.len < 0) break;
+      s += kTeams;
+      if (s >= S) s -= S, phase ^= 1u;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  // the last CTA to finish leaves the counter at 0 for the next launch
+  if (threadIdx.x == 0 && atomicAdd(a.counter + 1, 1ull) == gridDim.x - 1) {
+    a.counter[0] = 0;
+    a.counter[1] = 0;
+  }
+}
+
 // fp32 states <-> 8-bit states of whole blocks: a warp per block, grid over
 // all blocks of the state buffers.
 __global__ void __launch_bounds__(kListThreads) list_state_values_kernel(const int8_t* m8, const uint8_t* v8,
@@ -407,35 +676,6 @@ __global__ void __launch_bounds__(kListThreads) list_state_load_kernel(const flo
     ms[b] = s.s;
     vs[b] = t.s;
   }
-}
-
-// ---- launches (host) --------------------------------------------------------------
-
-fsp_status launch_adamw_list(const ListArgs& a, bool eight_bit, int64_t n_tiles, void* stream) {
-  if (n_tiles > INT32_MAX) return fail(FSP_EUNSUPPORTED, "more than 2^31 work tiles");
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (eight_bit)
-    adamw_list_kernel<true><<<unsigned(n_tiles), kListThreads, 0, st>>>(a);
-  else
-    adamw_list_kernel<false><<<unsigned(n_tiles), kListThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("AdamW list kernel launch", e));
-}
-
-fsp_status launch_list_state(bool load, void* m8, void* v8, float* ms, float* vs, float* m, float* v, int64_t len,
-                             void* stream) {
-  const int64_t n = len / kListBlock;
-  const int64_t ctas = (n + kListThreads / 32 - 1) / (kListThreads / 32);
-  if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "more than 2^31 work tiles");
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (load)
-    list_state_load_kernel<<<unsigned(ctas), kListThreads, 0, st>>>(m, v, static_cast<int8_t*>(m8),
-                                                                    static_cast<uint8_t*>(v8), ms, vs, n);
-  else
-    list_state_values_kernel<<<unsigned(ctas), kListThreads, 0, st>>>(static_cast<int8_t*>(m8),
-                                                                      static_cast<uint8_t*>(v8), ms, vs, m, v, n);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("AdamW state kernel launch", e));
 }
 
 }  // namespace fsp

@@ -13,7 +13,8 @@ constexpr int kListBlock = FSP_ADAMW_BLOCK;   // elements that share a scale
 constexpr int kListTile = 2048;               // most elements of one work tile
 
 constexpr int32_t kListParamBf16 = 1, kListGradBf16 = 2;
-constexpr int32_t kListVec = 4;   // param, grad and copy aligned to four elements
+constexpr int32_t kListVec = 4;    // param, grad and copy aligned to four elements
+constexpr int32_t kListBulk = 8;   // ... to 16 bytes
 
 // `len` elements of one tensor: its pointers at the tile's first element (a
 // multiple of kListBlock from the tensor's start) and the states' slot there.
@@ -29,6 +30,8 @@ static_assert(sizeof(ListTile) == 40, "list tile layout");
 
 struct ListArgs {
   const ListTile* tiles;
+  int64_t n_tiles, bulk_tiles;   // bulk_tiles: of tensors with kListBulk
+  unsigned long long* counter;   // two words, 0 between launches: tiles handed out, CTAs that are done
   void* m;
   void* v;
   float* m_scale;
@@ -39,8 +42,8 @@ struct ListArgs {
   Coeffs c;
 };
 
-// One CTA per tile (n_tiles > 0).
-fsp_status launch_adamw_list(const ListArgs& a, bool eight_bit, int64_t n_tiles, void* stream);
+// (n_tiles > 0)
+fsp_status launch_adamw_list(const ListArgs& a, bool eight_bit, void* stream);
 // fp32 states (len slots) into codes and scales (load), or back.
 fsp_status launch_list_state(bool load, void* m8, void* v8, float* ms, float* vs, float* m, float* v, int64_t len,
                              void* stream);

@@ -337,6 +337,48 @@ fsp_status grid_for(const KernelInfo& k, int* grid) {
   return FSP_OK;
 }
 
+// ---- AdamW over a list of tensors: launches (host side in fsp_adamw.cpp) ---------
+
+// Lists of at least this many tiles per CTA of the ring take it, if bulk copies can
+// move most of them.
+constexpr int64_t kRingMinTilesPerCta = 16;
+
+template <bool k8Bit>
+fsp_status launch_list(const ListArgs& a, cudaStream_t st) {
+  int grid = 0;
+  const fsp_status s = grid_for(
+      KernelInfo{reinterpret_cast<const void*>(&adamw_ring_kernel<k8Bit>), kRingThreads, Ring<k8Bit>::kSmem, true}, &grid);
+  if (s != FSP_OK) return s;
+  if (a.n_tiles >= kRingMinTilesPerCta * grid && 2 * a.bulk_tiles >= a.n_tiles)
+    adamw_ring_kernel<k8Bit><<<unsigned(grid), kRingThreads, Ring<k8Bit>::kSmem, st>>>(a);
+  else
+    adamw_list_kernel<k8Bit><<<unsigned(a.n_tiles), kListThreads, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("AdamW list kernel launch", e));
+}
+
+fsp_status launch_adamw_list(const ListArgs& a, bool eight_bit, void* stream) {
+  if (a.n_tiles > INT32_MAX) return fail(FSP_EUNSUPPORTED, "more than 2^31 work tiles");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return eight_bit ? launch_list<true>(a, st) : launch_list<false>(a, st);
+}
+
+fsp_status launch_list_state(bool load, void* m8, void* v8, float* ms, float* vs, float* m, float* v, int64_t len,
+                             void* stream) {
+  const int64_t n = len / kListBlock;
+  const int64_t ctas = (n + kListThreads / 32 - 1) / (kListThreads / 32);
+  if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "more than 2^31 work tiles");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (load)
+    list_state_load_kernel<<<unsigned(ctas), kListThreads, 0, st>>>(m, v, static_cast<int8_t*>(m8),
+                                                                    static_cast<uint8_t*>(v8), ms, vs, n);
+  else
+    list_state_values_kernel<<<unsigned(ctas), kListThreads, 0, st>>>(static_cast<int8_t*>(m8),
+                                                                      static_cast<uint8_t*>(v8), ms, vs, m, v, n);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("AdamW state kernel launch", e));
+}
+
 // Fills the AdamW scalars of update t (in double, as float pairs; the
 // bias corrections through bias_scalars, as the kernels compute them when t
 // is in device memory).

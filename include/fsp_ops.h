@@ -84,7 +84,9 @@ void fsp_adamw_list_destroy(fsp_adamw_list* list);
  *               coefficient, 1 / loss scale).
  * A gradient that is not finite makes its element's states NaN or infinite;
  * with 8-bit states it makes its block's scales, and so the block's states,
- * not finite.  A block of m or v whose largest value is 0 holds zeros. */
+ * not finite.  A block of m or v whose largest value is 0 holds zeros.  The list
+ * holds the launch's counter of work tiles: steps on one list must be ordered on
+ * the device (one stream, or events). */
 fsp_status fsp_adamw_list_step(const fsp_adamw_list* list, int32_t state_dtype, void* exp_avg, void* exp_avg_sq,
                                float* exp_avg_scale, float* exp_avg_sq_scale, const fsp_adamw_hparams* hp,
                                int64_t step, int64_t* step_dev, int32_t advance, const float* grad_scale,

@@ -67,15 +67,20 @@ class Lists:
 SIZES = [1, 255, 256, 257, 0, 2047, 2048, 2049, 5000, 3, 70001]
 
 
+# enough tiles (2048 elements) for the ring of stages, most of them whole; the last
+# tensors end off a multiple of 16, of 256 and of 2048, or are tiny
+LONG = [4_000_000, 2_000_016, 1_234_567, 1, 700, 2048 * 9 + 256, 0, 17]
+
+
 def _bf16(x):
     return OS.bf16_bits_to_f32(OS.bf16_rne(x))
 
 
-@pytest.mark.parametrize("shift", [0, 1, 2, 4])
+@pytest.mark.parametrize("sizes,shift", [(SIZES, 0), (SIZES, 1), (SIZES, 2), (SIZES, 4), (LONG, 0), (LONG, 4)])
 @pytest.mark.parametrize("param,grad,copies", [("f32", "f32", False), ("f32", "bf16", True), ("bf16", "bf16", False),
                                                (("f32", "bf16"), ("bf16", "f32", "f32"), True)])
-def test_fp32_states_match_the_oracle(param, grad, copies, shift):
-    c = Lists(SIZES, param, grad, copies, shift, seed=shift)
+def test_fp32_states_match_the_oracle(param, grad, copies, sizes, shift):
+    c = Lists(sizes, param, grad, copies, shift, seed=shift)
     c.opt.t = 9
     p, g = c.flat(c.params), c.flat(c.grads)
     c.opt.step()
@@ -96,8 +101,8 @@ def test_fp32_states_match_the_oracle(param, grad, copies, shift):
     assert c.intact() and c.opt.t == 10 and fsp.device_error() == 0
 
 
-def test_fp32_states_equal_the_sharded_step_bit_for_bit():
-    sizes = [4096, 513, 70000]
+@pytest.mark.parametrize("sizes", [[4096, 513, 70000], [6_000_000, 513, 70000]])
+def test_fp32_states_equal_the_sharded_step_bit_for_bit(sizes):
     c = Lists(sizes, copies=False, seed=5)
     plan = fsp.plan_layout([(n,) for n in sizes], 1, "fsdp2")
     seg = {s.param: s for s in plan.segments}
@@ -117,11 +122,11 @@ def test_fp32_states_equal_the_sharded_step_bit_for_bit():
             assert torch.equal(buf[seg[i].state_off:seg[i].state_off + n], mine)
 
 
-@pytest.mark.parametrize("shift", [0, 1, 4])
+@pytest.mark.parametrize("sizes,shift", [(SIZES, 0), (SIZES, 1), (SIZES, 4), (LONG, 0), (LONG, 4)])
 @pytest.mark.parametrize("param,grad,copies,scale", [("f32", "f32", False, None), ("f32", "bf16", True, 0.37),
                                                      ("bf16", "bf16", False, None)])
-def test_8_bit_states(param, grad, copies, scale, shift):
-    c = Lists(SIZES, param, grad, copies, shift, seed=10 + shift, bits=8)
+def test_8_bit_states(param, grad, copies, scale, sizes, shift):
+    c = Lists(sizes, param, grad, copies, shift, seed=10 + shift, bits=8)
     opt = c.opt
     q0, s0 = codes(c.m, 127, False)
     r0, t0 = codes(c.v, 255, True)
@@ -198,9 +203,10 @@ def test_non_finite_gradients_stay_in_their_element_or_block(bad):
         assert np.isfinite(m[rest]).all() and np.isfinite(v[rest]).all()
 
 
+@pytest.mark.parametrize("sizes", [[5000, 33], [6_000_000, 33]])
 @pytest.mark.parametrize("bits", [32, 8])
-def test_capturable_steps_replayed_from_a_graph_equal_host_steps(bits):
-    a, b = (Lists([5000, 33], bits=bits, seed=8, capturable=cap) for cap in (False, True))
+def test_capturable_steps_replayed_from_a_graph_equal_host_steps(bits, sizes):
+    a, b = (Lists(sizes, bits=bits, seed=8, capturable=cap) for cap in (False, True))
     b.opt.step()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
