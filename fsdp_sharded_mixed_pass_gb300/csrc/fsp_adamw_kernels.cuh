@@ -365,20 +365,21 @@ __global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel
 
 // ---- long lists: a ring of stages in shared memory ---------------------------------
 //
-// One CTA per SM.  A producer warp takes tiles in order from a counter and
-// streams each one's gradient, parameter and states into a stage with bulk
-// asynchronous copies (its scales with 4-byte asynchronous copies: they have no
-// 16-byte alignment); two teams of eight consumer warps take the stages in turn, a
-// block per warp, and leave the results in place; a storer thread writes them back
-// with bulk stores and frees the stage.  Warps then wait for shared memory only,
-// and loads are in flight whatever the arithmetic does.  A tile that bulk copies
-// cannot move (a tensor off 16-byte alignment, the last odd elements of one) gets
-// an empty stage, and the team does it from global memory.
+// One CTA per SM.  A producer warp takes tiles (in order from a counter, or with a
+// fixed stride) and streams each one's gradient, parameter and states into a stage
+// with bulk asynchronous copies (its scales with 4-byte asynchronous copies: they
+// have no 16-byte alignment); two teams of eight consumer warps take the stages in
+// turn, a block per warp, and leave the results in place; a storer thread writes
+// them back with bulk stores and frees the stage.  Warps then wait for shared memory
+// only, and loads are in flight whatever the arithmetic does.  A tile that bulk
+// copies cannot move (a tensor off 16-byte alignment, the last odd elements of one)
+// gets an empty stage, and the team does it from global memory.
 //
-// Against one CTA per tile (same box): see kRingMinTiles.
+// Measured (GB300): fp32 states, bf16 gradients and copies, 360.7 M elements 1442 us
+// = 7.0 TB/s (one CTA per tile 1640-1730); 8-bit states, 541.1 M elements 1426 us =
+// 6.1 TB/s (2000).
 
-constexpr int kTeamWarps = kListTile / kListBlock, kTeams = 2;
-constexpr int kRingThreads = 64 + 32 * kTeamWarps * kTeams;
+constexpr int kTeamWarps = kListTile / kListBlock;
 
 template <bool k8Bit>
 struct Ring {
@@ -386,7 +387,12 @@ struct Ring {
   static constexpr int kGrad = 0, kParam = kListTile * 4, kM = 2 * kListTile * 4, kV = kM + kStateBytes;
   static constexpr int kCopy = kV + kStateBytes, kScale = kCopy + kListTile * 2;   // kScale: [2][kTeamWarps] floats
   static constexpr int kStage = kScale + (k8Bit ? 128 : 0);
+  static constexpr bool kCounter = !k8Bit;
+  static constexpr int kTeams = 2;
+  static constexpr int kThreads = 64 + 32 * kTeamWarps * kTeams;
   static constexpr int kStages = k8Bit ? 8 : 6;
+  static constexpr int kLag = 1;   // stages whose stores may still be reading
+  static_assert(kStages % kTeams == 0, "a team's stages come round with the ring");
   static constexpr int kHeaders = 256;                  // after the barriers
   static constexpr int kBase = kHeaders + kStages * 64; // 64 bytes per header
   static constexpr int kSmem = (kBase + 127) / 128 * 128 + kStages * kStage;
@@ -402,6 +408,12 @@ __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
 // Arrives at `bar` once this thread's asynchronous copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// All but the N newest groups of bulk stores have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read_but() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // Four elements of a stage's array from element i.
@@ -485,7 +497,7 @@ __device__ __forceinline__ void update_stage(const ListArgs& a, const ListTile& 
 }
 
 template <bool k8Bit>
-__global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __grid_constant__ ListArgs a) {
+__global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(const __grid_constant__ ListArgs a) {
   using R = Ring<k8Bit>;
   constexpr int S = R::kStages;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -506,11 +518,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __gri
 
   if (warp == 0) {
     // ---- producer: the whole warp, lane 0 issues the bulk copies ----
-    auto claim = [&] {
-      unsigned long long t = 0;
-      if (lane == 0) t = atomicAdd(a.counter, 1ull);
-      return int64_t(__shfl_sync(0xffffffffu, t, 0));
-    };
     auto fetch = [&](int64_t i) {
       ListTile t{};
       if (i < a.n_tiles)
@@ -519,17 +526,42 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __gri
         t.len = -1;   // no more work
       return t;
     };
-    // claims two tiles ahead, descriptors one
-    ListTile tile = fetch(claim());
-    int64_t next = claim(), after = claim();
+    // Tile numbers.  fp32 states: in order from the counter, kPerClaim at a time and
+    // claimed two claims ahead (in lane 0, until they are handed round: the round trip,
+    // about 1 us, is most of a tile's time).  8-bit states move half the bytes per
+    // tile, and there a fixed stride is ahead.
+    constexpr int kPerClaim = 2;
+    unsigned long long next = 0, second = 0;
+    auto claim = [&] { return lane == 0 ? atomicAdd(a.counter, 1ull) : 0ull; };
+    int64_t at_number = R::kCounter ? 0 : int64_t(blockIdx.x);
+    int used = kPerClaim;
+    auto number = [&] {
+      if constexpr (R::kCounter) {
+        if (used == kPerClaim) {
+          at_number = int64_t(__shfl_sync(0xffffffffu, next, 0)) * kPerClaim;
+          next = second;
+          second = claim();
+          used = 0;
+        }
+        return at_number + used++;
+      } else {
+        const int64_t n = at_number;
+        at_number += gridDim.x;
+        return n;
+      }
+    };
+    if constexpr (R::kCounter) {
+      next = claim();
+      second = claim();
+    }
+    // (descriptors two tiles ahead)
+    ListTile tile = fetch(number()), ahead = fetch(number());
     int s = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
     int ends = 0;
     while (true) {
-      const ListTile ahead = fetch(next);
-      next = after;
-      if (ahead.len >= 0) after = claim();
+      const ListTile later = fetch(number());
       if (!mbar_wait(empty + 8 * s, phase ^ 1u)) {
         if (lane == 0) atomicOr(&g_fsp_device_error, kErrProducerWait);
         break;
@@ -561,8 +593,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __gri
       __syncwarp();
       ++issued;
       if (++s == S) s = 0, phase ^= 1u;
-      if (tile.len < 0 && ++ends == kTeams) break;   // each team gets an end
-      if (tile.len >= 0) tile = ahead;
+      if (tile.len < 0 && ++ends == R::kTeams) break;   // each team gets an end
+      if (tile.len >= 0) tile = ahead, ahead = later;
     }
     for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)   // what is in flight lands
       if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
@@ -570,8 +602,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __gri
     // ---- storer ----
     if (lane == 0) {
       int s = 0, ends = 0;
-      uint32_t phase = 0;
-      while (ends < kTeams) {
+      uint32_t phase = 0, stored = 0;
+      while (ends < R::kTeams) {
         if (!mbar_wait(computed + 8 * s, phase)) {
           atomicOr(&g_fsp_device_error, kErrConsumerWait);
           break;
@@ -585,12 +617,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __gri
           if (t.copy) bulk_store(t.copy, at + R::kCopy, n * 2);
           bulk_store(static_cast<char*>(a.m) + off, at + R::kM, n * (k8Bit ? 1 : 4));
           bulk_store(static_cast<char*>(a.v) + off, at + R::kV, n * (k8Bit ? 1 : 4));
-          bulk_commit();
-          bulk_wait_read_all();
         }
-        mbar_arrive(empty + 8 * s);
+        bulk_commit();
+        // a stage is free once its stores have read it: kLag stages later, so that
+        // stores follow each other without waiting
+        bulk_wait_read_but<R::kLag>();
+        if (stored >= R::kLag) mbar_arrive(empty + 8 * uint32_t((stored - R::kLag) % S));
+        ++stored;
         if (++s == S) s = 0, phase ^= 1u;
       }
+      // (nothing waits for the last kLag stages: the producer issues no more)
       bulk_wait_all();
     }
   } else {
@@ -619,14 +655,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) adamw_ring_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(computed + 8 * s);
       if (t.len < 0) break;
-      s += kTeams;
+      s += R::kTeams;
       if (s >= S) s -= S, phase ^= 1u;
     }
   }
   __syncwarp();
   __syncthreads();
   // the last CTA to finish leaves the counter at 0 for the next launch
-  if (threadIdx.x == 0 && atomicAdd(a.counter + 1, 1ull) == gridDim.x - 1) {
+  if (R::kCounter && threadIdx.x == 0 && atomicAdd(a.counter + 1, 1ull) == gridDim.x - 1) {
     a.counter[0] = 0;
     a.counter[1] = 0;
   }

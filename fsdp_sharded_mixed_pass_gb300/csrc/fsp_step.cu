@@ -340,17 +340,21 @@ fsp_status grid_for(const KernelInfo& k, int* grid) {
 // ---- AdamW over a list of tensors: launches (host side in fsp_adamw.cpp) ---------
 
 // Lists of at least this many tiles per CTA of the ring take it, if bulk copies can
-// move most of them.
-constexpr int64_t kRingMinTilesPerCta = 16;
+// move most of them.  Measured, ring against one CTA per tile (fp32 gradients and
+// bf16 copies, L2 flushed).  fp32 states: 2.2 M elements (7 tiles per CTA) 20.5 vs 16.4
+// us, 8.9 M (29) 49 vs 47, 17.8 M (57) 88 vs 88, 35.7 M (115) 162 vs 170.  8-bit states:
+// 2.2 M 16.4 vs 18.4, 8.9 M 35 vs 41, 35.7 M 110 vs 135.
+template <bool k8Bit>
+constexpr int64_t kRingMinTilesPerCta = k8Bit ? 4 : 64;
 
 template <bool k8Bit>
 fsp_status launch_list(const ListArgs& a, cudaStream_t st) {
   int grid = 0;
   const fsp_status s = grid_for(
-      KernelInfo{reinterpret_cast<const void*>(&adamw_ring_kernel<k8Bit>), kRingThreads, Ring<k8Bit>::kSmem, true}, &grid);
+      KernelInfo{reinterpret_cast<const void*>(&adamw_ring_kernel<k8Bit>), Ring<k8Bit>::kThreads, Ring<k8Bit>::kSmem, true}, &grid);
   if (s != FSP_OK) return s;
-  if (a.n_tiles >= kRingMinTilesPerCta * grid && 2 * a.bulk_tiles >= a.n_tiles)
-    adamw_ring_kernel<k8Bit><<<unsigned(grid), kRingThreads, Ring<k8Bit>::kSmem, st>>>(a);
+  if (a.n_tiles >= kRingMinTilesPerCta<k8Bit> * grid && 2 * a.bulk_tiles >= a.n_tiles)
+    adamw_ring_kernel<k8Bit><<<unsigned(grid), Ring<k8Bit>::kThreads, Ring<k8Bit>::kSmem, st>>>(a);
   else
     adamw_list_kernel<k8Bit><<<unsigned(a.n_tiles), kListThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();

@@ -70,15 +70,20 @@ SIZES = [1, 255, 256, 257, 0, 2047, 2048, 2049, 5000, 3, 70001]
 # enough tiles (2048 elements) for the ring of stages, most of them whole; the last
 # tensors end off a multiple of 16, of 256 and of 2048, or are tiny
 LONG = [4_000_000, 2_000_016, 1_234_567, 1, 700, 2048 * 9 + 256, 0, 17]
+LONG32 = [17_000_016] + LONG   # (fp32 states take it from more tiles on)
 
 
 def _bf16(x):
     return OS.bf16_bits_to_f32(OS.bf16_rne(x))
 
 
-@pytest.mark.parametrize("sizes,shift", [(SIZES, 0), (SIZES, 1), (SIZES, 2), (SIZES, 4), (LONG, 0), (LONG, 4)])
-@pytest.mark.parametrize("param,grad,copies", [("f32", "f32", False), ("f32", "bf16", True), ("bf16", "bf16", False),
-                                               (("f32", "bf16"), ("bf16", "f32", "f32"), True)])
+MIXED = (("f32", "bf16"), ("bf16", "f32", "f32"), True)
+
+
+@pytest.mark.parametrize("param,grad,copies,sizes,shift",
+                         [(*kinds, SIZES, shift) for shift in (0, 1, 2, 4)
+                          for kinds in (("f32", "f32", False), ("f32", "bf16", True), ("bf16", "bf16", False), MIXED)]
+                         + [("f32", "bf16", True, LONG32, 0), (*MIXED, LONG32, 0), (*MIXED, LONG32, 4)])
 def test_fp32_states_match_the_oracle(param, grad, copies, sizes, shift):
     c = Lists(sizes, param, grad, copies, shift, seed=shift)
     c.opt.t = 9
@@ -101,7 +106,7 @@ def test_fp32_states_match_the_oracle(param, grad, copies, sizes, shift):
     assert c.intact() and c.opt.t == 10 and fsp.device_error() == 0
 
 
-@pytest.mark.parametrize("sizes", [[4096, 513, 70000], [6_000_000, 513, 70000]])
+@pytest.mark.parametrize("sizes", [[4096, 513, 70000], [21_000_000, 513, 70000]])
 def test_fp32_states_equal_the_sharded_step_bit_for_bit(sizes):
     c = Lists(sizes, copies=False, seed=5)
     plan = fsp.plan_layout([(n,) for n in sizes], 1, "fsdp2")
@@ -203,7 +208,7 @@ def test_non_finite_gradients_stay_in_their_element_or_block(bad):
         assert np.isfinite(m[rest]).all() and np.isfinite(v[rest]).all()
 
 
-@pytest.mark.parametrize("sizes", [[5000, 33], [6_000_000, 33]])
+@pytest.mark.parametrize("sizes", [[5000, 33], [21_000_000, 33]])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_capturable_steps_replayed_from_a_graph_equal_host_steps(bits, sizes):
     a, b = (Lists(sizes, bits=bits, seed=8, capturable=cap) for cap in (False, True))
