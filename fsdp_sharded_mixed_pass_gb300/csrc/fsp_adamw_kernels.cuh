@@ -662,9 +662,13 @@ __global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(co
   __syncwarp();
   __syncthreads();
   // the last CTA to finish leaves the counter at 0 for the next launch
-  if (R::kCounter && threadIdx.x == 0 && atomicAdd(a.counter + 1, 1ull) == gridDim.x - 1) {
-    a.counter[0] = 0;
-    a.counter[1] = 0;
+  if (R::kCounter && threadIdx.x == 0) {
+    __threadfence();   // this thread made the CTA's claims: they are all in the counter
+    if (atomicAdd(a.counter + 1, 1ull) == gridDim.x - 1) {
+      __threadfence();
+      a.counter[0] = 0;
+      a.counter[1] = 0;
+    }
   }
 }
 

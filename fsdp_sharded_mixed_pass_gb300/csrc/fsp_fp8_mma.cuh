@@ -166,9 +166,9 @@ struct MmArgs {
   int vec;                    // C's rows are 16-byte aligned
 };
 
-// The epilogue's part of shared memory, per warp: 32 rows of 64 bytes.
-constexpr int kStagePitch = 64 + 16;              // bytes of a row: eight lanes' 16-byte stores meet no bank twice
-constexpr int kWarpStage = 32 * kStagePitch;
+// The epilogue's part of shared memory, per warp: 16 rows of 128 bytes.
+constexpr int kStagePitch = 128 + 16;             // bytes of a row: eight lanes' 16-byte stores meet no bank twice
+constexpr int kWarpStage = 16 * kStagePitch;
 
 // BN: rows of Q per tile.  kSwap: C is written transposed (C[q][p]).
 template <int BN>
@@ -206,38 +206,40 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Rows p0 .. p0 + 31 (a lane each), columns q0 .. q0 + 31 of C from registers,
-// through this warp's part of shared memory so that rows are written in runs of
-// 64 bytes: 32 columns of bf16, or 16 of fp32 at a time.
+// Rows p0 .. p0 + 31 (a lane each), columns q0 .. q0 + kCols - 1 of C from registers,
+// through this warp's part of shared memory, 16 rows at a time, so that rows are
+// written in whole lines: 128 bytes, 64 columns of bf16 or 32 of fp32.
+template <typename T>
+constexpr int kLineCols = 128 / int(sizeof(T));
 
 template <typename T>
-__device__ __forceinline__ void write_block(const MmArgs& g, const uint32_t* acc, unsigned char* stage, int lane, int64_t p0,
+__device__ __forceinline__ void write_lines(const MmArgs& g, const uint32_t* x, unsigned char* stage, int lane, int64_t p0,
                                             int64_t q0) {
-  constexpr int kCols = 64 / int(sizeof(T));
+  constexpr int kCols = kLineCols<T>;
   T* const c = static_cast<T*>(g.c) + p0 * g.c_stride + q0;
-  const int rows = int(min(int64_t(32), g.np - p0));
+  const int rows = int(min(int64_t(32), g.np - p0)), cols = int(min(int64_t(kCols), g.nq - q0));
 #pragma unroll
-  for (int h = 0; h < 32 / kCols; ++h) {
-    const uint32_t* x = acc + h * kCols;
-    const int cols = int(min(int64_t(kCols), g.nq - q0 - h * kCols));
-    if (cols <= 0) break;
-    uint4* mine = reinterpret_cast<uint4*>(stage + lane * kStagePitch);
+  for (int h = 0; h < 2; ++h) {
+    if (h * 16 >= rows) break;
+    if (lane >> 4 == h) {
+      uint4* mine = reinterpret_cast<uint4*>(stage + (lane & 15) * kStagePitch);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4)
-        mine[j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-      else
-        mine[j] = make_uint4(pack_bf16(x[8 * j], x[8 * j + 1]), pack_bf16(x[8 * j + 2], x[8 * j + 3]),
-                             pack_bf16(x[8 * j + 4], x[8 * j + 5]), pack_bf16(x[8 * j + 6], x[8 * j + 7]));
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(T) == 4)
+          mine[j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        else
+          mine[j] = make_uint4(pack_bf16(x[8 * j], x[8 * j + 1]), pack_bf16(x[8 * j + 2], x[8 * j + 3]),
+                               pack_bf16(x[8 * j + 4], x[8 * j + 5]), pack_bf16(x[8 * j + 6], x[8 * j + 7]));
+      }
     }
     __syncwarp();
     if (g.vec && cols == kCols) {
-      const int r = lane >> 2, v = lane & 3;   // eight rows of four 16-byte vectors at a time
-      uint4* dst = reinterpret_cast<uint4*>(c + r * g.c_stride + h * kCols) + v;
-      const int64_t step = g.c_stride * int(sizeof(T)) / 2;   // eight rows, in vectors
+      const int r = lane >> 3, v = lane & 7;   // four rows of eight 16-byte vectors at a time
+      uint4* dst = reinterpret_cast<uint4*>(c + (h * 16 + r) * g.c_stride) + v;
+      const int64_t step = g.c_stride * int(sizeof(T)) / 4;   // four rows, in vectors
 #pragma unroll
-      for (int i = 0; i < 32; i += 8, dst += step) {
-        if (i + r >= rows) break;
+      for (int i = 0; i < 16; i += 4, dst += step) {
+        if (h * 16 + i + r >= rows) break;
         uint4 y = *reinterpret_cast<const uint4*>(stage + (i + r) * kStagePitch + v * 16);
         if constexpr (sizeof(T) == 4) {
           if (g.accumulate) {
@@ -249,12 +251,10 @@ __device__ __forceinline__ void write_block(const MmArgs& g, const uint32_t* acc
         *dst = y;
       }
     } else {
-      // 32 / kCols rows at a time, a lane per element
-      const int r = lane / kCols, v = lane % kCols;
-      if (v < cols)
-        for (int i = r; i < rows; i += 32 / kCols) {
+      for (int i = 0; i < 16 && h * 16 + i < rows; ++i)   // a lane per element
+        for (int v = lane; v < cols; v += 32) {
           T y = *reinterpret_cast<const T*>(stage + i * kStagePitch + v * int(sizeof(T)));
-          T* dst = c + i * g.c_stride + h * kCols + v;
+          T* dst = c + (h * 16 + i) * g.c_stride + v;
           if constexpr (sizeof(T) == 4) {
             if (g.accumulate) y += *dst;
           }
@@ -263,6 +263,14 @@ __device__ __forceinline__ void write_block(const MmArgs& g, const uint32_t* acc
     }
     __syncwarp();
   }
+}
+// 64 columns from registers.
+template <typename T>
+__device__ __forceinline__ void write_block(const MmArgs& g, const uint32_t* acc, unsigned char* stage, int lane, int64_t p0,
+                                            int64_t q0) {
+#pragma unroll
+  for (int k = 0; k < 64; k += kLineCols<T>)
+    if (p0 < g.np && q0 + k < g.nq) write_lines<T>(g, acc + k, stage, lane, p0, q0 + k);
 }
 
 template <int BN, bool kSwap, typename T>
@@ -410,11 +418,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
           __syncwarp();
         }
       } else {
-        for (int j0 = 0; j0 < BN; j0 += 32) {
-          uint32_t acc[32];
+        static_assert(BN % 64 == 0 || kSwap, "whole blocks of 64 columns");
+#pragma unroll 1
+        for (int j0 = 0; j0 < BN; j0 += 64) {
+          uint32_t acc[64];
           tmem_load32(d + j0, acc);
+          tmem_load32(d + j0 + 32, acc + 32);
           tmem_wait_loads();
-          if (p0 < g.np && q0 + j0 < g.nq) write_block<T>(g, acc, stage, lane, p0, q0 + j0);
+          write_block<T>(g, acc, stage, lane, p0, q0 + j0);
         }
       }
       fence_before();
@@ -497,7 +508,10 @@ struct PairCfg {
   static constexpr int kScaleBase = 512 - 2 * kScaleCols;
   static constexpr int kSecond = kScaleBase - 256;      // first column of the second accumulator
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(256 - kSecond <= 32, "the overlap lies within one block of 32 columns of either accumulator");
+  static_assert(256 - kSecond <= 64, "the overlap lies within one block of 64 columns of either accumulator");
+  // a slot of scales is waited for by the barrier of a stage five blocks back, which
+  // must not have come round again
+  static_assert(kStages >= 5, "stages");
 };
 
 template <typename T>
@@ -641,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     mbar_wait(drained, 0);
   } else if (warp >= 2) {
     // ---- epilogue: this CTA's 128 rows ----
-    const int quarter = warp & 3, half = (warp - 2) >> 2;   // rows; alternate blocks of 32 columns
+    const int quarter = warp & 3, half = (warp - 2) >> 2;   // rows; alternate blocks of 64 columns
     unsigned char* stage = smem + (at_epi - base) + (warp - 2) * kWarpStage;
     int n = 0;
     for (int64_t t = blockIdx.x >> 1; t < tiles; t += step, ++n) {
@@ -652,18 +666,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       const uint32_t d = tmem + (buf ? Cfg::kSecond : 0) + (uint32_t(quarter * 32) << 16);
       const int64_t p0 = tile.p * Cfg::kTile + rank * 128 + quarter * 32, q0 = tile.q * Cfg::kTile;
 #pragma unroll 1
-      for (int j = 32 * half; j < Cfg::kTile; j += 64) {
+      for (int j = 64 * half; j < Cfg::kTile; j += 128) {
         // the first accumulator's last block, the second one's first, are what the other needs next
-        const int j0 = buf ? j : (j + 224) & 255;
-        uint32_t acc[32];
+        const int j0 = buf ? j : 192 - j;
+        uint32_t acc[64];
         tmem_load32(d + j0, acc);
+        tmem_load32(d + j0 + 32, acc + 32);
         tmem_wait_loads();
-        if (j < 64) {
+        if (j < 128) {
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(in_cta(acc_part + 8 * buf, 0));
         }
-        if (p0 < g.np && q0 + j0 < g.nq) write_block<T>(g, acc, stage, lane, p0, q0 + j0);
+        write_block<T>(g, acc, stage, lane, p0, q0 + j0);
       }
     }
   }
