@@ -111,6 +111,8 @@ constexpr int kRowsPerCta = kRowsPerWarp * kQuantThreads / 32;
 
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __grid_constant__ QuantArgs a, bool vec) {
+  launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t piece = blockIdx.x;
   const int64_t row0 = int64_t(blockIdx.y) * kRowsPerCta + (threadIdx.x >> 5) * kRowsPerWarp;
@@ -163,6 +165,8 @@ template <typename T>
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_cols_kernel(const __grid_constant__ QuantArgs a, uint8_t* out, Fp8Layout l, bool vec) {
   extern __shared__ __align__(16) unsigned char raw[];
+  launch_dependents();
+  grid_dependency_wait();
   ColsSmem<T>& sm = *reinterpret_cast<ColsSmem<T>*>(raw);
   const int tid = threadIdx.x;
   const int64_t c0 = int64_t(blockIdx.x) * 128, r0 = int64_t(blockIdx.y) * 128;
@@ -301,6 +305,8 @@ __device__ __forceinline__ void values16(uint4 c, float* f) {
 template <int M, typename T, typename O>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ float xv[];   // [M][blocks * 128], then [8 warps][16][M]
+  launch_dependents();
+  grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t width = a.l.blocks * 128;
   for (int64_t b = warp; b < a.l.blocks * M; b += kFewThreads / 32) {
@@ -397,6 +403,25 @@ fsp_status launched(const char* what) {
   return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
 }
 
+// Launches with programmatic stream serialisation: the CTAs of a pass's next kernel
+// are there when the one before it ends (every kernel here waits for that before
+// it touches a buffer).
+template <typename... P, typename... A>
+fsp_status launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const char* what, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
+}
+
 fsp_status check_dims(std::initializer_list<int64_t> dims) {
   for (int64_t d : dims)
     if (d < 0 || d > kMaxDim) return fail(FSP_EINVAL, "a size is out of range");
@@ -447,9 +472,8 @@ fsp_status run_quantize(const QuantArgs& in, void* out, void* out_t, bool vec, c
     a.out = static_cast<uint8_t*>(out_t);
     a.l = layout_of(a.cols, a.rows);
     if (a.l.blocks > 65535) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
-    quantize_cols_kernel<T><<<dim3(unsigned(a.l.row_tiles), unsigned(a.l.blocks)), kQuantThreads, kSmem, st>>>(
-        a, static_cast<uint8_t*>(out), l, vec);
-    return launched("transposing quantisation kernel launch");
+    return launch_next(quantize_cols_kernel<T>, dim3(unsigned(a.l.row_tiles), unsigned(a.l.blocks)), kQuantThreads, kSmem, st,
+                       "transposing quantisation kernel launch", a, static_cast<uint8_t*>(out), l, vec);
   }
   a.out = static_cast<uint8_t*>(out);
   a.l = l;
@@ -461,8 +485,8 @@ fsp_status run_quantize(const QuantArgs& in, void* out, void* out_t, bool vec, c
     part.x = static_cast<const T*>(a.x) + done * kRowsPerCta * a.stride;
     part.rows = std::min(a.rows - done * kRowsPerCta, kMost * kRowsPerCta);
     part.row_tile = done * kRowsPerCta / 128;
-    quantize_rows_kernel<T><<<dim3(unsigned(a.l.pieces), unsigned(std::min(kMost, ctas - done))), kQuantThreads, 0, st>>>(part, vec);
-    const fsp_status s = launched("quantisation kernel launch");
+    const fsp_status s = launch_next(quantize_rows_kernel<T>, dim3(unsigned(a.l.pieces), unsigned(std::min(kMost, ctas - done))),
+                                     kQuantThreads, 0, st, "quantisation kernel launch", part, vec);
     if (s != FSP_OK) return s;
   }
   return FSP_OK;
@@ -552,8 +576,8 @@ fsp_status launch_few_of(const FewArgs& a, cudaStream_t st) {
   const size_t smem = size_t(M) * size_t(a.l.blocks) * 512 + 8 * kFewRows * 4 * M;
   // x is quantised once per CTA: at most eight CTAs per SM, which then take turns
   const int64_t ctas = std::min<int64_t>((a.n + kFewRows - 1) / kFewRows, int64_t(sm_count()) * 8);
-  few_rows_kernel<M, T, O><<<unsigned(ctas), kFewThreads, smem, st>>>(a);
-  return launched("8-bit linear (few rows) kernel launch");
+  return launch_next(few_rows_kernel<M, T, O>, dim3(unsigned(ctas)), kFewThreads, smem, st,
+                     "8-bit linear (few rows) kernel launch", a);
 }
 template <typename T, typename O>
 fsp_status launch_few(const FewArgs& a, cudaStream_t st) {
@@ -569,8 +593,7 @@ fsp_status launch_product_of(const MmArgs& g, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return fail(FSP_ECUDA, "cannot read the number of SMs");
   const unsigned grid = unsigned(std::min<int64_t>(sms, g.tiles_p * g.tiles_q));
-  fp8_product_kernel<BN, kSwap, T><<<grid, kMmThreads, kSmem, st>>>(g);
-  return launched("8-bit product kernel launch");
+  return launch_next(fp8_product_kernel<BN, kSwap, T>, dim3(grid), kMmThreads, kSmem, st, "8-bit product kernel launch", g);
 }
 
 template <int BN, bool kSwap>
@@ -618,8 +641,7 @@ fsp_status launch_pairs_of(const MmArgs& g, cudaStream_t st) {
   const fsp_status s = resident_pairs<T>(&pairs);
   if (s != FSP_OK) return s;
   const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, g.tiles_p * g.tiles_q));
-  fp8_pair_kernel<T><<<grid, PairCfg::kThreads, PairCfg::kSmem, st>>>(g);
-  return launched("8-bit product kernel launch");
+  return launch_next(fp8_pair_kernel<T>, dim3(grid), PairCfg::kThreads, PairCfg::kSmem, st, "8-bit product kernel launch", g);
 }
 
 fsp_status launch_pairs(MmArgs& g, int32_t dtype, cudaStream_t st) {
@@ -632,8 +654,8 @@ fsp_status launch_pairs(MmArgs& g, int32_t dtype, cudaStream_t st) {
 fsp_status matmul_checked(const void* a, const void* b, int64_t m, int64_t n, int64_t k, void* c, int32_t dtype,
                           int64_t c_stride, bool accumulate, cudaStream_t st) {
   const Fp8Layout la = layout_of(m, k), lb = layout_of(n, k);
-  // Up to 64 rows of a: b's rows fill the 128 rows of the tiles, a's their columns.
-  const bool swap = m <= 64;
+  // Up to 128 rows of a: b's rows fill the 128 rows of the tiles, a's their columns.
+  const bool swap = m <= 128;
   MmArgs g{};
   g.p = static_cast<const uint8_t*>(swap ? b : a);
   g.q = static_cast<const uint8_t*>(swap ? a : b);
@@ -648,10 +670,18 @@ fsp_status matmul_checked(const void* a, const void* b, int64_t m, int64_t n, in
   g.accumulate = accumulate;
   g.vec = reinterpret_cast<uintptr_t>(c) % 16 == 0 && size_t(c_stride) * size_of(dtype) % 16 == 0;
   g.tiles_p = (g.np + kTileP - 1) / kTileP;
-  if (!swap && m > 128) return launch_pairs(g, dtype, st);
-  if (!swap) return launch_product<192, false>(g, dtype, st);
   if (m <= 16) return launch_product<16, true>(g, dtype, st);
-  return m <= 32 ? launch_product<32, true>(g, dtype, st) : launch_product<64, true>(g, dtype, st);
+  if (m <= 32) return launch_product<32, true>(g, dtype, st);
+  if (m <= 64) return launch_product<64, true>(g, dtype, st);
+  if (m <= 128) return launch_product<128, true>(g, dtype, st);
+  // The narrowest tiles that give every SM at most one: a product too small to fill
+  // the pairs spreads over more SMs (1024 x 2048 x 2048: tiles of 128 10.5 us, pairs
+  // 12.3; 333 x 1001 x 777: tiles of 64 12.3, of 128 15.5, pairs 18.5), a larger one
+  // gains from them (2048 x 2048 x 2048: pairs 12.4, tiles of 128 16.4).
+  const int64_t sms = sm_count();
+  if (g.tiles_p * ((n + 63) / 64) <= sms) return launch_product<64, false>(g, dtype, st);
+  if (g.tiles_p * ((n + 127) / 128) <= sms) return launch_product<128, false>(g, dtype, st);
+  return launch_pairs(g, dtype, st);
 }
 
 fsp_status sum_of_nothing(int64_t m, int64_t n, void* c, int32_t dtype, int64_t c_stride, cudaStream_t st) {
@@ -767,8 +797,8 @@ fsp_status linear_backward(const void* x, int32_t xd, int64_t xs, const void* dy
   char* qt = q + round256(layout_of(rows, out).bytes);
   char* xt = qt + round256(layout_of(out, rows).bytes);
   s = quantize_checked(dy, dyd, rows, out, dys, dx ? q : nullptr, dw ? qt : nullptr, st);
-  if (s == FSP_OK && dx) s = matmul_checked(q, wt, rows, in, out, dx, dxd, dxs, false, st);
   if (s == FSP_OK && dw) s = quantize_checked(x, xd, rows, in, xs, nullptr, xt, st);
+  if (s == FSP_OK && dx) s = matmul_checked(q, wt, rows, in, out, dx, dxd, dxs, false, st);
   if (s == FSP_OK && dw) s = matmul_checked(qt, xt, out, in, rows, dw, FSP_DTYPE_F32, dws, accumulate, st);
   return s;
 }

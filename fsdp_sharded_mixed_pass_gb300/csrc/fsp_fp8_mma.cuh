@@ -90,6 +90,11 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// Programmatic dependent launch: let the next launch on the stream that allows
+// it be scheduled; wait until the launches this grid depends on have completed.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
 }
@@ -251,15 +256,21 @@ __device__ __forceinline__ void write_lines(const MmArgs& g, const uint32_t* x, 
         *dst = y;
       }
     } else {
-      for (int i = 0; i < 16 && h * 16 + i < rows; ++i)   // a lane per element
-        for (int v = lane; v < cols; v += 32) {
+      const int n = min(16, rows - h * 16);
+#pragma unroll
+      for (int v0 = 0; v0 < kCols; v0 += 32) {   // a lane per element
+        const int v = v0 + lane;
+        if (v >= cols) continue;
+        T* dst = c + int64_t(h * 16) * g.c_stride + v;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, dst += g.c_stride) {
           T y = *reinterpret_cast<const T*>(stage + i * kStagePitch + v * int(sizeof(T)));
-          T* dst = c + (h * 16 + i) * g.c_stride + v;
           if constexpr (sizeof(T) == 4) {
             if (g.accumulate) y += *dst;
           }
           *dst = y;
         }
+      }
     }
     __syncwarp();
   }
@@ -304,6 +315,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
   fence_before();
   __syncthreads();
   fence_after();
+  launch_dependents();
+  grid_dependency_wait();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - base));
   const int64_t tiles = g.tiles_p * g.tiles_q;
   const int blocks = int(g.blocks);
@@ -548,6 +561,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   __syncthreads();
   cluster_sync_all();
   fence_after();
+  launch_dependents();
+  grid_dependency_wait();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - base));
   const int64_t tiles = g.tiles_p * g.tiles_q;
   const int64_t step = gridDim.x >> 1;

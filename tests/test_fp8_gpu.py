@@ -136,7 +136,7 @@ def test_product_repeats_bit_for_bit_and_sums_nothing():
     assert fsp.matmul_fp8(fsp.quantize_fp8(torch.zeros(0, 5, device="cuda")), fsp.quantize_fp8(torch.zeros(6, 5, device="cuda"))).shape == (0, 6)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 64, 96), (1, 2048, 1024), (37, 130, 257), (256, 384, 512), (1030, 520, 200)])
+@pytest.mark.parametrize("m,n,k", [(1, 64, 96), (1, 2048, 1024), (37, 130, 257), (256, 384, 512), (1030, 520, 200), (100, 3000, 300), (1024, 2300, 260)])
 def test_linear_layer(m, n, k):
     rng = np.random.default_rng(m * n)
     bf = lambda *s: torch.from_numpy(rng.normal(0, 1, s).astype(np.float32)).cuda().bfloat16()  # noqa: E731
