@@ -6,7 +6,8 @@
 // exponent per row and 32 elements of k inside the tensor core, so a scale per
 // 128 costs nothing: its byte is named for all four instructions of a block.
 //
-// A persistent CTA per SM, six warps:
+// Two kernels.  fp8_product_kernel, for products of few tiles, a persistent CTA per
+// SM with six warps:
 //   warp 0     producer: bulk copies of the operands' tiles (stored in the order
 //              that shared memory wants them, so each is one run of bytes) and
 //              of their scales into a ring of stages, a block of 128 of k each;
@@ -15,8 +16,15 @@
 //   warps 2-5  read a finished accumulator (32 lanes of tensor memory each),
 //              round it and write C, while the next tile is being summed in the
 //              other accumulator.
+// fp8_pair_kernel, for all others, two CTAs (SMs) per 256 x 256 tile: below.
 // Every mbarrier wait gives up after about 2 s, records a bit in the error word
 // and ends its role; the CTA then lets its copies land and frees its memory.
+//
+// Bound: the tensor cores (3.8 PFLOP/s taken as twice the measured bf16 rate), and
+// for short k the epilogue beside them.  Measured: 8192^3 308 us = 3571 TFLOP/s, 8192
+// x 5632 x 2048 64 us = 2947, 4096 x 151936 x 1024 425 us = 3000 (back to back, under
+// the power cap, 500 us).
+
 #pragma once
 
 #include <cuda_bf16.h>
@@ -175,14 +183,13 @@ struct MmArgs {
 constexpr int kStagePitch = 128 + 16;             // bytes of a row: eight lanes' 16-byte stores meet no bank twice
 constexpr int kWarpStage = 16 * kStagePitch;
 
-// BN: rows of Q per tile.  kSwap: C is written transposed (C[q][p]).
+// BN: rows of Q per tile, a part of a stored tile of 128.
 template <int BN>
 struct MmCfg {
-  static constexpr int kScaleChunks = BN > 128 ? 2 : 1;            // 128-row scale pieces a tile of Q touches
-  static constexpr int kScaleCols = 4 + 4 * kScaleChunks;          // tensor memory columns of a stage's scales
-  static constexpr int kStageBytes = kTileP * 128 + BN * 128 + 512 + 512 * kScaleChunks;
+  static constexpr int kScaleCols = 8;                              // tensor memory columns of a stage's scales: 4 of P, 4 of Q
+  static constexpr int kStageBytes = kTileP * 128 + BN * 128 + 1024;
   static constexpr int kEpilogue = 4 * kWarpStage;
-  static constexpr int kFixed = 1024 + 256 + kEpilogue;            // alignment, barriers, epilogue
+  static constexpr int kFixed = 1024 + 256 + kEpilogue;             // alignment, barriers, epilogue
   static constexpr int kFit = (232448 - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kAccCols = BN < 32 ? 32 : BN;
@@ -191,7 +198,7 @@ struct MmCfg {
   static constexpr int kCols = kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
   static_assert(kColsUsed <= 512, "tensor memory");
-  static_assert(BN % 16 == 0 && BN <= 256 && (BN * 128) % 1024 == 0, "tile of Q");
+  static_assert(128 % BN == 0 && BN % 16 == 0, "tile of Q");
 };
 
 struct TileAt {
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* smem = raw + (base - smem_addr(raw));
   const uint32_t at_p = base, at_q = at_p + S * kTileP * 128, at_sp = at_q + S * BN * 128;
-  const uint32_t at_sq = at_sp + S * 512, at_epi = at_sq + S * 512 * Cfg::kScaleChunks;
+  const uint32_t at_sq = at_sp + S * 512, at_epi = at_sq + S * 512;
   const uint32_t bars = at_epi + Cfg::kEpilogue;
   const uint32_t full = bars, empty = full + 8 * S, acc_full = empty + 8 * S, acc_empty = acc_full + 16;
   const uint32_t drained = acc_empty + 16, slot = drained + 8;
@@ -330,28 +337,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const TileAt tile = tile_at(g, t);
       const int64_t q0 = tile.q * BN, q_tile = q0 >> 7;
-      const int64_t q_tiles = (g.nq + 127) >> 7;
-      // rows of Q: from q_tile's row (q0 mod 128), and the next 128-row tile's first ones
-      const int first = min(BN, 128 - int(q0 & 127));
-      const int second = q_tile + 1 < q_tiles ? BN - first : 0;
-      const int sq_chunks = min(Cfg::kScaleChunks, int(q_tiles - q_tile));
-      const uint32_t bytes = uint32_t(kTileP + first + second) * 128u + 512u * uint32_t(1 + sq_chunks);
       const uint8_t* src_p = g.p + tile.p * g.blocks * kTileBytes;
       const uint8_t* src_q = g.q + q_tile * g.blocks * kTileBytes + (q0 & 127) * 128;
-      const uint8_t* src_q2 = g.q + (q_tile + 1) * g.blocks * kTileBytes;
       const uint8_t* src_sp = g.p + g.p_scales + tile.p * g.pieces * kScaleBytes;
       const uint8_t* src_sq = g.q + g.q_scales + q_tile * g.pieces * kScaleBytes;
       for (int k = 0; k < blocks; ++k) {
         if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1u))) break;
         const uint32_t bar = full + 8 * s;
-        mbar_expect(bar, bytes);
-        bulk_load(at_p + s * kTileP * 128, src_p + int64_t(k) * kTileBytes, kTileP * 128, bar);
-        bulk_load(at_q + s * BN * 128, src_q + int64_t(k) * kTileBytes, first * 128, bar);
-        if (second) bulk_load(at_q + s * BN * 128 + first * 128, src_q2 + int64_t(k) * kTileBytes, second * 128, bar);
         const int64_t piece = int64_t(k >> 2) * kScaleBytes;
+        mbar_expect(bar, Cfg::kStageBytes);
+        bulk_load(at_p + s * kTileP * 128, src_p + int64_t(k) * kTileBytes, kTileP * 128, bar);
+        bulk_load(at_q + s * BN * 128, src_q + int64_t(k) * kTileBytes, BN * 128, bar);
         bulk_load(at_sp + s * 512, src_sp + piece, 512, bar);
-        for (int j = 0; j < sq_chunks; ++j)
-          bulk_load(at_sq + (s * Cfg::kScaleChunks + j) * 512, src_sq + j * g.pieces * kScaleBytes + piece, 512, bar);
+        bulk_load(at_sq + s * 512, src_sq + piece, 512, bar);
         ++issued;
         if (++s == S) s = 0, phase ^= 1u;
       }
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const uint32_t sq_shift = uint32_t((tile_at(g, t).q * BN) & 127) / 32;   // columns of the scale pieces before q0
+      const uint32_t sq_shift = uint32_t((tile_at(g, t).q * BN) & 127) / 32;   // columns of the scales before q0
       if (!(ok = mbar_wait(acc_empty + 8 * buf, acc_phase ^ 1u))) break;
       fence_after();
       const uint32_t d = tmem + buf * Cfg::kAccCols;
@@ -380,8 +378,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
         const uint64_t dp = desc_p + uint64_t(s * (kTileP * 128 / 16)), dq = desc_q + uint64_t(s * (BN * 128 / 16));
         if (elect_one()) {
           scale_copy(sp, desc_sp + uint64_t(s * 32));
-#pragma unroll
-          for (int j = 0; j < Cfg::kScaleChunks; ++j) scale_copy(sq + 4 * j, desc_sq + uint64_t((s * Cfg::kScaleChunks + j) * 32));
+          scale_copy(sq, desc_sq + uint64_t(s * 32));
 #pragma unroll
           for (int i = 0; i < 4; ++i) mma_scaled(d, dp + 2 * i, dq + 2 * i, id, sp, sq + sq_shift, (k | i) != 0);
           mma_commit(empty + 8 * s);

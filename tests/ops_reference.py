@@ -68,11 +68,12 @@ def fp8(x):
     r, k = x.shape
     b = np.pad(x, ((0, 0), (0, -k % 128))).reshape(r, -1, 128)
     top = np.abs(b).max(2, keepdims=True)
-    e = np.full(top.shape, -127.0)
-    for i in np.ndindex(top.shape):   # the smallest e in [-127, 127] with top <= 448 2^e
-        if top[i] > 0 and np.isfinite(top[i]):
-            while top[i] > np.ldexp(448.0, int(e[i])):
-                e[i] += 1
+    # the smallest e in [-127, 127] with top <= 448 2^e
+    with np.errstate(invalid="ignore", divide="ignore"):
+        e = np.ceil(np.log2(np.where((top > 0) & np.isfinite(top), top, 2.0 ** -150) / 448))
+    e += top > 448 * np.exp2(e)          # (log2's own rounding)
+    e -= top <= 448 * np.exp2(e - 1)
+    e = np.maximum(e, -127.0)
     s = np.exp2(e)
     with np.errstate(invalid="ignore"):
         v = np.where(np.isfinite(top), e4m3(np.where(np.isfinite(top), b, 0) / s) * s, np.nan)
