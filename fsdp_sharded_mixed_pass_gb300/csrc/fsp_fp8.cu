@@ -95,12 +95,22 @@ __device__ __forceinline__ void load_row(const T* row, int64_t c, int64_t cols, 
   }
 }
 
+// The bits of the largest magnitude of V values, as fp32; NaN above all.  bf16: two
+// at a time, their magnitudes order as 16-bit numbers.
 template <typename T, int V>
-__device__ __forceinline__ uint32_t largest(const T* x) {   // the bits of the largest magnitude, NaN above all
-  uint32_t top = 0;
+__device__ __forceinline__ uint32_t largest(const T* x) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+    uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(widen(x[j])) & 0x7fffffffu);
-  return top;
+    for (int j = 0; j < V / 2; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+    return max(top << 16, top & 0xffff0000u);
+  } else {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+    return top;
+  }
 }
 
 // Blocks along the rows of x: a warp per row and four blocks, eight lanes of
@@ -162,7 +172,7 @@ struct ColsSmem {
 static_assert(sizeof(ColsSmem<__nv_bfloat16>) >= kTileBytes, "the codes take the tile's place");
 
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads)
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2)
     quantize_cols_kernel(const __grid_constant__ QuantArgs a, uint8_t* out, Fp8Layout l, bool vec) {
   extern __shared__ __align__(16) unsigned char raw[];
   launch_dependents();
@@ -211,20 +221,26 @@ __global__ void __launch_bounds__(kQuantThreads)
   }
   __syncthreads();
   const int c = (tid & 63) * 2, q = tid >> 6;   // two columns, a quarter of their block
-  float x[2][32];
+  alignas(8) T two[32][2];
   uint32_t top[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    alignas(8) T two[2];
     if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<uint2*>(two) = *reinterpret_cast<const uint2*>(&sm.x[q * 32 + j][c]);
+      *reinterpret_cast<uint2*>(two[j]) = *reinterpret_cast<const uint2*>(&sm.x[q * 32 + j][c]);
     else
-      *reinterpret_cast<uint32_t*>(two) = *reinterpret_cast<const uint32_t*>(&sm.x[q * 32 + j][c]);
+      *reinterpret_cast<uint32_t*>(two[j]) = *reinterpret_cast<const uint32_t*>(&sm.x[q * 32 + j][c]);
+  }
+  if constexpr (sizeof(T) == 2) {
+    uint32_t both = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      x[k][j] = widen(two[k]);
-      top[k] = max(top[k], __float_as_uint(x[k][j]) & 0x7fffffffu);
-    }
+    for (int j = 0; j < 32; ++j) both = __vmaxu2(both, *reinterpret_cast<const uint32_t*>(two[j]) & 0x7fff7fffu);
+    top[0] = both << 16;
+    top[1] = both & 0xffff0000u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) top[k] = max(top[k], __float_as_uint(two[j][k]) & 0x7fffffffu);
   }
   sm.tops[q][c] = top[0];
   sm.tops[q][c + 1] = top[1];
@@ -234,8 +250,13 @@ __global__ void __launch_bounds__(kQuantThreads)
     const int r = c + k;   // of the transpose's tile
     const int s = scale_byte(max(max(sm.tops[0][r], sm.tops[1][r]), max(sm.tops[2][r], sm.tops[3][r])));
     const float inv = inverse_scale(s);
-    *reinterpret_cast<uint4*>(raw + code_at(r, 2 * q)) = codes16(x[k], inv);
-    *reinterpret_cast<uint4*>(raw + code_at(r, 2 * q + 1)) = codes16(x[k] + 16, inv);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = widen(two[16 * h + j][k]);
+      *reinterpret_cast<uint4*>(raw + code_at(r, 2 * q + h)) = codes16(f, inv);
+    }
     if (q == 0 && c0 + r < a.cols)
       a.out[a.l.scale_offset + (int64_t(blockIdx.x) * a.l.pieces + (blockIdx.y >> 2)) * kScaleBytes +
             scale_at(r, int(blockIdx.y & 3))] = uint8_t(s);
