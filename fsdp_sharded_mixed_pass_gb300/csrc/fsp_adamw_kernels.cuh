@@ -354,7 +354,9 @@ __device__ __forceinline__ void update_block(const ListArgs& a, const ListTile& 
 
 template <bool k8Bit>
 __global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel(const __grid_constant__ ListArgs a) {
-  const ListTile tile = a.tiles[blockIdx.x];
+  launch_dependents();
+  const ListTile tile = a.tiles[blockIdx.x];   // (a table that no kernel writes)
+  grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int begin = warp * kListBlock;   // this warp's block in the tile
   if (begin >= tile.len) return;

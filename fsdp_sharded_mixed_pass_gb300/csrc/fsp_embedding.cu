@@ -7,8 +7,8 @@
 // named rows, when accumulating); no atomic addition touches a value, so the
 // result depends on the tokens alone.
 //
-// Gradient, three launches, the later two with programmatic stream serialisation
-// (their CTAs are there when the launch before them ends):
+// Gradient, three launches, with programmatic stream serialisation (their CTAs are
+// there when the launch before them ends):
 //   1. sort_tokens_kernel: one cluster sorts (token, position) pairs by token,
 //      stably (radix sort), and marks the tokens that occur in a bitmap;
 //   2. sum_rows_kernel: the sorted pairs in chunks of 32; a warp owns 32 x V columns
@@ -86,9 +86,9 @@ __device__ __forceinline__ void load_raw(const T* p, T* x) {
   constexpr int kBytes = int(sizeof(T)) * V;
   if constexpr (kBytes >= 16) {
 #pragma unroll
-    for (int k = 0; k < kBytes / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldcs(reinterpret_cast<const uint4*>(p) + k);
+    for (int k = 0; k < kBytes / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldg(reinterpret_cast<const uint4*>(p) + k);
   } else if constexpr (kBytes == 8) {
-    *reinterpret_cast<uint2*>(x) = __ldcs(reinterpret_cast<const uint2*>(p));
+    *reinterpret_cast<uint2*>(x) = __ldg(reinterpret_cast<const uint2*>(p));
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) x[j] = p[j];
@@ -129,9 +129,12 @@ struct LookupArgs {
   int index_bytes;
 };
 
-// A warp per token: the row in steps of 32 x V elements.
+// A warp per token: the row in steps of 32 x V elements, four in flight.
 template <typename W, typename O, int V>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const __grid_constant__ LookupArgs a) {
+  constexpr int kAhead = 4;
+  launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t i = int64_t(blockIdx.x) * (kLookupThreads / 32) + (threadIdx.x >> 5);
   if (i >= a.n_tokens) return;
@@ -140,13 +143,19 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const __grid_con
   if (!ok && lane == 0) atomicOr(&g_token_error, kErrToken);
   const W* row = static_cast<const W*>(a.weight) + (ok ? t : 0) * a.weight_stride;
   O* out = static_cast<O*>(a.out) + i * a.out_stride;
-#pragma unroll 4
-  for (int64_t c = int64_t(lane) * V; c < a.dim; c += 32 * V) {
-    float f[V];
-    load_vec<W, V>(row + c, f);
+  for (int64_t c0 = int64_t(lane) * V; c0 < a.dim; c0 += kAhead * 32 * V) {
+    alignas(16) W x[kAhead][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = ok ? f[j] * a.scale : 0.f;
-    store_vec<O, V>(out + c, f);
+    for (int k = 0; k < kAhead; ++k)
+      if (c0 + k * 32 * V < a.dim) load_raw<W, V>(row + c0 + k * 32 * V, x[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (c0 + k * 32 * V < a.dim) {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = ok ? widen(x[k][j]) * a.scale : 0.f;
+        store_vec<O, V>(out + c0 + k * 32 * V, f);
+      }
   }
 }
 
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const __grid_
       return __ldcg(p);
   };
   launch_dependents();
+  grid_dependency_wait();
   const int n_ctas = int(gridDim.x), cta = int(blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int i = cta * kSortThreads + tid; i < s.n_words; i += n_ctas * kSortThreads) s.present[i] = 0;
@@ -595,18 +605,33 @@ bool rows_fit(const void* p, int64_t stride, int32_t dtype, int v) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && size_t(stride) * size_of(dtype) % bytes == 0;
 }
 
-fsp_status launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+// Launches with programmatic stream serialisation (every kernel here waits for the
+// launch before it ahead of its first access), a cluster of `cluster` CTAs.
+template <typename A>
+fsp_status launch_next(void (*kernel)(A), dim3 grid, int threads, size_t smem, int cluster, const A& args, cudaStream_t st,
+                       const char* what) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
   return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
 }
 
 template <typename W, typename O>
-void launch_lookup(const LookupArgs& a, bool vec, cudaStream_t st) {
-  const unsigned ctas = unsigned((a.n_tokens + kLookupThreads / 32 - 1) / (kLookupThreads / 32));
-  if (vec)
-    lookup_kernel<W, O, 8><<<ctas, kLookupThreads, 0, st>>>(a);
-  else
-    lookup_kernel<W, O, 1><<<ctas, kLookupThreads, 0, st>>>(a);
+fsp_status launch_lookup(const LookupArgs& a, bool vec, cudaStream_t st) {
+  const dim3 ctas(unsigned((a.n_tokens + kLookupThreads / 32 - 1) / (kLookupThreads / 32)));
+  return launch_next(vec ? lookup_kernel<W, O, 8> : lookup_kernel<W, O, 1>, ctas, kLookupThreads, 0, 1, a, st,
+                     "embedding kernel launch");
 }
 
 fsp_status lookup(const void* weight, int32_t wd, int64_t vocab, int64_t dim, int64_t ws, const void* tokens,
@@ -627,10 +652,8 @@ fsp_status lookup(const void* weight, int32_t wd, int64_t vocab, int64_t dim, in
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
   if (wd == FSP_DTYPE_F32)
-    od == FSP_DTYPE_F32 ? launch_lookup<float, float>(a, vec, st) : launch_lookup<float, B>(a, vec, st);
-  else
-    od == FSP_DTYPE_F32 ? launch_lookup<B, float>(a, vec, st) : launch_lookup<B, B>(a, vec, st);
-  return launched("embedding kernel launch");
+    return od == FSP_DTYPE_F32 ? launch_lookup<float, float>(a, vec, st) : launch_lookup<float, B>(a, vec, st);
+  return od == FSP_DTYPE_F32 ? launch_lookup<B, float>(a, vec, st) : launch_lookup<B, B>(a, vec, st);
 }
 
 struct Workspace {   // byte offsets
@@ -656,22 +679,6 @@ fsp_status check_sizes(int64_t vocab, int64_t dim, int64_t n) {
   return FSP_OK;
 }
 
-// Launches with programmatic stream serialisation.
-template <typename K>
-fsp_status launch_next(K kernel, dim3 grid, int threads, const RowArgs& a, cudaStream_t st, const char* what) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
-}
-
 template <typename G, typename T, int V>
 fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
   a.cols = 32;
@@ -685,11 +692,11 @@ fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
   constexpr int kJoinV = V > 4 ? 4 : V;
   const int64_t join_cols = (a.dim + 32 * kJoinV - 1) / (32 * kJoinV);
   if (ctas > INT32_MAX || join_cols > 65535) return fail(FSP_EUNSUPPORTED, "too many tokens times columns");
-  const fsp_status s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(ctas)), kRowThreads, a, st,
+  const fsp_status s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(ctas)), kRowThreads, 0, 1, a, st,
                                    "embedding gradient (sum) kernel launch");
   if (s != FSP_OK || chunks <= 1) return s;
   return launch_next(join_rows_kernel<T, kJoinV>, dim3(unsigned((chunks + kJoinWarps - 1) / kJoinWarps), unsigned(join_cols)),
-                     kJoinThreads, a, st, "embedding gradient (join) kernel launch");
+                     kJoinThreads, 0, 1, a, st, "embedding gradient (join) kernel launch");
 }
 
 template <typename G, typename T>
@@ -699,33 +706,17 @@ fsp_status launch_rows_v(RowArgs& a, int v, cudaStream_t st) {
 
 fsp_status launch_sort(const SortArgs& s, cudaStream_t st) {
   if (s.n <= kSortOne) {
-    static const cudaError_t allowed =
-        cudaFuncSetAttribute(sort_tokens_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemOne);
-    if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (token sort)", allowed));
-    sort_tokens_kernel<true><<<1, kSortThreads, kSortSmemOne, st>>>(s);
-    return launched("token sort kernel launch");
+    const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&sort_tokens_kernel<true>), kSortSmemOne);
+    if (ok != FSP_OK) return ok;
+    return launch_next(sort_tokens_kernel<true>, dim3(1), kSortThreads, kSortSmemOne, 1, s, st, "token sort kernel launch");
   }
-  static const cudaError_t allowed = [] {   // clusters of 16 are beyond the size every device has to offer
-    cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(sort_tokens_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e;
-  }();
-  if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (token sort)", allowed));
+  // (clusters of 16 are beyond the size every device has to offer)
+  const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&sort_tokens_kernel<false>), kSortSmem, true);
+  if (ok != FSP_OK) return ok;
   int ctas = 4;
   while (ctas < kSortCluster && s.n > ctas * kSortPerCta) ctas *= 2;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(ctas);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = kSortSmem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_tokens_kernel<false>, s);
-  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("token sort kernel launch", e));
+  return launch_next(sort_tokens_kernel<false>, dim3(unsigned(ctas)), kSortThreads, kSortSmem, ctas, s, st,
+                     "token sort kernel launch");
 }
 
 fsp_status backward(const void* tokens, int32_t index_bytes, int64_t n, const void* grad, int32_t gd, int64_t dim,

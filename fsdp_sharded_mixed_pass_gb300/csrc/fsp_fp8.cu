@@ -11,7 +11,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <map>
+#include <mutex>
 #include <string>
+#include <utility>
 
 #include "fsp_host.h"
 #include "fsp_internal.h"
@@ -487,9 +490,8 @@ fsp_status run_quantize(const QuantArgs& in, void* out, void* out_t, bool vec, c
   const Fp8Layout l = layout_of(a.rows, a.cols);
   if (out_t) {
     constexpr int kSmem = int(sizeof(ColsSmem<T>));
-    static const cudaError_t allowed =
-        cudaFuncSetAttribute(quantize_cols_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (quantisation)", allowed));
+    const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&quantize_cols_kernel<T>), kSmem);
+    if (ok != FSP_OK) return ok;
     a.out = static_cast<uint8_t*>(out_t);
     a.l = layout_of(a.cols, a.rows);
     if (a.l.blocks > 65535) return fail(FSP_EUNSUPPORTED, "the matrix is too large");
@@ -573,17 +575,6 @@ fsp_status values(const void* q, int64_t rows, int64_t cols, float* out, void* s
   return launched("8-bit values kernel launch");
 }
 
-int sm_count() {
-  static const int n = [] {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return 0;
-    return sms;
-  }();
-  return n;
-}
-
 // Whether `rows` rows of `cols` values go through few_rows_kernel.
 constexpr int64_t kFewMost = 4;
 bool few(int64_t rows, int64_t cols) { return rows <= kFewMost && rows * ((cols + 127) / 128 * 128) * 4 <= kFewSmem; }
@@ -591,12 +582,13 @@ bool few(int64_t rows, int64_t cols) { return rows <= kFewMost && rows * ((cols 
 template <int M, typename T, typename O>
 fsp_status launch_few_of(const FewArgs& a, cudaStream_t st) {
   constexpr int kMost = int(kFewSmem) * 2 + 8 * kFewRows * 4 * M;   // (three rows run in the kernel of four)
-  static const cudaError_t allowed =
-      cudaFuncSetAttribute(few_rows_kernel<M, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (few rows)", allowed));
+  fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&few_rows_kernel<M, T, O>), kMost);
+  int sms = 0;
+  if (ok == FSP_OK) ok = sm_count(&sms);
+  if (ok != FSP_OK) return ok;
   const size_t smem = size_t(M) * size_t(a.l.blocks) * 512 + 8 * kFewRows * 4 * M;
   // x is quantised once per CTA: at most eight CTAs per SM, which then take turns
-  const int64_t ctas = std::min<int64_t>((a.n + kFewRows - 1) / kFewRows, int64_t(sm_count()) * 8);
+  const int64_t ctas = std::min<int64_t>((a.n + kFewRows - 1) / kFewRows, int64_t(sms) * 8);
   return launch_next(few_rows_kernel<M, T, O>, dim3(unsigned(ctas)), kFewThreads, smem, st,
                      "8-bit linear (few rows) kernel launch", a);
 }
@@ -608,11 +600,10 @@ fsp_status launch_few(const FewArgs& a, cudaStream_t st) {
 template <int BN, bool kSwap, typename T>
 fsp_status launch_product_of(const MmArgs& g, cudaStream_t st) {
   constexpr int kSmem = MmCfg<BN>::kSmem;
-  static const cudaError_t allowed =
-      cudaFuncSetAttribute(fp8_product_kernel<BN, kSwap, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (allowed != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute (8-bit product)", allowed));
-  const int sms = sm_count();
-  if (sms <= 0) return fail(FSP_ECUDA, "cannot read the number of SMs");
+  fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&fp8_product_kernel<BN, kSwap, T>), kSmem);
+  int sms = 0;
+  if (ok == FSP_OK) ok = sm_count(&sms);
+  if (ok != FSP_OK) return ok;
   const unsigned grid = unsigned(std::min<int64_t>(sms, g.tiles_p * g.tiles_q));
   return launch_next(fp8_product_kernel<BN, kSwap, T>, dim3(grid), kMmThreads, kSmem, st, "8-bit product kernel launch", g);
 }
@@ -629,30 +620,34 @@ fsp_status launch_product(MmArgs& g, int32_t dtype, cudaStream_t st) {
 // would double a launch's time.
 template <typename T>
 fsp_status resident_pairs(int* pairs) {
-  struct Got {
-    cudaError_t e;
-    int pairs;
-  };
-  static const Got got = [] {
-    cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::kSmem);
-    int n = 0;
-    if (e == cudaSuccess) {
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(unsigned(2 * std::max(1, sm_count() / 2)));
-      cfg.blockDim = dim3(PairCfg::kThreads);
-      cfg.dynamicSmemBytes = PairCfg::kSmem;
-      cudaLaunchAttribute attr{};
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = 2;
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel<T>, &cfg);
+  static std::mutex mu;
+  static std::map<int, int> known;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaGetDevice", e));
+  fsp_status s = allow_kernel(reinterpret_cast<const void*>(&fp8_pair_kernel<T>), PairCfg::kSmem);
+  if (s == FSP_OK) s = sm_count(&sms);
+  if (s != FSP_OK) return s;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[dev];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(sms / 2 * 2));
+    cfg.blockDim = dim3(PairCfg::kThreads);
+    cfg.dynamicSmemBytes = PairCfg::kSmem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel<T>, &cfg);
+    if (e != cudaSuccess || n < 1) {
+      n = 0;
+      return fail(FSP_ECUDA, cuda_msg("cudaOccupancyMaxActiveClusters", e));
     }
-    return Got{e, n};
-  }();
-  if (got.e != cudaSuccess || got.pairs < 1) return fail(FSP_ECUDA, cuda_msg("8-bit product set-up", got.e));
-  *pairs = got.pairs;
+  }
+  *pairs = n;
   return FSP_OK;
 }
 
@@ -699,7 +694,9 @@ fsp_status matmul_checked(const void* a, const void* b, int64_t m, int64_t n, in
   // the pairs spreads over more SMs (1024 x 2048 x 2048: tiles of 128 10.5 us, pairs
   // 12.3; 333 x 1001 x 777: tiles of 64 12.3, of 128 15.5, pairs 18.5), a larger one
   // gains from them (2048 x 2048 x 2048: pairs 12.4, tiles of 128 16.4).
-  const int64_t sms = sm_count();
+  int sms = 0;
+  const fsp_status s = sm_count(&sms);
+  if (s != FSP_OK) return s;
   if (g.tiles_p * ((n + 63) / 64) <= sms) return launch_product<64, false>(g, dtype, st);
   if (g.tiles_p * ((n + 127) / 128) <= sms) return launch_product<128, false>(g, dtype, st);
   return launch_pairs(g, dtype, st);

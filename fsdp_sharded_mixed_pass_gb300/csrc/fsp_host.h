@@ -57,6 +57,11 @@ fsp_status run_clipped_passes(const fsp_plan* p, StepArgs& a, float max_norm, fl
 fsp_status clipped_empty(float* norm_out, void* stream);
 // *step_dev += 1 on `stream` (one thread).
 fsp_status advance_step(int64_t* step_dev, void* stream);
+// Allows a kernel its dynamic shared memory, and with `wide_cluster` clusters of
+// more than eight CTAs, on the current device (once per kernel and device).
+fsp_status allow_kernel(const void* fn, int smem, bool wide_cluster = false);
+// SMs of the current device.
+fsp_status sm_count(int* sms);
 // Reads and clears the error bits of the embedding kernels (their part of the
 // device error word).
 cudaError_t take_token_error(unsigned* bits);

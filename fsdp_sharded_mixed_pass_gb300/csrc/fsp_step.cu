@@ -337,6 +337,41 @@ fsp_status grid_for(const KernelInfo& k, int* grid) {
   return FSP_OK;
 }
 
+fsp_status allow_kernel(const void* fn, int smem, bool wide_cluster) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> done;   // shared memory allowed so far
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaGetDevice", e));
+  std::lock_guard<std::mutex> lock(mu);
+  int& allowed = done[{fn, dev}];
+  if (allowed >= smem) return FSP_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && wide_cluster) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaFuncSetAttribute", e));
+  allowed = smem;
+  return FSP_OK;
+}
+
+fsp_status sm_count(int* sms) {
+  static std::mutex mu;
+  static std::map<int, int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("cudaGetDevice", e));
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[dev];
+  if (n == 0) {
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess || n <= 0) {
+      n = 0;
+      return fail(FSP_ECUDA, cuda_msg("cudaDeviceGetAttribute", e));
+    }
+  }
+  *sms = n;
+  return FSP_OK;
+}
+
 // ---- AdamW over a list of tensors: launches (host side in fsp_adamw.cpp) ---------
 
 // Lists of at least this many tiles per CTA of the ring take it, if bulk copies can
@@ -353,11 +388,22 @@ fsp_status launch_list(const ListArgs& a, cudaStream_t st) {
   const fsp_status s = grid_for(
       KernelInfo{reinterpret_cast<const void*>(&adamw_ring_kernel<k8Bit>), Ring<k8Bit>::kThreads, Ring<k8Bit>::kSmem, true}, &grid);
   if (s != FSP_OK) return s;
-  if (a.n_tiles >= kRingMinTilesPerCta<k8Bit> * grid && 2 * a.bulk_tiles >= a.n_tiles)
+  cudaError_t e;
+  if (a.n_tiles >= kRingMinTilesPerCta<k8Bit> * grid && 2 * a.bulk_tiles >= a.n_tiles) {
     adamw_ring_kernel<k8Bit><<<unsigned(grid), Ring<k8Bit>::kThreads, Ring<k8Bit>::kSmem, st>>>(a);
-  else
-    adamw_list_kernel<k8Bit><<<unsigned(a.n_tiles), kListThreads, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
+  } else {   // a short launch: programmatic stream serialisation, as the step's
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(a.n_tiles));
+    cfg.blockDim = dim3(kListThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, adamw_list_kernel<k8Bit>, a);
+  }
   return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg("AdamW list kernel launch", e));
 }
 
