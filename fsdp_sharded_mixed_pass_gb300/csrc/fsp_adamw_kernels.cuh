@@ -179,28 +179,44 @@ __device__ __forceinline__ float block_largest(const float2* x) {
 // `n` of the four inside the tensor.
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
+// Streaming loads, volatile: they stay behind the wait for the launch before.
+__device__ __forceinline__ float4 stream4(const float* p) {
+  float4 x;
+  asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint2 stream4(const uint16_t* p) {
+  uint2 x;
+  asm volatile("ld.global.cs.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint32_t stream4(const uint8_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.cs.b32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+
 __device__ __forceinline__ void load4(const void* base, bool bf16, bool vec, int64_t i, int n, float2* x) {
   if (bf16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + i;
     if (vec && n == 4) {
-      const uint2 b = __ldcs(reinterpret_cast<const uint2*>(p));
+      const uint2 b = stream4(p);
       x[0] = make_float2(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u));
       x[1] = make_float2(__uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        x[h] = make_float2(2 * h < n ? bf16_value(__ldcs(p + 2 * h)) : 0.f, 2 * h + 1 < n ? bf16_value(__ldcs(p + 2 * h + 1)) : 0.f);
+        x[h] = make_float2(2 * h < n ? bf16_value(p[2 * h]) : 0.f, 2 * h + 1 < n ? bf16_value(p[2 * h + 1]) : 0.f);
     }
   } else {
     const float* p = static_cast<const float*>(base) + i;
     if (vec && n == 4) {
-      const float4 f = __ldcs(reinterpret_cast<const float4*>(p));
+      const float4 f = stream4(p);
       x[0] = make_float2(f.x, f.y);
       x[1] = make_float2(f.z, f.w);
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        x[h] = make_float2(2 * h < n ? __ldcs(p + 2 * h) : 0.f, 2 * h + 1 < n ? __ldcs(p + 2 * h + 1) : 0.f);
+      for (int h = 0; h < 2; ++h) x[h] = make_float2(2 * h < n ? p[2 * h] : 0.f, 2 * h + 1 < n ? p[2 * h + 1] : 0.f);
     }
   }
 }
@@ -278,8 +294,8 @@ __device__ __forceinline__ void load_block(const ListArgs& a, const ListTile& t,
     load4(t.param, pb, vec, i, n, b.p + 2 * h);
     if (k8Bit) {
       const uint32_t in = n == 4 ? ~0u : (1u << (8 * n)) - 1u;   // nothing past the tensor's end
-      b.qm[h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + slot) + 32 * h + lane) & in;
-      b.qv[h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + slot) + 32 * h + lane) & in;
+      b.qm[h] = stream4(static_cast<const uint8_t*>(a.m) + slot + 4 * (32 * h + lane)) & in;
+      b.qv[h] = stream4(static_cast<const uint8_t*>(a.v) + slot + 4 * (32 * h + lane)) & in;
     } else {
       load4(static_cast<const float*>(a.m) + t.state_off, false, true, i, n, b.m + 2 * h);
       load4(static_cast<const float*>(a.v) + t.state_off, false, true, i, n, b.v + 2 * h);

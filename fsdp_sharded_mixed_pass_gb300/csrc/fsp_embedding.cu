@@ -39,8 +39,22 @@ __device__ unsigned int g_token_error = 0;
 
 // Programmatic dependent launch: let the next launch on the stream that allows
 // it be scheduled; wait until the launches this grid depends on have completed.
+// Loads after the wait are ordinary or volatile ones: what a compiler takes for a
+// load of constant memory (__ldg and the like) it may move ahead of the wait.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// From L2: written by another CTA of this grid.
+__device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 load_l2(const uint2* p) {
+  uint2 x;
+  asm volatile("ld.global.cg.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p) : "memory");
+  return x;
+}
 
 // ---- element access -----------------------------------------------------------
 
@@ -57,58 +71,52 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// V elements from p, 4 * V or 2 * V bytes, aligned to min(that, 16).
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float* f) {
-  constexpr int kBytes = int(sizeof(T)) * V;
-  if constexpr (kBytes >= 16) {
-#pragma unroll
-    for (int k = 0; k < kBytes / 16; ++k) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + k);
-      const T* t = reinterpret_cast<const T*>(&b);
-#pragma unroll
-      for (int j = 0; j < 16 / int(sizeof(T)); ++j) f[k * (16 / int(sizeof(T))) + j] = widen(t[j]);
-    }
-  } else if constexpr (kBytes == 8) {
-    const uint2 b = __ldg(reinterpret_cast<const uint2*>(p));
-    const T* t = reinterpret_cast<const T*>(&b);
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = widen(t[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = widen(p[j]);
-  }
-}
-
-// As load_vec, without widening.
+// V elements at p as one access of V * sizeof(T) bytes (4 to 32; p aligned to
+// that), or element by element for V = 1.  32 bytes are one access of a whole sector:
+// as two of 16 bytes, a warp's stores half-filled every sector twice.
 template <typename T, int V>
 __device__ __forceinline__ void load_raw(const T* p, T* x) {
   constexpr int kBytes = int(sizeof(T)) * V;
-  if constexpr (kBytes >= 16) {
-#pragma unroll
-    for (int k = 0; k < kBytes / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldg(reinterpret_cast<const uint4*>(p) + k);
-  } else if constexpr (kBytes == 8) {
-    *reinterpret_cast<uint2*>(x) = __ldg(reinterpret_cast<const uint2*>(p));
+  uint32_t* w = reinterpret_cast<uint32_t*>(x);
+  if constexpr (V == 1) {
+    x[0] = p[0];
+  } else if constexpr (kBytes == 32) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+  } else if constexpr (kBytes == 16) {
+    *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
   } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = p[j];
+    static_assert(kBytes == 8);
+    *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(p);
   }
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float* f) {
+  alignas(32) T x[V];
+  load_raw<T, V>(p, x);
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = widen(x[j]);
 }
 
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float* f) {
   constexpr int kBytes = int(sizeof(T)) * V;
-  alignas(16) T t[V];
+  alignas(32) T t[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) t[j] = narrow<T>(f[j]);
-  if constexpr (kBytes >= 16) {
-#pragma unroll
-    for (int k = 0; k < kBytes / 16; ++k) __stcs(reinterpret_cast<uint4*>(p) + k, reinterpret_cast<uint4*>(t)[k]);
-  } else if constexpr (kBytes == 8) {
-    __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<uint2*>(t));
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(t);
+  if constexpr (V == 1) {
+    p[0] = t[0];
+  } else if constexpr (kBytes == 32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else if constexpr (kBytes == 16) {
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(t));
   } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = t[j];
+    static_assert(kBytes == 8);
+    __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(t));
   }
 }
 
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const __grid_con
   const W* row = static_cast<const W*>(a.weight) + (ok ? t : 0) * a.weight_stride;
   O* out = static_cast<O*>(a.out) + i * a.out_stride;
   for (int64_t c0 = int64_t(lane) * V; c0 < a.dim; c0 += kAhead * 32 * V) {
-    alignas(16) W x[kAhead][V];
+    alignas(32) W x[kAhead][V];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
       if (c0 + k * 32 * V < a.dim) load_raw<W, V>(row + c0 + k * 32 * V, x[k]);
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const __grid_
     if constexpr (kOne)
       return *p;
     else
-      return __ldcg(p);
+      return load_l2(p);
   };
   launch_dependents();
   grid_dependency_wait();
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const __grid_
     } else if (tid < kBins) {
       uint32_t t[kSortCluster];
 #pragma unroll
-      for (int c = 0; c < kSortCluster; ++c) t[c] = c < n_ctas ? __ldcg(&s.totals[c * kBins + tid]) : 0u;
+      for (int c = 0; c < kSortCluster; ++c) t[c] = c < n_ctas ? load_l2(&s.totals[c * kBins + tid]) : 0u;
 #pragma unroll
       for (int c = 0; c < kSortCluster; ++c) {
         if (c < cta) before += t[c];
@@ -411,7 +419,7 @@ __device__ __forceinline__ void sum_chunk(const RowArgs& a, int64_t chunk, int64
 #pragma unroll
   for (int j = 0; j < V; ++j) acc[j] = 0.f;
   for (int k0 = 0; k0 < count; k0 += kAhead) {
-    alignas(16) G x[kAhead][V];
+    alignas(32) G x[kAhead][V];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const uint32_t at = __shfl_sync(0xffffffffu, it.y, (k0 + k) & 31);
@@ -601,7 +609,7 @@ bool overlap(const void* p, size_t pb, const void* q, size_t qb) {
 
 // Whether rows of V elements may be accessed as vectors.
 bool rows_fit(const void* p, int64_t stride, int32_t dtype, int v) {
-  const size_t bytes = std::min<size_t>(16, size_t(v) * size_of(dtype));
+  const size_t bytes = size_t(v) * size_of(dtype);
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && size_t(stride) * size_of(dtype) % bytes == 0;
 }
 
@@ -628,9 +636,9 @@ fsp_status launch_next(void (*kernel)(A), dim3 grid, int threads, size_t smem, i
 }
 
 template <typename W, typename O>
-fsp_status launch_lookup(const LookupArgs& a, bool vec, cudaStream_t st) {
+fsp_status launch_lookup(const LookupArgs& a, int v, cudaStream_t st) {
   const dim3 ctas(unsigned((a.n_tokens + kLookupThreads / 32 - 1) / (kLookupThreads / 32)));
-  return launch_next(vec ? lookup_kernel<W, O, 8> : lookup_kernel<W, O, 1>, ctas, kLookupThreads, 0, 1, a, st,
+  return launch_next(v == 8 ? lookup_kernel<W, O, 8> : v == 4 ? lookup_kernel<W, O, 4> : lookup_kernel<W, O, 1>, ctas, kLookupThreads, 0, 1, a, st,
                      "embedding kernel launch");
 }
 
@@ -648,12 +656,14 @@ fsp_status lookup(const void* weight, int32_t wd, int64_t vocab, int64_t dim, in
   if (vocab == 0) return fail(FSP_EINVAL, "tokens look up an empty table");
   if (n > int64_t(INT32_MAX) * (kLookupThreads / 32)) return fail(FSP_EUNSUPPORTED, "too many tokens");
   const LookupArgs a{weight, tokens, out, vocab, dim, ws, os, n, scale, index_bytes};
-  const bool vec = dim % 8 == 0 && rows_fit(weight, ws, wd, 8) && rows_fit(out, os, od, 8);
+  int v = 1;
+  for (int k : {8, 4})
+    if (v == 1 && dim % k == 0 && rows_fit(weight, ws, wd, k) && rows_fit(out, os, od, k)) v = k;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
   if (wd == FSP_DTYPE_F32)
-    return od == FSP_DTYPE_F32 ? launch_lookup<float, float>(a, vec, st) : launch_lookup<float, B>(a, vec, st);
-  return od == FSP_DTYPE_F32 ? launch_lookup<B, float>(a, vec, st) : launch_lookup<B, B>(a, vec, st);
+    return od == FSP_DTYPE_F32 ? launch_lookup<float, float>(a, v, st) : launch_lookup<float, B>(a, v, st);
+  return od == FSP_DTYPE_F32 ? launch_lookup<B, float>(a, v, st) : launch_lookup<B, B>(a, v, st);
 }
 
 struct Workspace {   // byte offsets
@@ -668,7 +678,7 @@ Workspace workspace_of(int64_t vocab, int64_t dim, int64_t n) {
   w.present = w.b + items;
   w.totals = w.present + round256(size_t((vocab + 31) / 32) * 4);
   w.parts = w.totals + size_t(kSortCluster) * kBins * 4;
-  w.bytes = w.parts + round256(chunks * 2 * size_t(dim) * 4);
+  w.bytes = w.parts + round256(chunks * 2 * size_t(dim) * 4) + 256;   // (the offsets count from a multiple of 256)
   return w;
 }
 
@@ -747,7 +757,7 @@ fsp_status backward(const void* tokens, int32_t index_bytes, int64_t n, const vo
       if (overlap(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
         return fail(FSP_EINVAL, std::string(bufs[i].name) + " overlaps " + bufs[j].name);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  char* base = static_cast<char*>(workspace);
+  char* base = reinterpret_cast<char*>(round256(reinterpret_cast<uintptr_t>(workspace)));
   SortArgs sa{};
   sa.tokens = tokens;
   sa.a = reinterpret_cast<uint2*>(base + w.a);

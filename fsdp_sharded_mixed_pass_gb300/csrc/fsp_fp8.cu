@@ -91,7 +91,7 @@ template <typename T, int V>
 __device__ __forceinline__ void load_row(const T* row, int64_t c, int64_t cols, bool vec, T* x) {
   if (vec && c + V <= cols) {
 #pragma unroll
-    for (int k = 0; k < V * int(sizeof(T)) / 16; ++k) reinterpret_cast<uint4*>(x)[k] = __ldg(reinterpret_cast<const uint4*>(row + c) + k);
+    for (int k = 0; k < V * int(sizeof(T)) / 16; ++k) reinterpret_cast<uint4*>(x)[k] = reinterpret_cast<const uint4*>(row + c)[k];
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) x[j] = c + j < cols ? row[c + j] : T(0.f);
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_cons
       float s[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[i] = __ldcs(reinterpret_cast<const uint4*>(src + code_at(r0 + 4 * i, p)));
-        s[i] = scale_value(__ldg(scales + scale_at(r0 + 4 * i, int(block & 3))));
+        c[i] = *reinterpret_cast<const uint4*>(src + code_at(r0 + 4 * i, p));
+        s[i] = scale_value(scales[scale_at(r0 + 4 * i, int(block & 3))]);
       }
       float x[M][16];
 #pragma unroll

@@ -100,6 +100,8 @@ __device__ __forceinline__ bool elect_one() {
 
 // Programmatic dependent launch: let the next launch on the stream that allows
 // it be scheduled; wait until the launches this grid depends on have completed.
+// Loads after the wait are ordinary or volatile ones: what a compiler takes for a
+// load of constant memory (__ldg and the like) it may move ahead of the wait.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -102,7 +102,7 @@ def test_offsets_past_32_bits():
 # tokens, vocab, dim, pad, shift: one token to many; one row; chunk edges (32 pairs); odd and wide rows
 GRAD = [(1, 1, 1, 0, 0), (1, 9, 64, 0, 0), (31, 7, 8, 0, 0), (32, 3, 12, 0, 0), (33, 1, 517, 0, 0), (64, 2, 40, 8, 0),
         (97, 1000, 33, 0, 0), (500, 30, 1024, 0, 0), (1000, 511, 96, 4, 4), (1000, 512, 96, 1, 1), (4096, 513, 16, 0, 0),
-        (4097, 5003, 24, 0, 0), (5000, 1, 8, 0, 0), (9001, 262143, 4, 0, 0), (9001, 262144, 4, 0, 0), (300, 20, 3000, 0, 0)]
+        (4097, 5003, 24, 0, 0), (5000, 1, 8, 0, 0), (9001, 262143, 4, 0, 0), (9001, 262144, 4, 0, 0), (300, 20, 3000, 0, 0), (3000, 70000, 1000, 0, 0)]
 
 
 @pytest.mark.parametrize("grad,weight", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
