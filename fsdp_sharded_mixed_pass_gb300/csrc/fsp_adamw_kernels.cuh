@@ -20,6 +20,10 @@
 // 4 l .. 4 l + 3 of each half, so that every access of a warp is one run of 512
 // (fp32), 256 (bf16) or 128 bytes (codes) and a block's largest value is one
 // reduction over the warp.
+//
+// A list with many tiles per SM goes through a ring of stages that bulk copies
+// fill and drain instead (adamw_ring_kernel, below): the same tiles, a warp per
+// block, with the copies of the next tiles in flight meanwhile.
 #pragma once
 
 #include "fsp_host.h"
