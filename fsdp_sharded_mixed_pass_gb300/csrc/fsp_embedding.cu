@@ -16,9 +16,9 @@
 //      lie within one chunk is finished there; the parts of one that spans chunks
 //      go to the workspace, so a token that fills half of a batch is spread over as
 //      many CTAs as any other half;
-//   3. join_rows_kernel: adds such a token's parts, eight warps a share each.  Between
-//      them, CTAs that write zeros into the rows that no token names (not when
-//      accumulating).
+//   3. join_rows_kernel: adds such a token's parts, eight warps a share each.
+// Zeros into the rows that no token names (not when accumulating) are written by
+// other CTAs of 2 or 3.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -382,8 +382,8 @@ struct RowArgs {
   int accumulate;
   int cols;                  // threads along the columns: 32, 64 or 128
   int col_ctas;              // CTAs along the columns
-  int join_cols;             // the join's CTAs along the columns
-  int64_t join_ctas, zero_ctas;
+  int64_t sum_ctas, zero_ctas;   // of the sums' launch
+  uint32_t join_zeros;            // CTAs of the join, per CTA along the columns, that write zeros
 };
 
 template <typename T, int V>
@@ -457,29 +457,46 @@ __device__ __forceinline__ void sum_chunk(const RowArgs& a, int64_t chunk, int64
     finish_row<T, V>(a, row, col, acc);
 }
 
+// Zeros into the rows of one word of the bitmap that no token of the batch has.
+template <typename T, int V, int kThreads>
+__device__ __forceinline__ void write_zeros(const RowArgs& a, int64_t word) {
+  const int64_t row0 = word * kZeroRows;
+  if (row0 >= a.vocab) return;
+  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
+  const uint32_t present = a.present[word];
+  const float zero[V] = {};
+  const int rows = int(min(int64_t(kZeroRows), a.vocab - row0));
+  for (int r = cy; r < rows; r += kThreads / a.cols) {
+    if (present >> r & 1u) continue;
+    T* p = static_cast<T*>(a.weight) + (row0 + r) * a.weight_stride;
+    for (int64_t c = int64_t(cx) * V; c < a.dim; c += a.cols * V) store_vec<T, V>(p + c, zero);
+  }
+}
+
 template <typename G, typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) sum_rows_kernel(const __grid_constant__ RowArgs a) {
   launch_dependents();
   grid_dependency_wait();
-  const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
-  const int64_t chunk = int64_t(blockIdx.x) / a.col_ctas * (kRowThreads / a.cols) + cy;
-  sum_chunk<G, T, V>(a, chunk, (blockIdx.x % a.col_ctas * a.cols + cx) * int64_t(V), threadIdx.x & 31);
-}
-
-// Zeros into the rows of one word of the bitmap that no token of the batch has: this
-// thread's are rows `cy`, cy + row_step, ... and vectors cx, cx + cols, ...
-template <typename T, int V>
-__device__ __forceinline__ void write_zeros(const RowArgs& a, int64_t word, int cx, int cols, int cy, int row_step) {
-  const int64_t row0 = word * kZeroRows;
-  const uint32_t present = a.present[word];
-  const float zero[V] = {};
-  const int rows = int(min(int64_t(kZeroRows), a.vocab - row0));
-  for (int r = cy; r < rows; r += row_step) {
-    if (present >> r & 1u) continue;
-    T* p = static_cast<T*>(a.weight) + (row0 + r) * a.weight_stride;
-    for (int64_t c = int64_t(cx) * V; c < a.dim; c += cols * V) store_vec<T, V>(p + c, zero);
+  // CTAs that sum and CTAs that write zeros, in proportion all along the grid:
+  // reads and writes then share the launch's time
+  const int64_t ctas = a.sum_ctas + a.zero_ctas, i = blockIdx.x;
+  const int64_t sums = i * a.sum_ctas / ctas;
+  if ((i + 1) * a.sum_ctas / ctas > sums) {
+    const int cx = threadIdx.x & (a.cols - 1), cy = threadIdx.x / a.cols;
+    const int64_t chunk = sums / a.col_ctas * (kRowThreads / a.cols) + cy;
+    sum_chunk<G, T, V>(a, chunk, (sums % a.col_ctas * a.cols + cx) * V, threadIdx.x & 31);
+  } else {
+    write_zeros<T, V, kRowThreads>(a, i - sums);
   }
 }
+
+// The join's additions wait for one another and leave the memory idle, so the zeros
+// of a large table are written beside them instead of beside the sums (text-like tokens,
+// fp32 rows of 1024: 65536 into 151936 rows 143 us, beside the sums 154; 4096 107 and 112;
+// 16384 into 32000 47 and 50).  Of a small table (4096 x 1024 into 66 MB: 30 us either
+// way) or of few tokens (300 into 151936 rows: 100 and 98) the sums hide as much.
+constexpr size_t kLateBytes = size_t(100) << 20;
+constexpr int64_t kLateChunks = 64;
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
@@ -491,9 +508,7 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 // took 40 us on 65536 text-like tokens.)
 constexpr int kAlone = 16;
 
-// The additions wait for one another and leave the memory idle, so the zeros are
-// written by other CTAs of the same launch, in accesses of VZ elements (65536 text-like
-// tokens into 151936 x 1024: 147 us with them here, 157 beside the sums).
+// VZ: elements of an access of a CTA that writes zeros.
 template <typename T, int V, int VZ>
 __global__ void __launch_bounds__(kJoinThreads) join_rows_kernel(const __grid_constant__ RowArgs a) {
   __shared__ float share[kJoinWarps][32 * V];
@@ -501,14 +516,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_rows_kernel(const __grid_co
   launch_dependents();
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t ctas = a.join_ctas + a.zero_ctas, i = blockIdx.x;
-  const int64_t zeros = i * a.zero_ctas / ctas;   // both kinds in proportion all along the grid
-  if ((i + 1) * a.zero_ctas / ctas > zeros) {
-    write_zeros<T, VZ>(a, zeros, threadIdx.x & (a.cols - 1), a.cols, threadIdx.x / a.cols, kJoinThreads / a.cols);
+  if (blockIdx.x < a.join_zeros) {
+    write_zeros<T, VZ, kJoinThreads>(a, int64_t(blockIdx.y) * a.join_zeros + blockIdx.x);
     return;
   }
-  const int64_t first = (i - zeros) / a.join_cols * kJoinWarps;
-  const int64_t col = ((i - zeros) % a.join_cols * 32 + lane) * V;
+  const int64_t first = int64_t(blockIdx.x - a.join_zeros) * kJoinWarps;
+  const int64_t col = (int64_t(blockIdx.y) * 32 + lane) * V;
   // parts begin, begin + step, ... of the token that begins in `chunk`
   float acc[V];
   auto add_parts = [&](int64_t chunk, int64_t begin, int64_t parts, int step) {
@@ -710,20 +723,20 @@ fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
   a.col_ctas = int((a.dim + int64_t(a.cols) * V - 1) / (int64_t(a.cols) * V));
   const int64_t chunks = (int64_t(a.n) + kChunk - 1) / kChunk;
   const int per_cta = kRowThreads / a.cols;
-  const int64_t sum_ctas = (chunks + per_cta - 1) / per_cta * a.col_ctas;
+  a.sum_ctas = (chunks + per_cta - 1) / per_cta * a.col_ctas;
   constexpr int kJoinV = V > 4 ? 4 : V;
-  a.join_cols = int((a.dim + 32 * kJoinV - 1) / (32 * kJoinV));
-  a.join_ctas = chunks > 1 ? (chunks + kJoinWarps - 1) / kJoinWarps * a.join_cols : 0;
-  a.zero_ctas = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-  const int64_t ctas = a.join_ctas + a.zero_ctas;
-  if (sum_ctas > INT32_MAX || ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "too many tokens times columns");
-  if (sum_ctas > 0) {
-    const fsp_status s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(sum_ctas)), kRowThreads, 0, 1, a, st,
-                                     "embedding gradient (sum) kernel launch");
-    if (s != FSP_OK) return s;
-  }
-  if (ctas == 0) return FSP_OK;
-  return launch_next(join_rows_kernel<T, kJoinV, V>, dim3(unsigned(ctas)), kJoinThreads, 0, 1, a, st,
+  const int64_t join_cols = (a.dim + 32 * kJoinV - 1) / (32 * kJoinV);
+  const int64_t words = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
+  const bool late = chunks >= kLateChunks && size_t(a.vocab) * size_t(a.dim) * sizeof(T) >= kLateBytes;
+  a.zero_ctas = late ? 0 : words;
+  a.join_zeros = late ? uint32_t((words + join_cols - 1) / join_cols) : 0u;
+  const int64_t ctas = a.sum_ctas + a.zero_ctas, join_ctas = a.join_zeros + (chunks + kJoinWarps - 1) / kJoinWarps;
+  if (ctas > INT32_MAX || join_ctas > INT32_MAX || join_cols > 65535)
+    return fail(FSP_EUNSUPPORTED, "too many tokens times columns");
+  const fsp_status s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(ctas)), kRowThreads, 0, 1, a, st,
+                                   "embedding gradient (sum) kernel launch");
+  if (s != FSP_OK || chunks <= 1) return s;
+  return launch_next(join_rows_kernel<T, kJoinV, V>, dim3(unsigned(join_ctas), unsigned(join_cols)), kJoinThreads, 0, 1, a, st,
                      "embedding gradient (join) kernel launch");
 }
 
