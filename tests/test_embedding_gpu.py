@@ -202,3 +202,26 @@ def test_refusals():
         fsp.embedding_backward(ids, dy, w, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(fsp.FspError, match="empty table"):
         fsp.embedding(w[:0], ids)
+
+
+@pytest.mark.parametrize("tokens,vocab,dim,pad,weight", [(2016, 60001, 517, 0, "f32"), (2017, 60001, 517, 0, "f32"),
+                                                         (5000, 70000, 380, 4, "f32"), (40000, 52000, 1032, 0, "bf16")])
+def test_gradient_of_large_tables(tokens, vocab, dim, pad, weight):
+    """Tables of 100 MB and more, on both sides of 64 runs of 32 tokens: every row is written."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    ids = (torch.rand(tokens, generator=g, device="cuda", dtype=torch.float64) ** 6 * vocab).long().clamp_(max=vocab - 1)
+    dy = torch.randn(tokens, dim, generator=g, device="cuda").bfloat16()
+    buf = torch.full((vocab, dim + pad), float("nan"), device="cuda", dtype=DT[weight])
+    fsp.embedding_backward(ids, dy, buf[:, :dim], scale=0.5)
+    add = lambda x: torch.zeros(vocab, dim, device="cuda", dtype=torch.float64).index_add_(0, ids, x * 0.5)  # noqa: E731
+    want, mag = add(dy.double()), add(dy.double().abs())
+    n = torch.bincount(ids, minlength=vocab)
+    # n additions and the scaling, each at most 2^-24 of the magnitudes that enter it; then bf16's rounding
+    tol = (n[:, None] + 2) * 2.0 ** -24 * mag
+    got = buf[:, :dim].double()
+    if weight == "bf16":
+        tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    assert bool(((got - want).abs() <= tol).all())
+    assert bool((got[n == 0] == 0).all()) and int((n == 0).sum()) > 0
+    assert bool(buf[:, dim:].isnan().all())
+    assert fsp.device_error() == 0
