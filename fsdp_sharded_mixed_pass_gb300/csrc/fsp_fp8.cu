@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <map>
 #include <mutex>
 #include <string>
@@ -302,6 +303,12 @@ __global__ void __launch_bounds__(kQuantThreads) values_kernel(const uint8_t* q,
 // for four rows of w (rows r, r + 4, ...), so that a warp's load is 512 bytes of
 // a tile in a run, and x's 16 values serve four rows.  The eight lanes of a row,
 // then the eight warps, are added in a fixed order.
+//
+// A sum of 16 values of x times codes of w is below 2^22 of x's scale, and w's scale
+// comes after it: with a scale of x above 2^104 the sum could leave fp32's range where
+// what it stands for does not.  The values of such a block are kept 2^16 smaller and
+// w's scale takes the factor.  A CTA without such a block runs a form without factors
+// (4 x 5632 x 4096 30 us; with a factor at every block 33).
 constexpr int kFewThreads = 256;
 constexpr int kFewRows = 16;             // of w, per CTA and turn
 constexpr int64_t kFewSmem = 64 * 1024;  // of x's values, at most
@@ -326,34 +333,13 @@ __device__ __forceinline__ void values16(uint4 c, float* f) {
   }
 }
 
-template <int M, typename T, typename O>
-__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_constant__ FewArgs a) {
-  extern __shared__ float xv[];   // [M][blocks * 128], then [8 warps][16][M]
-  launch_dependents();
-  grid_dependency_wait();
+// All rows of w of this CTA; kFactors: with the factors of x's blocks.
+template <int M, typename O, bool kFactors>
+__device__ __forceinline__ void few_rows_of_w(const FewArgs& a, float* xv) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t width = a.l.blocks * 128;
-  for (int64_t b = warp; b < a.l.blocks * M; b += kFewThreads / 32) {
-    const int64_t m = b / a.l.blocks, block = b % a.l.blocks, c = block * 128 + lane * 4;
-    const T* row = static_cast<const T*>(a.x) + m * a.x_stride;
-    float f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = m < a.rows && c + j < a.cols ? widen(row[c + j]) : 0.f;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-    const int s = scale_byte(__reduce_max_sync(0xffffffffu, top));
-    const uint32_t codes = codes4(f, inverse_scale(s));
-    const float scale = scale_value(uint8_t(s));
-    float4 v;
-    v.x = code_value(uint8_t(codes)) * scale;
-    v.y = code_value(uint8_t(codes >> 8)) * scale;
-    v.z = code_value(uint8_t(codes >> 16)) * scale;
-    v.w = code_value(uint8_t(codes >> 24)) * scale;
-    *reinterpret_cast<float4*>(xv + m * width + c) = v;
-  }
-  __syncthreads();
-  float* part = xv + M * width;
+  float* factors = xv + M * width;
+  float* part = factors + M * a.l.blocks;
   const int sub = lane >> 3, p = lane & 7;
   for (int64_t n0 = int64_t(blockIdx.x) * kFewRows; n0 < a.n; n0 += int64_t(gridDim.x) * kFewRows) {
     const int64_t tile = n0 >> 7;
@@ -390,7 +376,15 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_cons
 #pragma unroll
           for (int m = 0; m < M; ++m) sum[m] = fmaf(f[j], x[m][j], sum[m]);
 #pragma unroll
-        for (int m = 0; m < M; ++m) acc[i][m] = fmaf(sum[m], s[i], acc[i][m]);
+        for (int m = 0; m < M; ++m) {
+          float t = s[i];
+          if constexpr (kFactors) {
+            // (beyond fp32 its largest number serves: any sum but 0 times that is infinite, and 0 stays 0)
+            t *= factors[m * a.l.blocks + block];
+            if (t > FLT_MAX) t = FLT_MAX;
+          }
+          acc[i][m] = fmaf(sum[m], t, acc[i][m]);
+        }
       }
     }
 #pragma unroll
@@ -415,6 +409,50 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const __grid_cons
     }
     __syncthreads();
   }
+}
+// Out of line: beside it in one function the usual form was slower (1 x 151936 x 1024 46 us, so 40).
+template <int M, typename O>
+__device__ __noinline__ void few_rows_with_factors(const FewArgs& a, float* xv) {
+  few_rows_of_w<M, O, true>(a, xv);
+}
+
+// (One row: registers for four CTAs per SM, with three 1 x 151936 x 1024 takes 51 us.)
+template <int M, typename T, typename O>
+__global__ void __launch_bounds__(kFewThreads, M == 1 ? 4 : 2) few_rows_kernel(const __grid_constant__ FewArgs a) {
+  extern __shared__ float xv[];   // [M][blocks * 128], then [M][blocks] factors, then [8 warps][16][M]
+  launch_dependents();
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t width = a.l.blocks * 128;
+  float* factors = xv + M * width;
+  bool huge = false;
+  for (int64_t b = warp; b < a.l.blocks * M; b += kFewThreads / 32) {
+    const int64_t m = b / a.l.blocks, block = b % a.l.blocks, c = block * 128 + lane * 4;
+    const T* row = static_cast<const T*>(a.x) + m * a.x_stride;
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = m < a.rows && c + j < a.cols ? widen(row[c + j]) : 0.f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    const int s = scale_byte(__reduce_max_sync(0xffffffffu, top));
+    const uint32_t codes = codes4(f, inverse_scale(s));
+    const bool far = s > 127 + 104 && s < 255;
+    const float scale = scale_value(uint8_t(far ? s - 16 : s));
+    float4 v;
+    v.x = code_value(uint8_t(codes)) * scale;
+    v.y = code_value(uint8_t(codes >> 8)) * scale;
+    v.z = code_value(uint8_t(codes >> 16)) * scale;
+    v.w = code_value(uint8_t(codes >> 24)) * scale;
+    *reinterpret_cast<float4*>(xv + m * width + c) = v;
+    if (lane == 0) factors[b] = far ? 65536.f : 1.f;
+    huge = huge || far;
+  }
+  huge = __syncthreads_or(huge);
+  if (huge)
+    few_rows_with_factors<M, O>(a, xv);
+  else
+    few_rows_of_w<M, O, false>(a, xv);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -581,12 +619,12 @@ bool few(int64_t rows, int64_t cols) { return rows <= kFewMost && rows * ((cols 
 
 template <int M, typename T, typename O>
 fsp_status launch_few_of(const FewArgs& a, cudaStream_t st) {
-  constexpr int kMost = int(kFewSmem) * 2 + 8 * kFewRows * 4 * M;   // (three rows run in the kernel of four)
+  constexpr int kMost = int(kFewSmem) * 2 + int(kFewSmem) / 64 + 8 * kFewRows * 4 * M;   // (three rows run in the kernel of four)
   fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&few_rows_kernel<M, T, O>), kMost);
   int sms = 0;
   if (ok == FSP_OK) ok = sm_count(&sms);
   if (ok != FSP_OK) return ok;
-  const size_t smem = size_t(M) * size_t(a.l.blocks) * 512 + 8 * kFewRows * 4 * M;
+  const size_t smem = size_t(M) * size_t(a.l.blocks) * (512 + 4) + 8 * kFewRows * 4 * M;
   // x is quantised once per CTA: at most eight CTAs per SM, which then take turns
   const int64_t ctas = std::min<int64_t>((a.n + kFewRows - 1) / kFewRows, int64_t(sms) * 8);
   return launch_next(few_rows_kernel<M, T, O>, dim3(unsigned(ctas)), kFewThreads, smem, st,

@@ -245,3 +245,28 @@ def test_refusals():
         fsp.matmul_fp8(q, q, out=torch.zeros(4, 4, dtype=torch.bfloat16, device="cuda"), accumulate=True)
     with pytest.raises(fsp.FspError, match="overlaps"):
         fsp.matmul_fp8(q, q, out=q.data[:64].view(torch.float32).view(4, 4))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_few_rows_of_huge_and_tiny_values(rows, out):
+    """The scales of x and w may lie anywhere: what a product stands for is in range
+    although x's value times w's code is not."""
+    rng = np.random.default_rng(rows)
+    k, n = 700, 40
+    x, w = rng.normal(0, 1, (rows, k)), rng.normal(0, 1, (n, k))
+    ex = np.repeat([124, -120, 90, -122, 0, 60], 128)[:k].astype(np.float64)   # powers of two, by block
+    x *= np.exp2(ex) * 0.5
+    x = np.clip(x, -3.3e38, 3.3e38)
+    w *= np.exp2(-ex)
+    x[0, 5] = 3.4e38   # rounds to 2^128, beside a zero of w
+    w[:, 5] = 0
+    xd, wd = torch.from_numpy(x.astype(np.float32)).cuda(), torch.from_numpy(w.astype(np.float32)).cuda()
+    want, mag = _product(_values(xd), _values(wd))
+    assert np.isfinite(want).all() and np.abs(want).max() < 1e4
+    got = _values(fsp.Fp8Linear(wd).forward(xd, out_dtype=DT[out]))
+    tol = _tolerance(k, mag)
+    if out == "bf16":
+        assert rounds_to(got, want, tol).all()
+    else:
+        assert (np.abs(got - want) <= tol).all()
