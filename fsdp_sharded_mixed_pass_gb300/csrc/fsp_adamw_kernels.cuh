@@ -267,13 +267,13 @@ __device__ __forceinline__ void adamw_coarse(float2 g, float2& p, float2& m, flo
   p = __ffma2_rn(p, both(c.decay_hi), __fmul2_rn(u, both(-c.step_hi)));
 }
 
+// Thread 0 of block 0 reports a device-resident update index below 1 (taken as 1).
+__device__ __forceinline__ void report_step_index(const ListArgs& a) {
+  if (a.step_dev && threadIdx.x == 0 && blockIdx.x == 0 && *a.step_dev < 1) atomicOr(&g_fsp_device_error, kErrStepIndex);
+}
 __device__ __forceinline__ Coeffs list_coeffs(const ListArgs& a) {
   if (!a.step_dev) return a.c;
-  int64_t t = *a.step_dev;
-  if (t < 1) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_fsp_device_error, kErrStepIndex);
-    t = 1;
-  }
+  const int64_t t = max(*a.step_dev, int64_t(1));
   Coeffs c = a.c;
   bias_scalars(c, a.lr, t);
   return c;
@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int begin = warp * kListBlock;   // this warp's block in the tile
   if (begin >= tile.len) return;
+  report_step_index(a);
   ListBlock b;
   load_block<k8Bit>(a, tile, begin, lane, b);
   update_block<k8Bit>(a, tile, list_coeffs(a), a.grad_scale ? *a.grad_scale : 1.f, begin, lane, b);
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(co
     }
     fence_mbar_init();
   }
+  report_step_index(a);
   __syncthreads();
 
   if (warp == 0) {

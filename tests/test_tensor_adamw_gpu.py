@@ -283,3 +283,15 @@ def test_refusals():
     opt.exp_avg = opt._refs[1][0]   # a registered gradient in a state's place
     with pytest.raises(fsp.FspError):
         opt.step()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_device_t_below_one_is_reported_on_long_lists(bits):
+    n = 21_000_000   # enough tiles for the ring of stages
+    a, b = (Lists([n], bits=bits, seed=6, capturable=cap) for cap in (True, False))
+    a.opt._next_t.fill_(0)
+    a.opt.step()
+    assert fsp.device_error() == 8 and a.opt.t == 0
+    b.opt.step()   # t = 1, which the step above was taken as
+    assert fsp.device_error() == 0
+    assert torch.equal(a.params[0], b.params[0]) and torch.equal(a.opt.exp_avg_sq, b.opt.exp_avg_sq)
