@@ -181,6 +181,10 @@ constexpr int64_t kSortPerCta = 1024;       // tokens per CTA of a cluster from 
 constexpr int kSortSmem = kSortWarps * kBins * 4 + kBins * 4 + kSortWarps * 4;
 constexpr int kSortSmemOne = kSortSmem + 2 * kSortOne * 8;
 static_assert(kSortOne <= kSortThreads * kHeld, "one CTA holds its items");
+// Most tokens: the sort counts them in 32 bits, in steps of up to all of its threads
+// (the last step may end that far past the last token).
+constexpr int64_t kSortMost = int64_t(INT32_MAX) - kSortCluster * kSortThreads;
+static_assert(32 * kHeld <= kSortCluster * kSortThreads, "a warp's rounds end within the same reach");
 
 struct SortArgs {
   const void* tokens;
@@ -707,7 +711,8 @@ Workspace workspace_of(int64_t vocab, int64_t dim, int64_t n) {
 
 fsp_status check_sizes(int64_t vocab, int64_t dim, int64_t n) {
   if (vocab < 0 || dim < 0 || n < 0) return fail(FSP_EINVAL, "vocab, dim and n_tokens must be >= 0");
-  if (vocab >= INT32_MAX || n >= INT32_MAX - 4096) return fail(FSP_EUNSUPPORTED, "vocab and n_tokens must be below 2^31");
+  if (vocab >= INT32_MAX) return fail(FSP_EUNSUPPORTED, "vocab must be below 2^31 - 1");
+  if (n > kSortMost) return fail(FSP_EUNSUPPORTED, "n_tokens must be below 2^31 - 16384");
   if (dim > (int64_t(1) << 24)) return fail(FSP_EUNSUPPORTED, "dim must be at most 2^24");
   return FSP_OK;
 }

@@ -176,3 +176,14 @@ def test_reference_rounding_of_bf16():
     want = np.array([1.0, 1.0 + 2.0 ** -8, 7.50974])
     assert rounds_to(np.array([1.0, 1.0, 7.5]), want, np.zeros(3)).all()
     assert not rounds_to(np.array([1.0 + 2.0 ** -7, 1.0 + 2.0 ** -7, 7.53125]), want, np.zeros(3)).any()
+
+
+def test_embedding_backward_takes_no_more_tokens_than_its_sort_can_count(lib):
+    """The sort counts tokens in 32 bits and steps by up to 16384 past the last one."""
+    size = ctypes.c_size_t()
+    bytes_of = lambda n: lib.fsp_embedding_backward_workspace_bytes(10, 1, n, ctypes.byref(size))  # noqa: E731
+    most = 2 ** 31 - 1 - 16384
+    assert bytes_of(most) == B.FSP_OK and size.value >= 16 * most
+    for n in (most + 1, 2 ** 31 - 4098, 2 ** 31 - 1, 2 ** 31):
+        assert bytes_of(n) == B.FSP_EUNSUPPORTED, n
+        assert _backward(lib, n=n) == B.FSP_EUNSUPPORTED, n
