@@ -717,8 +717,24 @@ fsp_status check_sizes(int64_t vocab, int64_t dim, int64_t n) {
   return FSP_OK;
 }
 
+fsp_status launch_sort(const SortArgs& s, cudaStream_t st) {
+  if (s.n <= kSortOne) {
+    const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&sort_tokens_kernel<true>), kSortSmemOne);
+    if (ok != FSP_OK) return ok;
+    return launch_next(sort_tokens_kernel<true>, dim3(1), kSortThreads, kSortSmemOne, 1, s, st, "token sort kernel launch");
+  }
+  // (clusters of 16 are beyond the size every device has to offer)
+  const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&sort_tokens_kernel<false>), kSortSmem, true);
+  if (ok != FSP_OK) return ok;
+  int ctas = 4;
+  while (ctas < kSortCluster && s.n > ctas * kSortPerCta) ctas *= 2;
+  return launch_next(sort_tokens_kernel<false>, dim3(unsigned(ctas)), kSortThreads, kSortSmem, ctas, s, st,
+                     "token sort kernel launch");
+}
+
+// The three launches; what refuses them comes before the first.
 template <typename G, typename T, int V>
-fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
+fsp_status launch_rows(const SortArgs& sort, RowArgs& a, cudaStream_t st) {
   // the widest of 32, 64 and 128 threads that leaves the fewest columns over
   const int64_t vectors = (a.dim + V - 1) / V;
   auto padded = [&](int64_t c) { return (vectors + c - 1) / c * c; };
@@ -738,31 +754,17 @@ fsp_status launch_rows(RowArgs& a, cudaStream_t st) {
   const int64_t ctas = a.sum_ctas + a.zero_ctas, join_ctas = a.join_zeros + (chunks + kJoinWarps - 1) / kJoinWarps;
   if (ctas > INT32_MAX || join_ctas > INT32_MAX || join_cols > 65535)
     return fail(FSP_EUNSUPPORTED, "too many tokens times columns");
-  const fsp_status s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(ctas)), kRowThreads, 0, 1, a, st,
-                                   "embedding gradient (sum) kernel launch");
+  fsp_status s = launch_sort(sort, st);
+  if (s == FSP_OK)
+    s = launch_next(sum_rows_kernel<G, T, V>, dim3(unsigned(ctas)), kRowThreads, 0, 1, a, st, "embedding gradient (sum) kernel launch");
   if (s != FSP_OK || chunks <= 1) return s;
   return launch_next(join_rows_kernel<T, kJoinV, V>, dim3(unsigned(join_ctas), unsigned(join_cols)), kJoinThreads, 0, 1, a, st,
                      "embedding gradient (join) kernel launch");
 }
 
 template <typename G, typename T>
-fsp_status launch_rows_v(RowArgs& a, int v, cudaStream_t st) {
-  return v == 8 ? launch_rows<G, T, 8>(a, st) : v == 4 ? launch_rows<G, T, 4>(a, st) : launch_rows<G, T, 1>(a, st);
-}
-
-fsp_status launch_sort(const SortArgs& s, cudaStream_t st) {
-  if (s.n <= kSortOne) {
-    const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&sort_tokens_kernel<true>), kSortSmemOne);
-    if (ok != FSP_OK) return ok;
-    return launch_next(sort_tokens_kernel<true>, dim3(1), kSortThreads, kSortSmemOne, 1, s, st, "token sort kernel launch");
-  }
-  // (clusters of 16 are beyond the size every device has to offer)
-  const fsp_status ok = allow_kernel(reinterpret_cast<const void*>(&sort_tokens_kernel<false>), kSortSmem, true);
-  if (ok != FSP_OK) return ok;
-  int ctas = 4;
-  while (ctas < kSortCluster && s.n > ctas * kSortPerCta) ctas *= 2;
-  return launch_next(sort_tokens_kernel<false>, dim3(unsigned(ctas)), kSortThreads, kSortSmem, ctas, s, st,
-                     "token sort kernel launch");
+fsp_status launch_rows_v(const SortArgs& sort, RowArgs& a, int v, cudaStream_t st) {
+  return v == 8 ? launch_rows<G, T, 8>(sort, a, st) : v == 4 ? launch_rows<G, T, 4>(sort, a, st) : launch_rows<G, T, 1>(sort, a, st);
 }
 
 fsp_status backward(const void* tokens, int32_t index_bytes, int64_t n, const void* grad, int32_t gd, int64_t dim,
@@ -809,8 +811,6 @@ fsp_status backward(const void* tokens, int32_t index_bytes, int64_t n, const vo
   while ((vocab >> bits) != 0) ++bits;
   sa.passes = (bits + kDigitBits - 1) / kDigitBits;
   sa.bits = (bits + sa.passes - 1) / sa.passes;
-  s = launch_sort(sa, st);
-  if (s != FSP_OK) return s;
   RowArgs a{};
   a.items = sa.passes & 1 ? sa.a : sa.b;
   a.present = sa.present;
@@ -829,8 +829,8 @@ fsp_status backward(const void* tokens, int32_t index_bytes, int64_t n, const vo
     if (v == 1 && dim % k == 0 && rows_fit(grad, gs, gd, k) && rows_fit(weight, ws, wd, k)) v = k;
   using B = __nv_bfloat16;
   if (gd == FSP_DTYPE_F32)
-    return wd == FSP_DTYPE_F32 ? launch_rows_v<float, float>(a, v, st) : launch_rows_v<float, B>(a, v, st);
-  return wd == FSP_DTYPE_F32 ? launch_rows_v<B, float>(a, v, st) : launch_rows_v<B, B>(a, v, st);
+    return wd == FSP_DTYPE_F32 ? launch_rows_v<float, float>(sa, a, v, st) : launch_rows_v<float, B>(sa, a, v, st);
+  return wd == FSP_DTYPE_F32 ? launch_rows_v<B, float>(sa, a, v, st) : launch_rows_v<B, B>(sa, a, v, st);
 }
 
 }  // namespace

@@ -132,8 +132,9 @@ fsp_status fsp_embedding_backward_workspace_bytes(int64_t vocab, int64_t dim, in
  *            accumulate keeps its value); negative: none.
  *   workspace: 16-byte aligned, at least ..._workspace_bytes; free for other use
  *            once the stream has passed this call.
- * n_tokens < 2^31 - 16384, vocab < 2^31 - 1, dim <= 2^24.  A token outside [0, vocab) is dropped and sets
- * bit 16 of the device error word. */
+ * n_tokens < 2^31 - 16384, vocab < 2^31 - 1, dim <= 65535 * 32 (four times that where dim, the strides and
+ * the pointers allow accesses of four elements).  A token outside [0, vocab) is dropped and sets bit 16 of the
+ * device error word. */
 fsp_status fsp_embedding_backward(const void* tokens, int32_t index_bytes, int64_t n_tokens, const void* grad_out,
                                   int32_t grad_dtype, int64_t dim, int64_t grad_stride, void* grad_weight,
                                   int32_t weight_dtype, int64_t vocab, int64_t weight_stride, float scale,

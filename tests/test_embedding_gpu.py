@@ -225,3 +225,12 @@ def test_gradient_of_large_tables(tokens, vocab, dim, pad, weight):
     assert bool((got[n == 0] == 0).all()) and int((n == 0).sum()) > 0
     assert bool(buf[:, dim:].isnan().all())
     assert fsp.device_error() == 0
+
+
+def test_a_refused_gradient_launches_nothing():
+    dim = 65535 * 32 + 1   # one more column than the join's grid holds
+    dw = torch.full((1, dim), 2.0, device="cuda")
+    outside = torch.tensor([5], device="cuda")   # what the first launch would report
+    with pytest.raises(fsp.FspError, match="columns"):
+        fsp.embedding_backward(outside, torch.ones(1, dim, device="cuda"), dw)
+    assert fsp.device_error() == 0 and float((dw - 2).abs().max()) == 0
