@@ -234,3 +234,31 @@ def test_a_refused_gradient_launches_nothing():
     with pytest.raises(fsp.FspError, match="columns"):
         fsp.embedding_backward(outside, torch.ones(1, dim, device="cuda"), dw)
     assert fsp.device_error() == 0 and float((dw - 2).abs().max()) == 0
+
+
+# on both sides of what the sort keeps in registers (131072 tokens), in one, two and three passes
+@pytest.mark.parametrize("tokens,vocab,dim,index", [(131072, 70000, 4, 64), (131073, 70000, 4, 32), (131073, 500, 8, 64),
+                                                    (300001, 300000, 4, 32), (300001, 131071, 5, 64), (600000, 3, 1, 32)])
+def test_gradient_of_long_batches(tokens, vocab, dim, index):
+    g = torch.Generator(device="cuda").manual_seed(tokens + vocab)
+    u = torch.rand(tokens, generator=g, device="cuda", dtype=torch.float64)
+    ids = ((vocab + 1.0) ** u - 1).long().clamp_(max=vocab - 1)   # log-uniform: a few tokens hold much of the batch
+    dy = torch.randn(tokens, dim, generator=g, device="cuda")
+    old = torch.randn(vocab, dim, generator=g, device="cuda")
+    add = lambda x: torch.zeros(vocab, dim, device="cuda", dtype=torch.float64).index_add_(0, ids, x * 0.5)  # noqa: E731
+    want, mag = add(dy.double()), add(dy.double().abs())
+    n = torch.bincount(ids, minlength=vocab)
+    # n additions and the scaling, each at most 2^-24 of the magnitudes that enter it; the old value's addition
+    tol = (n[:, None] + 2) * 2.0 ** -24 * mag
+    for accumulate in (False, True):
+        dw = old.clone()
+        fsp.embedding_backward(ids.to(IX[index]), dy, dw, scale=0.5, accumulate=accumulate)
+        right = want + old if accumulate else want
+        assert bool(((dw - right).abs() <= tol + (2.0 ** -24 * right.abs() if accumulate else 0)).all())
+        assert torch.equal(dw[n == 0], old[n == 0] if accumulate else torch.zeros_like(old)[n == 0])
+    # the sums' order: stable, so that a token's rows are added first to last in runs of 32
+    again = torch.empty_like(old)
+    fsp.embedding_backward(ids, dy, again, scale=0.5)
+    first = torch.empty_like(old)
+    fsp.embedding_backward(ids.int(), dy, first, scale=0.5)
+    assert torch.equal(again, first) and fsp.device_error() == 0
