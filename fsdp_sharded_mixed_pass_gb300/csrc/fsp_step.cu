@@ -92,29 +92,35 @@ std::string cuda_msg(const char* what, cudaError_t e) {
   return std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
 }
 
+// A driver function (nullptr: not found).
+template <typename F>
+F driver_function(const char* name) {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q{};
+  if (cudaGetDriverEntryPointByVersion(name, &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<F>(fn);
+}
+
 // Whether [ptr, ptr + bytes) lies inside one live allocation of the driver.
 fsp_status check_allocation(const void* ptr, size_t bytes, const char* name) {
-  static PFN_cuMemGetAddressRange_v3020 get_range = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<PFN_cuMemGetAddressRange_v3020>(nullptr);
-    return reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(fn);
-  }();
-  if (!get_range) return fail(FSP_ECUDA, "cannot resolve cuMemGetAddressRange");
-  // The driver call needs a current context on this thread; a thread that has
-  // made no runtime call yet has none, so bind the current device's primary
-  // context (cudaSetDevice does that, and nothing else, when it is current).
-  // Once per thread: a later change of device binds that device's context itself.
-  static thread_local bool bound = false;
-  if (!bound) {
+  static const auto get_range = driver_function<PFN_cuMemGetAddressRange_v3020>("cuMemGetAddressRange");
+  static const auto get_context = driver_function<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent");
+  if (!get_range || !get_context) return fail(FSP_ECUDA, "cannot resolve cuMemGetAddressRange or cuCtxGetCurrent");
+  // The driver call needs a current context on this thread.  One that has made no
+  // runtime call yet has none, and another library may have taken it away or put its
+  // own there, so unless the context is the one that this bound last, bind the current
+  // device's primary context (cudaSetDevice does that; a change of device changes the
+  // context too).
+  static thread_local CUcontext bound = nullptr;
+  CUcontext now = nullptr;
+  if (!bound || get_context(&now) != CUDA_SUCCESS || now != bound) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaSetDevice(dev);
     if (e != cudaSuccess) return fail(FSP_ECUDA, cuda_msg("binding the device context", e));
-    bound = true;
+    if (get_context(&bound) != CUDA_SUCCESS) bound = nullptr;
   }
   CUdeviceptr base = 0;
   size_t size = 0;
