@@ -1,7 +1,8 @@
 """The operators of ``include/fsp_ops.h`` on torch tensors: AdamW over a list
 of tensors, the embedding with its gradient, and matrices in 8-bit floating
 point.  Argument marshalling and output buffers only; everything is computed by
-the library's kernels, asynchronously on ``stream`` (None: the current one).
+the library's kernels, asynchronously on ``stream`` (None: the current one) and the
+current device, where every tensor of a call has to be.
 """
 from __future__ import annotations
 
@@ -60,27 +61,42 @@ def _ready():
     _CODES.update({torch.float32: _fsp.DTYPES["f32"], torch.bfloat16: _fsp.DTYPES["bf16"]})
     _INDEX.update({torch.int64: 8, torch.int32: 4})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _device = getattr(torch._C, "_cuda_getDevice", None)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
     return _lib
 
 
-def _handle(stream):
-    """The cudaStream_t of a stream argument (None: the current stream)."""
-    if stream is None and _raw_stream is not None and _device is not None:
-        return _raw_stream(_device())
+def _current() -> int:
+    """The current device's index, on which a call's kernels run."""
+    if _torch is None:
+        _ready()
+    return _device()
+
+
+def _on(device: int, x, what: str) -> None:
+    """Refuses a tensor that is not on ``device``: a kernel must not be given another
+    device's memory."""
+    at = x.get_device()
+    if at != device:
+        raise ValueError(f"{what} is not on a CUDA device" if at < 0 else
+                         f"{what} is on cuda:{at}, the current device is cuda:{device}")
+
+
+def _handle(stream, device: int):
+    """The cudaStream_t of a stream argument (None: the current stream of ``device``,
+    the current device)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
     return _fsp._stream_handle(stream)
 
 
-def _dtype(x, what: str) -> int:
-    """The library's code of a CUDA tensor's dtype (fp32 or bf16)."""
-    if _torch is None:
-        _ready()
+def _dtype(x, what: str, device: int) -> int:
+    """The library's code of the dtype (fp32 or bf16) of a tensor on ``device``."""
     code = _CODES.get(x.dtype)
     if code is None:
         raise TypeError(f"{what}: unsupported dtype {x.dtype}")
-    if not x.is_cuda:
-        raise ValueError(f"{what} is not on a CUDA device")
+    if x.get_device() != device:
+        _on(device, x, what)
     return code
 
 
@@ -112,15 +128,13 @@ def _flat(x, features: int, what: str):
     return rows, max(1, features)
 
 
-def _tokens(tokens) -> int:
-    """Bytes per index of a token tensor."""
-    if _torch is None:
-        _ready()
+def _tokens(tokens, device: int) -> int:
+    """Bytes per index of a token tensor on ``device``."""
     size = _INDEX.get(tokens.dtype)
     if size is None:
         raise TypeError(f"tokens: unsupported dtype {tokens.dtype}")
-    if not tokens.is_cuda:
-        raise ValueError("tokens is not on a CUDA device")
+    if tokens.get_device() != device:
+        _on(device, tokens, "tokens")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
     return size
@@ -168,6 +182,7 @@ class TensorAdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         n = len(params)
+        here = _current()
         for i, (p, g, c) in enumerate(zip(params, grads, copies)):
             for x, what in ((p, "param"), (g, "grad"), (c, "copy")):
                 if x is None and what == "copy":
@@ -176,16 +191,18 @@ class TensorAdamW:
                     raise ValueError(f"{what} {i} has {x.numel()} elements, its parameter {p.numel()}")
                 if not x.is_contiguous():
                     raise ValueError(f"{what} {i} must be contiguous")
-            if c is not None and c.dtype != torch.bfloat16:
-                raise TypeError(f"copy {i} must be bf16")
+            if c is not None:
+                if c.dtype != torch.bfloat16:
+                    raise TypeError(f"copy {i} must be bf16")
+                _on(here, c, f"copy {i}")
         self._refs = (params, grads, copies)
         arr = lambda ty, xs: (ty * max(1, n))(*xs)  # noqa: E731
         ptrs = lambda xs: arr(ctypes.c_void_p, [None if x is None else x.data_ptr() for x in xs])  # noqa: E731
         out = ctypes.c_void_p()
         _fsp._check(_fsp.lib().fsp_adamw_list_create(
             n, arr(ctypes.c_int64, [p.numel() for p in params]), ptrs(params),
-            arr(ctypes.c_int32, [_dtype(p, f"param {i}") for i, p in enumerate(params)]), ptrs(grads),
-            arr(ctypes.c_int32, [_dtype(g, f"grad {i}") for i, g in enumerate(grads)]), ptrs(copies),
+            arr(ctypes.c_int32, [_dtype(p, f"param {i}", here) for i, p in enumerate(params)]), ptrs(grads),
+            arr(ctypes.c_int32, [_dtype(g, f"grad {i}", here) for i, g in enumerate(grads)]), ptrs(copies),
             ctypes.byref(out)), "fsp_adamw_list_create")
         self._h = out
         state_len, offsets = ctypes.c_int64(), (ctypes.c_int64 * max(1, n))()
@@ -231,20 +248,23 @@ class TensorAdamW:
                 self.exp_avg_sq_scale.data_ptr())
 
     def step(self, grad_scale=None, stream=None) -> None:
-        if grad_scale is not None and (_dtype(grad_scale, "grad_scale") != 0 or grad_scale.numel() != 1):
+        here = _current()
+        if grad_scale is not None and (_dtype(grad_scale, "grad_scale", here) != 0 or grad_scale.numel() != 1):
             raise ValueError("grad_scale must be one fp32 element")
-        status = (_lib or _ready()).fsp_adamw_list_step(
+        if self._next_t is not None:
+            _on(here, self._next_t, "the update index")
+        status = _lib.fsp_adamw_list_step(
             self._h, 0 if self.state_bits == 32 else 1, *self._states(), ctypes.byref(_fsp._hp(self.hparams)),
             self._t + 1, None if self._next_t is None else self._next_t.data_ptr(), 1,
-            None if grad_scale is None else grad_scale.data_ptr(), _handle(stream))
+            None if grad_scale is None else grad_scale.data_ptr(), _handle(stream, here))
         if status:
             _fsp._check(status, "fsp_adamw_list_step")
         if self._next_t is None:
             self._t += 1   # only once the step was accepted
 
-    def _fp32_states(self, m, v):
+    def _fp32_states(self, m, v, device: int):
         for x, what in ((m, "exp_avg"), (v, "exp_avg_sq")):
-            if _dtype(x, what) != 0 or x.numel() != self.state_len or not x.is_contiguous():
+            if _dtype(x, what, device) != 0 or x.numel() != self.state_len or not x.is_contiguous():
                 raise ValueError(f"{what} must be {self.state_len} contiguous fp32 elements")
         return m.data_ptr(), v.data_ptr()
 
@@ -254,22 +274,24 @@ class TensorAdamW:
         import torch
         if self.state_bits == 32:
             return self.exp_avg, self.exp_avg_sq
+        here = _current()
         m, v = out if out is not None else [_empty((self.state_len,), torch.float32, self.exp_avg.device, stream)
                                             for _ in range(2)]
-        _fsp._check(_fsp.lib().fsp_adamw_list_state_values(self._h, *self._states(), *self._fp32_states(m, v),
-                                                           _handle(stream)), "fsp_adamw_list_state_values")
+        _fsp._check(_fsp.lib().fsp_adamw_list_state_values(self._h, *self._states(), *self._fp32_states(m, v, here),
+                                                           _handle(stream, here)), "fsp_adamw_list_state_values")
         return m, v
 
     def load_state(self, exp_avg, exp_avg_sq, stream=None) -> None:
         """Sets the states from fp32 tensors of ``state_len`` elements."""
-        pm, pv = self._fp32_states(exp_avg, exp_avg_sq)
+        here = _current()
+        pm, pv = self._fp32_states(exp_avg, exp_avg_sq, here)
         if self.state_bits == 32:
             with _on_stream(stream):
                 self.exp_avg.copy_(exp_avg)
                 self.exp_avg_sq.copy_(exp_avg_sq)
             return
         _fsp._check(_fsp.lib().fsp_adamw_list_state_load(self._h, pm, pv, *self._states(),
-                                                         _handle(stream)), "fsp_adamw_list_state_load")
+                                                         _handle(stream, here)), "fsp_adamw_list_state_load")
 
     def close(self):
         if self._h is not None and self._h.value:
@@ -289,8 +311,9 @@ def embedding(weight, tokens, scale: float = 1.0, out=None, out_dtype=None, stre
     """``out[..., :] = scale * weight[tokens[...], :]``, multiplied in fp32 and
     rounded once to ``out_dtype`` (default: the weight's).  A token outside the
     table gives zeros and sets bit 16 of ``device_error()``."""
-    size = _tokens(tokens)
-    code = _dtype(weight, "weight")
+    here = _current()
+    size = _tokens(tokens, here)
+    code = _dtype(weight, "weight", here)
     vocab, dim, stride = _rows(weight, "weight")
     if out is None:
         out = _empty((*tokens.shape, dim), out_dtype or weight.dtype, weight.device, stream)
@@ -300,7 +323,7 @@ def embedding(weight, tokens, scale: float = 1.0, out=None, out_dtype=None, stre
             raise ValueError("out has another shape or dtype")
         out_stride = _flat(out, dim, "out")[1]
     status = _lib.fsp_embedding(weight.data_ptr(), code, vocab, dim, stride, tokens.data_ptr(), size, tokens.numel(),
-                                scale, out.data_ptr(), _dtype(out, "out"), out_stride, _handle(stream))
+                                scale, out.data_ptr(), _dtype(out, "out", here), out_stride, _handle(stream, here))
     if status:
         _fsp._check(status, "fsp_embedding")
     return out
@@ -321,20 +344,24 @@ def embedding_backward(tokens, grad_out, grad_weight, scale: float = 1.0, paddin
     embedding's slice of a rank's main-grad buffer.  ``padding_idx`` gets no
     gradient.  ``workspace``: a device tensor of at least
     ``embedding_backward_workspace_bytes`` bytes (None: allocated here)."""
-    size, n = _tokens(tokens), tokens.numel()
+    here = _current()
+    size, n = _tokens(tokens, here), tokens.numel()
     vocab, dim, stride = _rows(grad_weight, "grad_weight")
     if tuple(grad_out.shape) != (*tokens.shape, dim):
         raise ValueError(f"grad_out must have shape {(*tokens.shape, dim)}")
     grad_stride = _flat(grad_out, dim, "grad_out")[1]
     if padding_idx is not None and not 0 <= padding_idx < vocab:
         raise ValueError("padding_idx is not a row of grad_weight")
-    if workspace is None:
+    grad_code, code = _dtype(grad_out, "grad_out", here), _dtype(grad_weight, "grad_weight", here)
+    if workspace is not None:
+        _on(here, workspace, "workspace")
+    else:
         workspace = _empty(embedding_backward_workspace_bytes(vocab, dim, n), _torch.uint8, grad_weight.device, stream)
     status = _lib.fsp_embedding_backward(
-        tokens.data_ptr(), size, n, grad_out.data_ptr(), _dtype(grad_out, "grad_out"), dim, grad_stride,
-        grad_weight.data_ptr(), _dtype(grad_weight, "grad_weight"), vocab, stride, scale,
+        tokens.data_ptr(), size, n, grad_out.data_ptr(), grad_code, dim, grad_stride,
+        grad_weight.data_ptr(), code, vocab, stride, scale,
         -1 if padding_idx is None else padding_idx, 1 if accumulate else 0, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _handle(stream))
+        workspace.numel() * workspace.element_size(), _handle(stream, here))
     if status:
         _fsp._check(status, "fsp_embedding_backward")
     return grad_weight
@@ -355,8 +382,10 @@ class Fp8Matrix:
 
     def values(self, stream=None):
         """What the codes stand for, as an fp32 tensor."""
+        here = _current()
+        _on(here, self.data, "the matrix")
         out = _empty((self.rows, self.cols), _torch.float32, self.data.device, stream)
-        _fsp._check(_lib.fsp_fp8_values(self.data.data_ptr(), self.rows, self.cols, out.data_ptr(), _handle(stream)),
+        _fsp._check(_lib.fsp_fp8_values(self.data.data_ptr(), self.rows, self.cols, out.data_ptr(), _handle(stream, here)),
                     "fsp_fp8_values")
         return out
 
@@ -366,7 +395,8 @@ def quantize_fp8(x, rows=True, transposed=None, stream=None):
     in one pass: ``rows`` and ``transposed`` are each True (a new ``Fp8Matrix``), an
     ``Fp8Matrix`` to fill, or None / False (not wanted).  Returns the wanted one, or
     the pair."""
-    code = _dtype(x, "x")
+    here = _current()
+    code = _dtype(x, "x", here)
     r, c, stride = _rows(x, "x")
     got = []
     for want, shape in ((rows, (r, c)), (transposed, (c, r))):
@@ -374,11 +404,13 @@ def quantize_fp8(x, rows=True, transposed=None, stream=None):
             want = Fp8Matrix(*shape, device=x.device, stream=stream)
         elif want is False:
             want = None
-        if want is not None and (want.rows, want.cols) != shape:
-            raise ValueError(f"the matrix to fill is {want.rows} x {want.cols}, not {shape[0]} x {shape[1]}")
+        if want is not None:
+            if (want.rows, want.cols) != shape:
+                raise ValueError(f"the matrix to fill is {want.rows} x {want.cols}, not {shape[0]} x {shape[1]}")
+            _on(here, want.data, "the matrix to fill")
         got.append(want)
     _fsp._check(_lib.fsp_fp8_quantize(x.data_ptr(), code, r, c, stride,
-                                      *[None if q is None else q.data.data_ptr() for q in got], _handle(stream)),
+                                      *[None if q is None else q.data.data_ptr() for q in got], _handle(stream, here)),
                 "fsp_fp8_quantize")
     if got[0] is None:
         return got[1]
@@ -390,6 +422,9 @@ def matmul_fp8(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     default) or fp32; ``accumulate`` adds to an fp32 ``out``."""
     if a.cols != b.cols:
         raise ValueError(f"the operands sum over {a.cols} and {b.cols} elements")
+    here = _current()
+    _on(here, a.data, "a")
+    _on(here, b.data, "b")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -398,7 +433,7 @@ def matmul_fp8(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
         raise ValueError("out has another shape or dtype")
     m, n, stride = _rows(out, "out")
     _fsp._check(_lib.fsp_fp8_matmul(a.data.data_ptr(), b.data.data_ptr(), m, n, a.cols, out.data_ptr(),
-                                    _dtype(out, "out"), stride, 1 if accumulate else 0, _handle(stream)),
+                                    _dtype(out, "out", here), stride, 1 if accumulate else 0, _handle(stream, here)),
                 "fsp_fp8_matmul")
     return out
 
@@ -432,7 +467,11 @@ class Fp8Linear:
 
     def forward(self, x, out=None, out_dtype=None, stream=None):
         """``x W^T`` (bf16 unless ``out`` or ``out_dtype`` says fp32)."""
-        code = _dtype(x, "x")
+        here = _current()
+        code = _dtype(x, "x", here)
+        w = self.codes.data
+        if w.get_device() != here:
+            _on(here, w, "the layer's weight")
         rows, stride = _flat(x, self.in_features, "x")
         n = self.out_features
         if out is None:
@@ -443,10 +482,10 @@ class Fp8Linear:
                 raise ValueError("out has another shape or dtype")
             out_stride = _flat(out, n, "out")[1]
         work = self._workspace(rows, 0, x.device, stream)
-        status = _lib.fsp_fp8_linear(x.data_ptr(), code, rows, self.in_features, stride, self.codes.data.data_ptr(), n,
-                                     out.data_ptr(), _dtype(out, "out"), out_stride,
+        status = _lib.fsp_fp8_linear(x.data_ptr(), code, rows, self.in_features, stride, w.data_ptr(), n,
+                                     out.data_ptr(), _dtype(out, "out", here), out_stride,
                                      None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
-                                     _handle(stream))
+                                     _handle(stream, here))
         if status:
             _fsp._check(status, "fsp_fp8_linear")
         return out
@@ -465,6 +504,10 @@ class Fp8Linear:
             raise ValueError("x and grad_out must have as many rows")
         if not need_grad_x and grad_weight is None:
             return None
+        here = _current()
+        x_code, dy_code = _dtype(x, "x", here), _dtype(grad_out, "grad_out", here)
+        w = self.codes_t.data
+        _on(here, w, "the layer's weight")
         dx = dw = None
         dx_stride = dw_stride = max(1, k)
         dx_code = 1
@@ -472,18 +515,17 @@ class Fp8Linear:
             dx = out if out is not None else _empty(x.shape, _torch.bfloat16, x.device, stream)
             if dx.shape != x.shape:
                 raise ValueError("out must have x's shape")
-            dx_stride, dx_code = _flat(dx, k, "out")[1], _dtype(dx, "out")
+            dx_stride, dx_code = _flat(dx, k, "out")[1], _dtype(dx, "out", here)
         if grad_weight is not None:
-            if _dtype(grad_weight, "grad_weight") != 0:
+            if _dtype(grad_weight, "grad_weight", here) != 0:
                 raise TypeError("grad_weight must be fp32")
             if tuple(grad_weight.shape) != (n, k):
                 raise ValueError(f"grad_weight must have shape {(n, k)}")
             dw, dw_stride = grad_weight, _rows(grad_weight, "grad_weight")[2]
         work = self._workspace(rows, 1, x.device, stream)
         _fsp._check(_lib.fsp_fp8_linear_backward(
-            x.data_ptr(), _dtype(x, "x"), stride, grad_out.data_ptr(), _dtype(grad_out, "grad_out"), dy_stride, rows, k,
-            n, self.codes_t.data.data_ptr(), None if dx is None else dx.data_ptr(), dx_code, dx_stride,
-            None if dw is None else dw.data_ptr(), dw_stride, 1 if accumulate else 0,
-            None if work is None else work.data_ptr(), 0 if work is None else work.numel(), _handle(stream)),
+            x.data_ptr(), x_code, stride, grad_out.data_ptr(), dy_code, dy_stride, rows, k, n, w.data_ptr(),
+            None if dx is None else dx.data_ptr(), dx_code, dx_stride, None if dw is None else dw.data_ptr(), dw_stride, 1 if accumulate else 0,
+            None if work is None else work.data_ptr(), 0 if work is None else work.numel(), _handle(stream, here)),
             "fsp_fp8_linear_backward")
         return dx

@@ -187,3 +187,73 @@ def test_embedding_backward_takes_no_more_tokens_than_its_sort_can_count(lib):
     for n in (most + 1, 2 ** 31 - 4098, 2 ** 31 - 1, 2 ** 31):
         assert bytes_of(n) == B.FSP_EUNSUPPORTED, n
         assert _backward(lib, n=n) == B.FSP_EUNSUPPORTED, n
+
+
+# ---- tensors of another device -------------------------------------------------------------
+
+def _refused_elsewhere():
+    """Every tensor argument of the binding's calls, each in turn on another device than
+    the current one.  Host tensors stand in for device 0's (`here`) and device 1's."""
+    import torch
+    import fsdp_sharded_mixed_pass_gb300 as fsp
+
+    class Here(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    class There(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def make(there, name, *shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(There if name == there else Here)
+
+    def matrix(there, name, rows, cols):
+        q = fsp.Fp8Matrix(rows, cols, device="cpu")
+        q.data = make(there, name, q.data.numel(), dtype=torch.uint8)
+        return q
+
+    def layer(there):
+        m = fsp.Fp8Linear.__new__(fsp.Fp8Linear)
+        m.out_features, m.in_features, m.train = 6, 4, True
+        m.codes, m.codes_t = matrix(there, "weight", 6, 4), matrix(there, "weight", 4, 6)
+        return m
+    i64 = torch.int64
+    calls = {
+        "embedding": (("weight", "tokens", "out"), lambda t: fsp.embedding(
+            make(t, "weight", 5, 4), make(t, "tokens", 3, dtype=i64), out=make(t, "out", 3, 4))),
+        "embedding_backward": (("tokens", "grad_out", "grad_weight", "workspace"), lambda t: fsp.embedding_backward(
+            make(t, "tokens", 3, dtype=i64), make(t, "grad_out", 3, 4), make(t, "grad_weight", 5, 4),
+            workspace=make(t, "workspace", 100000, dtype=torch.uint8))),
+        "TensorAdamW": (("param", "grad", "copy"), lambda t: fsp.TensorAdamW(
+            [make(t, "param", 8)], [make(t, "grad", 8)], [make(t, "copy", 8, dtype=torch.bfloat16)])),
+        "quantize_fp8": (("x", "rows", "transposed"), lambda t: fsp.quantize_fp8(
+            make(t, "x", 6, 4), matrix(t, "rows", 6, 4), matrix(t, "transposed", 4, 6))),
+        "matmul_fp8": (("a", "b", "out"), lambda t: fsp.matmul_fp8(
+            matrix(t, "a", 6, 4), matrix(t, "b", 5, 4), out=make(t, "out", 6, 5))),
+        "values": (("matrix",), lambda t: matrix(t, "matrix", 6, 4).values()),
+        "forward": (("x", "weight", "out"), lambda t: layer(t).forward(make(t, "x", 3, 4), out=make(t, "out", 3, 6))),
+        "backward": (("x", "grad_out", "weight", "grad_weight", "out"), lambda t: layer(t).backward(
+            make(t, "x", 3, 4), make(t, "grad_out", 3, 6), make(t, "grad_weight", 6, 4), out=make(t, "out", 3, 4))),
+    }
+    return [(name, arg, call) for name, (args, call) in calls.items() for arg in args]
+
+
+def test_tensors_of_another_device_are_refused(lib, monkeypatch):
+    from fsdp_sharded_mixed_pass_gb300 import ops
+    ops._ready()
+    monkeypatch.setattr(ops, "_device", lambda: 0)
+
+    def launched(*args):
+        raise AssertionError("the library was called")
+    quiet = type("Lib", (), {n: staticmethod(launched) for n in ops.EXPORTS})
+    for n in ("fsp_fp8_bytes", "fsp_fp8_linear_workspace_bytes", "fsp_embedding_backward_workspace_bytes"):
+        setattr(quiet, n, staticmethod(getattr(lib, n)))
+    monkeypatch.setattr(ops, "_lib", quiet)
+    monkeypatch.setattr(ops._fsp, "lib", lambda: quiet)
+    monkeypatch.setattr(ops, "_handle", lambda *a: 0)
+    for name, arg, call in _refused_elsewhere():
+        with pytest.raises(ValueError, match="cuda:1"):
+            call(arg)
+        with pytest.raises(AssertionError, match="was called"):   # all of them here: nothing is refused
+            call(None)
