@@ -161,6 +161,21 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(128 >> 4) << 32 | uint64_t(1) << 46;
 }
 
+// A producer's last stages (it would fill stage s next, with parity `phase`), before the
+// CTA's memory is given back: the commits that free them have arrived - nobody else
+// waits for these, and one still on its way would land in the memory of whatever runs
+// here next - and with them the copies that the products read.  Where a wait runs out,
+// the copies in flight land.
+template <int S>
+__device__ __forceinline__ void wait_last_stages(uint32_t full, uint32_t empty, int s, uint32_t phase) {
+  bool ok = true;
+#pragma unroll 1
+  for (int j = 0; j < S && ok; ++j) ok = mbar_wait(empty + 8 * j, j < s ? phase : phase ^ 1u);   // (a stage never filled: passes)
+#pragma unroll 1
+  for (int j = 0; j < S && !ok; ++j)
+    if (!mbar_wait(full + 8 * j, j < s ? phase : phase ^ 1u)) break;
+}
+
 // ---- the kernel ----------------------------------------------------------------------
 
 constexpr int kMmThreads = 192;
@@ -334,7 +349,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     // ---- producer ----
     int s = 0;
     uint32_t phase = 0;
-    int64_t issued = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const TileAt tile = tile_at(g, t);
@@ -352,13 +366,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
         bulk_load(at_q + s * BN * 128, src_q + int64_t(k) * kTileBytes, BN * 128, bar);
         bulk_load(at_sp + s * 512, src_sp + piece, 512, bar);
         bulk_load(at_sq + s * 512, src_sq + piece, 512, bar);
-        ++issued;
         if (++s == S) s = 0, phase ^= 1u;
       }
     }
-    // the copies in flight land before the CTA's memory is given back
-    for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
-      if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
+    wait_last_stages<S>(full, empty, s, phase);
   } else if (warp == 1) {
     // ---- scales and MMAs ----
     const uint32_t idesc = uint32_t(BN >> 3) << 17 | 1u << 23 | uint32_t(kTileP >> 4) << 24;
@@ -495,6 +506,9 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {   // arrives at `bar
                "h"(uint16_t(3))
                : "memory");
 }
+__device__ __forceinline__ void pair_commit_here(uint32_t bar) {   // ... of this CTA alone
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void pair_scale_copy(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
@@ -571,7 +585,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     // ---- producer: this CTA's 128 rows of each operand ----
     int s = 0;
     uint32_t phase = 0;
-    int64_t issued = 0;
     bool ok = true;
     const int64_t p_tiles = (g.np + 127) >> 7, q_tiles = (g.nq + 127) >> 7;
     for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step) {
@@ -599,12 +612,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           for (int j = 0; j < q_scales; ++j)
             bulk_load(dst + 512 * (1 + j), src_sq + j * g.pieces * kScaleBytes + piece, 512, bar);
         }
-        ++issued;
         if (++s == S) s = 0, phase ^= 1u;
       }
     }
-    for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
-      if (!mbar_wait(full + 8 * uint32_t(i % S), uint32_t(i / S) & 1u)) break;
+    wait_last_stages<S>(full, empty, s, phase);
   } else if (warp == 1 && lane == 0 && rank != 0) {
     // ---- the other CTA: tells the leader what has landed here ----
     int s = 0;
@@ -664,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       if (elect_one()) pair_commit(acc_full + 8 * (n & 1));
       __syncwarp();
     }
-    if (elect_one()) pair_commit(drained);
+    if (elect_one()) pair_commit_here(drained);   // (the other CTA's epilogue and producer wait for the commits to them)
     __syncwarp();
     mbar_wait(drained, 0);
   } else if (warp >= 2) {
@@ -699,7 +710,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   __syncwarp();
   fence_before();
   __syncthreads();
-  cluster_sync_all();   // neither CTA's memory is read or signalled by the other any more
+  // Neither CTA's memory is read or signalled by the other any more: each has waited for
+  // every commit that arrives at its barriers (producer: the stages', epilogue: the
+  // accumulators', leader: drained), and the epilogue's arrivals come before this.
+  cluster_sync_all();
   fence_after();
   if (warp == 1) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");

@@ -270,3 +270,18 @@ def test_few_rows_of_huge_and_tiny_values(rows, out):
         assert rounds_to(got, want, tol).all()
     else:
         assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(257, 7680, 128), (300, 7680, 1), (384, 7700, 640), (700, 3457, 900), (300, 20000, 200)])
+def test_launches_that_follow_pairs_with_an_idle_second_cta(m, n, k):
+    """Tiles of 256 rows whose second half lies past the matrix: that CTA writes nothing
+    and is done as soon as the last sum is, while the next launch waits for its place."""
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    a = torch.randint(-8, 9, (m, k), generator=g, device="cuda").float()
+    b = torch.randint(-8, 9, (n, k), generator=g, device="cuda").float()
+    want = a.double() @ b.double().t()   # 8 bits hold the operands, fp32 the sums: exact
+    qa, qb = fsp.quantize_fp8(a), fsp.quantize_fp8(b)
+    outs = [torch.full((m, n), float("nan"), device="cuda") for _ in range(40)]
+    for y in outs:
+        fsp.matmul_fp8(qa, qb, out=y)
+    assert all(bool((y == want).all()) for y in outs) and fsp.device_error() == 0
