@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cfloat>
@@ -689,13 +690,34 @@ fsp_status resident_pairs(int* pairs) {
   return FSP_OK;
 }
 
+// `n` tiles of `rows` x 128 bytes, one after the other from `base`, as a tensor whose
+// box is a tile.
+fsp_status tile_map(const uint8_t* base, int64_t n, int rows, CUtensorMap* map) {
+  static const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(driver_function("cuTensorMapEncodeTiled"));
+  if (!encode) return fail(FSP_ECUDA, "cannot resolve cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {128, cuuint64_t(rows), cuuint64_t(n)}, strides[2] = {128, cuuint64_t(rows) * 128};
+  const cuuint32_t box[3] = {128, cuuint32_t(rows), 1}, steps[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FSP_OK : fail(FSP_ECUDA, "cuTensorMapEncodeTiled: error " + std::to_string(int(r)));
+}
+
 template <typename T>
 fsp_status launch_pairs_of(const MmArgs& g, cudaStream_t st) {
   int pairs = 0;
-  const fsp_status s = resident_pairs<T>(&pairs);
+  PairArgs a{};
+  a.g = g;
+  const int64_t rows_p = (g.np + 127) / 128, rows_q = (g.nq + 127) / 128;
+  fsp_status s = resident_pairs<T>(&pairs);
+  if (s == FSP_OK && std::max(rows_p, rows_q) * g.blocks > INT32_MAX) s = fail(FSP_EUNSUPPORTED, "the matrix is too large");
+  if (s == FSP_OK) s = tile_map(g.p, rows_p * g.blocks, 128, &a.p);
+  if (s == FSP_OK) s = tile_map(g.q, rows_q * g.blocks, 128, &a.q);
+  if (s == FSP_OK) s = tile_map(g.p + g.p_scales, rows_p * g.pieces, 4, &a.p_scales);
+  if (s == FSP_OK) s = tile_map(g.q + g.q_scales, rows_q * g.pieces, 4, &a.q_scales);
   if (s != FSP_OK) return s;
   const unsigned grid = unsigned(2 * std::min<int64_t>(pairs, g.tiles_p * g.tiles_q));
-  return launch_next(fp8_pair_kernel<T>, dim3(grid), PairCfg::kThreads, PairCfg::kSmem, st, "8-bit product kernel launch", g);
+  return launch_next(fp8_pair_kernel<T>, dim3(grid), PairCfg::kThreads, PairCfg::kSmem, st, "8-bit product kernel launch", a);
 }
 
 fsp_status launch_pairs(MmArgs& g, int32_t dtype, cudaStream_t st) {

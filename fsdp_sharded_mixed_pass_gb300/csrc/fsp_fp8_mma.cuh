@@ -21,12 +21,13 @@
 // and ends its role; the CTA then lets its copies land and frees its memory.
 //
 // Bound: the tensor cores (3.8 PFLOP/s taken as twice the measured bf16 rate), and
-// for short k the epilogue beside them.  Measured: 8192^3 308 us = 3571 TFLOP/s, 8192
-// x 5632 x 2048 64 us = 2947, 4096 x 151936 x 1024 425 us = 3000 (back to back, under
-// the power cap, 500 us).
+// for short k the epilogue beside them.  Measured, launches back to back in a graph:
+// 8192^3 304 us = 3617 TFLOP/s, 8192 x 5632 x 2048 57 us = 3314, 8192 x 2048 x 5632 56 us,
+// 4096 x 151936 x 1024 426-439 us = 2900-2990.
 
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -50,23 +51,35 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// kPair: what is waited for may come from the other CTA of a cluster.
+template <bool kPair>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
   return ok != 0;
 }
 // False once about 2 s have passed.
+template <bool kPair>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   for (uint32_t i = 1; i < (1u << 30); ++i) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<kPair>(bar, parity)) return true;
     if ((i & 255u) == 0) {
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
       if (t - t0 > 2000000000ull) break;
@@ -75,10 +88,11 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   atomicOr(&g_fp8_error, kErrProduct);
   return false;
 }
+template <bool kPair = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < 4; ++i)
-    if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity);
+    if (mbar_try<kPair>(bar, parity)) return true;
+  return mbar_wait_slow<kPair>(bar, parity);
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -165,15 +179,15 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 // CTA's memory is given back: the commits that free them have arrived - nobody else
 // waits for these, and one still on its way would land in the memory of whatever runs
 // here next - and with them the copies that the products read.  Where a wait runs out,
-// the copies in flight land.
-template <int S>
-__device__ __forceinline__ void wait_last_stages(uint32_t full, uint32_t empty, int s, uint32_t phase) {
+// the copies in flight land (`counts`: they count at this CTA's barriers).
+template <int S, bool kPair = false>
+__device__ __forceinline__ void wait_last_stages(uint32_t full, uint32_t empty, int s, uint32_t phase, bool counts = true) {
   bool ok = true;
 #pragma unroll 1
-  for (int j = 0; j < S && ok; ++j) ok = mbar_wait(empty + 8 * j, j < s ? phase : phase ^ 1u);   // (a stage never filled: passes)
+  for (int j = 0; j < S && ok; ++j) ok = mbar_wait<kPair>(empty + 8 * j, j < s ? phase : phase ^ 1u);   // (a stage never filled: passes)
 #pragma unroll 1
-  for (int j = 0; j < S && !ok; ++j)
-    if (!mbar_wait(full + 8 * j, j < s ? phase : phase ^ 1u)) break;
+  for (int j = 0; j < S && !ok && counts; ++j)
+    if (!mbar_wait<kPair>(full + 8 * j, j < s ? phase : phase ^ 1u)) break;
 }
 
 // ---- the kernel ----------------------------------------------------------------------
@@ -471,7 +485,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
 // Large products: two SMs work on one 256 x 256 tile (cta_group::2).  Each CTA
 // loads 128 rows of P and 128 rows of Q, and the tensor cores of both read both
 // halves of Q, so a byte loaded is used for twice as many products.  The leader
-// (rank 0 of the cluster) issues the MMAs of both.
+// (rank 0 of the cluster) issues the MMAs of both.  The copies of both count at the
+// leader's barrier, which tensor copies with cta_group::2 can do (a bulk copy signals
+// its own CTA only): the MMAs then wait for what they read itself, with no thread of
+// the other CTA to pass the word on.  Every wait here acquires at cluster scope.
 //
 // Tensor memory: two accumulators of 256 columns and the scales do not fit into
 // 512 columns, so the accumulators overlap by the scales' 24 columns.  The
@@ -489,17 +506,23 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   return a;
 }
-// Arrives at a barrier of the other CTA.  Relaxed: what it reports is done by the
-// asynchronous proxy (copies that an mbarrier has counted) or ordered by tcgen05
-// fences (reads of tensor memory); no ordinary access has to become visible
-// across the pair, and a release at cluster scope, a fence of every earlier
-// access of the thread, slowed each block of k down (8192^3: 631 us, 429 without).
+// Arrives at a barrier of the other CTA.  Relaxed: what it reports, reads of tensor
+// memory, is ordered by the tcgen05 fences on both sides.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Tile `t` of a map (its box at coordinates 0, 0, t) into this CTA's shared memory; its
+// bytes count at the barrier of the pair's leader.
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int32_t t, uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(t), "r"(leader_bar)
+      : "memory");
 }
 __device__ __forceinline__ void pair_commit(uint32_t bar) {   // arrives at `bar` of both CTAs
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
@@ -540,10 +563,17 @@ struct PairCfg {
   static_assert(kStages >= 5, "stages");
 };
 
+// The operands as tensors of tiles: 128 rows x 128 bytes of codes, 4 x 128 bytes of scales.
+struct PairArgs {
+  MmArgs g;
+  CUtensorMap p, q, p_scales, q_scales;
+};
+
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
-    fp8_pair_kernel(const __grid_constant__ MmArgs g) {
+    fp8_pair_kernel(const __grid_constant__ PairArgs a) {
   using Cfg = PairCfg;
+  const MmArgs& g = a.g;
   constexpr int S = Cfg::kStages;
   extern __shared__ unsigned char raw[];
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -558,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full + 8 * s, rank == 0 ? 2 : 1);   // the leader's: its own copies, and word of the other CTA's
+      mbar_init(full + 8 * s, 1);   // the leader's: both CTAs' copies (the other's is not used)
       mbar_init(empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -581,52 +611,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   const int64_t step = gridDim.x >> 1;
   const int blocks = int(g.blocks);
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---- producer: this CTA's 128 rows of each operand ----
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
     const int64_t p_tiles = (g.np + 127) >> 7, q_tiles = (g.nq + 127) >> 7;
+    const uint32_t leader_full = in_cta(full, 0);
     for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step) {
       const TileAt tile = tile_at(g, t);
-      const int64_t p_tile = tile.p * 2 + rank, q_first = tile.q * 2, q_tile = q_first + rank;
+      const int64_t p_first = tile.p * 2, q_first = tile.q * 2, p_tile = p_first + rank, q_tile = q_first + rank;
       const bool has_p = p_tile < p_tiles, has_q = q_tile < q_tiles;   // rows past the matrices are not loaded
-      const int q_scales = q_first + 1 < q_tiles ? 2 : 1;
-      const uint32_t bytes = uint32_t(has_p ? Cfg::kOperand : 0) + uint32_t(has_q ? Cfg::kOperand : 0);
-      const uint32_t scale_bytes = 512u * uint32_t(q_scales + (has_p ? 1 : 0));
-      const uint8_t* src_p = g.p + p_tile * g.blocks * kTileBytes;
-      const uint8_t* src_q = g.q + q_tile * g.blocks * kTileBytes;
-      const uint8_t* src_sp = g.p + g.p_scales + p_tile * g.pieces * kScaleBytes;
-      const uint8_t* src_sq = g.q + g.q_scales + q_first * g.pieces * kScaleBytes;
+      const uint32_t halves_p = p_first + 1 < p_tiles ? 2 : 1, halves_q = q_first + 1 < q_tiles ? 2 : 1;
+      // both CTAs': codes, and each one's rows of P and all of Q of the scales
+      const uint32_t bytes = (halves_p + halves_q) * uint32_t(Cfg::kOperand);
+      const uint32_t scale_bytes = 512u * (halves_p + 2 * halves_q);
+      const int32_t at_tile_p = int32_t(p_tile * g.blocks), at_tile_q = int32_t(q_tile * g.blocks);
+      const int32_t piece_p = int32_t(p_tile * g.pieces), piece_q = int32_t(q_first * g.pieces);
       for (int k = 0; k < blocks; ++k) {
-        if (!(ok = mbar_wait(empty + 8 * s, phase ^ 1u))) break;
-        const uint32_t bar = full + 8 * s;
+        if (!(ok = mbar_wait<true>(empty + 8 * s, phase ^ 1u))) break;
+        const uint32_t bar = leader_full + 8 * s;
         const bool scales = (k & 3) == 0;
-        mbar_expect(bar, bytes + (scales ? scale_bytes : 0u));
-        if (has_p) bulk_load(at_p + s * Cfg::kOperand, src_p + int64_t(k) * kTileBytes, Cfg::kOperand, bar);
-        if (has_q) bulk_load(at_q + s * Cfg::kOperand, src_q + int64_t(k) * kTileBytes, Cfg::kOperand, bar);
-        if (scales) {
-          const int64_t piece = int64_t(k >> 2) * kScaleBytes;
-          const uint32_t dst = at_s + s * Cfg::kScales;
-          if (has_p) bulk_load(dst, src_sp + piece, 512, bar);
-          for (int j = 0; j < q_scales; ++j)
-            bulk_load(dst + 512 * (1 + j), src_sq + j * g.pieces * kScaleBytes + piece, 512, bar);
+        if (elect_one()) {
+          if (rank == 0) mbar_expect(full + 8 * s, bytes + (scales ? scale_bytes : 0u));
+          if (has_p) pair_load(at_p + s * Cfg::kOperand, &a.p, at_tile_p + k, bar);
+          if (has_q) pair_load(at_q + s * Cfg::kOperand, &a.q, at_tile_q + k, bar);
+          if (scales) {
+            const uint32_t dst = at_s + s * Cfg::kScales;
+            if (has_p) pair_load(dst, &a.p_scales, piece_p + (k >> 2), bar);
+            for (uint32_t j = 0; j < halves_q; ++j)
+              pair_load(dst + 512 * (1 + j), &a.q_scales, piece_q + int32_t(j * g.pieces) + (k >> 2), bar);
+          }
         }
+        __syncwarp();
         if (++s == S) s = 0, phase ^= 1u;
       }
     }
-    wait_last_stages<S>(full, empty, s, phase);
-  } else if (warp == 1 && lane == 0 && rank != 0) {
-    // ---- the other CTA: tells the leader what has landed here ----
-    int s = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step)
-      for (int k = 0; k < blocks; ++k) {
-        if (!(ok = mbar_wait(full + 8 * s, phase))) break;
-        mbar_arrive_at(in_cta(full + 8 * s, 0));
-        if (++s == S) s = 0, phase ^= 1u;
-      }
+    wait_last_stages<S, true>(full, empty, s, phase, rank == 0);
   } else if (warp == 1 && rank == 0) {
     // ---- leader: scales and MMAs of both CTAs ----
     const uint32_t idesc = uint32_t(Cfg::kTile >> 3) << 17 | 1u << 23 | uint32_t(Cfg::kTile >> 4) << 24;
@@ -638,14 +659,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step, ++n) {
       // the columns that this tile's accumulator shares with the one before it have been read
-      if (n > 0 && !(ok = mbar_wait(acc_part + 8 * ((n - 1) & 1), uint32_t((n - 1) >> 1) & 1u))) break;
+      if (n > 0 && !(ok = mbar_wait<true>(acc_part + 8 * ((n - 1) & 1), uint32_t((n - 1) >> 1) & 1u))) break;
       fence_after();
       const uint32_t d = tmem + (n & 1 ? Cfg::kSecond : 0);
       uint32_t sp = 0;
       for (int k = 0; k < blocks; ++k) {
-        if (!(ok = mbar_wait(full + 8 * s, phase))) break;
+        if (!(ok = mbar_wait<true>(full + 8 * s, phase))) break;
         if ((k & 3) == 0) {
-          if (group >= 2 && !(ok = mbar_wait(group & 1 ? bar1 : bar0, group & 1 ? par1 : par0))) break;
+          if (group >= 2 && !(ok = mbar_wait<true>(group & 1 ? bar1 : bar0, group & 1 ? par1 : par0))) break;
           sp = tmem + Cfg::kScaleBase + (group & 1) * Cfg::kScaleCols;
         }
         fence_after();
@@ -677,7 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     }
     if (elect_one()) pair_commit_here(drained);   // (the other CTA's epilogue and producer wait for the commits to them)
     __syncwarp();
-    mbar_wait(drained, 0);
+    mbar_wait<true>(drained, 0);
   } else if (warp >= 2) {
     // ---- epilogue: this CTA's 128 rows ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;   // rows; alternate blocks of 64 columns
@@ -686,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     for (int64_t t = blockIdx.x >> 1; t < tiles; t += step, ++n) {
       const TileAt tile = tile_at(g, t);
       const int buf = n & 1;
-      if (!mbar_wait(acc_full + 8 * buf, uint32_t(n >> 1) & 1u)) break;
+      if (!mbar_wait<true>(acc_full + 8 * buf, uint32_t(n >> 1) & 1u)) break;
       fence_after();
       const uint32_t d = tmem + (buf ? Cfg::kSecond : 0) + (uint32_t(quarter * 32) << 16);
       const int64_t p0 = tile.p * Cfg::kTile + rank * 128 + quarter * 32, q0 = tile.q * Cfg::kTile;

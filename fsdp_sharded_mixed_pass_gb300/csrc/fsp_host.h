@@ -60,6 +60,8 @@ fsp_status advance_step(int64_t* step_dev, void* stream);
 // Allows a kernel its dynamic shared memory, and with `wide_cluster` clusters of
 // more than eight CTAs, on the current device (once per kernel and device).
 fsp_status allow_kernel(const void* fn, int smem, bool wide_cluster = false);
+// A function of the driver by its name (nullptr: not found).
+void* driver_function(const char* name);
 // SMs of the current device.
 fsp_status sm_count(int* sms);
 // Reads and clears the error bits of the embedding kernels (their part of the

@@ -92,21 +92,19 @@ std::string cuda_msg(const char* what, cudaError_t e) {
   return std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
 }
 
-// A driver function (nullptr: not found).
-template <typename F>
-F driver_function(const char* name) {
+void* driver_function(const char* name) {
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q{};
   if (cudaGetDriverEntryPointByVersion(name, &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
       q != cudaDriverEntryPointSuccess)
     return nullptr;
-  return reinterpret_cast<F>(fn);
+  return fn;
 }
 
 // Whether [ptr, ptr + bytes) lies inside one live allocation of the driver.
 fsp_status check_allocation(const void* ptr, size_t bytes, const char* name) {
-  static const auto get_range = driver_function<PFN_cuMemGetAddressRange_v3020>("cuMemGetAddressRange");
-  static const auto get_context = driver_function<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent");
+  static const auto get_range = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(driver_function("cuMemGetAddressRange"));
+  static const auto get_context = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_function("cuCtxGetCurrent"));
   if (!get_range || !get_context) return fail(FSP_ECUDA, "cannot resolve cuMemGetAddressRange or cuCtxGetCurrent");
   // The driver call needs a current context on this thread.  One that has made no
   // runtime call yet has none, and another library may have taken it away or put its

@@ -285,3 +285,18 @@ def test_launches_that_follow_pairs_with_an_idle_second_cta(m, n, k):
     for y in outs:
         fsp.matmul_fp8(qa, qb, out=y)
     assert all(bool((y == want).all()) for y in outs) and fsp.device_error() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 2600, 4100), (4099, 3001, 1030), (256, 40000, 8200)])
+def test_pairs_read_what_both_ctas_copied(m, n, k):
+    """Many rounds of the ring of stages, on operands written just before, each launch on
+    others: a stage read before either CTA's copies have landed shows the last ones."""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    y = torch.empty(m, n, device="cuda")
+    for _ in range(8):
+        a = torch.randint(-8, 9, (m, k), generator=g, device="cuda").float()
+        b = torch.randint(-8, 9, (n, k), generator=g, device="cuda").float()
+        fsp.matmul_fp8(fsp.quantize_fp8(a), fsp.quantize_fp8(b), out=y)
+        # 8 bits hold the operands, fp32 the sums (below 64 x 8200): exact
+        assert torch.equal(y, (a.double() @ b.double().t()).float())
+    assert fsp.device_error() == 0
