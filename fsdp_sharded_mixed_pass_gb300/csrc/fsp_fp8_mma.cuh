@@ -22,8 +22,8 @@
 //
 // Bound: the tensor cores (3.8 PFLOP/s taken as twice the measured bf16 rate), and
 // for short k the epilogue beside them.  Measured, launches back to back in a graph:
-// 8192^3 304 us = 3617 TFLOP/s, 8192 x 5632 x 2048 57 us = 3314, 8192 x 2048 x 5632 56 us,
-// 4096 x 151936 x 1024 426-439 us = 2900-2990.
+// 8192^3 307 us = 3582 TFLOP/s, 8192 x 5632 x 2048 59 us = 3203, 8192 x 2048 x 5632 57 us,
+// 4096 x 151936 x 1024 440-457 us = 2790-2900.
 
 #pragma once
 
@@ -74,12 +74,11 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // False once about 2 s have passed.
-template <bool kPair>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   for (uint32_t i = 1; i < (1u << 30); ++i) {
-    if (mbar_try<kPair>(bar, parity)) return true;
+    if (mbar_try<false>(bar, parity)) return true;
     if ((i & 255u) == 0) {
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
       if (t - t0 > 2000000000ull) break;
@@ -88,11 +87,32 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   atomicOr(&g_fp8_error, kErrProduct);
   return false;
 }
-template <bool kPair = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < 4; ++i)
-    if (mbar_try<kPair>(bar, parity)) return true;
-  return mbar_wait_slow<kPair>(bar, parity);
+    if (mbar_try<false>(bar, parity)) return true;
+  return mbar_wait_slow<false>(bar, parity);
+}
+// The same by a whole warp, whose lanes agree on whether it ran out (what they do next
+// elects one of them).
+template <bool kPair>
+__device__ __noinline__ bool mbar_wait_slow_all(uint32_t bar, uint32_t parity) {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (__all_sync(0xffffffffu, mbar_try<kPair>(bar, parity))) return true;
+    if ((i & 255u) == 0) {
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (__any_sync(0xffffffffu, t - t0 > 2000000000ull)) break;
+    }
+  }
+  if ((threadIdx.x & 31) == 0) atomicOr(&g_fp8_error, kErrProduct);
+  return false;
+}
+template <bool kPair = false>
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
+  bool ok = false;
+  for (int i = 0; i < 4 && !ok; ++i) ok = mbar_try<kPair>(bar, parity);
+  return __all_sync(0xffffffffu, ok) || mbar_wait_slow_all<kPair>(bar, parity);
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -179,15 +199,17 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 // CTA's memory is given back: the commits that free them have arrived - nobody else
 // waits for these, and one still on its way would land in the memory of whatever runs
 // here next - and with them the copies that the products read.  Where a wait runs out,
-// the copies in flight land (`counts`: they count at this CTA's barriers).
+// the copies in flight land (`counts`: they count at this CTA's barriers).  kPair: by a
+// whole warp of a pair's CTA, else by one thread.
 template <int S, bool kPair = false>
 __device__ __forceinline__ void wait_last_stages(uint32_t full, uint32_t empty, int s, uint32_t phase, bool counts = true) {
+  auto wait = [](uint32_t bar, uint32_t parity) { return kPair ? mbar_wait_all<true>(bar, parity) : mbar_wait(bar, parity); };
   bool ok = true;
 #pragma unroll 1
-  for (int j = 0; j < S && ok; ++j) ok = mbar_wait<kPair>(empty + 8 * j, j < s ? phase : phase ^ 1u);   // (a stage never filled: passes)
+  for (int j = 0; j < S && ok; ++j) ok = wait(empty + 8 * j, j < s ? phase : phase ^ 1u);   // (a stage never filled: passes)
 #pragma unroll 1
   for (int j = 0; j < S && !ok && counts; ++j)
-    if (!mbar_wait<kPair>(full + 8 * j, j < s ? phase : phase ^ 1u)) break;
+    if (!wait(full + 8 * j, j < s ? phase : phase ^ 1u)) break;
 }
 
 // ---- the kernel ----------------------------------------------------------------------
@@ -394,11 +416,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     bool ok = true;
     for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const uint32_t sq_shift = uint32_t((tile_at(g, t).q * BN) & 127) / 32;   // columns of the scales before q0
-      if (!(ok = mbar_wait(acc_empty + 8 * buf, acc_phase ^ 1u))) break;
+      if (!(ok = mbar_wait_all(acc_empty + 8 * buf, acc_phase ^ 1u))) break;
       fence_after();
       const uint32_t d = tmem + buf * Cfg::kAccCols;
       for (int k = 0; k < blocks; ++k) {
-        if (!(ok = mbar_wait(full + 8 * s, phase))) break;
+        if (!(ok = mbar_wait_all(full + 8 * s, phase))) break;
         fence_after();
         const uint32_t sp = tmem + Cfg::kScaleBase + s * Cfg::kScaleCols, sq = sp + 4;
         const uint32_t id = idesc | uint32_t(k & 3) << 4 | uint32_t(k & 3) << 29;   // which byte of a row's four
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     }
     if (elect_one()) mma_commit(drained);   // nothing issued here runs on when the tensor memory is given back
     __syncwarp();
-    mbar_wait(drained, 0);
+    mbar_wait_all(drained, 0);
   } else if (warp >= 2) {
     // ---- epilogue ----
     const int quarter = warp & 3;   // the tensor memory lanes this warp may read
@@ -429,7 +451,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_product_kernel(const __grid
     uint32_t phase = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
       const TileAt tile = tile_at(g, t);
-      if (!mbar_wait(acc_full + 8 * buf, phase)) break;
+      if (!mbar_wait_all(acc_full + 8 * buf, phase)) break;
       fence_after();
       const uint32_t d = tmem + buf * Cfg::kAccCols + (uint32_t(quarter * 32) << 16);
       const int64_t p0 = tile.p * kTileP + quarter * 32, q0 = tile.q * BN;
@@ -629,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       const int32_t at_tile_p = int32_t(p_tile * g.blocks), at_tile_q = int32_t(q_tile * g.blocks);
       const int32_t piece_p = int32_t(p_tile * g.pieces), piece_q = int32_t(q_first * g.pieces);
       for (int k = 0; k < blocks; ++k) {
-        if (!(ok = mbar_wait<true>(empty + 8 * s, phase ^ 1u))) break;
+        if (!(ok = mbar_wait_all<true>(empty + 8 * s, phase ^ 1u))) break;
         const uint32_t bar = leader_full + 8 * s;
         const bool scales = (k & 3) == 0;
         if (elect_one()) {
@@ -659,14 +681,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += step, ++n) {
       // the columns that this tile's accumulator shares with the one before it have been read
-      if (n > 0 && !(ok = mbar_wait<true>(acc_part + 8 * ((n - 1) & 1), uint32_t((n - 1) >> 1) & 1u))) break;
+      if (n > 0 && !(ok = mbar_wait_all<true>(acc_part + 8 * ((n - 1) & 1), uint32_t((n - 1) >> 1) & 1u))) break;
       fence_after();
       const uint32_t d = tmem + (n & 1 ? Cfg::kSecond : 0);
       uint32_t sp = 0;
       for (int k = 0; k < blocks; ++k) {
-        if (!(ok = mbar_wait<true>(full + 8 * s, phase))) break;
+        if (!(ok = mbar_wait_all<true>(full + 8 * s, phase))) break;
         if ((k & 3) == 0) {
-          if (group >= 2 && !(ok = mbar_wait<true>(group & 1 ? bar1 : bar0, group & 1 ? par1 : par0))) break;
+          if (group >= 2 && !(ok = mbar_wait_all<true>(group & 1 ? bar1 : bar0, group & 1 ? par1 : par0))) break;
           sp = tmem + Cfg::kScaleBase + (group & 1) * Cfg::kScaleCols;
         }
         fence_after();
@@ -698,7 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     }
     if (elect_one()) pair_commit_here(drained);   // (the other CTA's epilogue and producer wait for the commits to them)
     __syncwarp();
-    mbar_wait<true>(drained, 0);
+    mbar_wait_all<true>(drained, 0);
   } else if (warp >= 2) {
     // ---- epilogue: this CTA's 128 rows ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;   // rows; alternate blocks of 64 columns
@@ -707,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     for (int64_t t = blockIdx.x >> 1; t < tiles; t += step, ++n) {
       const TileAt tile = tile_at(g, t);
       const int buf = n & 1;
-      if (!mbar_wait<true>(acc_full + 8 * buf, uint32_t(n >> 1) & 1u)) break;
+      if (!mbar_wait_all<true>(acc_full + 8 * buf, uint32_t(n >> 1) & 1u)) break;
       fence_after();
       const uint32_t d = tmem + (buf ? Cfg::kSecond : 0) + (uint32_t(quarter * 32) << 16);
       const int64_t p0 = tile.p * Cfg::kTile + rank * 128 + quarter * 32, q0 = tile.q * Cfg::kTile;
