@@ -459,6 +459,17 @@ __device__ __forceinline__ void stage_store4(unsigned char* base, bool bf16, int
     *reinterpret_cast<float4*>(base + 4 * i) = f;
 }
 
+// mbar_wait by a whole warp, whose lanes agree on whether it ran out.
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255u) == 0 && __any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) return false;
+  }
+  return false;
+}
+
 // One block of a stage, in place.
 template <bool k8Bit>
 __device__ __forceinline__ void update_stage(const ListArgs& a, const ListTile& t, const Coeffs& c, float coef, int begin,
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(co
     int ends = 0;
     while (true) {
       const ListTile later = fetch(number());
-      if (!mbar_wait(empty + 8 * s, phase ^ 1u)) {
+      if (!mbar_wait_all(empty + 8 * s, phase ^ 1u)) {   // (the lanes agree: they go on as a warp)
         if (lane == 0) atomicOr(&g_fsp_device_error, kErrProducerWait);
         break;
       }
@@ -661,7 +672,7 @@ __global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(co
     int s = team;
     uint32_t phase = 0;
     while (true) {
-      if (!mbar_wait(full + 8 * s, phase)) {
+      if (!mbar_wait_all(full + 8 * s, phase)) {
         if (lane == 0) atomicOr(&g_fsp_device_error, kErrConsumerWait);
         break;
       }
