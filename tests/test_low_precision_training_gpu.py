@@ -73,3 +73,59 @@ def test_gradients_against_the_same_model_in_64_bits():
     for k, g in model.grads.items():
         got = g.cpu().numpy().astype(np.float64)
         assert np.linalg.norm(got - want[k]) < 2.0 ** -7 * np.linalg.norm(want[k]), k
+
+
+@pytest.mark.parametrize("mode", ["fsdp2", "distopt"])
+def test_the_operators_between_sharded_steps(mode):
+    """Two ranks' training steps on the buffers of the sharded update: the embedding and
+    the 8-bit layers read what the step gathered, their gradients (two micro-batches, the
+    second accumulated) go into the ranks' main-grad buffers, and the step averages those.
+    Beside it AdamW over the list of the same tensors, given the averaged gradients."""
+    vocab, dim, hidden, ranks = 257, 64, 96, 2
+    shapes = [(vocab, dim), (hidden, dim), (vocab, hidden)]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    opt = fsp.ShardedAdamW(shapes, ranks, mode=mode, lr=3e-3, betas=(0.9, 0.95), weight_decay=0.01)
+    cut = lambda buf: [buf[o:o + r * c].view(r, c) for o, (r, c) in zip(opt.plan.param_offsets, shapes)]  # noqa: E731
+    zeros = lambda dt: torch.zeros(opt.plan.full_len_padded, dtype=dt, device="cuda")  # noqa: E731
+    params, grads, full = [zeros(torch.bfloat16) for _ in range(ranks)], [zeros(torch.float32) for _ in range(ranks)], zeros(torch.float32)
+    for w in cut(full):
+        w.copy_(torch.randn(w.shape, generator=gen, device="cuda") * w.shape[1] ** -0.5)
+    opt.load_full(full)
+    opt.unshard(params)
+    mean = [torch.zeros(s, device="cuda") for s in shapes]
+    copies = [w.clone() for w in cut(params[0])]
+    listed = fsp.TensorAdamW([w.clone() for w in cut(full)], mean, copies, lr=3e-3, betas=(0.9, 0.95), weight_decay=0.01)
+    layers = [(fsp.Fp8Linear(cut(p)[1], train=True), fsp.Fp8Linear(cut(p)[2], train=True)) for p in params]
+    successor = torch.randperm(vocab, generator=gen, device="cuda")
+    losses = []
+    for _ in range(60):
+        total = 0.0
+        for q in range(ranks):
+            (table, w_up, w_head), (g_table, g_up, g_head), (up, head) = cut(params[q]), cut(grads[q]), layers[q]
+            up.update(w_up)
+            head.update(w_head)
+            for micro in range(2):
+                tokens = torch.randint(0, vocab, (300,), generator=gen, device="cuda")
+                x = fsp.embedding(table, tokens, scale=dim ** 0.5)
+                pre = up.forward(x)
+                act = torch.relu(pre)
+                logits = head.forward(act, out_dtype=torch.float32)
+                log_p = logits - logits.logsumexp(-1, keepdim=True)
+                rows = torch.arange(300, device="cuda")
+                total = total - log_p[rows, successor[tokens]].mean() / (2 * ranks)
+                d = log_p.exp_()
+                d[rows, successor[tokens]] -= 1
+                d_act = head.backward(act, (d / 600).bfloat16(), g_head, accumulate=micro > 0)
+                d_x = up.backward(x, torch.where(pre > 0, d_act, torch.zeros_like(d_act)), g_up, accumulate=micro > 0)
+                fsp.embedding_backward(tokens, d_x, g_table, scale=dim ** 0.5, accumulate=micro > 0)
+        losses.append(total)
+        for m, a, b in zip(mean, cut(grads[0]), cut(grads[1])):
+            torch.add(a, b, out=m).mul_(0.5)
+        opt.step(grads, params)
+        listed.step()
+        for q in range(ranks):   # every rank's gathered copy: the list's, bit for bit
+            for w, c in zip(cut(params[q]), copies):
+                assert torch.equal(w, c)
+    # uniform guessing over 257 tokens costs ln 257 = 5.5; a learnt table nothing
+    assert losses[0] > 5 and losses[-1] < 1
+    assert fsp.device_error() == 0
