@@ -267,13 +267,16 @@ __device__ __forceinline__ void adamw_coarse(float2 g, float2& p, float2& m, flo
   p = __ffma2_rn(p, both(c.decay_hi), __fmul2_rn(u, both(-c.step_hi)));
 }
 
-// Thread 0 of block 0 reports a device-resident update index below 1 (taken as 1).
-__device__ __forceinline__ void report_step_index(const ListArgs& a) {
-  if (a.step_dev && threadIdx.x == 0 && blockIdx.x == 0 && *a.step_dev < 1) atomicOr(&g_fsp_device_error, kErrStepIndex);
-}
+// The update's scalars.  Thread 0 of block 0 reports a device-resident update index
+// below 1 (taken as 1): here, or where it does not come here (kReport false) on its own.
+template <bool kReport>
 __device__ __forceinline__ Coeffs list_coeffs(const ListArgs& a) {
   if (!a.step_dev) return a.c;
-  const int64_t t = max(*a.step_dev, int64_t(1));
+  int64_t t = *a.step_dev;
+  if (t < 1) {
+    if (kReport && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_fsp_device_error, kErrStepIndex);
+    t = 1;
+  }
   Coeffs c = a.c;
   bias_scalars(c, a.lr, t);
   return c;
@@ -380,10 +383,9 @@ __global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int begin = warp * kListBlock;   // this warp's block in the tile
   if (begin >= tile.len) return;
-  report_step_index(a);
   ListBlock b;
   load_block<k8Bit>(a, tile, begin, lane, b);
-  update_block<k8Bit>(a, tile, list_coeffs(a), a.grad_scale ? *a.grad_scale : 1.f, begin, lane, b);
+  update_block<k8Bit>(a, tile, list_coeffs<true>(a), a.grad_scale ? *a.grad_scale : 1.f, begin, lane, b);
 }
 
 // ---- long lists: a ring of stages in shared memory ---------------------------------
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(co
     }
     fence_mbar_init();
   }
-  report_step_index(a);
+  if (threadIdx.x == 0 && blockIdx.x == 0 && a.step_dev && *a.step_dev < 1) atomicOr(&g_fsp_device_error, kErrStepIndex);
   __syncthreads();
 
   if (warp == 0) {
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(Ring<k8Bit>::kThreads, 1) adamw_ring_kernel(co
     // ---- consumers: team k takes stages k, k + kTeams, ... ----
     const int team = (warp - 2) / kTeamWarps, begin = (warp - 2) % kTeamWarps * kListBlock;
     const float coef = a.grad_scale ? *a.grad_scale : 1.f;
-    const Coeffs c = list_coeffs(a);
+    const Coeffs c = list_coeffs<false>(a);
     int s = team;
     uint32_t phase = 0;
     while (true) {
