@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kListThreads, k8Bit ? 5 : 4) adamw_list_kernel
 // gets an empty stage, and the team does it from global memory.
 //
 // Measured (GB300): fp32 states, bf16 gradients and copies, 360.7 M elements 1442 us
-// = 7.0 TB/s (one CTA per tile 1640-1730); 8-bit states, 541.1 M elements 1426 us =
+// = 7.0 TB/s (one CTA per tile 1640-1730); 8-bit states, 541.1 M elements 1434 us =
 // 6.1 TB/s (2000).
 
 constexpr int kTeamWarps = kListTile / kListBlock;

@@ -751,9 +751,9 @@ fsp_status matmul_checked(const void* a, const void* b, int64_t m, int64_t n, in
   if (m <= 64) return launch_product<64, true>(g, dtype, st);
   if (m <= 128) return launch_product<128, true>(g, dtype, st);
   // The narrowest tiles that give every SM at most one: a product too small to fill
-  // the pairs spreads over more SMs (1024 x 2048 x 2048: tiles of 128 10.5 us, pairs
-  // 12.3; 333 x 1001 x 777: tiles of 64 12.3, of 128 15.5, pairs 18.5), a larger one
-  // gains from them (2048 x 2048 x 2048: pairs 12.4, tiles of 128 16.4).
+  // the pairs spreads over more SMs (1024 x 2048 x 2048: tiles of 128 8.0 us, pairs
+  // 8.7; 333 x 1001 x 777: tiles of 64 5.0, of 128 6.1, pairs 7.5), a larger one
+  // gains from them (2048 x 2048 x 2048: pairs 9.3, tiles of 128 13.2).
   int sms = 0;
   const fsp_status s = sm_count(&sms);
   if (s != FSP_OK) return s;

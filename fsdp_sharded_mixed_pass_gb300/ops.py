@@ -310,7 +310,8 @@ class TensorAdamW:
 def embedding(weight, tokens, scale: float = 1.0, out=None, out_dtype=None, stream=None):
     """``out[..., :] = scale * weight[tokens[...], :]``, multiplied in fp32 and
     rounded once to ``out_dtype`` (default: the weight's).  A token outside the
-    table gives zeros and sets bit 16 of ``device_error()``."""
+    table gives zeros and sets bit 16 of ``device_error()``.  Nothing is recorded for
+    autograd: the gradient is ``embedding_backward``'s."""
     here = _current()
     size = _tokens(tokens, here)
     code = _dtype(weight, "weight", here)
@@ -445,7 +446,8 @@ class Fp8Linear:
 
     ``Fp8Linear(weight)`` lays the out x in weight out for ``forward``; with
     ``train=True`` for ``backward`` too.  ``update(weight)`` does so again after an
-    optimizer step.
+    optimizer step.  Nothing is recorded for autograd: the gradients are
+    ``backward``'s.
     """
 
     def __init__(self, weight, train: bool = False, stream=None):
