@@ -710,7 +710,7 @@ fsp_status launch_pairs_of(const MmArgs& g, cudaStream_t st) {
   a.g = g;
   const int64_t rows_p = (g.np + 127) / 128, rows_q = (g.nq + 127) / 128;
   fsp_status s = resident_pairs<T>(&pairs);
-  if (s == FSP_OK && std::max(rows_p, rows_q) * g.blocks > INT32_MAX) s = fail(FSP_EUNSUPPORTED, "the matrix is too large");
+  // (tile numbers fit 32 bits: 2^31 tiles of 16 KB are more than any device holds)
   if (s == FSP_OK) s = tile_map(g.p, rows_p * g.blocks, 128, &a.p);
   if (s == FSP_OK) s = tile_map(g.q, rows_q * g.blocks, 128, &a.q);
   if (s == FSP_OK) s = tile_map(g.p + g.p_scales, rows_p * g.pieces, 4, &a.p_scales);

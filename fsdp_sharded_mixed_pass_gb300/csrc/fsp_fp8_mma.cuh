@@ -90,7 +90,7 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < 4; ++i)
     if (mbar_try<false>(bar, parity)) return true;
-  return mbar_wait_slow<false>(bar, parity);
+  return mbar_wait_slow(bar, parity);
 }
 // The same by a whole warp, whose lanes agree on whether it ran out (what they do next
 // elects one of them).

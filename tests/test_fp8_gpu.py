@@ -300,3 +300,18 @@ def test_pairs_read_what_both_ctas_copied(m, n, k):
         # 8 bits hold the operands, fp32 the sums (below 64 x 8200): exact
         assert torch.equal(y, (a.double() @ b.double().t()).float())
     assert fsp.device_error() == 0
+
+
+@pytest.mark.parametrize("m,n", [(64, 64), (200, 130)])
+def test_waits_of_milliseconds(m, n):
+    """One tile's sum over four million terms: its readers wait for it far longer than
+    one attempt of the hardware's does."""
+    k = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(m)
+    a = torch.randint(-1, 2, (m, k), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    b = torch.randint(-1, 2, (n, k), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    y = fsp.matmul_fp8(fsp.quantize_fp8(a), fsp.quantize_fp8(b), out_dtype=torch.float32)
+    want = torch.zeros(m, n, device="cuda")
+    for c in range(0, k, 1 << 18):   # (each part, and their sum, is a whole number below 2^24)
+        want += a[:, c:c + (1 << 18)].float() @ b[:, c:c + (1 << 18)].float().t()
+    assert torch.equal(y, want) and fsp.device_error() == 0
