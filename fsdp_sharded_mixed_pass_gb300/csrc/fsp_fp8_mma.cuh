@@ -22,8 +22,8 @@
 //
 // Bound: the tensor cores (3.8 PFLOP/s taken as twice the measured bf16 rate), and
 // for short k the epilogue beside them.  Measured, launches back to back in a graph:
-// 8192^3 307 us = 3582 TFLOP/s, 8192 x 5632 x 2048 59 us = 3203, 8192 x 2048 x 5632 57 us,
-// 4096 x 151936 x 1024 440-457 us = 2790-2900.
+// 8192^3 304-313 us = 3510-3620 TFLOP/s (box to box), 8192 x 5632 x 2048 58.6 us = 3225,
+// 8192 x 2048 x 5632 57 us, 4096 x 151936 x 1024 431-445 us = 2860-2960.
 
 #pragma once
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return mbar_wait_slow(bar, parity);
 }
 // The same by a whole warp, whose lanes agree on whether it ran out (what they do next
-// elects one of them).
+// elects one of them, or wants them all).
 template <bool kPair>
 __device__ __noinline__ bool mbar_wait_slow_all(uint32_t bar, uint32_t parity) {
   uint64_t t0, t;
@@ -110,9 +110,8 @@ __device__ __noinline__ bool mbar_wait_slow_all(uint32_t bar, uint32_t parity) {
 }
 template <bool kPair = false>
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
-  bool ok = false;
-  for (int i = 0; i < 4 && !ok; ++i) ok = mbar_try<kPair>(bar, parity);
-  return __all_sync(0xffffffffu, ok) || mbar_wait_slow_all<kPair>(bar, parity);
+  if (__all_sync(0xffffffffu, mbar_try<kPair>(bar, parity))) return true;
+  return mbar_wait_slow_all<kPair>(bar, parity);
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
