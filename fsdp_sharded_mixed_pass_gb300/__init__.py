@@ -5,8 +5,9 @@ one GPU: rank-ordered fp32 reduce-scatter averaged by N_d, AdamW on the fp32
 master / m / v shard, bf16 cast and all-gather into every rank's param buffer,
 fused into one streaming CUDA kernel behind the C ABI in ``include/fsp.h``.
 Beside it (``include/fsp_ops.h``): AdamW over a list of tensors with 32- or
-8-bit states, the embedding with its gradient, and linear layers on 8-bit
-floating-point operands.
+8-bit states, the embedding with its gradient, linear layers on 8-bit
+floating-point operands, layer norm with its gradients, dropout and rotary
+positions.
 
     from fsdp_sharded_mixed_pass_gb300 import plan_layout, sharded_step
 """
@@ -42,10 +43,16 @@ from .ops import (  # noqa: F401,E402
     EXPORTS as _OPS_EXPORTS,
     Fp8Linear,
     Fp8Matrix,
+    Rotary,
     TensorAdamW,
+    dropout,
+    dropout_backward,
     embedding,
     embedding_backward,
     embedding_backward_workspace_bytes,
+    layer_norm,
+    layer_norm_backward,
+    layer_norm_backward_workspace_bytes,
     matmul_fp8,
     quantize_fp8,
 )

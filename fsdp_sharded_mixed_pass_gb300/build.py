@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfsp.so")
 SOURCES = ("fsp_plan.cpp", "fsp_step.cu", "fsp_host.cu", "fsp_unshard.cu", "fsp_params.cu",
-           "fsp_adamw.cpp", "fsp_embedding.cu", "fsp_fp8.cu")
+           "fsp_adamw.cpp", "fsp_embedding.cu", "fsp_fp8.cu", "fsp_layer_norm.cu", "fsp_dropout.cu", "fsp_rotary.cu")
 ARCH = ("-gencode", "arch=compute_103a,code=sm_103a")
 
 

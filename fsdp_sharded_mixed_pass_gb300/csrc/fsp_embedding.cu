@@ -20,15 +20,10 @@
 // Zeros into the rows that no token names (not when accumulating) are written by
 // other CTAs of 2 or 3.
 #include <cooperative_groups.h>
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
 
 #include <algorithm>
-#include <string>
 
-#include "fsp_host.h"
-#include "fsp_internal.h"
-#include "fsp_ops.h"
+#include "fsp_rows.cuh"
 
 namespace fsp {
 namespace {
@@ -37,13 +32,6 @@ namespace cg = cooperative_groups;
 
 constexpr unsigned kErrToken = 16u;   // a token outside [0, vocab)
 __device__ unsigned int g_token_error = 0;
-
-// Programmatic dependent launch: let the next launch on the stream that allows
-// it be scheduled; wait until the launches this grid depends on have completed.
-// Loads after the wait are ordinary or volatile ones: what a compiler takes for a
-// load of constant memory (__ldg and the like) it may move ahead of the wait.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // From L2: written by another CTA of this grid.
 __device__ __forceinline__ uint32_t load_l2(const uint32_t* p) {
@@ -55,70 +43,6 @@ __device__ __forceinline__ uint2 load_l2(const uint2* p) {
   uint2 x;
   asm volatile("ld.global.cg.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p) : "memory");
   return x;
-}
-
-// ---- element access -----------------------------------------------------------
-
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T narrow(float x);
-template <>
-__device__ __forceinline__ float narrow<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-
-// V elements at p as one access of V * sizeof(T) bytes (4 to 32; p aligned to
-// that), or element by element for V = 1.  32 bytes are one access of a whole sector:
-// as two of 16 bytes, a warp's stores half-filled every sector twice.
-template <typename T, int V>
-__device__ __forceinline__ void load_raw(const T* p, T* x) {
-  constexpr int kBytes = int(sizeof(T)) * V;
-  uint32_t* w = reinterpret_cast<uint32_t*>(x);
-  if constexpr (V == 1) {
-    x[0] = p[0];
-  } else if constexpr (kBytes == 32) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-        : "l"(p));
-  } else if constexpr (kBytes == 16) {
-    *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
-  } else {
-    static_assert(kBytes == 8);
-    *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(p);
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float* f) {
-  alignas(32) T x[V];
-  load_raw<T, V>(p, x);
-#pragma unroll
-  for (int j = 0; j < V; ++j) f[j] = widen(x[j]);
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float* f) {
-  constexpr int kBytes = int(sizeof(T)) * V;
-  alignas(32) T t[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) t[j] = narrow<T>(f[j]);
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(t);
-  if constexpr (V == 1) {
-    p[0] = t[0];
-  } else if constexpr (kBytes == 32) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else if constexpr (kBytes == 16) {
-    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(t));
-  } else {
-    static_assert(kBytes == 8);
-    __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(t));
-  }
 }
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, int index_bytes, int64_t i) {
@@ -600,26 +524,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_rows_kernel(const __grid_co
 
 // ---- host ----------------------------------------------------------------------------
 
-size_t size_of(int32_t dtype) { return dtype == FSP_DTYPE_F32 ? 4 : 2; }
-bool known(int32_t dtype) { return dtype == FSP_DTYPE_F32 || dtype == FSP_DTYPE_BF16; }
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-
-// Bytes from a matrix's first to past its last element.
-size_t span_bytes(int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
-  return rows > 0 && cols > 0 ? (size_t(rows - 1) * size_t(stride) + size_t(cols)) * size_of(dtype) : 0;
-}
-
-fsp_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t stride, int32_t dtype, const char* name) {
-  if (!known(dtype)) return fail(FSP_EINVAL, std::string("unknown dtype of ") + name);
-  if (stride < cols || (rows > 0 && stride > (int64_t(1) << 58) / rows))
-    return fail(FSP_EINVAL, std::string(name) + "'s rows overlap or their stride is out of range");
-  const size_t bytes = span_bytes(rows, cols, stride, dtype);
-  if (!bytes) return FSP_OK;
-  if (!p) return fail(FSP_EINVAL, std::string(name) + " is NULL");
-  if (reinterpret_cast<uintptr_t>(p) % size_of(dtype)) return fail(FSP_EINVAL, std::string(name) + " is not aligned to its elements");
-  return check_allocation(p, bytes, name);
-}
-
 fsp_status check_tokens(const void* tokens, int32_t index_bytes, int64_t n) {
   if (index_bytes != 4 && index_bytes != 8) return fail(FSP_EINVAL, "index_bytes must be 4 or 8");
   if (n < 0 || n > (int64_t(1) << 58)) return fail(FSP_EINVAL, "n_tokens is out of range");
@@ -627,39 +531,6 @@ fsp_status check_tokens(const void* tokens, int32_t index_bytes, int64_t n) {
   if (!tokens) return fail(FSP_EINVAL, "tokens is NULL");
   if (reinterpret_cast<uintptr_t>(tokens) % size_t(index_bytes)) return fail(FSP_EINVAL, "tokens is not aligned to its elements");
   return check_allocation(tokens, size_t(n) * size_t(index_bytes), "tokens");
-}
-
-bool overlap(const void* p, size_t pb, const void* q, size_t qb) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return pb && qb && a < b + qb && b < a + pb;
-}
-
-// Whether rows of V elements may be accessed as vectors.
-bool rows_fit(const void* p, int64_t stride, int32_t dtype, int v) {
-  const size_t bytes = size_t(v) * size_of(dtype);
-  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && size_t(stride) * size_of(dtype) % bytes == 0;
-}
-
-// Launches with programmatic stream serialisation (every kernel here waits for the
-// launch before it ahead of its first access), a cluster of `cluster` CTAs.
-template <typename A>
-fsp_status launch_next(void (*kernel)(A), dim3 grid, int threads, size_t smem, int cluster, const A& args, cudaStream_t st,
-                       const char* what) {
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(cluster);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
-  return e == cudaSuccess ? FSP_OK : fail(FSP_ECUDA, cuda_msg(what, e));
 }
 
 template <typename W, typename O>

@@ -1,0 +1,398 @@
+// Layer norm and its gradients (sm_103a).
+//
+//   m = mean x (0 if not centred), r = 1 / sqrt(mean (x - m)^2 + eps), h = (x - m) r, y = h w + b
+//   g = dy w,  dx = r (g - mean g (0 if not centred) - h mean(g h)) + add
+//   dw (+)= sum over rows of dy h,  db (+)= sum over rows of dy
+//
+// Bound: HBM (about 7 operations an element forward, 14 backward).
+#include <algorithm>
+
+#include "fsp_rows.cuh"
+
+namespace fsp {
+namespace {
+
+constexpr int64_t kMostDim = int64_t(1) << 20;   // a thread of the widest rows adds 1024 elements
+constexpr int kParts = 152;                      // most partial sums of the weight's gradient: one per SM
+
+__device__ __forceinline__ float load_any(const void* p, bool f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : widen(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+template <int V>
+__device__ __forceinline__ void store_any(void* p, bool f32, int64_t i, const float* f) {
+  if (f32)
+    store_vec<float, V>(static_cast<float*>(p) + i, f);
+  else
+    store_vec<__nv_bfloat16, V>(static_cast<__nv_bfloat16*>(p) + i, f);
+}
+
+struct NormArgs {
+  const void* x;
+  const void* weight;   // NULL: ones
+  const void* bias;     // NULL: zeros
+  void* out;
+  float2* stats;        // (m, r) of each row, or NULL
+  int64_t rows, dim, x_stride, out_stride;
+  float eps;
+  bool center, param_f32, out_f32;
+};
+
+struct GradArgs {
+  const void* x;
+  const float2* stats;
+  const void* grad;
+  const void* weight;   // NULL: ones
+  const void* add;      // NULL: zeros
+  void* grad_x;         // NULL: not wanted
+  float* parts;         // [kParts][2][dim]
+  void* grad_weight;    // NULL: not wanted
+  void* grad_bias;
+  int64_t rows, dim, x_stride, grad_stride, add_stride, grad_x_stride;
+  int n_parts;
+  bool center, weight_f32, grad_param_f32, accumulate;
+};
+
+// The sums over the CTA of N values per thread, in every thread.
+template <int N>
+__device__ __forceinline__ void cta_sum(float (&v)[N], float (*share)[N]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+    if (lane == 0) share[warp][j] = v[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    v[j] = lane < int(blockDim.x >> 5) ? share[lane][j] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+  }
+  __syncthreads();
+}
+
+// ---- rows of any length: a CTA per row, which reads it again for each pass ------------
+
+constexpr int kWideThreads = 1024;
+
+template <typename X, int V>
+__global__ void __launch_bounds__(kWideThreads) wide_norm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float share[32][1];
+  launch_dependents();
+  grid_dependency_wait();
+  const int64_t row = blockIdx.x, first = int64_t(threadIdx.x) * V, step = int64_t(blockDim.x) * V;
+  const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
+  float f[V], m = 0.f, s[1];
+  if (a.center) {
+    s[0] = 0.f;
+    for (int64_t c = first; c < a.dim; c += step) {
+      load_vec<X, V>(x + c, f);
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) t += f[j];
+      s[0] += t;
+    }
+    cta_sum<1>(s, share);
+    m = s[0] / float(a.dim);
+  }
+  s[0] = 0.f;
+  for (int64_t c = first; c < a.dim; c += step) {
+    load_vec<X, V>(x + c, f);
+    float t = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) t = __fmaf_rn(f[j] - m, f[j] - m, t);
+    s[0] += t;
+  }
+  cta_sum<1>(s, share);
+  const float r = 1.f / sqrtf(s[0] / float(a.dim) + a.eps);
+  if (a.stats && threadIdx.x == 0) a.stats[row] = make_float2(m, r);
+  for (int64_t c = first; c < a.dim; c += step) {
+    load_vec<X, V>(x + c, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float h = (f[j] - m) * r;
+      f[j] = __fmaf_rn(h, a.weight ? load_any(a.weight, a.param_f32, c + j) : 1.f,
+                       a.bias ? load_any(a.bias, a.param_f32, c + j) : 0.f);
+    }
+    store_any<V>(a.out, a.out_f32, row * a.out_stride + c, f);
+  }
+}
+
+template <typename X, typename G, int V>
+__global__ void __launch_bounds__(kWideThreads) wide_grad_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ float share[32][2];
+  launch_dependents();
+  grid_dependency_wait();
+  const int64_t row = blockIdx.x, first = int64_t(threadIdx.x) * V, step = int64_t(blockDim.x) * V;
+  const X* x = static_cast<const X*>(a.x) + row * a.x_stride;
+  const G* dy = static_cast<const G*>(a.grad) + row * a.grad_stride;
+  const float2 st = a.stats[row];
+  float h[V], g[V], s[2] = {0.f, 0.f};
+  auto load = [&](int64_t c) {
+    load_vec<X, V>(x + c, h);
+    load_vec<G, V>(dy + c, g);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      h[j] = (h[j] - st.x) * st.y;
+      if (a.weight) g[j] *= load_any(a.weight, a.weight_f32, c + j);
+    }
+  };
+  for (int64_t c = first; c < a.dim; c += step) {
+    load(c);
+    float t = 0.f, u = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      t += g[j];
+      u = __fmaf_rn(g[j], h[j], u);
+    }
+    s[0] += t;
+    s[1] += u;
+  }
+  cta_sum<2>(s, share);
+  const float mean_g = a.center ? s[0] / float(a.dim) : 0.f, mean_gh = s[1] / float(a.dim);
+  for (int64_t c = first; c < a.dim; c += step) {
+    load(c);
+    float add[V] = {};
+    if (a.add) load_vec<X, V>(static_cast<const X*>(a.add) + row * a.add_stride + c, add);
+#pragma unroll
+    for (int j = 0; j < V; ++j) g[j] = __fmaf_rn(st.y, g[j] - mean_g - h[j] * mean_gh, add[j]);
+    store_vec<X, V>(static_cast<X*>(a.grad_x) + row * a.grad_x_stride + c, g);
+  }
+}
+
+// The weight's and the bias's gradient: part p of the rows, 32 x V columns a CTA.
+constexpr int kColumnWarps = 8;
+
+template <typename X, typename G, int V>
+__global__ void __launch_bounds__(kColumnWarps * 32) column_sums_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ float share[kColumnWarps][2][32 * V];
+  launch_dependents();
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t col = (int64_t(blockIdx.x) * 32 + lane) * V;
+  const int64_t begin = a.rows * blockIdx.y / a.n_parts, end = a.rows * (blockIdx.y + 1) / a.n_parts;
+  float dw[V] = {}, db[V] = {};
+  if (col < a.dim)
+    for (int64_t row = begin + warp; row < end; row += kColumnWarps) {
+      float h[V], g[V];
+      load_vec<X, V>(static_cast<const X*>(a.x) + row * a.x_stride + col, h);
+      load_vec<G, V>(static_cast<const G*>(a.grad) + row * a.grad_stride + col, g);
+      const float2 st = a.stats[row];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        dw[j] = __fmaf_rn(g[j], (h[j] - st.x) * st.y, dw[j]);
+        db[j] += g[j];
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    share[warp][0][j * 32 + lane] = dw[j];
+    share[warp][1][j * 32 + lane] = db[j];
+  }
+  __syncthreads();
+  if (warp < 2 && col < a.dim) {
+    float sum[V] = {};
+    for (int w = 0; w < kColumnWarps; ++w)
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] += share[w][warp][j * 32 + lane];
+    store_vec<float, V>(a.parts + (int64_t(blockIdx.y) * 2 + warp) * a.dim + col, sum);
+  }
+}
+
+// Adds the parts, 32 columns of one of the two gradients a CTA; warp w adds parts w, w + 8, ...
+__global__ void __launch_bounds__(kColumnWarps * 32) join_columns_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ float share[kColumnWarps][32];
+  launch_dependents();
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  void* out = blockIdx.y == 0 ? a.grad_weight : a.grad_bias;
+  if (!out) return;
+  const int64_t col = int64_t(blockIdx.x) * 32 + lane;
+  float sum = 0.f;
+  if (col < a.dim)
+    for (int p = warp; p < a.n_parts; p += kColumnWarps) sum += a.parts[(int64_t(p) * 2 + blockIdx.y) * a.dim + col];
+  share[warp][lane] = sum;
+  __syncthreads();
+  if (warp > 0 || col >= a.dim) return;
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kColumnWarps; ++w) sum += share[w][lane];
+  if (a.accumulate) sum += load_any(out, a.grad_param_f32, col);
+  store_any<1>(out, a.grad_param_f32, col, &sum);
+}
+
+// ---- host -----------------------------------------------------------------------------
+
+fsp_status check_sizes(int64_t rows, int64_t dim) {
+  if (rows < 0 || dim < 0) return fail(FSP_EINVAL, "rows and dim must be >= 0");
+  if (dim > kMostDim) return fail(FSP_EUNSUPPORTED, "dim must be at most 2^20");
+  if (rows > INT32_MAX) return fail(FSP_EUNSUPPORTED, "rows must be below 2^31");
+  return FSP_OK;
+}
+
+fsp_status check_vector(const void* p, int64_t dim, int32_t dtype, const char* name) {
+  return p ? check_form(p, 1, dim, std::max<int64_t>(1, dim), dtype, name) : FSP_OK;
+}
+Operand vector_operand(const void* p, int64_t dim, int32_t dtype, const char* name) {
+  return {p, p ? size_t(dim) * size_of(dtype) : 0, name};
+}
+
+fsp_status check_stats(const float* stats) {
+  return reinterpret_cast<uintptr_t>(stats) % 8 ? fail(FSP_EINVAL, "stats is not 8-byte aligned") : FSP_OK;
+}
+
+fsp_status norm(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs, const void* weight, const void* bias,
+                int32_t pd, float eps, int32_t center, void* out, int32_t od, int64_t os, float* stats, void* stream) {
+  fsp_status s = check_sizes(rows, dim);
+  if (s != FSP_OK) return s;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return fail(FSP_EINVAL, "eps must be finite and >= 0");
+  if ((weight || bias) && !known(pd)) return fail(FSP_EINVAL, "unknown dtype of the parameters");
+  s = check_form(x, rows, dim, xs, xd, "x");
+  if (s == FSP_OK) s = check_vector(weight, dim, pd, "weight");
+  if (s == FSP_OK) s = check_vector(bias, dim, pd, "bias");
+  if (s == FSP_OK) s = check_form(out, rows, dim, os, od, "out");
+  if (s == FSP_OK) s = check_stats(stats);
+  if (s != FSP_OK || rows == 0 || dim == 0) return s;
+  const Operand outs[] = {rows_operand(out, rows, dim, os, od, "out"), {stats, stats ? size_t(rows) * 8 : 0, "stats"}};
+  const Operand ins[] = {rows_operand(x, rows, dim, xs, xd, "x"), vector_operand(weight, dim, pd, "weight"),
+                         vector_operand(bias, dim, pd, "bias")};
+  s = check_operands(outs, 2, ins, 3);
+  if (s != FSP_OK) return s;
+  NormArgs a{x, weight, bias, out, reinterpret_cast<float2*>(stats), rows, dim, xs, os, eps, center != 0, pd == FSP_DTYPE_F32, od == FSP_DTYPE_F32};
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(out, os, od, 8);
+  using B = __nv_bfloat16;
+  const int threads = int(std::min<int64_t>(kWideThreads, (dim / (vec ? 8 : 1) + 31) / 32 * 32));
+  void (*kernel)(NormArgs) = xd == FSP_DTYPE_F32 ? (vec ? wide_norm_kernel<float, 8> : wide_norm_kernel<float, 1>)
+                                                  : (vec ? wide_norm_kernel<B, 8> : wide_norm_kernel<B, 1>);
+  return launch_next(kernel, dim3(unsigned(rows)), std::max(32, threads), 0, 1, a, st, "layer norm kernel launch");
+}
+
+int64_t parts_of(int64_t rows) { return std::min<int64_t>(kParts, rows); }
+size_t workspace_of(int64_t rows, int64_t dim) { return size_t(parts_of(rows)) * 2 * size_t(dim) * 4 + 256; }   // (from a multiple of 256)
+
+template <typename X, typename G, int V>
+fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
+  fsp_status s = FSP_OK;
+  if (a.grad_weight || a.grad_bias) {   // (first: grad_x may take the place of x or grad_out)
+    const dim3 grid(unsigned((a.dim + 32 * V - 1) / (32 * V)), unsigned(a.n_parts));
+    if (a.rows > 0)
+      s = launch_next(column_sums_kernel<X, G, V>, grid, kColumnWarps * 32, 0, 1, a, st, "layer norm gradient (columns) kernel launch");
+    if (s == FSP_OK)
+      s = launch_next(join_columns_kernel, dim3(unsigned((a.dim + 31) / 32), 2), kColumnWarps * 32, 0, 1, a, st,
+                      "layer norm gradient (join) kernel launch");
+  }
+  if (s != FSP_OK || !a.grad_x || a.rows == 0) return s;
+  const int threads = int(std::min<int64_t>(kWideThreads, (a.dim / V + 31) / 32 * 32));
+  return launch_next(wide_grad_kernel<X, G, V>, dim3(unsigned(a.rows)), std::max(32, threads), 0, 1, a, st,
+                     "layer norm gradient kernel launch");
+}
+
+template <typename X, typename G>
+fsp_status launch_grad_v(const GradArgs& a, bool vec, cudaStream_t st) {
+  return vec ? launch_grad<X, G, 8>(a, st) : launch_grad<X, G, 1>(a, st);
+}
+
+fsp_status backward(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs, const float* stats, int32_t center,
+                    const void* grad, int32_t gd, int64_t gs, const void* weight, int32_t wd, const void* add, int64_t as,
+                    void* grad_x, int64_t ds, void* grad_weight, void* grad_bias, int32_t pd, int32_t accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  fsp_status s = check_sizes(rows, dim);
+  if (s != FSP_OK) return s;
+  const bool columns = grad_weight || grad_bias;
+  if (weight && !known(wd)) return fail(FSP_EINVAL, "unknown dtype of weight");
+  if (columns && !known(pd)) return fail(FSP_EINVAL, "unknown dtype of the parameters' gradients");
+  if (add && !grad_x) return fail(FSP_EINVAL, "add needs grad_x");
+  s = check_form(x, rows, dim, xs, xd, "x");
+  if (s == FSP_OK) s = check_form(grad, rows, dim, gs, gd, "grad_out");
+  if (s == FSP_OK && rows > 0 && dim > 0 && !stats) s = fail(FSP_EINVAL, "stats is NULL");
+  if (s == FSP_OK) s = check_stats(stats);
+  if (s == FSP_OK) s = check_vector(weight, dim, wd, "weight");
+  if (s == FSP_OK && add) s = check_form(add, rows, dim, as, xd, "add");
+  if (s == FSP_OK && grad_x) s = check_form(grad_x, rows, dim, ds, xd, "grad_x");
+  if (s == FSP_OK) s = check_vector(grad_weight, dim, pd, "grad_weight");
+  if (s == FSP_OK) s = check_vector(grad_bias, dim, pd, "grad_bias");
+  if (s != FSP_OK) return s;
+  if (dim == 0 || (!grad_x && !columns) || (rows == 0 && (!columns || accumulate))) return FSP_OK;
+  const size_t need = columns && rows > 0 ? workspace_of(rows, dim) : 0;
+  if (need) {
+    if (!workspace) return fail(FSP_EINVAL, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return fail(FSP_EINVAL, "workspace is not 16-byte aligned");
+    if (workspace_bytes < need) return fail(FSP_EINVAL, "workspace is smaller than fsp_layer_norm_backward_workspace_bytes");
+  }
+  const Operand outs[] = {rows_operand(grad_x, rows, dim, ds, xd, "grad_x"),
+                          vector_operand(grad_weight, dim, pd, "grad_weight"),
+                          vector_operand(grad_bias, dim, pd, "grad_bias"), {workspace, need, "workspace"}};
+  const Operand ins[] = {rows_operand(x, rows, dim, xs, xd, "x"), rows_operand(grad, rows, dim, gs, gd, "grad_out"),
+                         rows_operand(add, rows, dim, as, xd, "add"), vector_operand(weight, dim, wd, "weight"),
+                         {stats, size_t(rows) * 8, "stats"}};
+  s = check_operands(outs, 4, ins, 5);
+  if (s != FSP_OK) return s;
+  GradArgs a{};
+  a.x = x;
+  a.stats = reinterpret_cast<const float2*>(stats);
+  a.grad = grad;
+  a.weight = weight;
+  a.add = add;
+  a.grad_x = grad_x;
+  a.parts = reinterpret_cast<float*>(round256(reinterpret_cast<uintptr_t>(workspace)));
+  a.grad_weight = grad_weight;
+  a.grad_bias = grad_bias;
+  a.rows = rows;
+  a.dim = dim;
+  a.x_stride = xs;
+  a.grad_stride = gs;
+  a.add_stride = as;
+  a.grad_x_stride = ds;
+  a.n_parts = int(parts_of(rows));
+  a.center = center != 0;
+  a.weight_f32 = wd == FSP_DTYPE_F32;
+  a.grad_param_f32 = pd == FSP_DTYPE_F32;
+  a.accumulate = accumulate != 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(grad, gs, gd, 8) && (!add || rows_fit(add, as, xd, 8)) &&
+                   (!grad_x || rows_fit(grad_x, ds, xd, 8));
+  using B = __nv_bfloat16;
+  if (xd == FSP_DTYPE_F32)
+    return gd == FSP_DTYPE_F32 ? launch_grad_v<float, float>(a, vec, st) : launch_grad_v<float, B>(a, vec, st);
+  return gd == FSP_DTYPE_F32 ? launch_grad_v<B, float>(a, vec, st) : launch_grad_v<B, B>(a, vec, st);
+}
+
+}  // namespace
+}  // namespace fsp
+
+extern "C" fsp_status fsp_layer_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                                     const void* weight, const void* bias, int32_t param_dtype, float eps, int32_t center,
+                                     void* out, int32_t out_dtype, int64_t out_stride, float* stats, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::norm(x, x_dtype, rows, dim, x_stride, weight, bias, param_dtype, eps, center, out, out_dtype, out_stride,
+                     stats, cuda_stream);
+  });
+}
+
+extern "C" fsp_status fsp_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim, size_t* bytes) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    if (!bytes) return fsp::fail(FSP_EINVAL, "bytes is NULL");
+    const fsp_status s = fsp::check_sizes(rows, dim);
+    if (s == FSP_OK) *bytes = fsp::workspace_of(rows, dim);
+    return s;
+  });
+}
+
+extern "C" fsp_status fsp_layer_norm_backward(const void* x, int32_t x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                                              const float* stats, int32_t center, const void* grad_out,
+                                              int32_t grad_dtype, int64_t grad_stride, const void* weight,
+                                              int32_t weight_dtype, const void* add, int64_t add_stride, void* grad_x,
+                                              int64_t grad_x_stride, void* grad_weight, void* grad_bias,
+                                              int32_t grad_param_dtype, int32_t accumulate, void* workspace,
+                                              size_t workspace_bytes, void* cuda_stream) {
+  return fsp::guard([&]() -> fsp_status {
+    fsp::clear_error();
+    return fsp::backward(x, x_dtype, rows, dim, x_stride, stats, center, grad_out, grad_dtype, grad_stride, weight,
+                         weight_dtype, add, add_stride, grad_x, grad_x_stride, grad_weight, grad_bias, grad_param_dtype,
+                         accumulate, workspace, workspace_bytes, cuda_stream);
+  });
+}

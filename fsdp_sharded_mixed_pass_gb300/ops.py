@@ -1,12 +1,13 @@
 """The operators of ``include/fsp_ops.h`` on torch tensors: AdamW over a list
-of tensors, the embedding with its gradient, and matrices in 8-bit floating
-point.  Argument marshalling and output buffers only; everything is computed by
+of tensors, the embedding with its gradient, matrices in 8-bit floating point,
+layer norm with its gradients, dropout and rotary positions.  Argument marshalling and output buffers only; everything is computed by
 the library's kernels, asynchronously on ``stream`` (None: the current one) and the
 current device, where every tensor of a call has to be.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 
 from . import fsp as _fsp
 from .optim import _on_stream
@@ -17,7 +18,13 @@ EXPORTS = ("fsp_adamw_list_create", "fsp_adamw_list_info", "fsp_adamw_list_destr
            "fsp_adamw_list_state_values", "fsp_adamw_list_state_load", "fsp_embedding",
            "fsp_embedding_backward_workspace_bytes", "fsp_embedding_backward", "fsp_fp8_bytes", "fsp_fp8_quantize",
            "fsp_fp8_values", "fsp_fp8_matmul", "fsp_fp8_linear", "fsp_fp8_linear_backward",
-           "fsp_fp8_linear_workspace_bytes")
+           "fsp_fp8_linear_workspace_bytes", "fsp_layer_norm", "fsp_layer_norm_backward_workspace_bytes",
+           "fsp_layer_norm_backward", "fsp_dropout", "fsp_rotary_phases", "fsp_rotary")
+
+
+class _RotaryTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("x_strides", ctypes.c_int64 * 3), ("out_strides", ctypes.c_int64 * 3)]
 
 
 def bind(L) -> None:
@@ -42,6 +49,13 @@ def bind(L) -> None:
         "fsp_fp8_linear_backward": [vp, i32, i64, vp, i32, i64, i64, i64, i64, vp, vp, i32, i64, vp, i64, i32, vp, size,
                                     vp],
         "fsp_fp8_linear_workspace_bytes": [i64, i64, i64, i32, P(size)],
+        "fsp_layer_norm": [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, i32, i64, vp, vp],
+        "fsp_layer_norm_backward_workspace_bytes": [i64, i64, P(size)],
+        "fsp_layer_norm_backward": [vp, i32, i64, i64, i64, vp, i32, vp, i32, i64, vp, i32, vp, i64, vp, i64, vp, vp, i32,
+                                    i32, vp, size, vp],
+        "fsp_dropout": [vp, i32, i64, i64, i64, ctypes.c_double, ctypes.c_uint64, i64, vp, vp, i32, i64, vp, i32, i64, vp],
+        "fsp_rotary_phases": [P(ctypes.c_double), i64, P(ctypes.c_uint64)],
+        "fsp_rotary": [P(_RotaryTensor), i32, i32, i64, i64, vp, i32, i64, vp, i64, i32, f32, i32, vp],
     }.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -531,3 +545,310 @@ class Fp8Linear:
             None if work is None else work.data_ptr(), 0 if work is None else work.numel(), _handle(stream, here)),
             "fsp_fp8_linear_backward")
         return dx
+
+
+# ---- layer norm ------------------------------------------------------------------------
+
+def _param(x, dim: int, what: str, device: int) -> int:
+    """The library's code of a parameter's dtype, a vector of ``dim`` adjacent elements."""
+    code = _dtype(x, what, device)
+    if tuple(x.shape) != (dim,) or (dim > 1 and x.stride(0) != 1):
+        raise ValueError(f"{what} must be {dim} adjacent elements")
+    return code
+
+
+def _pair(x, y, what: str, dim: int, device: int):
+    """The one dtype code of two parameters, each of which may be None."""
+    codes = [_param(t, dim, name, device) for t, name in zip((x, y), what.split()) if t is not None]
+    if len(set(codes)) > 1:
+        raise TypeError(f"{what.replace(' ', ' and ')} must have the same dtype")
+    return codes[0] if codes else 0
+
+
+def _like(out, x, what: str, dtype):
+    """Checks a buffer given for a result of x's shape."""
+    if out.shape != x.shape or (dtype is not None and out.dtype != dtype):
+        raise ValueError(f"{what} has another shape or dtype")
+
+
+def _stats(stats, x, device: int):
+    """Checks the (mean, 1 / deviation) pairs of x's rows."""
+    if _dtype(stats, "stats", device) != 0 or tuple(stats.shape) != (*x.shape[:-1], 2) or not stats.is_contiguous():
+        raise ValueError(f"stats must be contiguous fp32 of shape {(*x.shape[:-1], 2)}")
+    return stats.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, out=None, out_dtype=None, stats=None,
+               stream=None):
+    """``(x - m) / sqrt(mean((x - m)^2) + eps) * weight + bias`` over the last dimension,
+    ``m`` its mean, or 0 with ``center=False`` (the norm by the root mean square); in
+    fp32, rounded once to ``out_dtype`` (default: x's).  ``out`` may be ``x``.
+
+    ``stats``: True (a new tensor), an fp32 tensor of shape ``(*x.shape[:-1], 2)`` to fill,
+    or None; with it the call returns ``(out, stats)``, what ``layer_norm_backward``
+    reads.  Nothing is recorded for autograd."""
+    here = _current()
+    code = _dtype(x, "x", here)
+    dim = x.shape[-1] if x.dim() else 0
+    rows, stride = _flat(x, dim, "x")
+    param = _pair(weight, bias, "weight bias", dim, here)
+    if out is None:
+        out = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
+        out_stride = max(1, dim)
+    else:
+        _like(out, x, "out", out_dtype)
+        out_stride = _flat(out, dim, "out")[1]
+    if stats is True:
+        stats = _empty((*x.shape[:-1], 2), _torch.float32, x.device, stream)
+    elif stats is False:
+        stats = None
+    status = _lib.fsp_layer_norm(x.data_ptr(), code, rows, dim, stride, None if weight is None else weight.data_ptr(),
+                                 None if bias is None else bias.data_ptr(), param, eps, 1 if center else 0,
+                                 out.data_ptr(), _dtype(out, "out", here), out_stride,
+                                 None if stats is None else _stats(stats, x, here), _handle(stream, here))
+    if status:
+        _fsp._check(status, "fsp_layer_norm")
+    return out if stats is None else (out, stats)
+
+
+def layer_norm_backward_workspace_bytes(rows: int, dim: int) -> int:
+    """Device workspace bytes ``layer_norm_backward`` needs for the parameters' gradients."""
+    out = ctypes.c_size_t(0)
+    _fsp._check((_lib or _ready()).fsp_layer_norm_backward_workspace_bytes(rows, dim, ctypes.byref(out)),
+                "fsp_layer_norm_backward_workspace_bytes")
+    return out.value
+
+
+def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, grad_weight=None, grad_bias=None,
+                        accumulate: bool = False, need_grad_x: bool = True, add=None, out=None, workspace=None,
+                        stream=None):
+    """The gradient of x (x's dtype, or ``out``'s buffer) from the forward pass's ``x``,
+    ``stats`` and ``center``; ``add``, a tensor like x (the residual stream's gradient), is
+    added to it.  ``grad_weight`` and ``grad_bias`` (fp32 or bf16, where given) receive
+    (``accumulate``: are increased by) the sums over the rows.  ``out`` may be ``x``,
+    ``grad_out`` or ``add``.  ``workspace``: a device tensor of at least
+    ``layer_norm_backward_workspace_bytes`` bytes (None: allocated here)."""
+    here = _current()
+    code, dy_code = _dtype(x, "x", here), _dtype(grad_out, "grad_out", here)
+    dim = x.shape[-1] if x.dim() else 0
+    rows, stride = _flat(x, dim, "x")
+    if grad_out.shape != x.shape:
+        raise ValueError("grad_out must have x's shape")
+    dy_stride = _flat(grad_out, dim, "grad_out")[1]
+    stats_ptr = _stats(stats, x, here)
+    w_code = 0 if weight is None else _param(weight, dim, "weight", here)
+    grad_code = _pair(grad_weight, grad_bias, "grad_weight grad_bias", dim, here)
+    columns = grad_weight is not None or grad_bias is not None
+    if not need_grad_x and (add is not None or out is not None):
+        raise ValueError("add and out need need_grad_x")
+    add_stride = dx_stride = max(1, dim)
+    if add is not None:
+        _on(here, add, "add")
+        _like(add, x, "add", x.dtype)
+        add_stride = _flat(add, dim, "add")[1]
+    if not need_grad_x:
+        out = None
+        if not columns:
+            return None
+    elif out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    else:
+        _on(here, out, "out")
+        _like(out, x, "out", x.dtype)
+        dx_stride = _flat(out, dim, "out")[1]
+    if not columns:
+        workspace = None
+    elif workspace is not None:
+        _on(here, workspace, "workspace")
+    else:
+        workspace = _empty(layer_norm_backward_workspace_bytes(rows, dim), _torch.uint8, x.device, stream)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    status = _lib.fsp_layer_norm_backward(
+        x.data_ptr(), code, rows, dim, stride, stats_ptr, 1 if center else 0, grad_out.data_ptr(), dy_code, dy_stride,
+        ptr(weight), w_code, ptr(add), add_stride, ptr(out), dx_stride, ptr(grad_weight), ptr(grad_bias), grad_code,
+        1 if accumulate else 0, ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _handle(stream, here))
+    if status:
+        _fsp._check(status, "fsp_layer_norm_backward")
+    return out
+
+
+# ---- dropout ---------------------------------------------------------------------------
+
+def dropout(x, p: float, seed: int, call=0, residual=None, out=None, out_dtype=None, stream=None):
+    """``x`` with each element dropped with probability ``p`` (a multiple of 2^-16, the
+    nearest) or divided by 1 - p, plus ``residual`` where it is given; in fp32, rounded
+    once to ``out_dtype`` (default: the residual's, or x's).  ``out`` may be ``x`` or
+    ``residual``.
+
+    Which elements go is a function of ``seed`` (64 bits), ``call`` (an int, or a device
+    int64 tensor of one element: the form to capture in a CUDA graph) and the element's
+    index, so no mask is stored: ``dropout_backward`` takes the same seed and call, and
+    any two calls of a run should differ in one of them."""
+    here = _current()
+    code = _dtype(x, "x", here)
+    dim = x.shape[-1] if x.dim() else 1
+    rows, stride = _flat(x, dim, "x") if x.dim() else (1, 1)
+    call_ptr = None
+    if not isinstance(call, int):
+        if call.dtype != _torch.int64 or call.numel() != 1:
+            raise ValueError("call must be an int or one int64 element")
+        _on(here, call, "call")
+        call, call_ptr = 0, call.data_ptr()
+    r_code, r_stride = 0, stride
+    if residual is not None:
+        r_code = _dtype(residual, "residual", here)
+        _like(residual, x, "residual", None)
+        r_stride = _flat(residual, dim, "residual")[1] if x.dim() else 1
+    if out is None:
+        out = _empty(x.shape, out_dtype or (x if residual is None else residual).dtype, x.device, stream)
+        out_stride = max(1, dim)
+    else:
+        _like(out, x, "out", out_dtype)
+        out_stride = _flat(out, dim, "out")[1] if x.dim() else 1
+    status = _lib.fsp_dropout(x.data_ptr(), code, rows, dim, stride, p, seed & 0xFFFFFFFFFFFFFFFF, call, call_ptr,
+                              None if residual is None else residual.data_ptr(), r_code, r_stride, out.data_ptr(),
+                              _dtype(out, "out", here), out_stride, _handle(stream, here))
+    if status:
+        _fsp._check(status, "fsp_dropout")
+    return out
+
+
+def dropout_backward(grad_out, p: float, seed: int, call=0, out=None, out_dtype=None, stream=None):
+    """The gradient of ``dropout``'s x, with the forward pass's ``p``, ``seed`` and ``call``
+    (that of its residual is ``grad_out`` itself)."""
+    return dropout(grad_out, p, seed, call, out=out, out_dtype=out_dtype, stream=stream)
+
+
+# ---- rotary positions ------------------------------------------------------------------
+
+class Rotary:
+    """Rotary positions over the first ``dim`` elements of each head: pair j turns by its
+    token's position times ``frequencies[j]``.
+
+    ``layout``: ``"half"`` (pair j is elements j and j + dim / 2) or ``"interleaved"``
+    (2 j and 2 j + 1).  The frequencies are ``base^(-2 j / dim)``, or for contexts longer
+    than the trained one scaled by ``factor``: ``"linear"`` divides them by it, ``"ntk"``
+    raises the base to ``base * factor^(dim / (dim - 2))``, and ``"yarn"`` (Peng, Quesnelle,
+    Fan and Shippole, "YaRN: Efficient context window extension of large language models",
+    2023) divides those that turn fewer than ``turns[0]`` times over ``original_length``
+    positions, keeps those that turn more than ``turns[1]`` times, goes linearly from one
+    to the other, and multiplies the rotated elements by ``0.1 ln(factor) + 1``.
+    ``frequencies`` (radians per position) takes their place, ``scale`` that of the
+    multiplier.
+
+    ``forward`` and ``backward`` take a tensor, or a pair (queries and keys, one launch), of
+    shape (tokens, heads, head_dim) or (batch, tokens, heads, head_dim), its last
+    dimension adjacent and the others of any strides, and int32 or int64 positions of shape
+    (tokens,) or (batch, tokens).  Nothing is recorded for autograd."""
+
+    def __init__(self, dim: int, base: float = 10000.0, layout: str = "half", scaling: str | None = None, factor: float = 1.0,
+                 original_length: int | None = None, turns=(1.0, 32.0), scale: float | None = None, frequencies=None,
+                 device="cuda"):
+        if _torch is None:
+            _ready()
+        if dim < 2 or dim % 2:
+            raise ValueError("dim must be even and at least 2")
+        if layout not in ("half", "interleaved"):
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        if frequencies is None:
+            frequencies = _frequencies(dim, base, scaling, factor, original_length, turns)
+            if scale is None and scaling == "yarn":
+                scale = 0.1 * math.log(factor) + 1.0
+        elif scaling is not None:
+            raise ValueError("frequencies and scaling exclude each other")
+        self.frequencies = tuple(float(f) for f in frequencies)
+        if len(self.frequencies) != dim // 2:
+            raise ValueError(f"{dim // 2} frequencies are needed")
+        self.dim, self.layout, self.scale = dim, layout, 1.0 if scale is None else float(scale)
+        host = (ctypes.c_uint64 * (dim // 2))()
+        _fsp._check(_lib.fsp_rotary_phases((ctypes.c_double * (dim // 2))(*self.frequencies), dim // 2, host),
+                    "fsp_rotary_phases")
+        self.phases = _torch.frombuffer(host, dtype=_torch.int64).to(device)
+
+    def forward(self, x, positions, out=None, stream=None):
+        """x (or the pair) rotated, in a new tensor or in ``out`` (a pair for a pair; x
+        itself: in place).  Elements past ``dim`` are copied."""
+        return self._run(x, positions, out, 0, stream)
+
+    def backward(self, grad_out, positions, out=None, stream=None):
+        """The gradient of ``forward``'s x: rotated back."""
+        return self._run(grad_out, positions, out, 1, stream)
+
+    def _run(self, x, positions, out, inverse: int, stream):
+        here = _current()
+        pair = isinstance(x, (tuple, list))
+        xs = tuple(x) if pair else (x,)
+        if not 1 <= len(xs) <= 2:
+            raise ValueError("one tensor or a pair is rotated by a call")
+        outs = (None,) * len(xs) if out is None else tuple(out) if pair else (out,)
+        if len(outs) != len(xs):
+            raise ValueError("out must be as many tensors")
+        code = _dtype(xs[0], "x", here)
+        shape = xs[0].shape[:-2]
+        if xs[0].dim() not in (3, 4):
+            raise ValueError("x must have 3 or 4 dimensions")
+        batch, tokens = (1, *shape) if len(shape) == 1 else shape
+        if positions.get_device() != here:
+            _on(here, positions, "positions")
+        index = _INDEX.get(positions.dtype)
+        if index is None:
+            raise TypeError(f"positions: unsupported dtype {positions.dtype}")
+        if tuple(positions.shape) == tuple(shape):
+            positions_stride = tokens
+        elif tuple(positions.shape) == (tokens,):
+            positions_stride = 0
+        else:
+            raise ValueError(f"positions must have shape {tuple(shape)} or {(tokens,)}")
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+        if self.phases.get_device() != here:
+            _on(here, self.phases, "the frequencies")
+        tensors = (_RotaryTensor * len(xs))()
+        got = []
+        for t, x_i, o in zip(tensors, xs, outs):
+            if x_i.shape[:-2] != shape or x_i.dim() != len(shape) + 2:
+                raise ValueError("the tensors must have the same batch and tokens")
+            if x_i.dtype != xs[0].dtype:
+                raise TypeError("the tensors must have the same dtype")
+            if o is None:
+                o = _empty(x_i.shape, x_i.dtype, x_i.device, stream)
+            elif o.shape != x_i.shape or o.dtype != x_i.dtype:
+                raise ValueError("out has another shape or dtype")
+            for what, y, strides in (("x", x_i, t.x_strides), ("out", o, t.out_strides)):
+                if y.get_device() != here:
+                    _on(here, y, what)
+                s = y.stride()
+                if s[-1] != 1 and y.shape[-1] > 1:
+                    raise ValueError(f"{what}: the elements of a head must be adjacent")
+                strides[:] = (0, *s[:2]) if len(s) == 3 else s[:3]
+            t.x, t.out, t.heads, t.head_dim = x_i.data_ptr(), o.data_ptr(), x_i.shape[-2], x_i.shape[-1]
+            got.append(o)
+        status = _lib.fsp_rotary(tensors, len(xs), code, batch, tokens, positions.data_ptr(), index, positions_stride,
+                                 self.phases.data_ptr(), self.dim, 0 if self.layout == "half" else 1, self.scale, inverse,
+                                 _handle(stream, here))
+        if status:
+            _fsp._check(status, "fsp_rotary")
+        return tuple(got) if pair else got[0]
+
+
+def _frequencies(dim: int, base: float, scaling, factor: float, length, turns):
+    """Radians per position of each pair."""
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("scaling must be 'linear', 'ntk', 'yarn' or None")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be above 0")
+    if scaling == "ntk" and dim > 2:
+        base *= factor ** (dim / (dim - 2))
+    f = [base ** (-2 * j / dim) for j in range(dim // 2)]
+    if scaling == "linear":
+        return [x / factor for x in f]
+    if scaling != "yarn":
+        return f
+    if not length or length < 0:
+        raise ValueError("yarn needs original_length")
+    few, many = turns
+    if not few < many:
+        raise ValueError("turns must increase")
+    kept = [min(max((x * length / math.tau - few) / (many - few), 0.0), 1.0) for x in f]
+    return [x / factor * (1 - k) + x * k for x, k in zip(f, kept)]

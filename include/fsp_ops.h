@@ -7,7 +7,9 @@
  *   - the embedding lookup with scaling and its gradient by sorted tokens (the
  *     gradient goes straight into a parameter's slice of a main-grad buffer);
  *   - matrices in 8-bit floating point with one scale per block of 128, and
- *     their product (a linear layer's forward pass and both of its gradients).
+ *     their product (a linear layer's forward pass and both of its gradients);
+ *   - what stands between a block's products: layer norm with its gradients,
+ *     dropout from a counter-based generator, rotary positions.
  *
  * The conventions of fsp.h hold: host-side checks before anything is launched,
  * a status and fsp_last_error() on refusal, buffers and streams owned by the
@@ -196,6 +198,99 @@ fsp_status fsp_fp8_linear_backward(const void* x, int32_t x_dtype, int64_t x_str
  * fsp_fp8_linear_backward (backward 1). */
 fsp_status fsp_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features, int32_t backward,
                                           size_t* bytes);
+
+/* ---- layer norm ------------------------------------------------------------------- */
+
+/* Each row of x: m its mean (center 0: m = 0, the norm by the root mean square),
+ * r = 1 / sqrt(mean (x - m)^2 + eps), out = (x - m) r weight + bias; computed in
+ * fp32 from the row's values, rounded once.
+ *   x: rows x dim of x_dtype, rows x_stride (>= dim) elements apart; out likewise
+ *            (out may be x itself: same pointer, type and stride).
+ *   weight, bias: dim elements of param_dtype; NULL: ones, zeros.
+ *   eps:     >= 0.
+ *   stats:   NULL, or rows x 2 fp32, 8-byte aligned: receives (m, r).
+ * rows < 2^31, dim <= 2^20. */
+fsp_status fsp_layer_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                          const void* weight, const void* bias, int32_t param_dtype, float eps, int32_t center,
+                          void* out, int32_t out_dtype, int64_t out_stride, float* stats, void* cuda_stream);
+
+/* Device workspace, in bytes, of fsp_layer_norm_backward where it computes
+ * grad_weight or grad_bias (otherwise it needs none). */
+fsp_status fsp_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim, size_t* bytes);
+
+/* The gradients, from the forward pass's x, stats and center.  With
+ * h = (x - m) r and g = grad_out weight, per row:
+ *   grad_x = r (g - mean g (center 0: without) - h mean(g h)) + add
+ *            (x_dtype, as add; NULL: not wanted).
+ *   add:     NULL, or a gradient that joins it (that of the residual stream).
+ *   grad_weight, grad_bias: dim elements of grad_param_dtype: (accumulate: +) the
+ *            sums over the rows of grad_out h and of grad_out, added in fp32 in an order that
+ *            the sizes, types and alignment alone decide, rounded once; NULL: not wanted.
+ *   workspace: 16-byte aligned; free for other use once the stream has passed
+ *            this call.  Calls that may run at the same time need one each.
+ * grad_x may be x, grad_out or add itself (same pointer, type and stride). */
+fsp_status fsp_layer_norm_backward(const void* x, int32_t x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                                   const float* stats, int32_t center, const void* grad_out, int32_t grad_dtype,
+                                   int64_t grad_stride, const void* weight, int32_t weight_dtype, const void* add,
+                                   int64_t add_stride, void* grad_x, int64_t grad_x_stride, void* grad_weight,
+                                   void* grad_bias, int32_t grad_param_dtype, int32_t accumulate, void* workspace,
+                                   size_t workspace_bytes, void* cuda_stream);
+
+/* ---- dropout ---------------------------------------------------------------------- */
+
+/* out = (u < T ? 0 : x * 65536 / (65536 - T)) + residual, T = floor(65536 p + 1/2),
+ * computed in fp32 and rounded once.  Element i (counted along the rows, without
+ * their gaps) has u = 16 bits of Philox-4x32 with ten rounds (Salmon et al., SC
+ * 2011): key (seed's lower and upper word), counter (i / 8's lower and upper
+ * word, call's lower and upper word), word (i % 8) / 2 of the four, its lower
+ * half for even i.  So a mask is a function of (seed, call, i), alike for every
+ * type and stride, and is never stored: the gradient is this function of grad_out
+ * without residual.  Calls of one training run differ in seed or call.
+ *   x, residual (NULL: zeros), out: rows x dim of their types, rows `stride` apart;
+ *            out may be x or residual itself (same pointer, type and stride).
+ *   p:       0 to 1 (from 1 - 2^-17 on all is dropped).
+ *   call_dev: NULL, or a device int64 that is read instead of `call` - the form to
+ *            capture in a CUDA graph.
+ * What is dropped does not enter out, also where it is not finite. */
+fsp_status fsp_dropout(const void* x, int32_t x_dtype, int64_t rows, int64_t dim, int64_t x_stride, double p,
+                       uint64_t seed, int64_t call, const int64_t* call_dev, const void* residual,
+                       int32_t residual_dtype, int64_t residual_stride, void* out, int32_t out_dtype,
+                       int64_t out_stride, void* cuda_stream);
+
+/* ---- rotary positions ------------------------------------------------------------- */
+
+typedef enum {
+  FSP_ROTARY_HALF = 0,          /* pair j: elements j and j + rotary_dim / 2 of a head */
+  FSP_ROTARY_INTERLEAVED = 1    /* pair j: elements 2 j and 2 j + 1                    */
+} fsp_rotary_layout;
+
+/* A tensor of batch x tokens x heads x head_dim elements, a head's elements
+ * adjacent; strides in elements of the batches, tokens and heads. */
+typedef struct {
+  const void* x;
+  void* out;               /* may be x itself, with the same strides */
+  int64_t heads, head_dim; /* head_dim >= rotary_dim, at most 65536; heads at most 2^20 */
+  int64_t x_strides[3];    /* >= 0 */
+  int64_t out_strides[3];  /* every element has a place of its own */
+} fsp_rotary_tensor;
+
+/* Host: n frequencies (radians per position, finite) in units of 2^-64 turn per
+ * position, without whole turns - what fsp_rotary reads on the device. */
+fsp_status fsp_rotary_phases(const double* frequencies, int64_t n, uint64_t* phases);
+
+/* Turns pair j = 0 ... rotary_dim / 2 - 1 of every head, (a, b), by the angle of its
+ * token's position t: out = scale (a cos - b sin, b cos + a sin)(t f_j); elements
+ * past rotary_dim are copied.  t f_j is exact modulo a turn for any int64 t; sine,
+ * cosine and products in fp32, rounded once.  inverse: by the negated angle, which
+ * is the gradient.
+ *   tensors: n (1 or 2: queries and keys in one launch) of `dtype`.
+ *   positions: int32 (index_bytes 4) or int64 (8), batch b's tokens from
+ *            b * positions_stride on (0: the same for every batch).
+ *   phases:  device, rotary_dim / 2 of fsp_rotary_phases.
+ *   rotary_dim: even, at least 2. */
+fsp_status fsp_rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, int64_t batch, int64_t tokens,
+                      const void* positions, int32_t index_bytes, int64_t positions_stride, const uint64_t* phases,
+                      int64_t rotary_dim, int32_t layout, float scale, int32_t inverse, void* cuda_stream);
 
 #ifdef __cplusplus
 }
