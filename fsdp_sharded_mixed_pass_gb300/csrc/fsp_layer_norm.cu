@@ -6,6 +6,7 @@
 //
 // Bound: HBM (about 7 operations an element forward, 14 backward).
 #include <algorithm>
+#include <type_traits>
 
 #include "fsp_rows.cuh"
 
@@ -17,6 +18,13 @@ constexpr int kParts = 152;                      // most partial sums of the wei
 
 __device__ __forceinline__ float load_any(const void* p, bool f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i] : widen(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+template <int V>
+__device__ __forceinline__ void load_any(const void* p, bool f32, int64_t i, float* f) {
+  if (f32)
+    load_vec<float, V>(static_cast<const float*>(p) + i, f);
+  else
+    load_vec<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(p) + i, f);
 }
 template <int V>
 __device__ __forceinline__ void store_any(void* p, bool f32, int64_t i, const float* f) {
@@ -70,6 +78,225 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float (*share)[N]) {
     for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
   }
   __syncthreads();
+}
+
+// ---- rows that fit in registers -------------------------------------------------------
+
+// T threads hold a row, E elements each: accesses of V elements, T * V apart.  T < 32 divides
+// a warp among rows.
+template <int T>
+__device__ __forceinline__ float row_sum(float v) {   // over T <= 32 lanes
+#pragma unroll
+  for (int o = T / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Rows of T threads, R of them in flight per thread.  A warp or less per row needs no
+// barrier; a longer row has a CTA of its own.
+template <typename X, int V, int T, int E, int R>
+__global__ void __launch_bounds__(T > 256 ? T : 256) norm_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kThreads = T > 256 ? T : 256, N = E / V, kRows = kThreads / T;
+  static_assert(T <= 32 || R == 1);
+  __shared__ float share[2][T > 32 ? kThreads / 32 : 1];
+  launch_dependents();
+  grid_dependency_wait();
+  const int t = threadIdx.x % T;
+  const int64_t row0 = (int64_t(blockIdx.x) * kRows + threadIdx.x / T) * R;
+  auto sum = [&](float v, int which) {
+    if constexpr (T <= 32) {
+      return row_sum<T>(v);
+    } else {
+      constexpr int W = T / 32;
+      v = row_sum<32>(v);
+      float* mine = share[which] + threadIdx.x / T * W;
+      if (threadIdx.x % 32 == 0) mine[t / 32] = v;
+      __syncthreads();
+      v = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) v += mine[k];
+      return v;
+    }
+  };
+  alignas(32) X raw[R][N][V];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * T + t) * V;
+      if (row0 + i < a.rows && c < a.dim) {
+        load_raw<X, V>(static_cast<const X*>(a.x) + (row0 + i) * a.x_stride + c, raw[i][n]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) raw[i][n][j] = narrow<X>(0.f);
+      }
+    }
+  const float count = float(a.dim);
+  float m[R], r[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    m[i] = 0.f;
+    if (a.center) {
+      float v = 0.f;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v += widen(raw[i][n][j]);
+      m[i] = sum(v, 0) / count;
+    }
+    float v = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if ((n * T + t) * V < a.dim) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = widen(raw[i][n][j]) - m[i];
+          v = __fmaf_rn(d, d, v);
+        }
+      }
+    r[i] = 1.f / sqrtf(sum(v, 1) / count + a.eps);
+    if (a.stats && t == 0 && row0 + i < a.rows) a.stats[row0 + i] = make_float2(m[i], r[i]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * T + t) * V;
+    if (c >= a.dim) break;
+    float w[V], b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      w[j] = 1.f;
+      b[j] = 0.f;
+    }
+    if (a.weight) load_any<V>(a.weight, a.param_f32, c, w);
+    if (a.bias) load_any<V>(a.bias, a.param_f32, c, b);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float f[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[j] = __fmaf_rn((widen(raw[i][n][j]) - m[i]) * r[i], w[j], b[j]);
+      if (row0 + i < a.rows) store_any<V>(a.out, a.out_f32, (row0 + i) * a.out_stride + c, f);
+    }
+  }
+}
+
+// All gradients in one pass over x and dy.  A thread holds the same columns of every row it
+// takes part in, and adds their terms of dw and db in registers; the CTA's rows are joined
+// in shared memory at the end, so that a launch leaves one pair of partial sums per CTA.
+// The next row's loads are in flight while a row is reduced.
+constexpr int kGradThreads = 512;
+
+template <typename X, typename G, int V, int T, int E>
+__global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_constant__ GradArgs a) {
+  constexpr int N = E / V, kGroups = kGradThreads / T;
+  extern __shared__ __align__(16) float joined[];   // [2][kGroups][T * E]
+  __shared__ float2 share[2][kGradThreads / 32];
+  launch_dependents();
+  grid_dependency_wait();
+  const int group = threadIdx.x / T, t = threadIdx.x % T;
+  // rows of a warp's groups advance together: `first` is that of its first group
+  const int64_t step = int64_t(gridDim.x) * kGroups;
+  int64_t row = int64_t(blockIdx.x) * kGroups + group;
+  int64_t first = int64_t(blockIdx.x) * kGroups + threadIdx.x / (T < 32 ? 32 : T) * (T < 32 ? 32 / T : 1);
+  float w[E], dw[E] = {}, db[E] = {};
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * T + t) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[n * V + j] = 1.f;
+    if (a.weight && c < a.dim) load_any<V>(a.weight, a.weight_f32, c, &w[n * V]);
+  }
+  alignas(32) X xr[N][V], ar[N][V];
+  alignas(32) G gr[N][V];
+  float2 st;
+  auto fetch = [&](auto* to, const auto* from, int64_t stride) {
+    using Y = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * T + t) * V;
+      if (row < a.rows && c < a.dim) {
+        load_raw<Y, V>(from + row * stride + c, to[n]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) to[n][j] = narrow<Y>(0.f);
+      }
+    }
+  };
+  auto fetch_row = [&] {
+    fetch(xr, static_cast<const X*>(a.x), a.x_stride);
+    fetch(gr, static_cast<const G*>(a.grad), a.grad_stride);
+    st = row < a.rows ? a.stats[row] : make_float2(0.f, 0.f);
+  };
+  fetch_row();
+  if (a.add) fetch(ar, static_cast<const X*>(a.add), a.add_stride);
+  const float count = float(a.dim);
+  for (int which = 0; first < a.rows; which ^= 1) {
+    float h[E], g[E], s0 = 0.f, s1 = 0.f;
+    const float r = st.y;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = n * V + j;
+        const float dy = widen(gr[n][j]);
+        h[e] = (widen(xr[n][j]) - st.x) * r;
+        dw[e] = __fmaf_rn(dy, h[e], dw[e]);
+        db[e] += dy;
+        g[e] = dy * w[e];
+        s0 += g[e];
+        s1 = __fmaf_rn(g[e], h[e], s1);
+      }
+    const int64_t now = row;
+    first += step;
+    row += step;
+    fetch_row();
+    if (a.grad_x) {
+      s0 = row_sum<(T < 32 ? T : 32)>(s0);
+      s1 = row_sum<(T < 32 ? T : 32)>(s1);
+      if constexpr (T > 32) {
+        constexpr int W = T / 32;
+        float2* mine = share[which] + group * W;
+        if (threadIdx.x % 32 == 0) mine[t / 32] = make_float2(s0, s1);
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
+        s0 = s1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          s0 += mine[k].x;
+          s1 += mine[k].y;
+        }
+      }
+      const float mean_g = a.center ? s0 / count : 0.f, mean_gh = s1 / count;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * T + t) * V;
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int e = n * V + j;
+          f[j] = __fmaf_rn(r, __fmaf_rn(-h[e], mean_gh, g[e] - mean_g), a.add ? widen(ar[n][j]) : 0.f);
+        }
+        if (now < a.rows && c < a.dim) store_vec<X, V>(static_cast<X*>(a.grad_x) + now * a.grad_x_stride + c, f);
+      }
+      if (a.add) fetch(ar, static_cast<const X*>(a.add), a.add_stride);
+    }
+  }
+  if (!a.grad_weight && !a.grad_bias) return;
+  constexpr int kCols = T * E;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (n * T + t) * V + j;
+      joined[group * kCols + c] = dw[n * V + j];
+      joined[(kGroups + group) * kCols + c] = db[n * V + j];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kCols; i += kGradThreads) {
+    const int which = i / kCols, c = i % kCols;
+    if (c >= a.dim || !(which ? a.grad_bias : a.grad_weight)) continue;
+    float v = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < kGroups; ++k) v += joined[(which * kGroups + k) * kCols + c];
+    a.parts[(int64_t(blockIdx.x) * 2 + which) * a.dim + c] = v;
+  }
 }
 
 // ---- rows of any length: a CTA per row, which reads it again for each pass ------------
@@ -200,9 +427,11 @@ __global__ void __launch_bounds__(kColumnWarps * 32) column_sums_kernel(const __
   }
 }
 
-// Adds the parts, 32 columns of one of the two gradients a CTA; warp w adds parts w, w + 8, ...
-__global__ void __launch_bounds__(kColumnWarps * 32) join_columns_kernel(const __grid_constant__ GradArgs a) {
-  __shared__ float share[kColumnWarps][32];
+// Adds the parts, 32 columns of one of the two gradients a CTA; warp w adds parts w, w + 32, ...
+constexpr int kJoinWarps = 32;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) join_columns_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ float share[kJoinWarps][32];
   launch_dependents();
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -210,14 +439,19 @@ __global__ void __launch_bounds__(kColumnWarps * 32) join_columns_kernel(const _
   if (!out) return;
   const int64_t col = int64_t(blockIdx.x) * 32 + lane;
   float sum = 0.f;
-  if (col < a.dim)
-    for (int p = warp; p < a.n_parts; p += kColumnWarps) sum += a.parts[(int64_t(p) * 2 + blockIdx.y) * a.dim + col];
+  if (col < a.dim) {
+#pragma unroll
+    for (int k = 0; k < (kParts + kJoinWarps - 1) / kJoinWarps; ++k) {
+      const int p = warp + k * kJoinWarps;
+      if (p < a.n_parts) sum += a.parts[(int64_t(p) * 2 + blockIdx.y) * a.dim + col];
+    }
+  }
   share[warp][lane] = sum;
   __syncthreads();
   if (warp > 0 || col >= a.dim) return;
   sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kColumnWarps; ++w) sum += share[w][lane];
+  for (int w = 0; w < kJoinWarps; ++w) sum += share[w][lane];
   if (a.accumulate) sum += load_any(out, a.grad_param_f32, col);
   store_any<1>(out, a.grad_param_f32, col, &sum);
 }
@@ -242,6 +476,25 @@ fsp_status check_stats(const float* stats) {
   return reinterpret_cast<uintptr_t>(stats) % 8 ? fail(FSP_EINVAL, "stats is not 8-byte aligned") : FSP_OK;
 }
 
+template <typename X, int V, int T, int E, int R>
+fsp_status launch_rows(const NormArgs& a, cudaStream_t st) {
+  constexpr int kThreads = T > 256 ? T : 256, kRows = kThreads / T * R;
+  return launch_next(norm_kernel<X, V, T, E, R>, dim3(unsigned((a.rows + kRows - 1) / kRows)), kThreads, 0, 1, a, st, "layer norm kernel launch");
+}
+
+template <typename X, int V>
+fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
+  if (a.dim <= 128) return launch_rows<X, V, 16, 8, 4>(a, st);
+  if (a.dim <= 256) return launch_rows<X, V, 32, 8, 4>(a, st);
+  if (a.dim <= 512) return launch_rows<X, V, 32, 16, 2>(a, st);
+  if (a.dim <= 1024) return launch_rows<X, V, 32, 32, 1>(a, st);
+  if (a.dim <= 2048) return launch_rows<X, V, 32, 64, 1>(a, st);
+  if (a.dim <= 4096) return launch_rows<X, V, 128, 32, 1>(a, st);
+  if (a.dim <= 8192) return launch_rows<X, V, 256, 32, 1>(a, st);
+  if (a.dim <= 16384) return launch_rows<X, V, 512, 32, 1>(a, st);
+  return launch_next(wide_norm_kernel<X, V>, dim3(unsigned(a.rows)), kWideThreads, 0, 1, a, st, "layer norm kernel launch");
+}
+
 fsp_status norm(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs, const void* weight, const void* bias,
                 int32_t pd, float eps, int32_t center, void* out, int32_t od, int64_t os, float* stats, void* stream) {
   fsp_status s = check_sizes(rows, dim);
@@ -261,32 +514,58 @@ fsp_status norm(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs
   if (s != FSP_OK) return s;
   NormArgs a{x, weight, bias, out, reinterpret_cast<float2*>(stats), rows, dim, xs, os, eps, center != 0, pd == FSP_DTYPE_F32, od == FSP_DTYPE_F32};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(out, os, od, 8);
+  const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(out, os, od, 8) && (!weight || rows_fit(weight, 0, pd, 8)) &&
+                   (!bias || rows_fit(bias, 0, pd, 8));
   using B = __nv_bfloat16;
-  const int threads = int(std::min<int64_t>(kWideThreads, (dim / (vec ? 8 : 1) + 31) / 32 * 32));
-  void (*kernel)(NormArgs) = xd == FSP_DTYPE_F32 ? (vec ? wide_norm_kernel<float, 8> : wide_norm_kernel<float, 1>)
-                                                  : (vec ? wide_norm_kernel<B, 8> : wide_norm_kernel<B, 1>);
-  return launch_next(kernel, dim3(unsigned(rows)), std::max(32, threads), 0, 1, a, st, "layer norm kernel launch");
+  if (xd == FSP_DTYPE_F32) return vec ? launch_norm<float, 8>(a, st) : launch_norm<float, 1>(a, st);
+  return vec ? launch_norm<B, 8>(a, st) : launch_norm<B, 1>(a, st);
 }
 
 int64_t parts_of(int64_t rows) { return std::min<int64_t>(kParts, rows); }
 size_t workspace_of(int64_t rows, int64_t dim) { return size_t(parts_of(rows)) * 2 * size_t(dim) * 4 + 256; }   // (from a multiple of 256)
 
+fsp_status launch_join(const GradArgs& a, cudaStream_t st) {
+  return launch_next(join_columns_kernel, dim3(unsigned((a.dim + 31) / 32), 2), kJoinWarps * 32, 0, 1, a, st,
+                     "layer norm gradient (join) kernel launch");
+}
+
+template <typename X, typename G, int V, int T, int E>
+fsp_status launch_rows_grad(GradArgs a, cudaStream_t st) {
+  constexpr int kGroups = kGradThreads / T, kSmem = 2 * kGroups * T * E * 4;
+  void (*kernel)(GradArgs) = grad_kernel<X, G, V, T, E>;
+  fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
+  if (s != FSP_OK) return s;
+  a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
+  if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kGradThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
+  return s == FSP_OK && (a.grad_weight || a.grad_bias) ? launch_join(a, st) : s;
+}
+
 template <typename X, typename G, int V>
-fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
+fsp_status launch_wide_grad(const GradArgs& a, cudaStream_t st) {
   fsp_status s = FSP_OK;
   if (a.grad_weight || a.grad_bias) {   // (first: grad_x may take the place of x or grad_out)
     const dim3 grid(unsigned((a.dim + 32 * V - 1) / (32 * V)), unsigned(a.n_parts));
     if (a.rows > 0)
       s = launch_next(column_sums_kernel<X, G, V>, grid, kColumnWarps * 32, 0, 1, a, st, "layer norm gradient (columns) kernel launch");
-    if (s == FSP_OK)
-      s = launch_next(join_columns_kernel, dim3(unsigned((a.dim + 31) / 32), 2), kColumnWarps * 32, 0, 1, a, st,
-                      "layer norm gradient (join) kernel launch");
+    if (s == FSP_OK) s = launch_join(a, st);
   }
   if (s != FSP_OK || !a.grad_x || a.rows == 0) return s;
-  const int threads = int(std::min<int64_t>(kWideThreads, (a.dim / V + 31) / 32 * 32));
-  return launch_next(wide_grad_kernel<X, G, V>, dim3(unsigned(a.rows)), std::max(32, threads), 0, 1, a, st,
-                     "layer norm gradient kernel launch");
+  return launch_next(wide_grad_kernel<X, G, V>, dim3(unsigned(a.rows)), kWideThreads, 0, 1, a, st, "layer norm gradient kernel launch");
+}
+
+template <typename X, typename G, int V>
+fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
+  // sixteen elements a thread, eight where fp32 rows would not leave the registers for the row ahead
+  constexpr int E = sizeof(X) + sizeof(G) > 4 ? 8 : 16;
+  if (a.dim <= 8 * E) return launch_rows_grad<X, G, V, 8, E>(a, st);
+  if (a.dim <= 16 * E) return launch_rows_grad<X, G, V, 16, E>(a, st);
+  if (a.dim <= 32 * E) return launch_rows_grad<X, G, V, 32, E>(a, st);
+  if (a.dim <= 64 * E) return launch_rows_grad<X, G, V, 64, E>(a, st);
+  if (a.dim <= 128 * E) return launch_rows_grad<X, G, V, 128, E>(a, st);
+  if (a.dim <= 256 * E) return launch_rows_grad<X, G, V, 256, E>(a, st);
+  if (a.dim <= 512 * E) return launch_rows_grad<X, G, V, 512, E>(a, st);
+  if (a.dim <= 1024 * E) return launch_rows_grad<X, G, V, 512, 2 * E>(a, st);
+  return launch_wide_grad<X, G, V>(a, st);
 }
 
 template <typename X, typename G>
@@ -352,7 +631,7 @@ fsp_status backward(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_
   a.accumulate = accumulate != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(grad, gs, gd, 8) && (!add || rows_fit(add, as, xd, 8)) &&
-                   (!grad_x || rows_fit(grad_x, ds, xd, 8));
+                   (!grad_x || rows_fit(grad_x, ds, xd, 8)) && (!weight || rows_fit(weight, 0, wd, 8));
   using B = __nv_bfloat16;
   if (xd == FSP_DTYPE_F32)
     return gd == FSP_DTYPE_F32 ? launch_grad_v<float, float>(a, vec, st) : launch_grad_v<float, B>(a, vec, st);
