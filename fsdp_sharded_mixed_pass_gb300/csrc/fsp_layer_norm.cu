@@ -299,6 +299,267 @@ __global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_cons
   }
 }
 
+// ---- rows through shared memory -------------------------------------------------------
+//
+// Many rows: each CTA stays and takes every gridDim.x-th set of 512 / T rows.  A thread
+// holds the same E columns of every row it takes part in, so its parameters are read once,
+// and copies those columns of the rows ahead into its own part of a ring of stages in shared
+// memory (cp.async): the copies of kStages - 1 rows are in flight while a row is reduced,
+// without registers for them, and what a thread copied is read by itself alone, so that the
+// ring needs no barriers.
+
+constexpr int kRingThreads = 512;
+constexpr int kHold = 16;   // columns of a thread (bf16 and fp32 rows)
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {   // 16 bytes, or zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // until at most N groups of this thread's copies are in flight
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+// A thread's columns of one row of Y, as N accesses of V elements, T * V apart: in a stage
+// [n][thread] of accesses.
+template <typename Y, int V, int T, int N>
+struct Columns {
+  static constexpr int kBytes = int(sizeof(Y)) * V;
+  static constexpr int kStage = N * kRingThreads * kBytes;
+  static_assert(kBytes % 16 == 0);
+  static __device__ __forceinline__ void copy(char* stage, const void* from, int64_t stride, int64_t row, int64_t rows, int64_t dim, int t) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = (n * T + t) * V;
+      const bool there = row < rows && c < dim;
+      const char* src = reinterpret_cast<const char*>(static_cast<const Y*>(from) + (there ? row * stride + c : 0));
+      const uint32_t dst = smem_at(stage) + (n * kRingThreads + threadIdx.x) * kBytes;
+#pragma unroll
+      for (int k = 0; k < kBytes; k += 16) copy_async(dst + k, src + k, there);
+    }
+  }
+  static __device__ __forceinline__ void read(const char* stage, int n, float* f) {
+    alignas(16) Y y[V];
+    const uint4* from = reinterpret_cast<const uint4*>(stage + (n * kRingThreads + threadIdx.x) * kBytes);
+#pragma unroll
+    for (int k = 0; k < kBytes / 16; ++k) reinterpret_cast<uint4*>(y)[k] = from[k];
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = widen(y[j]);
+  }
+};
+
+// Sums over the T threads of a group, of which a CTA has several.  `which` alternates from
+// sum to sum: a thread is past the barrier of a sum only when all have read the one before.
+template <int T, int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], float (*share)[kRingThreads / 32][K], int which) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = row_sum<(T < 32 ? T : 32)>(v[k]);
+  if constexpr (T > 32) {
+    const int group = threadIdx.x / T;
+    float(*mine)[K] = share[which] + group * (T / 32);
+    if (threadIdx.x % 32 == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) mine[threadIdx.x % T / 32][k] = v[k];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += mine[w][k];
+  }
+}
+
+// The rows of a thread: `row` its group's, `first` that of its warp's first group (the groups
+// of a warp advance together), `step` to the next.
+template <int T>
+struct Walk {
+  int64_t row, first, step;
+  int t;
+  __device__ __forceinline__ Walk() {
+    constexpr int kGroups = kRingThreads / T, kUnit = T < 32 ? 32 : T;
+    t = threadIdx.x % T;
+    step = int64_t(gridDim.x) * kGroups;
+    row = int64_t(blockIdx.x) * kGroups + threadIdx.x / T;
+    first = int64_t(blockIdx.x) * kGroups + threadIdx.x / kUnit * (kUnit / T);
+  }
+};
+
+template <typename X, int V, int T, int kStages>
+__global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int E = kHold, N = E / V;
+  using C = Columns<X, V, T, N>;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float share[2][kRingThreads / 32][1];
+  launch_dependents();
+  grid_dependency_wait();
+  Walk<T> at;
+  const int t = at.t;
+#pragma unroll
+  for (int d = 0; d < kStages; ++d) {
+    C::copy(ring + d * C::kStage, a.x, a.x_stride, at.row + d * at.step, a.rows, a.dim, t);
+    copies_issued();
+  }
+  float w[E], b[E];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * T + t) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      w[n * V + j] = 1.f;
+      b[n * V + j] = 0.f;
+    }
+    if (a.weight && c < a.dim) load_any<V>(a.weight, a.param_f32, c, &w[n * V]);
+    if (a.bias && c < a.dim) load_any<V>(a.bias, a.param_f32, c, &b[n * V]);
+  }
+  const float count = float(a.dim);
+  int slot = 0, which = 0;
+  for (; at.first < a.rows; at.first += at.step, at.row += at.step, which ^= 1) {
+    char* stage = ring + slot * C::kStage;
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    copies_wait<kStages - 1>();
+    float f[E], m = 0.f, s[1];
+#pragma unroll
+    for (int n = 0; n < N; ++n) C::read(stage, n, &f[n * V]);
+    if (a.center) {
+      s[0] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] += f[e];
+      group_sum<T>(s, share, 0);
+      m = s[0] / count;
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = n * V + j;
+        f[e] -= m;
+        if ((n * T + t) * V < a.dim) s[0] = __fmaf_rn(f[e], f[e], s[0]);
+      }
+    group_sum<T>(s, share, a.center ? 1 : which);
+    C::copy(stage, a.x, a.x_stride, at.row + kStages * at.step, a.rows, a.dim, t);   // (what was read is in registers)
+    copies_issued();
+    const float r = 1.f / sqrtf(s[0] / count + a.eps);
+    if (at.row < a.rows) {
+      if (a.stats && t == 0) a.stats[at.row] = make_float2(m, r);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * T + t) * V;
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = __fmaf_rn(f[n * V + j] * r, w[n * V + j], b[n * V + j]);
+        if (c < a.dim) store_any<V>(a.out, a.out_f32, at.row * a.out_stride + c, y);
+      }
+    }
+  }
+  copies_wait<0>();
+}
+
+// All gradients in one pass over x and dy.  A thread adds its columns' terms of dw and db in
+// registers; the CTA's groups are joined in shared memory at the end, so that a launch leaves
+// one pair of partial sums per CTA.
+template <typename X, typename G, int V, int T, int kStages>
+__global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid_constant__ GradArgs a) {
+  constexpr int E = kHold, N = E / V, kGroups = kRingThreads / T;
+  using CX = Columns<X, V, T, N>;
+  using CG = Columns<G, V, T, N>;
+  constexpr int kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float share[2][kRingThreads / 32][2];
+  launch_dependents();
+  grid_dependency_wait();
+  Walk<T> at;
+  const int t = at.t;
+  auto copy_row = [&](char* stage, int64_t row) {
+    CG::copy(stage, a.grad, a.grad_stride, row, a.rows, a.dim, t);
+    CX::copy(stage + CG::kStage, a.x, a.x_stride, row, a.rows, a.dim, t);
+    if (a.add) CX::copy(stage + CG::kStage + CX::kStage, a.add, a.add_stride, row, a.rows, a.dim, t);
+    copies_issued();
+  };
+#pragma unroll
+  for (int d = 0; d < kStages; ++d) copy_row(ring + d * kStage, at.row + d * at.step);
+  float w[E], dw[E] = {}, db[E] = {};
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * T + t) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[n * V + j] = 1.f;
+    if (a.weight && c < a.dim) load_any<V>(a.weight, a.weight_f32, c, &w[n * V]);
+  }
+  const float count = float(a.dim);
+  float2 next = at.row < a.rows ? a.stats[at.row] : make_float2(0.f, 0.f);
+  int slot = 0;
+  for (int which = 0; at.first < a.rows; which ^= 1) {
+    char* stage = ring + slot * kStage;
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    const float2 st = next;
+    if (at.row + at.step < a.rows) next = a.stats[at.row + at.step];
+    copies_wait<kStages - 1>();
+    float h[E], g[E], s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      CG::read(stage, n, &g[n * V]);
+      CX::read(stage + CG::kStage, n, &h[n * V]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = n * V + j;
+        h[e] = (h[e] - st.x) * st.y;
+        dw[e] = __fmaf_rn(g[e], h[e], dw[e]);
+        db[e] += g[e];
+        g[e] *= w[e];
+        s[0] += g[e];
+        s[1] = __fmaf_rn(g[e], h[e], s[1]);
+      }
+    }
+    if (a.grad_x) {
+      group_sum<T>(s, share, which);
+      const float mean_g = a.center ? s[0] / count : 0.f, mean_gh = s[1] / count;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * T + t) * V;
+        float f[V] = {};
+        if (a.add) CX::read(stage + CG::kStage + CX::kStage, n, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int e = n * V + j;
+          f[j] = __fmaf_rn(st.y, __fmaf_rn(-h[e], mean_gh, g[e] - mean_g), f[j]);
+        }
+        if (at.row < a.rows && c < a.dim) store_vec<X, V>(static_cast<X*>(a.grad_x) + at.row * a.grad_x_stride + c, f);
+      }
+    }
+    copy_row(stage, at.row + kStages * at.step);
+    at.first += at.step;
+    at.row += at.step;
+  }
+  copies_wait<0>();
+  if (!a.grad_weight && !a.grad_bias) return;
+  __syncthreads();
+  constexpr int kCols = T * E;
+  float* joined = reinterpret_cast<float*>(ring);   // [2][kGroups][kCols]
+  static_assert(2 * kGroups * kCols * 4 <= kStages * kStage);
+  const int group = threadIdx.x / T;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (n * T + t) * V + j;
+      joined[group * kCols + c] = dw[n * V + j];
+      joined[(kGroups + group) * kCols + c] = db[n * V + j];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kCols; i += kRingThreads) {
+    const int which = i / kCols, c = i % kCols;
+    if (c >= a.dim || !(which ? a.grad_bias : a.grad_weight)) continue;
+    float v = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < kGroups; ++k) v += joined[(which * kGroups + k) * kCols + c];
+    a.parts[(int64_t(blockIdx.x) * 2 + which) * a.dim + c] = v;
+  }
+}
+
 // ---- rows of any length: a CTA per row, which reads it again for each pass ------------
 
 constexpr int kWideThreads = 1024;
@@ -482,8 +743,31 @@ fsp_status launch_rows(const NormArgs& a, cudaStream_t st) {
   return launch_next(norm_kernel<X, V, T, E, R>, dim3(unsigned((a.rows + kRows - 1) / kRows)), kThreads, 0, 1, a, st, "layer norm kernel launch");
 }
 
+template <typename X, int V, int T>
+fsp_status launch_ring(const NormArgs& a, cudaStream_t st) {
+  constexpr int kStages = sizeof(X) == 2 ? 6 : 4, kSmem = kStages * Columns<X, V, T, kHold / V>::kStage;
+  void (*kernel)(NormArgs) = norm_ring_kernel<X, V, T, kStages>;
+  const fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
+  if (s != FSP_OK) return s;
+  const int64_t ctas = std::min<int64_t>(kParts, (a.rows + kRingThreads / T - 1) / (kRingThreads / T));
+  return launch_next(kernel, dim3(unsigned(ctas)), kRingThreads, kSmem, 1, a, st, "layer norm kernel launch");
+}
+
+template <typename X>
+fsp_status launch_norm_vec(const NormArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / int(sizeof(X));
+  if (a.dim <= 8 * kHold) return launch_ring<X, V, 8>(a, st);
+  if (a.dim <= 16 * kHold) return launch_ring<X, V, 16>(a, st);
+  if (a.dim <= 32 * kHold) return launch_ring<X, V, 32>(a, st);
+  if (a.dim <= 64 * kHold) return launch_ring<X, V, 64>(a, st);
+  if (a.dim <= 128 * kHold) return launch_ring<X, V, 128>(a, st);
+  if (a.dim <= 256 * kHold) return launch_ring<X, V, 256>(a, st);
+  return launch_ring<X, V, 512>(a, st);
+}
+
 template <typename X, int V>
 fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
+  if (V > 1 && a.rows >= 1024 && a.dim <= 512 * kHold) return launch_norm_vec<X>(a, st);
   if (a.dim <= 128) return launch_rows<X, V, 16, 8, 4>(a, st);
   if (a.dim <= 256) return launch_rows<X, V, 32, 8, 4>(a, st);
   if (a.dim <= 512) return launch_rows<X, V, 32, 16, 2>(a, st);
@@ -540,6 +824,30 @@ fsp_status launch_rows_grad(GradArgs a, cudaStream_t st) {
   return s == FSP_OK && (a.grad_weight || a.grad_bias) ? launch_join(a, st) : s;
 }
 
+template <typename X, typename G, int T>
+fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
+  constexpr int V = sizeof(X) + sizeof(G) == 8 ? 4 : 8, N = kHold / V, kGroups = kRingThreads / T;
+  constexpr int kStages = sizeof(X) == 4 ? 2 : sizeof(G) == 4 ? 3 : 4;
+  constexpr int kSmem = kStages * (2 * Columns<X, V, T, N>::kStage + Columns<G, V, T, N>::kStage);
+  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, V, T, kStages>;
+  fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
+  if (s != FSP_OK) return s;
+  a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
+  if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kRingThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
+  return s == FSP_OK && (a.grad_weight || a.grad_bias) ? launch_join(a, st) : s;
+}
+
+template <typename X, typename G>
+fsp_status launch_grad_vec(const GradArgs& a, cudaStream_t st) {
+  if (a.dim <= 8 * kHold) return launch_ring_grad<X, G, 8>(a, st);
+  if (a.dim <= 16 * kHold) return launch_ring_grad<X, G, 16>(a, st);
+  if (a.dim <= 32 * kHold) return launch_ring_grad<X, G, 32>(a, st);
+  if (a.dim <= 64 * kHold) return launch_ring_grad<X, G, 64>(a, st);
+  if (a.dim <= 128 * kHold) return launch_ring_grad<X, G, 128>(a, st);
+  if (a.dim <= 256 * kHold) return launch_ring_grad<X, G, 256>(a, st);
+  return launch_ring_grad<X, G, 512>(a, st);
+}
+
 template <typename X, typename G, int V>
 fsp_status launch_wide_grad(const GradArgs& a, cudaStream_t st) {
   fsp_status s = FSP_OK;
@@ -555,6 +863,7 @@ fsp_status launch_wide_grad(const GradArgs& a, cudaStream_t st) {
 
 template <typename X, typename G, int V>
 fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
+  if (V > 1 && a.dim <= 512 * kHold) return launch_grad_vec<X, G>(a, st);
   // sixteen elements a thread, eight where fp32 rows would not leave the registers for the row ahead
   constexpr int E = sizeof(X) + sizeof(G) > 4 ? 8 : 16;
   if (a.dim <= 8 * E) return launch_rows_grad<X, G, V, 8, E>(a, st);
