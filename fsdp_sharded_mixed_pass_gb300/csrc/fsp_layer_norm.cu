@@ -80,8 +80,6 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float (*share)[N]) {
   __syncthreads();
 }
 
-// ---- rows that fit in registers -------------------------------------------------------
-
 // T threads hold a row, E elements each: accesses of V elements, T * V apart.  T < 32 divides
 // a warp among rows.
 template <int T>
@@ -91,225 +89,87 @@ __device__ __forceinline__ float row_sum(float v) {   // over T <= 32 lanes
   return v;
 }
 
-// Rows of T threads, R of them in flight per thread.  A warp or less per row needs no
-// barrier; a longer row has a CTA of its own.
-template <typename X, int V, int T, int E, int R>
-__global__ void __launch_bounds__(T > 256 ? T : 256) norm_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int kThreads = T > 256 ? T : 256, N = E / V, kRows = kThreads / T;
-  static_assert(T <= 32 || R == 1);
-  __shared__ float share[2][T > 32 ? kThreads / 32 : 1];
+// ---- few rows: in registers -----------------------------------------------------------
+
+// Everything that a row needs is asked for at once, and eight elements a thread keep the
+// sums short: what counts is a launch's latency.
+template <typename X, int V, int T, int E>
+__global__ void __launch_bounds__(T > 128 ? T : 128) norm_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kThreads = T > 128 ? T : 128, N = E / V, kRows = kThreads / T;
+  __shared__ float share[2][kThreads / 32];
   launch_dependents();
   grid_dependency_wait();
   const int t = threadIdx.x % T;
-  const int64_t row0 = (int64_t(blockIdx.x) * kRows + threadIdx.x / T) * R;
+  const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / T;
   auto sum = [&](float v, int which) {
-    if constexpr (T <= 32) {
-      return row_sum<T>(v);
-    } else {
-      constexpr int W = T / 32;
-      v = row_sum<32>(v);
-      float* mine = share[which] + threadIdx.x / T * W;
+    v = row_sum<32>(v);
+    if constexpr (T > 32) {
+      float* mine = share[which] + threadIdx.x / T * (T / 32);
       if (threadIdx.x % 32 == 0) mine[t / 32] = v;
       __syncthreads();
-      v = 0.f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) v += mine[k];
-      return v;
+      v = threadIdx.x % 32 < T / 32 ? mine[threadIdx.x % 32] : 0.f;
+      v = row_sum<32>(v);
     }
+    return v;
   };
-  alignas(32) X raw[R][N][V];
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * T + t) * V;
-      if (row0 + i < a.rows && c < a.dim) {
-        load_raw<X, V>(static_cast<const X*>(a.x) + (row0 + i) * a.x_stride + c, raw[i][n]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) raw[i][n][j] = narrow<X>(0.f);
-      }
-    }
-  const float count = float(a.dim);
-  float m[R], r[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    m[i] = 0.f;
-    if (a.center) {
-      float v = 0.f;
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int j = 0; j < V; ++j) v += widen(raw[i][n][j]);
-      m[i] = sum(v, 0) / count;
-    }
-    float v = 0.f;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-      if ((n * T + t) * V < a.dim) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float d = widen(raw[i][n][j]) - m[i];
-          v = __fmaf_rn(d, d, v);
-        }
-      }
-    r[i] = 1.f / sqrtf(sum(v, 1) / count + a.eps);
-    if (a.stats && t == 0 && row0 + i < a.rows) a.stats[row0 + i] = make_float2(m[i], r[i]);
-  }
+  float f[E], w[E], b[E];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int c = (n * T + t) * V;
-    if (c >= a.dim) break;
-    float w[V], b[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      w[j] = 1.f;
-      b[j] = 0.f;
+      f[n * V + j] = b[n * V + j] = 0.f;
+      w[n * V + j] = 1.f;
     }
-    if (a.weight) load_any<V>(a.weight, a.param_f32, c, w);
-    if (a.bias) load_any<V>(a.bias, a.param_f32, c, b);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      float f[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) f[j] = __fmaf_rn((widen(raw[i][n][j]) - m[i]) * r[i], w[j], b[j]);
-      if (row0 + i < a.rows) store_any<V>(a.out, a.out_f32, (row0 + i) * a.out_stride + c, f);
+    if (c < a.dim) {
+      if (row < a.rows) load_vec<X, V>(static_cast<const X*>(a.x) + row * a.x_stride + c, &f[n * V]);
+      if (a.weight) load_any<V>(a.weight, a.param_f32, c, &w[n * V]);
+      if (a.bias) load_any<V>(a.bias, a.param_f32, c, &b[n * V]);
     }
   }
-}
-
-// All gradients in one pass over x and dy.  A thread holds the same columns of every row it
-// takes part in, and adds their terms of dw and db in registers; the CTA's rows are joined
-// in shared memory at the end, so that a launch leaves one pair of partial sums per CTA.
-// The next row's loads are in flight while a row is reduced.
-constexpr int kGradThreads = 512;
-
-template <typename X, typename G, int V, int T, int E>
-__global__ void __launch_bounds__(kGradThreads, 1) grad_kernel(const __grid_constant__ GradArgs a) {
-  constexpr int N = E / V, kGroups = kGradThreads / T;
-  extern __shared__ __align__(16) float joined[];   // [2][kGroups][T * E]
-  __shared__ float2 share[2][kGradThreads / 32];
-  launch_dependents();
-  grid_dependency_wait();
-  const int group = threadIdx.x / T, t = threadIdx.x % T;
-  // rows of a warp's groups advance together: `first` is that of its first group
-  const int64_t step = int64_t(gridDim.x) * kGroups;
-  int64_t row = int64_t(blockIdx.x) * kGroups + group;
-  int64_t first = int64_t(blockIdx.x) * kGroups + threadIdx.x / (T < 32 ? 32 : T) * (T < 32 ? 32 / T : 1);
-  float w[E], dw[E] = {}, db[E] = {};
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int c = (n * T + t) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) w[n * V + j] = 1.f;
-    if (a.weight && c < a.dim) load_any<V>(a.weight, a.weight_f32, c, &w[n * V]);
-  }
-  alignas(32) X xr[N][V], ar[N][V];
-  alignas(32) G gr[N][V];
-  float2 st;
-  auto fetch = [&](auto* to, const auto* from, int64_t stride) {
-    using Y = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * T + t) * V;
-      if (row < a.rows && c < a.dim) {
-        load_raw<Y, V>(from + row * stride + c, to[n]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) to[n][j] = narrow<Y>(0.f);
-      }
-    }
-  };
-  auto fetch_row = [&] {
-    fetch(xr, static_cast<const X*>(a.x), a.x_stride);
-    fetch(gr, static_cast<const G*>(a.grad), a.grad_stride);
-    st = row < a.rows ? a.stats[row] : make_float2(0.f, 0.f);
-  };
-  fetch_row();
-  if (a.add) fetch(ar, static_cast<const X*>(a.add), a.add_stride);
   const float count = float(a.dim);
-  for (int which = 0; first < a.rows; which ^= 1) {
-    float h[E], g[E], s0 = 0.f, s1 = 0.f;
-    const float r = st.y;
+  float m = 0.f, v = 0.f;
+  if (a.center) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = n * V + j;
-        const float dy = widen(gr[n][j]);
-        h[e] = (widen(xr[n][j]) - st.x) * r;
-        dw[e] = __fmaf_rn(dy, h[e], dw[e]);
-        db[e] += dy;
-        g[e] = dy * w[e];
-        s0 += g[e];
-        s1 = __fmaf_rn(g[e], h[e], s1);
-      }
-    const int64_t now = row;
-    first += step;
-    row += step;
-    fetch_row();
-    if (a.grad_x) {
-      s0 = row_sum<(T < 32 ? T : 32)>(s0);
-      s1 = row_sum<(T < 32 ? T : 32)>(s1);
-      if constexpr (T > 32) {
-        constexpr int W = T / 32;
-        float2* mine = share[which] + group * W;
-        if (threadIdx.x % 32 == 0) mine[t / 32] = make_float2(s0, s1);
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
-        s0 = s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-          s0 += mine[k].x;
-          s1 += mine[k].y;
-        }
-      }
-      const float mean_g = a.center ? s0 / count : 0.f, mean_gh = s1 / count;
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int c = (n * T + t) * V;
-        float f[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int e = n * V + j;
-          f[j] = __fmaf_rn(r, __fmaf_rn(-h[e], mean_gh, g[e] - mean_g), a.add ? widen(ar[n][j]) : 0.f);
-        }
-        if (now < a.rows && c < a.dim) store_vec<X, V>(static_cast<X*>(a.grad_x) + now * a.grad_x_stride + c, f);
-      }
-      if (a.add) fetch(ar, static_cast<const X*>(a.add), a.add_stride);
-    }
+    for (int e = 0; e < E; ++e) v += f[e];
+    m = sum(v, 0) / count;
+    v = 0.f;
   }
-  if (!a.grad_weight && !a.grad_bias) return;
-  constexpr int kCols = T * E;
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int c = (n * T + t) * V + j;
-      joined[group * kCols + c] = dw[n * V + j];
-      joined[(kGroups + group) * kCols + c] = db[n * V + j];
+      const int e = n * V + j;
+      f[e] -= m;
+      if ((n * T + t) * V < a.dim) v = __fmaf_rn(f[e], f[e], v);
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * kCols; i += kGradThreads) {
-    const int which = i / kCols, c = i % kCols;
-    if (c >= a.dim || !(which ? a.grad_bias : a.grad_weight)) continue;
-    float v = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < kGroups; ++k) v += joined[(which * kGroups + k) * kCols + c];
-    a.parts[(int64_t(blockIdx.x) * 2 + which) * a.dim + c] = v;
+  const float r = 1.f / sqrtf(sum(v, 1) / count + a.eps);
+  if (row >= a.rows) return;
+  if (a.stats && t == 0) a.stats[row] = make_float2(m, r);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * T + t) * V;
+    if (c >= a.dim) break;
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) y[j] = __fmaf_rn(f[n * V + j] * r, w[n * V + j], b[n * V + j]);
+    store_any<V>(a.out, a.out_f32, row * a.out_stride + c, y);
   }
 }
 
-// ---- rows through shared memory -------------------------------------------------------
+// ---- many rows: through shared memory ---------------------------------------------------
 //
-// Many rows: each CTA stays and takes every gridDim.x-th set of 512 / T rows.  A thread
-// holds the same E columns of every row it takes part in, so its parameters are read once,
-// and copies those columns of the rows ahead into its own part of a ring of stages in shared
-// memory (cp.async): the copies of kStages - 1 rows are in flight while a row is reduced,
-// without registers for them, and what a thread copied is read by itself alone, so that the
-// ring needs no barriers.
+// Each CTA stays and takes every gridDim.x-th set of 512 / T rows.  The T threads of a group
+// hold the same columns of every row that the group takes, and copy the rows ahead into the
+// group's part of a ring of stages in shared memory (cp.async): the copies of kStages - 1
+// rows are in flight while a row is reduced, without registers for them.
+//
+// Rows that begin and end at multiples of 16 bytes (V > 1): a thread copies what it reads
+// itself, so that the ring needs no barriers.  Others (V = 1): the group copies the 16-byte
+// pieces that cover the row and reads element by element, T apart.  A piece that reaches
+// past the matrix's first or last byte is filled with the elements that are the matrix's.
 
 constexpr int kRingThreads = 512;
-constexpr int kHold = 16;   // columns of a thread (bf16 and fp32 rows)
 
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {   // 16 bytes, or zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -321,48 +181,28 @@ __device__ __forceinline__ void copies_wait() {   // until at most N groups of t
 }
 __device__ __forceinline__ uint32_t smem_at(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 
-// A thread's columns of one row of Y, as N accesses of V elements, T * V apart: in a stage
-// [n][thread] of accesses.
-template <typename Y, int V, int T, int N>
-struct Columns {
-  static constexpr int kBytes = int(sizeof(Y)) * V;
-  static constexpr int kStage = N * kRingThreads * kBytes;
-  static_assert(kBytes % 16 == 0);
-  static __device__ __forceinline__ void copy(char* stage, const void* from, int64_t stride, int64_t row, int64_t rows, int64_t dim, int t) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * T + t) * V;
-      const bool there = row < rows && c < dim;
-      const char* src = reinterpret_cast<const char*>(static_cast<const Y*>(from) + (there ? row * stride + c : 0));
-      const uint32_t dst = smem_at(stage) + (n * kRingThreads + threadIdx.x) * kBytes;
-#pragma unroll
-      for (int k = 0; k < kBytes; k += 16) copy_async(dst + k, src + k, there);
-    }
-  }
-  static __device__ __forceinline__ void read(const char* stage, int n, float* f) {
-    alignas(16) Y y[V];
-    const uint4* from = reinterpret_cast<const uint4*>(stage + (n * kRingThreads + threadIdx.x) * kBytes);
-#pragma unroll
-    for (int k = 0; k < kBytes / 16; ++k) reinterpret_cast<uint4*>(y)[k] = from[k];
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = widen(y[j]);
-  }
-};
+// The barrier of the T threads that this one's group (T < 32: its warp) has.
+template <int T>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (T <= 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(int(threadIdx.x) / T + 1), "n"(T) : "memory");
+}
 
-// Sums over the T threads of a group, of which a CTA has several.  `which` alternates from
-// sum to sum: a thread is past the barrier of a sum only when all have read the one before.
+// Sums over the threads of a group.  `which` alternates from sum to sum: a thread is past the
+// barrier of one only when all have read the one before.
 template <int T, int K>
 __device__ __forceinline__ void group_sum(float (&v)[K], float (*share)[kRingThreads / 32][K], int which) {
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = row_sum<(T < 32 ? T : 32)>(v[k]);
   if constexpr (T > 32) {
-    const int group = threadIdx.x / T;
-    float(*mine)[K] = share[which] + group * (T / 32);
+    float(*mine)[K] = share[which] + threadIdx.x / T * (T / 32);
     if (threadIdx.x % 32 == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) mine[threadIdx.x % T / 32][k] = v[k];
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
+    group_sync<T>();
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = 0.f;
 #pragma unroll
@@ -372,87 +212,215 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*share)[kRingThr
   }
 }
 
+// Two elements an instruction, each rounded as its own.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
+
 // The rows of a thread: `row` its group's, `first` that of its warp's first group (the groups
-// of a warp advance together), `step` to the next.
+// of a warp advance together), `step` to the next.  (Below 2^32, also those past the last.)
 template <int T>
 struct Walk {
-  int64_t row, first, step;
-  int t;
+  uint32_t row, first, step;
   __device__ __forceinline__ Walk() {
     constexpr int kGroups = kRingThreads / T, kUnit = T < 32 ? 32 : T;
-    t = threadIdx.x % T;
-    step = int64_t(gridDim.x) * kGroups;
-    row = int64_t(blockIdx.x) * kGroups + threadIdx.x / T;
-    first = int64_t(blockIdx.x) * kGroups + threadIdx.x / kUnit * (kUnit / T);
+    step = gridDim.x * kGroups;
+    row = blockIdx.x * kGroups + threadIdx.x / T;
+    first = blockIdx.x * kGroups + threadIdx.x / kUnit * (kUnit / T);
+  }
+  __device__ __forceinline__ void next() {
+    row += step;
+    first += step;
   }
 };
 
-template <typename X, int V, int T, int kStages>
+// One of the matrices that go through the ring.
+struct Stream {
+  const void* p;
+  int64_t stride;
+};
+
+// Rows of Y in a stage of the ring: E columns of them a thread's, as accesses n of V elements
+// from n T V + t V on, or V = 1: columns n T + t, two of them (n, n + 1) at a time.
+template <typename Y, int V, int T, int E>
+struct Columns {
+  static constexpr int kSize = int(sizeof(Y)), kBytes = kSize * V;
+  static constexpr int kGroup = T * E * kSize + (V == 1 ? 16 : 0);   // of a group: V = 1: and the bytes before the row
+  static constexpr int kStage = kRingThreads / T * kGroup;
+  static_assert(kGroup % 16 == 0 && (V == 1 || kBytes % 16 == 0));
+
+  static __device__ __forceinline__ const char* address(Stream s, uint32_t row) {
+    return static_cast<const char*>(s.p) + int64_t(row) * s.stride * kSize;
+  }
+  // Zeros for the columns past a row's end, which no copy writes.
+  static __device__ __forceinline__ void clear(char* stage, int dim) {
+    if constexpr (V > 1) {
+      const int t = threadIdx.x % T;
+      stage += threadIdx.x / T * kGroup + t * kBytes;
+#pragma unroll
+      for (int n = 0; n < E / V; ++n)
+        if (n * T * V >= dim - t * V) {
+#pragma unroll
+          for (int k = 0; k < kBytes; k += 16) *reinterpret_cast<uint4*>(stage + n * T * kBytes + k) = make_uint4(0, 0, 0, 0);
+        }
+    }
+  }
+  // Starts the copies of a row; past the last, zeros where other groups of the warp go on (T < 32).
+  static __device__ __forceinline__ void copy(char* stage, Stream s, uint32_t row, uint32_t rows, int dim) {
+    const int t = threadIdx.x % T;
+    stage += threadIdx.x / T * kGroup;
+    if constexpr (V > 1) {
+      const bool there = row < rows;
+      if (T >= 32 && !there) return;
+      const char* src = address(s, there ? row : 0) + t * kBytes;
+      const uint32_t dst = smem_at(stage) + t * kBytes;
+#pragma unroll
+      for (int n = 0; n < E / V; ++n)
+        if (n * T * V < dim - t * V) {
+#pragma unroll
+          for (int k = 0; k < kBytes; k += 16) copy_async(dst + n * T * kBytes + k, src + n * T * kBytes + k, there);
+        }
+    } else if (row < rows) {
+      const uintptr_t begin = reinterpret_cast<uintptr_t>(address(s, row)), end = begin + dim * kSize, base = begin & ~uintptr_t(15);
+      const uintptr_t lowest = reinterpret_cast<uintptr_t>(s.p), highest = reinterpret_cast<uintptr_t>(address(s, rows - 1)) + dim * kSize;
+      for (uintptr_t p = base + t * 16; p < end; p += T * 16) {
+        if (p >= lowest && p + 16 <= highest) {
+          copy_async(smem_at(stage) + uint32_t(p - base), reinterpret_cast<const void*>(p), true);
+        } else {
+          for (uintptr_t q = p < lowest ? lowest : p; q < p + 16 && q < highest; q += kSize)
+            *reinterpret_cast<Y*>(stage + (q - base)) = *reinterpret_cast<const Y*>(q);
+        }
+      }
+    }
+  }
+  // This thread's columns e ... e + W - 1 (W = V, or two) of the row; V = 1: zeros past its end.
+  static constexpr int W = V == 1 ? 2 : V;
+  static __device__ __forceinline__ void read(const char* stage, int skip, int dim, int e, float2* f) {
+    const int t = threadIdx.x % T;
+    stage += threadIdx.x / T * kGroup;
+    if constexpr (V > 1) {
+      const uint4* from = reinterpret_cast<const uint4*>(stage + t * kBytes + e * T * kSize);
+#pragma unroll
+      for (int k = 0; k < kBytes / 16; ++k) {
+        const uint4 q = from[k];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        if constexpr (kSize == 2) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+        } else {
+          f[2 * k] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+          f[2 * k + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+        }
+      }
+    } else {
+      const Y* from = reinterpret_cast<const Y*>(stage + skip) + t + e * T;
+      f->x = e * T < dim - t ? widen(from[0]) : 0.f;
+      f->y = (e + 1) * T < dim - t ? widen(from[T]) : 0.f;
+    }
+  }
+  // Bytes of a stage before a row's first.
+  static __device__ __forceinline__ int skip(Stream s, uint32_t row) {
+    return V == 1 ? int(reinterpret_cast<uintptr_t>(address(s, row)) & 15) : 0;
+  }
+};
+
+// A thread's columns e ... e + W - 1 of a vector of parameters, `otherwise` where there is none.
+template <int V, int T>
+__device__ __forceinline__ void load_params(const void* p, bool f32, int dim, int e, float otherwise, float* f) {
+  constexpr int W = V == 1 ? 2 : V;
+  const int t = threadIdx.x % T;
+#pragma unroll
+  for (int k = 0; k < W; k += V) {
+    const int c = (e + k) * T + t * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[k + j] = otherwise;
+    if (p && c < dim) load_any<V>(p, f32, c, f + k);
+  }
+}
+
+// And of a row of results.
+template <int V, int T, typename Store>
+__device__ __forceinline__ void store_columns(int dim, int e, const float2* f, Store store) {
+  constexpr int W = V == 1 ? 2 : V;
+  const int t = threadIdx.x % T;
+#pragma unroll
+  for (int k = 0; k < W; k += V) {
+    const int c = (e + k) * T + t * V;
+    if (c < dim) store(c, reinterpret_cast<const float*>(f) + k);
+  }
+}
+
+template <typename X, int V, int T, int E, int kStages>
 __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int E = kHold, N = E / V;
-  using C = Columns<X, V, T, N>;
+  using C = Columns<X, V, T, E>;
+  constexpr int W = C::W;
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][1];
   launch_dependents();
   grid_dependency_wait();
   Walk<T> at;
-  const int t = at.t;
+  const Stream x{a.x, a.x_stride};
+  const int dim = int(a.dim), t = threadIdx.x % T;
+  const uint32_t rows = uint32_t(a.rows);
 #pragma unroll
   for (int d = 0; d < kStages; ++d) {
-    C::copy(ring + d * C::kStage, a.x, a.x_stride, at.row + d * at.step, a.rows, a.dim, t);
+    C::clear(ring + d * C::kStage, dim);
+    C::copy(ring + d * C::kStage, x, at.row + d * at.step, rows, dim);
     copies_issued();
   }
-  float w[E], b[E];
+  alignas(8) float w[E], b[E];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int c = (n * T + t) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      w[n * V + j] = 1.f;
-      b[n * V + j] = 0.f;
-    }
-    if (a.weight && c < a.dim) load_any<V>(a.weight, a.param_f32, c, &w[n * V]);
-    if (a.bias && c < a.dim) load_any<V>(a.bias, a.param_f32, c, &b[n * V]);
+  for (int e = 0; e < E; e += W) {
+    load_params<V, T>(a.weight, a.param_f32, dim, e, 1.f, w + e);
+    load_params<V, T>(a.bias, a.param_f32, dim, e, 0.f, b + e);
   }
-  const float count = float(a.dim);
-  int slot = 0, which = 0;
-  for (; at.first < a.rows; at.first += at.step, at.row += at.step, which ^= 1) {
+  const float count = float(dim);
+  int slot = 0;
+  for (int which = 0; at.first < rows; at.next(), which ^= 1) {
     char* stage = ring + slot * C::kStage;
     slot = slot + 1 == kStages ? 0 : slot + 1;
     copies_wait<kStages - 1>();
-    float f[E], m = 0.f, s[1];
+    if constexpr (V == 1) group_sync<T>();
+    const int skip = C::skip(x, at.row);
+    float2 f[E / 2], part[2] = {};
+    float m = 0.f, s[1];
 #pragma unroll
-    for (int n = 0; n < N; ++n) C::read(stage, n, &f[n * V]);
+    for (int e = 0; e < E; e += W) C::read(stage, skip, dim, e, f + e / 2);
     if (a.center) {
-      s[0] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[0] += f[e];
+      for (int i = 0; i < E / 2; ++i) part[i & 1] = __fadd2_rn(part[i & 1], f[i]);
+      s[0] = sum_of(__fadd2_rn(part[0], part[1]));
       group_sum<T>(s, share, 0);
       m = s[0] / count;
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) f[i] = __fadd2_rn(f[i], both(-m));
+      part[0] = part[1] = both(0.f);
     }
-    s[0] = 0.f;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int e = 0; e < E; e += W) {
+      if constexpr (V > 1) {
+        if (e * T < dim - t * V) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = n * V + j;
-        f[e] -= m;
-        if ((n * T + t) * V < a.dim) s[0] = __fmaf_rn(f[e], f[e], s[0]);
+          for (int i = e / 2; i < (e + V) / 2; ++i) part[i & 1] = __ffma2_rn(f[i], f[i], part[i & 1]);
+        }
+      } else {
+        if (e * T < dim - t) part[0].x = __fmaf_rn(f[e / 2].x, f[e / 2].x, part[0].x);
+        if ((e + 1) * T < dim - t) part[0].y = __fmaf_rn(f[e / 2].y, f[e / 2].y, part[0].y);
       }
+    }
+    s[0] = sum_of(__fadd2_rn(part[0], part[1]));
     group_sum<T>(s, share, a.center ? 1 : which);
-    C::copy(stage, a.x, a.x_stride, at.row + kStages * at.step, a.rows, a.dim, t);   // (what was read is in registers)
+    C::copy(stage, x, at.row + kStages * at.step, rows, dim);   // (all that was read has entered the sum)
     copies_issued();
     const float r = 1.f / sqrtf(s[0] / count + a.eps);
-    if (at.row < a.rows) {
-      if (a.stats && t == 0) a.stats[at.row] = make_float2(m, r);
+    if (at.row >= rows) continue;
+    if (a.stats && t == 0) a.stats[at.row] = make_float2(m, r);
+    const int64_t out = int64_t(at.row) * a.out_stride;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int c = (n * T + t) * V;
-        float y[V];
+    for (int e = 0; e < E; e += W) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = __fmaf_rn(f[n * V + j] * r, w[n * V + j], b[n * V + j]);
-        if (c < a.dim) store_any<V>(a.out, a.out_f32, at.row * a.out_stride + c, y);
-      }
+      for (int i = e / 2; i < (e + W) / 2; ++i)
+        f[i] = __ffma2_rn(__fmul2_rn(f[i], both(r)), make_float2(w[2 * i], w[2 * i + 1]), make_float2(b[2 * i], b[2 * i + 1]));
+      store_columns<V, T>(dim, e, f + e / 2, [&](int c, const float* y) { store_any<V>(a.out, a.out_f32, out + c, y); });
     }
   }
   copies_wait<0>();
@@ -460,103 +428,128 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
 
 // All gradients in one pass over x and dy.  A thread adds its columns' terms of dw and db in
 // registers; the CTA's groups are joined in shared memory at the end, so that a launch leaves
-// one pair of partial sums per CTA.
-template <typename X, typename G, int V, int T, int kStages>
+// one pair of partial sums per CTA.  kKeep: h and g stay in registers from the sums to dx
+// (E = 16); otherwise they are read again.
+template <typename X, typename G, int V, int T, int E, int kStages>
 __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid_constant__ GradArgs a) {
-  constexpr int E = kHold, N = E / V, kGroups = kRingThreads / T;
-  using CX = Columns<X, V, T, N>;
-  using CG = Columns<G, V, T, N>;
-  constexpr int kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
+  constexpr int kGroups = kRingThreads / T;
+  constexpr bool kKeep = E <= 16;
+  using CX = Columns<X, V, T, E>;
+  using CG = Columns<G, V, T, E>;
+  constexpr int W = CX::W, kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][2];
   launch_dependents();
   grid_dependency_wait();
   Walk<T> at;
-  const int t = at.t;
-  auto copy_row = [&](char* stage, int64_t row) {
-    CG::copy(stage, a.grad, a.grad_stride, row, a.rows, a.dim, t);
-    CX::copy(stage + CG::kStage, a.x, a.x_stride, row, a.rows, a.dim, t);
-    if (a.add) CX::copy(stage + CG::kStage + CX::kStage, a.add, a.add_stride, row, a.rows, a.dim, t);
+  const Stream x{a.x, a.x_stride}, dy{a.grad, a.grad_stride}, add{a.add, a.add_stride};
+  const int dim = int(a.dim), t = threadIdx.x % T;
+  const uint32_t rows = uint32_t(a.rows);
+  auto copy_row = [&](char* stage, uint32_t row) {
+    CG::copy(stage, dy, row, rows, dim);
+    CX::copy(stage + CG::kStage, x, row, rows, dim);
+    if (a.add) CX::copy(stage + CG::kStage + CX::kStage, add, row, rows, dim);
     copies_issued();
   };
 #pragma unroll
-  for (int d = 0; d < kStages; ++d) copy_row(ring + d * kStage, at.row + d * at.step);
-  float w[E], dw[E] = {}, db[E] = {};
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int c = (n * T + t) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) w[n * V + j] = 1.f;
-    if (a.weight && c < a.dim) load_any<V>(a.weight, a.weight_f32, c, &w[n * V]);
+  for (int d = 0; d < kStages; ++d) {
+    CG::clear(ring + d * kStage, dim);
+    CX::clear(ring + d * kStage + CG::kStage, dim);
+    copy_row(ring + d * kStage, at.row + d * at.step);
   }
-  const float count = float(a.dim);
-  float2 next = at.row < a.rows ? a.stats[at.row] : make_float2(0.f, 0.f);
+  alignas(8) float w[E];
+  float2 dw[E / 2] = {}, db[E / 2] = {};
+#pragma unroll
+  for (int e = 0; e < E; e += W) load_params<V, T>(a.weight, a.weight_f32, dim, e, 1.f, w + e);
+  const float count = float(dim);
+  float2 next = at.row < rows ? a.stats[at.row] : make_float2(0.f, 0.f);
   int slot = 0;
-  for (int which = 0; at.first < a.rows; which ^= 1) {
+  for (int which = 0; at.first < rows; at.next(), which ^= 1) {
     char* stage = ring + slot * kStage;
     slot = slot + 1 == kStages ? 0 : slot + 1;
-    const float2 st = next;
-    if (at.row + at.step < a.rows) next = a.stats[at.row + at.step];
+    const float2 st = at.row < rows ? next : make_float2(0.f, 0.f);
+    if (at.row + at.step < rows) next = a.stats[at.row + at.step];
     copies_wait<kStages - 1>();
-    float h[E], g[E], s[2] = {0.f, 0.f};
+    if constexpr (V == 1) group_sync<T>();
+    const int skip_dy = CG::skip(dy, at.row), skip_x = CX::skip(x, at.row);
+    const int there = at.row < rows ? dim : 0;   // V = 1: nothing of what an earlier row left
+    float2 h[(kKeep ? E : W) / 2], g[(kKeep ? E : W) / 2], sg = both(0.f), sgh = both(0.f);
+    auto read = [&](int e) {   // columns of dy and h
+      const int i0 = kKeep ? e / 2 : 0;
+      CG::read(stage, skip_dy, there, e, g + i0);
+      CX::read(stage + CG::kStage, skip_x, there, e, h + i0);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      CG::read(stage, n, &g[n * V]);
-      CX::read(stage + CG::kStage, n, &h[n * V]);
+      for (int i = i0; i < i0 + W / 2; ++i) h[i] = __fmul2_rn(__fadd2_rn(h[i], both(-st.x)), both(st.y));
+    };
+    auto weight = [&](int e, int i) { return make_float2(w[e + 2 * i], w[e + 2 * i + 1]); };
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = n * V + j;
-        h[e] = (h[e] - st.x) * st.y;
-        dw[e] = __fmaf_rn(g[e], h[e], dw[e]);
-        db[e] += g[e];
-        g[e] *= w[e];
-        s[0] += g[e];
-        s[1] = __fmaf_rn(g[e], h[e], s[1]);
+    for (int e = 0; e < E; e += W) {
+      read(e);
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const int k = kKeep ? e / 2 + i : i;
+        dw[e / 2 + i] = __ffma2_rn(g[k], h[k], dw[e / 2 + i]);
+        db[e / 2 + i] = __fadd2_rn(db[e / 2 + i], g[k]);
+        g[k] = __fmul2_rn(g[k], weight(e, i));
+        sg = __fadd2_rn(sg, g[k]);
+        sgh = __ffma2_rn(g[k], h[k], sgh);
       }
     }
     if (a.grad_x) {
+      float s[2] = {sum_of(sg), sum_of(sgh)};
       group_sum<T>(s, share, which);
-      const float mean_g = a.center ? s[0] / count : 0.f, mean_gh = s[1] / count;
+      const float2 mean_g = both(a.center ? -s[0] / count : 0.f), mean_gh = both(-s[1] / count), r = both(st.y);
+      const int skip_add = CX::skip(add, at.row);
+      const int64_t out = int64_t(at.row) * a.grad_x_stride;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int c = (n * T + t) * V;
-        float f[V] = {};
-        if (a.add) CX::read(stage + CG::kStage + CX::kStage, n, f);
+      for (int e = 0; e < E; e += W) {
+        float2 f[W / 2] = {};
+        if (a.add) CX::read(stage + CG::kStage + CX::kStage, skip_add, there, e, f);
+        if constexpr (!kKeep) {
+          read(e);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int e = n * V + j;
-          f[j] = __fmaf_rn(st.y, __fmaf_rn(-h[e], mean_gh, g[e] - mean_g), f[j]);
+          for (int i = 0; i < W / 2; ++i) g[i] = __fmul2_rn(g[i], weight(e, i));
         }
-        if (at.row < a.rows && c < a.dim) store_vec<X, V>(static_cast<X*>(a.grad_x) + at.row * a.grad_x_stride + c, f);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const int k = kKeep ? e / 2 + i : i;
+          f[i] = __ffma2_rn(r, __ffma2_rn(h[k], mean_gh, __fadd2_rn(g[k], mean_g)), f[i]);
+        }
+        if (at.row < rows)
+          store_columns<V, T>(dim, e, f, [&](int c, const float* y) { store_vec<X, V>(static_cast<X*>(a.grad_x) + out + c, y); });
       }
     }
+    if constexpr (V == 1) group_sync<T>();   // all have read the stage
     copy_row(stage, at.row + kStages * at.step);
-    at.first += at.step;
-    at.row += at.step;
   }
   copies_wait<0>();
   if (!a.grad_weight && !a.grad_bias) return;
   __syncthreads();
   constexpr int kCols = T * E;
-  float* joined = reinterpret_cast<float*>(ring);   // [2][kGroups][kCols]
-  static_assert(2 * kGroups * kCols * 4 <= kStages * kStage);
+  float* joined = reinterpret_cast<float*>(ring);   // [kGroups][kCols], of dw and then of db
+  static_assert(kGroups * kCols * 4 <= kStages * kStage);
   const int group = threadIdx.x / T;
 #pragma unroll
-  for (int n = 0; n < N; ++n)
+  for (int which = 0; which < 2; ++which) {
+    if (!(which ? a.grad_bias : a.grad_weight)) continue;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (n * T + t) * V + j;
-      joined[group * kCols + c] = dw[n * V + j];
-      joined[(kGroups + group) * kCols + c] = db[n * V + j];
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * kCols; i += kRingThreads) {
-    const int which = i / kCols, c = i % kCols;
-    if (c >= a.dim || !(which ? a.grad_bias : a.grad_weight)) continue;
-    float v = 0.f;
+    for (int e = 0; e < E; e += W)
+      store_columns<V, T>(kCols, e, (which ? db : dw) + e / 2, [&](int c, const float* y) {
+        if constexpr (V == 1) {
+          joined[group * kCols + c] = y[0];
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(&joined[group * kCols + c + j]) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        }
+      });
+    __syncthreads();
+    for (int c = threadIdx.x; c < kCols && c < dim; c += kRingThreads) {
+      float v = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < kGroups; ++k) v += joined[(which * kGroups + k) * kCols + c];
-    a.parts[(int64_t(blockIdx.x) * 2 + which) * a.dim + c] = v;
+      for (int k = 0; k < kGroups; ++k) v += joined[k * kCols + c];
+      a.parts[(int64_t(blockIdx.x) * 2 + which) * a.dim + c] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -737,45 +730,48 @@ fsp_status check_stats(const float* stats) {
   return reinterpret_cast<uintptr_t>(stats) % 8 ? fail(FSP_EINVAL, "stats is not 8-byte aligned") : FSP_OK;
 }
 
-template <typename X, int V, int T, int E, int R>
-fsp_status launch_rows(const NormArgs& a, cudaStream_t st) {
-  constexpr int kThreads = T > 256 ? T : 256, kRows = kThreads / T * R;
-  return launch_next(norm_kernel<X, V, T, E, R>, dim3(unsigned((a.rows + kRows - 1) / kRows)), kThreads, 0, 1, a, st, "layer norm kernel launch");
+template <typename X, int V, int T, int E>
+fsp_status launch_few(const NormArgs& a, cudaStream_t st) {
+  constexpr int kThreads = T > 128 ? T : 128, kRows = kThreads / T;
+  return launch_next(norm_kernel<X, V, T, E>, dim3(unsigned((a.rows + kRows - 1) / kRows)), kThreads, 0, 1, a, st, "layer norm kernel launch");
 }
 
-template <typename X, int V, int T>
+template <typename X, int V, int T, int E>
 fsp_status launch_ring(const NormArgs& a, cudaStream_t st) {
-  constexpr int kStages = sizeof(X) == 2 ? 6 : 4, kSmem = kStages * Columns<X, V, T, kHold / V>::kStage;
-  void (*kernel)(NormArgs) = norm_ring_kernel<X, V, T, kStages>;
+  constexpr int kVec = V == 1 ? 1 : 16 / int(sizeof(X));
+  using C = Columns<X, kVec, T, E>;
+  constexpr int kStages = C::kStage > 48 << 10 ? 3 : C::kStage > 24 << 10 ? 4 : 6;
+  constexpr int kSmem = kStages * C::kStage;
+  static_assert(kSmem <= 226 << 10);
+  void (*kernel)(NormArgs) = norm_ring_kernel<X, kVec, T, E, kStages>;
   const fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   const int64_t ctas = std::min<int64_t>(kParts, (a.rows + kRingThreads / T - 1) / (kRingThreads / T));
   return launch_next(kernel, dim3(unsigned(ctas)), kRingThreads, kSmem, 1, a, st, "layer norm kernel launch");
 }
 
-template <typename X>
-fsp_status launch_norm_vec(const NormArgs& a, cudaStream_t st) {
-  constexpr int V = 16 / int(sizeof(X));
-  if (a.dim <= 8 * kHold) return launch_ring<X, V, 8>(a, st);
-  if (a.dim <= 16 * kHold) return launch_ring<X, V, 16>(a, st);
-  if (a.dim <= 32 * kHold) return launch_ring<X, V, 32>(a, st);
-  if (a.dim <= 64 * kHold) return launch_ring<X, V, 64>(a, st);
-  if (a.dim <= 128 * kHold) return launch_ring<X, V, 128>(a, st);
-  if (a.dim <= 256 * kHold) return launch_ring<X, V, 256>(a, st);
-  return launch_ring<X, V, 512>(a, st);
-}
-
+#ifndef RING_ROWS
+#define RING_ROWS 2048
+#endif
 template <typename X, int V>
 fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
-  if (V > 1 && a.rows >= 1024 && a.dim <= 512 * kHold) return launch_norm_vec<X>(a, st);
-  if (a.dim <= 128) return launch_rows<X, V, 16, 8, 4>(a, st);
-  if (a.dim <= 256) return launch_rows<X, V, 32, 8, 4>(a, st);
-  if (a.dim <= 512) return launch_rows<X, V, 32, 16, 2>(a, st);
-  if (a.dim <= 1024) return launch_rows<X, V, 32, 32, 1>(a, st);
-  if (a.dim <= 2048) return launch_rows<X, V, 32, 64, 1>(a, st);
-  if (a.dim <= 4096) return launch_rows<X, V, 128, 32, 1>(a, st);
-  if (a.dim <= 8192) return launch_rows<X, V, 256, 32, 1>(a, st);
-  if (a.dim <= 16384) return launch_rows<X, V, 512, 32, 1>(a, st);
+  if (a.rows < RING_ROWS) {
+    if (a.dim <= 256) return launch_few<X, V, 32, 8>(a, st);
+    if (a.dim <= 512) return launch_few<X, V, 64, 8>(a, st);
+    if (a.dim <= 1024) return launch_few<X, V, 128, 8>(a, st);
+    if (a.dim <= 2048) return launch_few<X, V, 256, 8>(a, st);
+    if (a.dim <= 4096) return launch_few<X, V, 512, 8>(a, st);
+    if (a.dim <= 8192) return launch_few<X, V, 1024, 8>(a, st);
+  } else {
+    if (a.dim <= 128) return launch_ring<X, V, 8, 16>(a, st);
+    if (a.dim <= 256) return launch_ring<X, V, 16, 16>(a, st);
+    if (a.dim <= 512) return launch_ring<X, V, 32, 16>(a, st);
+    if (a.dim <= 1024) return launch_ring<X, V, 32, 32>(a, st);
+    if (a.dim <= 2048) return launch_ring<X, V, 64, 32>(a, st);
+    if (a.dim <= 4096) return launch_ring<X, V, 128, 32>(a, st);
+    if (a.dim <= 8192) return launch_ring<X, V, 256, 32>(a, st);
+  }
+  if (a.dim <= 16384) return launch_ring<X, V, 512, 32>(a, st);
   return launch_next(wide_norm_kernel<X, V>, dim3(unsigned(a.rows)), kWideThreads, 0, 1, a, st, "layer norm kernel launch");
 }
 
@@ -814,38 +810,16 @@ fsp_status launch_join(const GradArgs& a, cudaStream_t st) {
 }
 
 template <typename X, typename G, int V, int T, int E>
-fsp_status launch_rows_grad(GradArgs a, cudaStream_t st) {
-  constexpr int kGroups = kGradThreads / T, kSmem = 2 * kGroups * T * E * 4;
-  void (*kernel)(GradArgs) = grad_kernel<X, G, V, T, E>;
-  fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
-  if (s != FSP_OK) return s;
-  a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
-  if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kGradThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
-  return s == FSP_OK && (a.grad_weight || a.grad_bias) ? launch_join(a, st) : s;
-}
-
-template <typename X, typename G, int T>
 fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
-  constexpr int V = sizeof(X) + sizeof(G) == 8 ? 4 : 8, N = kHold / V, kGroups = kRingThreads / T;
-  constexpr int kStages = sizeof(X) == 4 ? 2 : sizeof(G) == 4 ? 3 : 4;
-  constexpr int kSmem = kStages * (2 * Columns<X, V, T, N>::kStage + Columns<G, V, T, N>::kStage);
-  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, V, T, kStages>;
+  constexpr int kVec = V == 1 ? 1 : sizeof(X) + sizeof(G) == 8 ? 4 : 8, kGroups = kRingThreads / T;
+  constexpr int kStage = 2 * Columns<X, kVec, T, E>::kStage + Columns<G, kVec, T, E>::kStage;
+  constexpr int kStages = std::min(4, (220 << 10) / kStage), kSmem = kStages * kStage;
+  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, kVec, T, E, kStages>;
   fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
   if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kRingThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
   return s == FSP_OK && (a.grad_weight || a.grad_bias) ? launch_join(a, st) : s;
-}
-
-template <typename X, typename G>
-fsp_status launch_grad_vec(const GradArgs& a, cudaStream_t st) {
-  if (a.dim <= 8 * kHold) return launch_ring_grad<X, G, 8>(a, st);
-  if (a.dim <= 16 * kHold) return launch_ring_grad<X, G, 16>(a, st);
-  if (a.dim <= 32 * kHold) return launch_ring_grad<X, G, 32>(a, st);
-  if (a.dim <= 64 * kHold) return launch_ring_grad<X, G, 64>(a, st);
-  if (a.dim <= 128 * kHold) return launch_ring_grad<X, G, 128>(a, st);
-  if (a.dim <= 256 * kHold) return launch_ring_grad<X, G, 256>(a, st);
-  return launch_ring_grad<X, G, 512>(a, st);
 }
 
 template <typename X, typename G, int V>
@@ -863,17 +837,14 @@ fsp_status launch_wide_grad(const GradArgs& a, cudaStream_t st) {
 
 template <typename X, typename G, int V>
 fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
-  if (V > 1 && a.dim <= 512 * kHold) return launch_grad_vec<X, G>(a, st);
-  // sixteen elements a thread, eight where fp32 rows would not leave the registers for the row ahead
-  constexpr int E = sizeof(X) + sizeof(G) > 4 ? 8 : 16;
-  if (a.dim <= 8 * E) return launch_rows_grad<X, G, V, 8, E>(a, st);
-  if (a.dim <= 16 * E) return launch_rows_grad<X, G, V, 16, E>(a, st);
-  if (a.dim <= 32 * E) return launch_rows_grad<X, G, V, 32, E>(a, st);
-  if (a.dim <= 64 * E) return launch_rows_grad<X, G, V, 64, E>(a, st);
-  if (a.dim <= 128 * E) return launch_rows_grad<X, G, V, 128, E>(a, st);
-  if (a.dim <= 256 * E) return launch_rows_grad<X, G, V, 256, E>(a, st);
-  if (a.dim <= 512 * E) return launch_rows_grad<X, G, V, 512, E>(a, st);
-  if (a.dim <= 1024 * E) return launch_rows_grad<X, G, V, 512, 2 * E>(a, st);
+  if (a.dim <= 128) return launch_ring_grad<X, G, V, 8, 16>(a, st);
+  if (a.dim <= 256) return launch_ring_grad<X, G, V, 16, 16>(a, st);
+  if (a.dim <= 512) return launch_ring_grad<X, G, V, 32, 16>(a, st);
+  if (a.dim <= 1024) return launch_ring_grad<X, G, V, 64, 16>(a, st);
+  if (a.dim <= 2048) return launch_ring_grad<X, G, V, 128, 16>(a, st);
+  if (a.dim <= 4096) return launch_ring_grad<X, G, V, 256, 16>(a, st);
+  if (a.dim <= 8192) return launch_ring_grad<X, G, V, 512, 16>(a, st);
+  if (a.dim <= 16384) return launch_ring_grad<X, G, V, 512, 32>(a, st);
   return launch_wide_grad<X, G, V>(a, st);
 }
 
