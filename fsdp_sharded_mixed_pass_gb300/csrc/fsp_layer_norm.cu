@@ -164,10 +164,11 @@ __global__ void __launch_bounds__(T > 128 ? T : 128) norm_kernel(const __grid_co
 // group's part of a ring of stages in shared memory (cp.async): the copies of kStages - 1
 // rows are in flight while a row is reduced, without registers for them.
 //
-// Rows that begin and end at multiples of 16 bytes (V > 1): a thread copies what it reads
-// itself, so that the ring needs no barriers.  Others (V = 1): the group copies the 16-byte
-// pieces that cover the row and reads element by element, T apart.  A piece that reaches
-// past the matrix's first or last byte is filled with the elements that are the matrix's.
+// Rows that begin and end at multiples of 16 bytes: a thread copies what it reads itself, so
+// that the ring needs no barriers.  Others (kShift): the group copies the 16-byte pieces that
+// cover the row, and a thread reads pairs of elements from wherever they begin; a row of
+// results is laid down in shared memory likewise and leaves in 16-byte pieces.  A piece that
+// reaches past a matrix's first or last byte is filled with the elements that are the matrix's.
 
 constexpr int kRingThreads = 512;
 
@@ -239,25 +240,73 @@ struct Stream {
   int64_t stride;
 };
 
-// Rows of Y in a stage of the ring: E columns of them a thread's, as accesses n of V elements
-// from n T V + t V on, or V = 1: columns n T + t, two of them (n, n + 1) at a time.
+// Which columns a thread of a group of T holds, as E / 2 pairs.  Rows at multiples of 16 bytes:
+// accesses n of V elements, from column (n T + t) V on (V = 4 or 8).  kShift: pair i is columns
+// 2 (i T + t) and the next (V = 2), or 2 i T + t and T further (V = 1, fp32 alone), so that a
+// warp reads words of shared memory side by side.
+template <int V, int T, int E>
+struct Held {
+  static constexpr bool kShift = V < 4;
+  static constexpr int N = kShift ? E / 2 : E / V;        // accesses, or pairs
+  static constexpr int W = kShift ? 2 : V;                // elements of one
+  static constexpr int kStep = V == 1 ? T : 1;            // between the two columns of a pair
+  static __device__ __forceinline__ int thread() { return threadIdx.x % T; }
+  static __device__ __forceinline__ int column(int n) { return V == 1 ? 2 * n * T + thread() : (n * T + thread()) * W; }
+  // Zeros for what lies past the row's end.
+  static __device__ __forceinline__ void mask(int dim, float2 (&f)[E / 2]) {
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) {
+      if ((n + 1) * T * W <= dim) break;   // (whole from here on, for the whole group)
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const int c = column(n) + 2 * i;
+        if (c >= dim) f[n * W / 2 + i].x = 0.f;
+        if (c + kStep >= dim) f[n * W / 2 + i].y = 0.f;
+      }
+    }
+  }
+  // Its columns of a vector of parameters, `otherwise` where there is none.
+  static __device__ __forceinline__ void load(const void* p, bool f32, int dim, float otherwise, float2 (&f)[E / 2]) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) f[i] = both(otherwise);
+    if (!p) return;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = column(n);
+      if constexpr (kShift) {
+        if (c < dim) f[n].x = load_any(p, f32, c);
+        if (c + kStep < dim) f[n].y = load_any(p, f32, c + kStep);
+      } else if (c < dim) {
+        float y[V];
+        load_any<V>(p, f32, c, y);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) f[n * V / 2 + i] = make_float2(y[2 * i], y[2 * i + 1]);
+      }
+    }
+  }
+};
+
+// Rows of Y in a stage of the ring.
 template <typename Y, int V, int T, int E>
 struct Columns {
+  using H = Held<V, T, E>;
+  static constexpr bool kShift = H::kShift;
   static constexpr int kSize = int(sizeof(Y)), kBytes = kSize * V;
-  static constexpr int kGroup = T * E * kSize + (V == 1 ? 16 : 0);   // of a group: V = 1: and the bytes before the row
+  static constexpr int kGroup = T * E * kSize + (kShift ? 32 : 0);   // of a group; kShift: and what surrounds a row
   static constexpr int kStage = kRingThreads / T * kGroup;
-  static_assert(kGroup % 16 == 0 && (V == 1 || kBytes % 16 == 0));
+  static_assert(kGroup % 16 == 0 && (kShift || kBytes % 16 == 0));
 
+  static __device__ __forceinline__ char* group(char* stage) { return stage + threadIdx.x / T * kGroup; }
   static __device__ __forceinline__ const char* address(Stream s, uint32_t row) {
     return static_cast<const char*>(s.p) + int64_t(row) * s.stride * kSize;
   }
   // Zeros for the columns past a row's end, which no copy writes.
   static __device__ __forceinline__ void clear(char* stage, int dim) {
-    if constexpr (V > 1) {
-      const int t = threadIdx.x % T;
-      stage += threadIdx.x / T * kGroup + t * kBytes;
+    if constexpr (!kShift) {
+      const int t = H::thread();
+      stage = group(stage) + t * kBytes;
 #pragma unroll
-      for (int n = 0; n < E / V; ++n)
+      for (int n = 0; n < H::N; ++n)
         if (n * T * V >= dim - t * V) {
 #pragma unroll
           for (int k = 0; k < kBytes; k += 16) *reinterpret_cast<uint4*>(stage + n * T * kBytes + k) = make_uint4(0, 0, 0, 0);
@@ -266,100 +315,148 @@ struct Columns {
   }
   // Starts the copies of a row; past the last, zeros where other groups of the warp go on (T < 32).
   static __device__ __forceinline__ void copy(char* stage, Stream s, uint32_t row, uint32_t rows, int dim) {
-    const int t = threadIdx.x % T;
-    stage += threadIdx.x / T * kGroup;
-    if constexpr (V > 1) {
+    const int t = H::thread();
+    stage = group(stage);
+    if constexpr (!kShift) {
       const bool there = row < rows;
       if (T >= 32 && !there) return;
       const char* src = address(s, there ? row : 0) + t * kBytes;
       const uint32_t dst = smem_at(stage) + t * kBytes;
 #pragma unroll
-      for (int n = 0; n < E / V; ++n)
+      for (int n = 0; n < H::N; ++n)
         if (n * T * V < dim - t * V) {
 #pragma unroll
           for (int k = 0; k < kBytes; k += 16) copy_async(dst + n * T * kBytes + k, src + n * T * kBytes + k, there);
         }
     } else if (row < rows) {
-      const uintptr_t begin = reinterpret_cast<uintptr_t>(address(s, row)), end = begin + dim * kSize, base = begin & ~uintptr_t(15);
+      const uintptr_t begin = reinterpret_cast<uintptr_t>(address(s, row)), base = begin & ~uintptr_t(15);
+      const int bytes = (int(begin - base) + dim * kSize + 15) & ~15;
       const uintptr_t lowest = reinterpret_cast<uintptr_t>(s.p), highest = reinterpret_cast<uintptr_t>(address(s, rows - 1)) + dim * kSize;
-      for (uintptr_t p = base + t * 16; p < end; p += T * 16) {
-        if (p >= lowest && p + 16 <= highest) {
-          copy_async(smem_at(stage) + uint32_t(p - base), reinterpret_cast<const void*>(p), true);
-        } else {
-          for (uintptr_t q = p < lowest ? lowest : p; q < p + 16 && q < highest; q += kSize)
-            *reinterpret_cast<Y*>(stage + (q - base)) = *reinterpret_cast<const Y*>(q);
+      if (base >= lowest && base + bytes <= highest) {
+        for (int k = t * 16; k < bytes; k += T * 16) copy_async(smem_at(stage) + k, reinterpret_cast<const void*>(base + k), true);
+      } else {
+        for (uintptr_t p = base + t * 16; p < base + bytes; p += T * 16) {
+          if (p >= lowest && p + 16 <= highest) {
+            copy_async(smem_at(stage) + uint32_t(p - base), reinterpret_cast<const void*>(p), true);
+          } else {
+            for (uintptr_t q = p < lowest ? lowest : p; q < p + 16 && q < highest; q += kSize)
+              *reinterpret_cast<Y*>(stage + (q - base)) = *reinterpret_cast<const Y*>(q);
+          }
         }
       }
-    }
-  }
-  // This thread's columns e ... e + W - 1 (W = V, or two) of the row; V = 1: zeros past its end.
-  static constexpr int W = V == 1 ? 2 : V;
-  static __device__ __forceinline__ void read(const char* stage, int skip, int dim, int e, float2* f) {
-    const int t = threadIdx.x % T;
-    stage += threadIdx.x / T * kGroup;
-    if constexpr (V > 1) {
-      const uint4* from = reinterpret_cast<const uint4*>(stage + t * kBytes + e * T * kSize);
-#pragma unroll
-      for (int k = 0; k < kBytes / 16; ++k) {
-        const uint4 q = from[k];
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        if constexpr (kSize == 2) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-        } else {
-          f[2 * k] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-          f[2 * k + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-        }
-      }
-    } else {
-      const Y* from = reinterpret_cast<const Y*>(stage + skip) + t + e * T;
-      f->x = e * T < dim - t ? widen(from[0]) : 0.f;
-      f->y = (e + 1) * T < dim - t ? widen(from[T]) : 0.f;
     }
   }
   // Bytes of a stage before a row's first.
   static __device__ __forceinline__ int skip(Stream s, uint32_t row) {
-    return V == 1 ? int(reinterpret_cast<uintptr_t>(address(s, row)) & 15) : 0;
+    return kShift ? int(reinterpret_cast<uintptr_t>(address(s, row)) & 15) : 0;
+  }
+  static __device__ __forceinline__ float2 pair_of(uint32_t w) {   // bf16
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  // This thread's access n of the row, at multiples of 16 bytes.
+  static __device__ __forceinline__ void read(char* stage, int n, float2* f) {
+    const uint4* from = reinterpret_cast<const uint4*>(group(stage) + (n * T + H::thread()) * kBytes);
+#pragma unroll
+    for (int k = 0; k < kBytes / 16; ++k) {
+      const uint4 q = from[k];
+      if constexpr (kSize == 2) {
+        f[0] = pair_of(q.x);
+        f[1] = pair_of(q.y);
+        f[2] = pair_of(q.z);
+        f[3] = pair_of(q.w);
+      } else {
+        f[2 * k] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+        f[2 * k + 1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+      }
+    }
+  }
+  // All of this thread's columns, zeros past the row's end.
+  static __device__ __forceinline__ void read_row(char* stage, int skip, int dim, float2 (&f)[E / 2]) {
+    if constexpr (!kShift) {
+#pragma unroll
+      for (int n = 0; n < H::N; ++n) read(stage, n, f + n * V / 2);
+    } else {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(group(stage) + (skip & ~3));
+      if constexpr (kSize == 4) {
+        from += H::column(0);
+#pragma unroll
+        for (int n = 0; n < H::N; ++n) f[n] = make_float2(__uint_as_float(from[2 * n * T]), __uint_as_float(from[2 * n * T + H::kStep]));
+      } else {
+        from += H::thread();
+        if (skip & 2) {   // (the same for the whole group) pairs across two words
+#pragma unroll
+          for (int n = 0; n < H::N; ++n)
+            f[n] = make_float2(__uint_as_float(from[n * T] & 0xffff0000u), __uint_as_float(from[n * T + 1] << 16));
+        } else {
+#pragma unroll
+          for (int n = 0; n < H::N; ++n) f[n] = pair_of(from[n * T]);
+        }
+      }
+      H::mask(dim, f);
+    }
   }
 };
 
-// A thread's columns e ... e + W - 1 of a vector of parameters, `otherwise` where there is none.
-template <int V, int T>
-__device__ __forceinline__ void load_params(const void* p, bool f32, int dim, int e, float otherwise, float* f) {
-  constexpr int W = V == 1 ? 2 : V;
-  const int t = threadIdx.x % T;
+// A row of results: result(n, f) gives access (or pair) n of a thread.  kShift: by way of
+// `staging`, 16 bytes more than the group's E * T elements in shared memory, which the barriers
+// of the sums before it have left free.  there: whether the group has a row.
+template <typename O, int V, int T, int E, typename Result>
+__device__ __forceinline__ void write_row(O* out, int dim, bool there, char* staging, Result result) {
+  using H = Held<V, T, E>;
+  const int t = H::thread();
+  if constexpr (!H::kShift) {
+    if (!there) return;
 #pragma unroll
-  for (int k = 0; k < W; k += V) {
-    const int c = (e + k) * T + t * V;
+    for (int n = 0; n < H::N; ++n) {
+      float2 f[V / 2];
+      result(n, f);
+      if (H::column(n) < dim) store_vec<O, V>(out + H::column(n), reinterpret_cast<const float*>(f));
+    }
+  } else {
+    // laid down as far from a multiple of 16 bytes as it is in memory, so that whole pieces leave
+    constexpr int kSize = int(sizeof(O));
+    const int ahead = int(reinterpret_cast<uintptr_t>(out) & 15), end = ahead + (there ? dim * kSize : 0);
+    O* to = reinterpret_cast<O*>(staging + ahead) + H::column(0);
+    constexpr int kNext = V == 1 ? 2 * T : T * 2;   // columns from pair to pair
+    float2 f;
+    if (kSize == 2 && V == 2 && (ahead & 2) == 0) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[k + j] = otherwise;
-    if (p && c < dim) load_any<V>(p, f32, c, f + k);
-  }
-}
-
-// And of a row of results.
-template <int V, int T, typename Store>
-__device__ __forceinline__ void store_columns(int dim, int e, const float2* f, Store store) {
-  constexpr int W = V == 1 ? 2 : V;
-  const int t = threadIdx.x % T;
+      for (int n = 0; n < H::N; ++n) {
+        result(n, &f);
+        *reinterpret_cast<__nv_bfloat162*>(to + n * kNext) = __floats2bfloat162_rn(f.x, f.y);
+      }
+    } else {
 #pragma unroll
-  for (int k = 0; k < W; k += V) {
-    const int c = (e + k) * T + t * V;
-    if (c < dim) store(c, reinterpret_cast<const float*>(f) + k);
+      for (int n = 0; n < H::N; ++n) {
+        result(n, &f);
+        to[n * kNext] = narrow<O>(f.x);
+        to[n * kNext + H::kStep] = narrow<O>(f.y);
+      }
+    }
+    group_sync<T>();
+    char* base = reinterpret_cast<char*>(out) - ahead;
+    const int whole = ahead > 0 ? 16 : 0;   // the first whole piece
+    for (int k = whole + t * 16; k + 16 <= end; k += T * 16)
+      __stcs(reinterpret_cast<uint4*>(base + k), *reinterpret_cast<const uint4*>(staging + k));
+    const int head = ahead + t * kSize, tail = max(whole, end & ~15) + t * kSize;   // elements before and after them
+    if (t < 16 / kSize) {
+      if (head < min(whole, end)) *reinterpret_cast<O*>(base + head) = *reinterpret_cast<const O*>(staging + head);
+      if (tail < end) *reinterpret_cast<O*>(base + tail) = *reinterpret_cast<const O*>(staging + tail);
+    }
   }
 }
 
 template <typename X, int V, int T, int E, int kStages>
 __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormArgs a) {
   using C = Columns<X, V, T, E>;
-  constexpr int W = C::W;
+  using H = Held<V, T, E>;
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][1];
   launch_dependents();
   grid_dependency_wait();
   Walk<T> at;
   const Stream x{a.x, a.x_stride};
-  const int dim = int(a.dim), t = threadIdx.x % T;
+  const int dim = int(a.dim);
   const uint32_t rows = uint32_t(a.rows);
 #pragma unroll
   for (int d = 0; d < kStages; ++d) {
@@ -367,24 +464,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
     C::copy(ring + d * C::kStage, x, at.row + d * at.step, rows, dim);
     copies_issued();
   }
-  alignas(8) float w[E], b[E];
-#pragma unroll
-  for (int e = 0; e < E; e += W) {
-    load_params<V, T>(a.weight, a.param_f32, dim, e, 1.f, w + e);
-    load_params<V, T>(a.bias, a.param_f32, dim, e, 0.f, b + e);
-  }
+  float2 w[E / 2], b[E / 2];
+  H::load(a.weight, a.param_f32, dim, 1.f, w);
+  H::load(a.bias, a.param_f32, dim, 0.f, b);
   const float count = float(dim);
   int slot = 0;
   for (int which = 0; at.first < rows; at.next(), which ^= 1) {
     char* stage = ring + slot * C::kStage;
     slot = slot + 1 == kStages ? 0 : slot + 1;
     copies_wait<kStages - 1>();
-    if constexpr (V == 1) group_sync<T>();
-    const int skip = C::skip(x, at.row);
+    if constexpr (H::kShift) group_sync<T>();
     float2 f[E / 2], part[2] = {};
     float m = 0.f, s[1];
-#pragma unroll
-    for (int e = 0; e < E; e += W) C::read(stage, skip, dim, e, f + e / 2);
+    C::read_row(stage, C::skip(x, at.row), dim, f);
     if (a.center) {
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) part[i & 1] = __fadd2_rn(part[i & 1], f[i]);
@@ -393,35 +485,34 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
       m = s[0] / count;
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) f[i] = __fadd2_rn(f[i], both(-m));
+      H::mask(dim, f);
       part[0] = part[1] = both(0.f);
     }
 #pragma unroll
-    for (int e = 0; e < E; e += W) {
-      if constexpr (V > 1) {
-        if (e * T < dim - t * V) {
-#pragma unroll
-          for (int i = e / 2; i < (e + V) / 2; ++i) part[i & 1] = __ffma2_rn(f[i], f[i], part[i & 1]);
-        }
-      } else {
-        if (e * T < dim - t) part[0].x = __fmaf_rn(f[e / 2].x, f[e / 2].x, part[0].x);
-        if ((e + 1) * T < dim - t) part[0].y = __fmaf_rn(f[e / 2].y, f[e / 2].y, part[0].y);
-      }
-    }
+    for (int i = 0; i < E / 2; ++i) part[i & 1] = __ffma2_rn(f[i], f[i], part[i & 1]);
     s[0] = sum_of(__fadd2_rn(part[0], part[1]));
     group_sum<T>(s, share, a.center ? 1 : which);
     C::copy(stage, x, at.row + kStages * at.step, rows, dim);   // (all that was read has entered the sum)
     copies_issued();
     const float r = 1.f / sqrtf(s[0] / count + a.eps);
-    if (at.row >= rows) continue;
-    if (a.stats && t == 0) a.stats[at.row] = make_float2(m, r);
-    const int64_t out = int64_t(at.row) * a.out_stride;
+    const bool there = at.row < rows;
+    if (a.stats && H::thread() == 0 && there) a.stats[at.row] = make_float2(m, r);
+    auto result = [&](int n, float2* y) {
 #pragma unroll
-    for (int e = 0; e < E; e += W) {
-#pragma unroll
-      for (int i = e / 2; i < (e + W) / 2; ++i)
-        f[i] = __ffma2_rn(__fmul2_rn(f[i], both(r)), make_float2(w[2 * i], w[2 * i + 1]), make_float2(b[2 * i], b[2 * i + 1]));
-      store_columns<V, T>(dim, e, f + e / 2, [&](int c, const float* y) { store_any<V>(a.out, a.out_f32, out + c, y); });
-    }
+      for (int i = 0; i < H::W / 2; ++i) {
+        const int k = n * H::W / 2 + i;
+        y[i] = __ffma2_rn(__fmul2_rn(f[k], both(r)), w[k], b[k]);
+      }
+    };
+    auto write = [&](auto* out) {
+      using O = std::remove_pointer_t<decltype(out)>;
+      char* staging = ring + kStages * C::kStage + threadIdx.x / T * (T * E * int(sizeof(O)) + 16);
+      write_row<O, V, T, E>(out + (there ? at.row : 0) * a.out_stride, dim, there, staging, result);
+    };
+    if (a.out_f32)
+      write(static_cast<float*>(a.out));
+    else
+      write(static_cast<__nv_bfloat16*>(a.out));
   }
   copies_wait<0>();
 }
@@ -429,21 +520,23 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
 // All gradients in one pass over x and dy.  A thread adds its columns' terms of dw and db in
 // registers; the CTA's groups are joined in shared memory at the end, so that a launch leaves
 // one pair of partial sums per CTA.  kKeep: h and g stay in registers from the sums to dx
-// (E = 16); otherwise they are read again.
+// (E = 16; kShift: dx then takes x's place in the stage); otherwise they are read again.
 template <typename X, typename G, int V, int T, int E, int kStages>
 __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid_constant__ GradArgs a) {
   constexpr int kGroups = kRingThreads / T;
   constexpr bool kKeep = E <= 16;
+  using H = Held<V, T, E>;
   using CX = Columns<X, V, T, E>;
   using CG = Columns<G, V, T, E>;
-  constexpr int W = CX::W, kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
+  static_assert(kKeep || !H::kShift);
+  constexpr int kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][2];
   launch_dependents();
   grid_dependency_wait();
   Walk<T> at;
   const Stream x{a.x, a.x_stride}, dy{a.grad, a.grad_stride}, add{a.add, a.add_stride};
-  const int dim = int(a.dim), t = threadIdx.x % T;
+  const int dim = int(a.dim);
   const uint32_t rows = uint32_t(a.rows);
   auto copy_row = [&](char* stage, uint32_t row) {
     CG::copy(stage, dy, row, rows, dim);
@@ -457,69 +550,89 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     CX::clear(ring + d * kStage + CG::kStage, dim);
     copy_row(ring + d * kStage, at.row + d * at.step);
   }
-  alignas(8) float w[E];
-  float2 dw[E / 2] = {}, db[E / 2] = {};
-#pragma unroll
-  for (int e = 0; e < E; e += W) load_params<V, T>(a.weight, a.weight_f32, dim, e, 1.f, w + e);
+  float2 w[E / 2], dw[E / 2] = {}, db[E / 2] = {};
+  H::load(a.weight, a.weight_f32, dim, 1.f, w);
   const float count = float(dim);
   float2 next = at.row < rows ? a.stats[at.row] : make_float2(0.f, 0.f);
   int slot = 0;
   for (int which = 0; at.first < rows; at.next(), which ^= 1) {
     char* stage = ring + slot * kStage;
     slot = slot + 1 == kStages ? 0 : slot + 1;
-    const float2 st = at.row < rows ? next : make_float2(0.f, 0.f);
+    const bool there = at.row < rows;
+    const float2 st = there ? next : make_float2(0.f, 0.f);
     if (at.row + at.step < rows) next = a.stats[at.row + at.step];
     copies_wait<kStages - 1>();
-    if constexpr (V == 1) group_sync<T>();
-    const int skip_dy = CG::skip(dy, at.row), skip_x = CX::skip(x, at.row);
-    const int there = at.row < rows ? dim : 0;   // V = 1: nothing of what an earlier row left
-    float2 h[(kKeep ? E : W) / 2], g[(kKeep ? E : W) / 2], sg = both(0.f), sgh = both(0.f);
-    auto read = [&](int e) {   // columns of dy and h
-      const int i0 = kKeep ? e / 2 : 0;
-      CG::read(stage, skip_dy, there, e, g + i0);
-      CX::read(stage + CG::kStage, skip_x, there, e, h + i0);
-#pragma unroll
-      for (int i = i0; i < i0 + W / 2; ++i) h[i] = __fmul2_rn(__fadd2_rn(h[i], both(-st.x)), both(st.y));
+    if constexpr (H::kShift) group_sync<T>();
+    const int end = there ? dim : 0;   // kShift: nothing of what an earlier row left
+    float2 h[(kKeep ? E : V) / 2], g[(kKeep ? E : V) / 2], sg = both(0.f), sgh = both(0.f);
+    auto normalise = [&](float2& x) { x = __fmul2_rn(__fadd2_rn(x, both(-st.x)), both(st.y)); };
+    auto add_terms = [&](int e, float2& g, float2 h) {   // pair e; g becomes dy w
+      dw[e] = __ffma2_rn(g, h, dw[e]);
+      db[e] = __fadd2_rn(db[e], g);
+      g = __fmul2_rn(g, w[e]);
+      sg = __fadd2_rn(sg, g);
+      sgh = __ffma2_rn(g, h, sgh);
     };
-    auto weight = [&](int e, int i) { return make_float2(w[e + 2 * i], w[e + 2 * i + 1]); };
+    if constexpr (kKeep) {
+      CG::read_row(stage, CG::skip(dy, at.row), end, g);
+      CX::read_row(stage + CG::kStage, CX::skip(x, at.row), end, h);
 #pragma unroll
-    for (int e = 0; e < E; e += W) {
-      read(e);
+      for (int e = 0; e < E / 2; ++e) {
+        normalise(h[e]);
+        add_terms(e, g[e], h[e]);
+      }
+    } else {
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) {
-        const int k = kKeep ? e / 2 + i : i;
-        dw[e / 2 + i] = __ffma2_rn(g[k], h[k], dw[e / 2 + i]);
-        db[e / 2 + i] = __fadd2_rn(db[e / 2 + i], g[k]);
-        g[k] = __fmul2_rn(g[k], weight(e, i));
-        sg = __fadd2_rn(sg, g[k]);
-        sgh = __ffma2_rn(g[k], h[k], sgh);
+      for (int n = 0; n < H::N; ++n) {
+        CG::read(stage, n, g);
+        CX::read(stage + CG::kStage, n, h);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          normalise(h[i]);
+          add_terms(n * V / 2 + i, g[i], h[i]);
+        }
       }
     }
     if (a.grad_x) {
       float s[2] = {sum_of(sg), sum_of(sgh)};
       group_sum<T>(s, share, which);
       const float2 mean_g = both(a.center ? -s[0] / count : 0.f), mean_gh = both(-s[1] / count), r = both(st.y);
-      const int skip_add = CX::skip(add, at.row);
-      const int64_t out = int64_t(at.row) * a.grad_x_stride;
+      float2 plus[H::kShift ? E / 2 : 1];
+      if constexpr (H::kShift) {
+        if (a.add) {
+          CX::read_row(stage + CG::kStage + CX::kStage, CX::skip(add, at.row), end, plus);
+        } else {
 #pragma unroll
-      for (int e = 0; e < E; e += W) {
-        float2 f[W / 2] = {};
-        if (a.add) CX::read(stage + CG::kStage + CX::kStage, skip_add, there, e, f);
+          for (int i = 0; i < E / 2; ++i) plus[i] = both(0.f);
+        }
+      }
+      auto result = [&](int n, float2* f) {
+        if constexpr (H::kShift) {
+          f[0] = plus[n];
+        } else {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) f[i] = both(0.f);
+          if (a.add) CX::read(stage + CG::kStage + CX::kStage, n, f);
+        }
         if constexpr (!kKeep) {
-          read(e);
+          CG::read(stage, n, g);
+          CX::read(stage + CG::kStage, n, h);
 #pragma unroll
-          for (int i = 0; i < W / 2; ++i) g[i] = __fmul2_rn(g[i], weight(e, i));
+          for (int i = 0; i < V / 2; ++i) {
+            normalise(h[i]);
+            g[i] = __fmul2_rn(g[i], w[n * V / 2 + i]);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          const int k = kKeep ? e / 2 + i : i;
+        for (int i = 0; i < H::W / 2; ++i) {
+          const int k = kKeep ? n * H::W / 2 + i : i;
           f[i] = __ffma2_rn(r, __ffma2_rn(h[k], mean_gh, __fadd2_rn(g[k], mean_g)), f[i]);
         }
-        if (at.row < rows)
-          store_columns<V, T>(dim, e, f, [&](int c, const float* y) { store_vec<X, V>(static_cast<X*>(a.grad_x) + out + c, y); });
-      }
+      };
+      write_row<X, V, T, E>(static_cast<X*>(a.grad_x) + (there ? at.row : 0) * a.grad_x_stride, dim, there, CX::group(stage + CG::kStage),
+                            result);
     }
-    if constexpr (V == 1) group_sync<T>();   // all have read the stage
+    if constexpr (H::kShift) group_sync<T>();   // all have read the stage
     copy_row(stage, at.row + kStages * at.step);
   }
   copies_wait<0>();
@@ -532,16 +645,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (!(which ? a.grad_bias : a.grad_weight)) continue;
+    const float2* y = which ? db : dw;
+    float* to = joined + group * kCols;
 #pragma unroll
-    for (int e = 0; e < E; e += W)
-      store_columns<V, T>(kCols, e, (which ? db : dw) + e / 2, [&](int c, const float* y) {
-        if constexpr (V == 1) {
-          joined[group * kCols + c] = y[0];
-        } else {
+    for (int n = 0; n < H::N; ++n) {
+      if constexpr (H::kShift) {
+        to[H::column(n)] = y[n].x;
+        to[H::column(n) + H::kStep] = y[n].y;
+      } else {
 #pragma unroll
-          for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(&joined[group * kCols + c + j]) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-        }
-      });
+        for (int i = 0; i < V / 2; i += 2)
+          *reinterpret_cast<float4*>(&to[H::column(n) + 2 * i]) = make_float4(y[n * V / 2 + i].x, y[n * V / 2 + i].y, y[n * V / 2 + i + 1].x, y[n * V / 2 + i + 1].y);
+      }
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < kCols && c < dim; c += kRingThreads) {
       float v = 0.f;
@@ -736,26 +852,31 @@ fsp_status launch_few(const NormArgs& a, cudaStream_t st) {
   return launch_next(norm_kernel<X, V, T, E>, dim3(unsigned((a.rows + kRows - 1) / kRows)), kThreads, 0, 1, a, st, "layer norm kernel launch");
 }
 
-template <typename X, int V, int T, int E>
+// Most shared memory that a ring takes.
+constexpr int kRingBytes = 224 << 10;
+
+template <typename X, bool kShift, int T, int E>
 fsp_status launch_ring(const NormArgs& a, cudaStream_t st) {
-  constexpr int kVec = V == 1 ? 1 : 16 / int(sizeof(X));
-  using C = Columns<X, kVec, T, E>;
-  constexpr int kStages = C::kStage > 48 << 10 ? 3 : C::kStage > 24 << 10 ? 4 : 6;
-  constexpr int kSmem = kStages * C::kStage;
-  static_assert(kSmem <= 226 << 10);
-  void (*kernel)(NormArgs) = norm_ring_kernel<X, kVec, T, E, kStages>;
+  constexpr int V = !kShift ? 16 / int(sizeof(X)) : sizeof(X) == 4 ? 1 : 2;
+  using C = Columns<X, V, T, E>;
+  constexpr int kStaging = kShift ? kRingThreads / T * (T * E * 4 + 16) : 0;
+  constexpr int kStages = std::min((kRingBytes - kStaging) / C::kStage, C::kStage > 48 << 10 ? 3 : C::kStage > 24 << 10 ? 4 : 6);
+  constexpr int kSmem = kStages * C::kStage + kStaging;
+  void (*kernel)(NormArgs) = norm_ring_kernel<X, V, T, E, kStages>;
   const fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   const int64_t ctas = std::min<int64_t>(kParts, (a.rows + kRingThreads / T - 1) / (kRingThreads / T));
   return launch_next(kernel, dim3(unsigned(ctas)), kRingThreads, kSmem, 1, a, st, "layer norm kernel launch");
 }
 
-#ifndef RING_ROWS
-#define RING_ROWS 2048
-#endif
+// From this many elements on the ring pays for its start (few rows or many, us: 256 x 1024
+// 2.1 and 3.0, 1024 x 1024 3.1 and 3.1, 2048 x 1024 5.1 and 3.3; 2048 x 128 2.3 and 2.7,
+// 8192 x 128 3.8 and 2.7; 64 x 8192 2.8 and 3.4, 256 x 8192 6.1 and 3.9).
+constexpr int64_t kRingElements = 3 << 18;
+
 template <typename X, int V>
 fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
-  if (a.rows < RING_ROWS) {
+  if (a.rows * a.dim < kRingElements) {
     if (a.dim <= 256) return launch_few<X, V, 32, 8>(a, st);
     if (a.dim <= 512) return launch_few<X, V, 64, 8>(a, st);
     if (a.dim <= 1024) return launch_few<X, V, 128, 8>(a, st);
@@ -763,15 +884,15 @@ fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
     if (a.dim <= 4096) return launch_few<X, V, 512, 8>(a, st);
     if (a.dim <= 8192) return launch_few<X, V, 1024, 8>(a, st);
   } else {
-    if (a.dim <= 128) return launch_ring<X, V, 8, 16>(a, st);
-    if (a.dim <= 256) return launch_ring<X, V, 16, 16>(a, st);
-    if (a.dim <= 512) return launch_ring<X, V, 32, 16>(a, st);
-    if (a.dim <= 1024) return launch_ring<X, V, 32, 32>(a, st);
-    if (a.dim <= 2048) return launch_ring<X, V, 64, 32>(a, st);
-    if (a.dim <= 4096) return launch_ring<X, V, 128, 32>(a, st);
-    if (a.dim <= 8192) return launch_ring<X, V, 256, 32>(a, st);
+    if (a.dim <= 128) return launch_ring<X, V == 1, 8, 16>(a, st);
+    if (a.dim <= 256) return launch_ring<X, V == 1, 16, 16>(a, st);
+    if (a.dim <= 512) return launch_ring<X, V == 1, 32, 16>(a, st);
+    if (a.dim <= 1024) return launch_ring<X, V == 1, 32, 32>(a, st);
+    if (a.dim <= 2048) return launch_ring<X, V == 1, 64, 32>(a, st);
+    if (a.dim <= 4096) return launch_ring<X, V == 1, 128, 32>(a, st);
+    if (a.dim <= 8192) return launch_ring<X, V == 1, 256, 32>(a, st);
   }
-  if (a.dim <= 16384) return launch_ring<X, V, 512, 32>(a, st);
+  if (a.dim <= 16384) return launch_ring<X, V == 1, 512, 32>(a, st);
   return launch_next(wide_norm_kernel<X, V>, dim3(unsigned(a.rows)), kWideThreads, 0, 1, a, st, "layer norm kernel launch");
 }
 
@@ -809,12 +930,13 @@ fsp_status launch_join(const GradArgs& a, cudaStream_t st) {
                      "layer norm gradient (join) kernel launch");
 }
 
-template <typename X, typename G, int V, int T, int E>
+template <typename X, typename G, bool kShift, int T, int E>
 fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
-  constexpr int kVec = V == 1 ? 1 : sizeof(X) + sizeof(G) == 8 ? 4 : 8, kGroups = kRingThreads / T;
-  constexpr int kStage = 2 * Columns<X, kVec, T, E>::kStage + Columns<G, kVec, T, E>::kStage;
-  constexpr int kStages = std::min(4, (220 << 10) / kStage), kSmem = kStages * kStage;
-  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, kVec, T, E, kStages>;
+  constexpr bool kWide = sizeof(X) + sizeof(G) == 8;
+  constexpr int V = kShift ? (kWide ? 1 : 2) : kWide ? 4 : 8, kGroups = kRingThreads / T;
+  constexpr int kStage = 2 * Columns<X, V, T, E>::kStage + Columns<G, V, T, E>::kStage;
+  constexpr int kStages = std::min(4, kRingBytes / kStage), kSmem = kStages * kStage;
+  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, V, T, E, kStages>;
   fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
@@ -837,14 +959,14 @@ fsp_status launch_wide_grad(const GradArgs& a, cudaStream_t st) {
 
 template <typename X, typename G, int V>
 fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
-  if (a.dim <= 128) return launch_ring_grad<X, G, V, 8, 16>(a, st);
-  if (a.dim <= 256) return launch_ring_grad<X, G, V, 16, 16>(a, st);
-  if (a.dim <= 512) return launch_ring_grad<X, G, V, 32, 16>(a, st);
-  if (a.dim <= 1024) return launch_ring_grad<X, G, V, 64, 16>(a, st);
-  if (a.dim <= 2048) return launch_ring_grad<X, G, V, 128, 16>(a, st);
-  if (a.dim <= 4096) return launch_ring_grad<X, G, V, 256, 16>(a, st);
-  if (a.dim <= 8192) return launch_ring_grad<X, G, V, 512, 16>(a, st);
-  if (a.dim <= 16384) return launch_ring_grad<X, G, V, 512, 32>(a, st);
+  if (a.dim <= 128) return launch_ring_grad<X, G, V == 1, 8, 16>(a, st);
+  if (a.dim <= 256) return launch_ring_grad<X, G, V == 1, 16, 16>(a, st);
+  if (a.dim <= 512) return launch_ring_grad<X, G, V == 1, 32, 16>(a, st);
+  if (a.dim <= 1024) return launch_ring_grad<X, G, V == 1, 64, 16>(a, st);
+  if (a.dim <= 2048) return launch_ring_grad<X, G, V == 1, 128, 16>(a, st);
+  if (a.dim <= 4096) return launch_ring_grad<X, G, V == 1, 256, 16>(a, st);
+  if (a.dim <= 8192) return launch_ring_grad<X, G, V == 1, 512, 16>(a, st);
+  if (V > 1 && a.dim <= 16384) return launch_ring_grad<X, G, false, 512, 32>(a, st);
   return launch_wide_grad<X, G, V>(a, st);
 }
 
