@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 8;   // elements that a block of the generator serves
+constexpr int kRounds = 10;
 
 struct DropoutArgs {
   const void* x;
@@ -26,20 +27,20 @@ struct DropoutArgs {
   const int64_t* call_dev;   // NULL: `call`
   int64_t n, dim, x_stride, residual_stride, out_stride;
   int64_t call;
-  uint32_t key[2];
-  uint32_t dropped;          // of 65536
+  uint32_t key[kRounds][2];  // of each round
+  uint32_t dropped;          // T
   float scale;
 };
 
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+__device__ __forceinline__ void philox(uint32_t (&c)[4], const DropoutArgs& a) {
 #pragma unroll
-  for (int round = 0; round < 10; ++round) {
-    const uint64_t u = uint64_t(0xD2511F53u) * c.x, v = uint64_t(0xCD9E8D57u) * c.z;
-    c = make_uint4(uint32_t(v >> 32) ^ c.y ^ k0, uint32_t(v), uint32_t(u >> 32) ^ c.w ^ k1, uint32_t(u));
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+  for (int round = 0; round < kRounds; ++round) {
+    const uint64_t u = uint64_t(0xD2511F53u) * c[0], v = uint64_t(0xCD9E8D57u) * c[2];
+    c[0] = uint32_t(v >> 32) ^ c[1] ^ a.key[round][0];
+    c[2] = uint32_t(u >> 32) ^ c[3] ^ a.key[round][1];
+    c[1] = uint32_t(v);
+    c[3] = uint32_t(u);
   }
-  return c;
 }
 
 struct None {};   // no residual
@@ -50,56 +51,83 @@ __device__ __forceinline__ float one(float x, float scale, float residual, bool 
   return keep ? x * scale : 0.f;   // (a select: what is dropped may be infinite or NaN)
 }
 
-// One thread: a block of the generator.  kVec: its elements are one access each (of a flat
-// buffer, or within a row); otherwise element by element.
-template <typename X, typename R, typename O, bool kVec>
+enum Shape { kFlat, kRows, kAny };   // blocks that are one access each: of a flat buffer, or within its rows; any other
+
+// A thread: kPer blocks of the generator, kThreads apart.  The loads of all of them come first
+// and none waits for the generator.  (CTAs that stay and prefetch: 2^26 bf16 elements 50 to 57
+// us, with a residual 64 to 79.)
+template <typename X, typename R, typename O, Shape kShape, int kPer>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutArgs a) {
   constexpr bool kAdd = !std::is_same_v<R, None>;
+  using RT = std::conditional_t<kAdd, R, float>;
   launch_dependents();
   grid_dependency_wait();
-  const int64_t b = int64_t(blockIdx.x) * kThreads + threadIdx.x, i0 = b * kBlock;
-  if (i0 >= a.n) return;
+  const int64_t first = int64_t(blockIdx.x) * (kThreads * kPer) + threadIdx.x;
   const int64_t call = a.call_dev ? *a.call_dev : a.call;
-  const uint4 w4 = philox(make_uint4(uint32_t(b), uint32_t(b >> 32), uint32_t(call), uint32_t(uint64_t(call) >> 32)), a.key[0], a.key[1]);
-  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-  auto keep = [&](int j) { return (j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu) >= a.dropped; };
-  const int64_t row = i0 / a.dim, col = i0 - row * a.dim;
-  if (kVec && i0 + kBlock <= a.n) {
-    float f[kBlock], r[kBlock] = {};
-    load_vec<X, kBlock>(static_cast<const X*>(a.x) + row * a.x_stride + col, f);
-    if constexpr (kAdd) load_vec<R, kBlock>(static_cast<const R*>(a.residual) + row * a.residual_stride + col, r);
+  const X* x = static_cast<const X*>(a.x);
+  const RT* residual = static_cast<const RT*>(a.residual);
+  O* out = static_cast<O*>(a.out);
+  // element i's place, by a row stride
+  auto place = [&](int64_t i, int64_t stride) { return kShape == kFlat ? i : i / a.dim * stride + i % a.dim; };
+  alignas(32) X xs[kPer][kBlock];
+  alignas(32) RT rs[kPer][kBlock];
 #pragma unroll
-    for (int j = 0; j < kBlock; ++j) f[j] = one<kAdd>(f[j], a.scale, r[j], keep(j));
-    store_vec<O, kBlock>(static_cast<O*>(a.out) + row * a.out_stride + col, f);
-    return;
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t i0 = (first + k * kThreads) * kBlock;
+    if (kShape != kAny && i0 + kBlock <= a.n) {
+      load_raw<X, kBlock>(x + place(i0, a.x_stride), xs[k]);
+      if constexpr (kAdd) load_raw<RT, kBlock>(residual + place(i0, a.residual_stride), rs[k]);
+    }
   }
-  int64_t y = row, c = col;
 #pragma unroll
-  for (int j = 0; j < kBlock; ++j) {
-    if (i0 + j >= a.n) break;
-    float r = 0.f;
-    if constexpr (kAdd) r = widen(static_cast<const R*>(a.residual)[y * a.residual_stride + c]);
-    const float f = one<kAdd>(widen(static_cast<const X*>(a.x)[y * a.x_stride + c]), a.scale, r, keep(j));
-    static_cast<O*>(a.out)[y * a.out_stride + c] = narrow<O>(f);
-    if (++c == a.dim) {
-      c = 0;
-      ++y;
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t b = first + k * kThreads, i0 = b * kBlock;
+    if (i0 >= a.n) return;
+    uint32_t w[4] = {uint32_t(b), uint32_t(uint64_t(b) >> 32), uint32_t(call), uint32_t(uint64_t(call) >> 32)};
+    philox(w, a);
+    auto keep = [&](int j) { return (j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu) >= a.dropped; };
+    if (kShape != kAny && i0 + kBlock <= a.n) {
+      float f[kBlock];
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) f[j] = one<kAdd>(widen(xs[k][j]), a.scale, kAdd ? widen(rs[k][j]) : 0.f, keep(j));
+      store_vec<O, kBlock>(out + place(i0, a.out_stride), f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) {
+        const int64_t i = i0 + j;
+        if (i >= a.n) break;
+        float r = 0.f;
+        if constexpr (kAdd) r = widen(residual[place(i, a.residual_stride)]);
+        out[place(i, a.out_stride)] = narrow<O>(one<kAdd>(widen(x[place(i, a.x_stride)]), a.scale, r, keep(j)));
+      }
     }
   }
 }
 
-template <typename X, typename R, typename O>
-fsp_status launch_dropout(const DropoutArgs& a, bool vec, cudaStream_t st) {
-  const int64_t ctas = ((a.n + kBlock - 1) / kBlock + kThreads - 1) / kThreads;
+// With a residual a thread takes four blocks from this many elements on (bf16, us, one block
+// and four: 2^22 5.7 and 6.1, 2^23 9.6 and 9.3, 2^24 17.2 and 15.9, 2^26 63.0 and 57.2); without
+// one a block (2^24 12.4 and 13.8, 2^26 44.0 and 46.0).
+constexpr int64_t kManyElements = int64_t(1) << 23;
+
+template <typename X, typename R, typename O, Shape kShape, int kPer>
+fsp_status launch_blocks(const DropoutArgs& a, cudaStream_t st) {
+  const int64_t blocks = (a.n + kBlock - 1) / kBlock, ctas = (blocks + kThreads * kPer - 1) / (kThreads * kPer);
   if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "too many elements");
-  return launch_next(vec ? dropout_kernel<X, R, O, true> : dropout_kernel<X, R, O, false>, dim3(unsigned(ctas)), kThreads, 0, 1, a, st,
-                     "dropout kernel launch");
+  return launch_next(dropout_kernel<X, R, O, kShape, kPer>, dim3(unsigned(ctas)), kThreads, 0, 1, a, st, "dropout kernel launch");
+}
+
+template <typename X, typename R, typename O>
+fsp_status launch_dropout(const DropoutArgs& a, Shape shape, cudaStream_t st) {
+  if (shape == kAny) return launch_blocks<X, R, O, kAny, 1>(a, st);
+  if constexpr (!std::is_same_v<R, None>)
+    if (a.n >= kManyElements) return shape == kFlat ? launch_blocks<X, R, O, kFlat, 4>(a, st) : launch_blocks<X, R, O, kRows, 4>(a, st);
+  return shape == kFlat ? launch_blocks<X, R, O, kFlat, 1>(a, st) : launch_blocks<X, R, O, kRows, 1>(a, st);
 }
 
 template <typename X, typename O>
-fsp_status launch_residual(const DropoutArgs& a, int32_t rd, bool vec, cudaStream_t st) {
-  if (!a.residual) return launch_dropout<X, None, O>(a, vec, st);
-  return rd == FSP_DTYPE_F32 ? launch_dropout<X, float, O>(a, vec, st) : launch_dropout<X, __nv_bfloat16, O>(a, vec, st);
+fsp_status launch_residual(const DropoutArgs& a, int32_t rd, Shape shape, cudaStream_t st) {
+  if (!a.residual) return launch_dropout<X, None, O>(a, shape, st);
+  return rd == FSP_DTYPE_F32 ? launch_dropout<X, float, O>(a, shape, st) : launch_dropout<X, __nv_bfloat16, O>(a, shape, st);
 }
 
 fsp_status dropout(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs, double p, uint64_t seed, int64_t call,
@@ -117,19 +145,36 @@ fsp_status dropout(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t
                          {call_dev, call_dev ? size_t(8) : 0, "call_dev"}};
   s = check_operands(&to, 1, ins, 3);
   if (s != FSP_OK) return s;
-  DropoutArgs a{x, residual, out, call_dev, rows * dim, dim, xs, rs, os, call, {uint32_t(seed), uint32_t(seed >> 32)}, 0, 0.f};
+  DropoutArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.out = out;
+  a.call_dev = call_dev;
+  a.n = rows * dim;
+  a.dim = dim;
+  a.x_stride = xs;
+  a.residual_stride = rs;
+  a.out_stride = os;
+  a.call = call;
+  uint32_t key[2] = {uint32_t(seed), uint32_t(seed >> 32)};
+  for (auto& k : a.key) {
+    k[0] = key[0];
+    k[1] = key[1];
+    key[0] += 0x9E3779B9u;
+    key[1] += 0xBB67AE85u;
+  }
   a.dropped = uint32_t(p * 65536.0 + 0.5);
   a.scale = a.dropped < 65536u ? float(65536.0 / double(65536u - a.dropped)) : 0.f;
-  // rows without gaps are one flat row
-  if (rows == 1 || (xs == dim && os == dim && (!residual || rs == dim))) a.dim = a.n;
-  const bool aligned = rows_fit(x, 0, xd, kBlock) && rows_fit(out, 0, od, kBlock) && (!residual || rows_fit(residual, 0, rd, kBlock));
-  const bool vec = aligned && (a.dim == a.n || (dim % kBlock == 0 && rows_fit(x, xs, xd, kBlock) && rows_fit(out, os, od, kBlock) &&
-                                                (!residual || rows_fit(residual, rs, rd, kBlock))));
+  const bool flat = rows == 1 || (xs == dim && os == dim && (!residual || rs == dim));   // no gaps between the rows
+  auto fits = [&](int64_t fx, int64_t fo, int64_t fr) {
+    return rows_fit(x, fx, xd, kBlock) && rows_fit(out, fo, od, kBlock) && (!residual || rows_fit(residual, fr, rd, kBlock));
+  };
+  const Shape shape = flat && fits(0, 0, 0) ? kFlat : dim % kBlock == 0 && fits(xs, os, rs) ? kRows : kAny;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   using B = __nv_bfloat16;
   if (xd == FSP_DTYPE_F32)
-    return od == FSP_DTYPE_F32 ? launch_residual<float, float>(a, rd, vec, st) : launch_residual<float, B>(a, rd, vec, st);
-  return od == FSP_DTYPE_F32 ? launch_residual<B, float>(a, rd, vec, st) : launch_residual<B, B>(a, rd, vec, st);
+    return od == FSP_DTYPE_F32 ? launch_residual<float, float>(a, rd, shape, st) : launch_residual<float, B>(a, rd, shape, st);
+  return od == FSP_DTYPE_F32 ? launch_residual<B, float>(a, rd, shape, st) : launch_residual<B, B>(a, rd, shape, st);
 }
 
 }  // namespace
