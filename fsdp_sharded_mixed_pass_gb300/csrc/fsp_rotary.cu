@@ -36,12 +36,35 @@ struct RotaryArgs {
   int64_t n_threads, tokens;
   float scale;
   int index_bytes;
-  int groups;                 // threads along a head
+  int turning;                // threads along the rotated part of a head
+  int units;                  // and along all of it
   int splits;                 // threads along the heads of a token
   int heads;                  // of both tensors
   int rotary_dim;
+  int run_step, second;       // elements from unit to unit of the rotated part, and from its first run to its second
   bool inverse;
 };
+
+// Sine and cosine of an angle in units of 2^-32 turn.  The nearest quarter is taken off in
+// whole numbers; what is left, r in [-pi/4, pi/4], goes through the Taylor series up to r^9 / 9!
+// and r^10 / 10! (what follows is below 2^-29 and 2^-32 of the result).
+__device__ __forceinline__ void sine_cosine(uint32_t angle, float* sine, float* cosine) {
+  const uint32_t quarter = (angle + 0x20000000u) >> 30;
+  const float r = float(int32_t(angle - (quarter << 30))) * 1.46291807926715968e-9f;   // pi / 2^31
+  const float q = r * r;
+  float s = __fmaf_rn(q, 1.f / 362880.f, -1.f / 5040.f), c = __fmaf_rn(q, -1.f / 3628800.f, 1.f / 40320.f);
+  s = __fmaf_rn(q, s, 1.f / 120.f);
+  c = __fmaf_rn(q, c, -1.f / 720.f);
+  s = __fmaf_rn(q, s, -1.f / 6.f);
+  c = __fmaf_rn(q, c, 1.f / 24.f);
+  s = __fmaf_rn(r * q, s, r);
+  c = __fmaf_rn(q, c, -0.5f);
+  c = __fmaf_rn(q, c, 1.f);
+  // quarters 1 and 3 swap the two; the sine is negative in 2 and 3, the cosine in 1 and 2
+  const float a = quarter & 1u ? c : s, b = quarter & 1u ? s : c;
+  *sine = __uint_as_float(__float_as_uint(a) ^ ((quarter & 2u) << 30));
+  *cosine = __uint_as_float(__float_as_uint(b) ^ (((quarter + 1u) & 2u) << 30));
+}
 
 // (spelt out, so that every layout and width rounds alike)
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
@@ -50,76 +73,87 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = p;
 }
 
-// A thread: P pairs of every splits-th head of one token.  kHalf: pair j is elements j and
-// j + rotary_dim / 2, otherwise 2 j and 2 j + 1.  V: elements of an access.
-template <typename T, int V, bool kHalf>
+// A thread: one unit of every splits-th head of one token, so that its sines and cosines are
+// computed once.  A unit is a few pairs of the rotated part - kRuns = 2: the pairs of a run of V
+// elements with another one, kRuns = 1: V / 2 pairs of neighbours - or V elements that are
+// copied.  The loads of kHeads heads come before their stores.
+template <typename T, int V, int kRuns>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-  constexpr int P = kHalf ? V : (V > 1 ? V / 2 : 1);
+  constexpr int kPairs = V * kRuns / 2;
+  constexpr int kHeads = V * int(sizeof(T)) * kRuns > 32 ? 2 : 4;
   launch_dependents();
   grid_dependency_wait();
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= a.n_threads) return;
-  const int group = int(i % a.groups);
-  const int64_t rest = i / a.groups;
-  const int split = int(rest % a.splits);
-  const int64_t token = rest / a.splits, batch = token / a.tokens, at = token - batch * a.tokens;
-  const int64_t index = batch * a.positions_stride + at;
-  const int64_t pos = a.index_bytes == 8 ? static_cast<const int64_t*>(a.positions)[index] : static_cast<const int32_t*>(a.positions)[index];
-  float c[P], s[P];
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    const int pair = group * P + j;
-    // turns, as a signed fraction of 2^32 (below half a unit of 2^-31 half turns is cut off)
-    const int32_t part = pair < a.rotary_dim / 2 ? int32_t(uint64_t(pos) * a.phases[pair] >> 32) : 0;
-    sincospif(float(part) * 0x1p-31f, &s[j], &c[j]);
-    c[j] *= a.scale;
-    s[j] *= a.inverse ? -a.scale : a.scale;
+  int unit, split;
+  int64_t token, batch, at;
+  if (a.n_threads <= UINT32_MAX) {   // (32-bit divisions)
+    uint32_t k = uint32_t(i);
+    unit = int(k % uint32_t(a.units));
+    k /= uint32_t(a.units);
+    split = int(k % uint32_t(a.splits));
+    k /= uint32_t(a.splits);
+    token = k;
+    batch = k / uint32_t(a.tokens);
+    at = k % uint32_t(a.tokens);
+  } else {
+    int64_t k = i;
+    unit = int(k % a.units);
+    k /= a.units;
+    split = int(k % a.splits);
+    token = k / a.splits;
+    batch = token / a.tokens;
+    at = token % a.tokens;
   }
-  for (int h = split; h < a.heads; h += a.splits) {
-    const bool second = h >= a.t[0].heads;
-    const Tensor& t = second ? a.t[1] : a.t[0];
-    const int head = second ? h - a.t[0].heads : h;
-    const T* x = static_cast<const T*>(t.x) + batch * t.x_stride[0] + at * t.x_stride[1] + head * t.x_stride[2];
-    T* out = static_cast<T*>(t.out) + batch * t.out_stride[0] + at * t.out_stride[1] + head * t.out_stride[2];
-    if constexpr (kHalf) {
-      const int first = group * P;
-      if (first < a.rotary_dim / 2) {
-        float u[V], v[V];
-        load_vec<T, V>(x + first, u);
-        load_vec<T, V>(x + a.rotary_dim / 2 + first, v);
+  const bool turns = unit < a.turning;
+  float c[kPairs], s[kPairs];
+  if (turns) {
+    const int64_t index = batch * a.positions_stride + at;
+    const int64_t pos = a.index_bytes == 8 ? static_cast<const int64_t*>(a.positions)[index] : static_cast<const int32_t*>(a.positions)[index];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          turn(u[j], v[j], c[j], s[j]);
-        }
-        store_vec<T, V>(out + first, u);
-        store_vec<T, V>(out + a.rotary_dim / 2 + first, v);
-      }
-    } else {
-      const int first = group * 2 * P;
-      if (first < a.rotary_dim) {
-        float u[2 * P];
-        if constexpr (V == 1) {
-          u[0] = widen(x[first]);
-          u[1] = widen(x[first + 1]);
-        } else {
-          load_vec<T, V>(x + first, u);
-        }
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          turn(u[2 * j], u[2 * j + 1], c[j], s[j]);
-        }
-        if constexpr (V == 1) {
-          out[first] = narrow<T>(u[0]);
-          out[first + 1] = narrow<T>(u[1]);
-        } else {
-          store_vec<T, V>(out + first, u);
-        }
-      }
+    for (int j = 0; j < kPairs; ++j) {
+      sine_cosine(uint32_t(uint64_t(pos) * a.phases[unit * kPairs + j] >> 32), &s[j], &c[j]);
+      c[j] *= a.scale;
+      s[j] *= a.inverse ? -a.scale : a.scale;
     }
-    for (int k = group * V; k < t.rest; k += a.groups * V) {
-      alignas(32) float f[V];
-      load_vec<T, V>(x + a.rotary_dim + k, f);
-      store_vec<T, V>(out + a.rotary_dim + k, f);
+  }
+  const int begin = turns ? unit * a.run_step : a.rotary_dim + (unit - a.turning) * V;
+  for (int h0 = split; h0 < a.heads; h0 += kHeads * a.splits) {
+    alignas(32) T x[kHeads][kRuns][V];
+    T* out[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int h = h0 + k * a.splits;
+      out[k] = nullptr;
+      if (h >= a.heads) continue;
+      const bool later = h >= a.t[0].heads;
+      const Tensor& t = later ? a.t[1] : a.t[0];
+      if (!turns && begin - a.rotary_dim >= t.rest) continue;
+      const int head = later ? h - a.t[0].heads : h;
+      const T* from = static_cast<const T*>(t.x) + batch * t.x_stride[0] + at * t.x_stride[1] + head * t.x_stride[2] + begin;
+      out[k] = static_cast<T*>(t.out) + batch * t.out_stride[0] + at * t.out_stride[1] + head * t.out_stride[2] + begin;
+      load_raw<T, V>(from, x[k][0]);
+      if (kRuns == 2 && turns) load_raw<T, V>(from + a.second, x[k][kRuns - 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      if (!out[k]) continue;
+      float f[kRuns][V];
+#pragma unroll
+      for (int n = 0; n < kRuns; ++n)
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[n][j] = widen(x[k][n][j]);
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          if constexpr (kRuns == 2)
+            turn(f[0][j], f[kRuns - 1][j], c[j], s[j]);
+          else
+            turn(f[0][2 * j], f[0][2 * j + 1], c[j], s[j]);
+        }
+      }
+      store_vec<T, V>(out[k], f[0]);
+      if (kRuns == 2 && turns) store_vec<T, V>(out[k] + a.second, f[kRuns - 1]);
     }
   }
 }
@@ -205,13 +239,21 @@ bool fits(const View& v, int elems) {
   return ok;
 }
 
-template <typename T, int V>
-fsp_status launch_rotary(const RotaryArgs& a, bool half, cudaStream_t st) {
+template <typename T, int V, int kRuns>
+fsp_status launch_rotary(const RotaryArgs& a, cudaStream_t st) {
   const int64_t ctas = (a.n_threads + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "too many tokens");
-  return launch_next(half ? rotary_kernel<T, V, true> : rotary_kernel<T, V, false>, dim3(unsigned(ctas)), kThreads, 0, 1, a, st,
-                     "rotary kernel launch");
+  return launch_next(rotary_kernel<T, V, kRuns>, dim3(unsigned(ctas)), kThreads, 0, 1, a, st, "rotary kernel launch");
 }
+
+template <typename T>
+fsp_status launch_width(const RotaryArgs& a, int v, int runs, cudaStream_t st) {
+  if (runs == 1) return v == 8 ? launch_rotary<T, 8, 1>(a, st) : launch_rotary<T, 2, 1>(a, st);
+  return v == 8 ? launch_rotary<T, 8, 2>(a, st) : v == 2 ? launch_rotary<T, 2, 2>(a, st) : launch_rotary<T, 1, 2>(a, st);
+}
+
+// Threads that a launch spreads a token's heads for, where there are few tokens.
+constexpr int64_t kEnoughThreads = 152 * 1536;
 
 fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, int64_t batch, int64_t tokens,
                   const void* positions, int32_t index_bytes, int64_t positions_stride, const uint64_t* phases,
@@ -271,25 +313,32 @@ fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, in
   for (int i = 0; i < n_views && s == FSP_OK; ++i)
     s = check_allocation(views[i].p, size_t(span_of(views[i]) * views[i].size), views[i].name.c_str());
   if (s != FSP_OK) return s;
-  // accesses of eight elements where every head, half and rest begins at a multiple of them
+  // the widest accesses at which every head, half and rest begins
   const bool half = layout == FSP_ROTARY_HALF;
-  bool vec = rotary_dim % (half ? 16 : 8) == 0;
-  for (int i = 0; i < n_views; ++i) vec = vec && fits(views[i], 8) && views[i].head_dim % 8 == 0;
-  const int pairs = vec ? (half ? 8 : 4) : 1;
+  auto fit = [&](int k) {
+    bool ok = rotary_dim % (half ? 2 * k : k) == 0;
+    for (int i = 0; i < n_views; ++i) ok = ok && fits(views[i], k) && views[i].head_dim % k == 0;
+    return ok;
+  };
+  const int v = fit(8) ? 8 : fit(2) ? 2 : 1;
+  const int runs = half || v == 1 ? 2 : 1;
   a.positions = positions;
   a.phases = phases;
   a.positions_stride = positions_stride;
   a.tokens = tokens;
   a.scale = scale;
   a.index_bytes = index_bytes;
-  a.groups = int(rotary_dim / 2 / pairs);
-  a.splits = std::min(a.heads, 4);
+  a.turning = int(rotary_dim / (v * runs));
+  a.units = a.turning + (std::max(a.t[0].rest, a.t[1].rest) + v - 1) / v;
   a.rotary_dim = int(rotary_dim);
+  a.run_step = half ? v : v * runs;
+  a.second = half ? int(rotary_dim / 2) : 1;
   a.inverse = inverse != 0;
-  a.n_threads = batch * tokens * a.splits * a.groups;
+  const int64_t alone = batch * tokens * a.units;
+  a.splits = int(std::clamp<int64_t>(kEnoughThreads / alone, 1, a.heads));
+  a.n_threads = alone * a.splits;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == FSP_DTYPE_F32) return vec ? launch_rotary<float, 8>(a, half, st) : launch_rotary<float, 1>(a, half, st);
-  return vec ? launch_rotary<__nv_bfloat16, 8>(a, half, st) : launch_rotary<__nv_bfloat16, 1>(a, half, st);
+  return dtype == FSP_DTYPE_F32 ? launch_width<float>(a, v, runs, st) : launch_width<__nv_bfloat16>(a, v, runs, st);
 }
 
 }  // namespace

@@ -52,9 +52,11 @@ __device__ __forceinline__ void load_raw(const T* p, T* x) {
         : "l"(p));
   } else if constexpr (kBytes == 16) {
     *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
-  } else {
-    static_assert(kBytes == 8);
+  } else if constexpr (kBytes == 8) {
     *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(p);
+  } else {
+    static_assert(kBytes == 4);
+    *w = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 template <typename T, int V>
@@ -80,9 +82,11 @@ __device__ __forceinline__ void store_vec(T* p, const float* f) {
                  : "memory");
   } else if constexpr (kBytes == 16) {
     __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(t));
-  } else {
-    static_assert(kBytes == 8);
+  } else if constexpr (kBytes == 8) {
     __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(t));
+  } else {
+    static_assert(kBytes == 4);
+    __stcs(reinterpret_cast<uint32_t*>(p), *w);
   }
 }
 
