@@ -10,6 +10,7 @@
 // arithmetic in 64-bit floating point.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fsp_rows.cuh"
 
@@ -77,10 +78,14 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // computed once.  A unit is a few pairs of the rotated part - kRuns = 2: the pairs of a run of V
 // elements with another one, kRuns = 1: V / 2 pairs of neighbours - or V elements that are
 // copied.  The loads of kHeads heads come before their stores.
+#ifndef HEADS
+#define HEADS 4
+#define MINB 1
+#endif
 template <typename T, int V, int kRuns>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, kRuns == 1 ? 4 : 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int kPairs = V * kRuns / 2;
-  constexpr int kHeads = V * int(sizeof(T)) * kRuns > 32 ? 2 : 4;
+  constexpr int kHeads = HEADS;
   launch_dependents();
   grid_dependency_wait();
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -118,43 +123,53 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     }
   }
   const int begin = turns ? unit * a.run_step : a.rotary_dim + (unit - a.turning) * V;
-  for (int h0 = split; h0 < a.heads; h0 += kHeads * a.splits) {
-    alignas(32) T x[kHeads][kRuns][V];
-    T* out[kHeads];
+  // kHeads heads from the one at `from`, a step apart, or as many as are left
+  auto some = [&](auto turning, auto all_there, int left, const T* from, T* to, int64_t from_step, int64_t to_step) {
+    constexpr bool kTurn = decltype(turning)::value, kAll = decltype(all_there)::value;
+    constexpr int kUsed = kTurn ? kRuns : 1;
+    alignas(32) T x[kHeads][kUsed][V];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k)
+      if (kAll || k < left) {
+#pragma unroll
+        for (int n = 0; n < kUsed; ++n) load_raw<T, V>(from + k * from_step + n * a.second, x[k][n]);
+      }
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
-      const int h = h0 + k * a.splits;
-      out[k] = nullptr;
-      if (h >= a.heads) continue;
-      const bool later = h >= a.t[0].heads;
-      const Tensor& t = later ? a.t[1] : a.t[0];
-      if (!turns && begin - a.rotary_dim >= t.rest) continue;
-      const int head = later ? h - a.t[0].heads : h;
-      const T* from = static_cast<const T*>(t.x) + batch * t.x_stride[0] + at * t.x_stride[1] + head * t.x_stride[2] + begin;
-      out[k] = static_cast<T*>(t.out) + batch * t.out_stride[0] + at * t.out_stride[1] + head * t.out_stride[2] + begin;
-      load_raw<T, V>(from, x[k][0]);
-      if (kRuns == 2 && turns) load_raw<T, V>(from + a.second, x[k][kRuns - 1]);
-    }
+      if (!kAll && k >= left) return;
+      float f[kUsed][V];
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-      if (!out[k]) continue;
-      float f[kRuns][V];
-#pragma unroll
-      for (int n = 0; n < kRuns; ++n)
+      for (int n = 0; n < kUsed; ++n)
 #pragma unroll
         for (int j = 0; j < V; ++j) f[n][j] = widen(x[k][n][j]);
-      if (turns) {
+      if constexpr (kTurn) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           if constexpr (kRuns == 2)
-            turn(f[0][j], f[kRuns - 1][j], c[j], s[j]);
+            turn(f[0][j], f[1][j], c[j], s[j]);
           else
             turn(f[0][2 * j], f[0][2 * j + 1], c[j], s[j]);
         }
       }
-      store_vec<T, V>(out[k], f[0]);
-      if (kRuns == 2 && turns) store_vec<T, V>(out[k] + a.second, f[kRuns - 1]);
+#pragma unroll
+      for (int n = 0; n < kUsed; ++n) store_vec<T, V>(to + k * to_step + n * a.second, f[n]);
     }
+  };
+  auto all = [&](auto turning, const Tensor& t) {
+    const T* from = static_cast<const T*>(t.x) + batch * t.x_stride[0] + at * t.x_stride[1] + split * t.x_stride[2] + begin;
+    T* to = static_cast<T*>(t.out) + batch * t.out_stride[0] + at * t.out_stride[1] + split * t.out_stride[2] + begin;
+    const int64_t from_step = a.splits * t.x_stride[2], to_step = a.splits * t.out_stride[2];
+    int left = (t.heads - split + a.splits - 1) / a.splits;   // (split is below the heads of both tensors together)
+    for (; left >= kHeads; left -= kHeads, from += kHeads * from_step, to += kHeads * to_step)
+      some(turning, std::true_type{}, left, from, to, from_step, to_step);
+    if (left > 0) some(turning, std::false_type{}, left, from, to, from_step, to_step);
+  };
+  if (turns) {
+    all(std::true_type{}, a.t[0]);
+    all(std::true_type{}, a.t[1]);
+  } else {
+    if (begin - a.rotary_dim < a.t[0].rest) all(std::false_type{}, a.t[0]);
+    if (begin - a.rotary_dim < a.t[1].rest) all(std::false_type{}, a.t[1]);
   }
 }
 
@@ -253,7 +268,10 @@ fsp_status launch_width(const RotaryArgs& a, int v, int runs, cudaStream_t st) {
 }
 
 // Threads that a launch spreads a token's heads for, where there are few tokens.
-constexpr int64_t kEnoughThreads = 152 * 1536;
+#ifndef ENOUGH
+#define ENOUGH 1536
+#endif
+constexpr int64_t kEnoughThreads = 152 * ENOUGH;
 
 fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, int64_t batch, int64_t tokens,
                   const void* positions, int32_t index_bytes, int64_t positions_stride, const uint64_t* phases,
