@@ -75,17 +75,14 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 }
 
 // A thread: one unit of every splits-th head of one token, so that its sines and cosines are
-// computed once.  A unit is a few pairs of the rotated part - kRuns = 2: the pairs of a run of V
-// elements with another one, kRuns = 1: V / 2 pairs of neighbours - or V elements that are
-// copied.  The loads of kHeads heads come before their stores.
-#ifndef HEADS
-#define HEADS 4
-#define MINB 1
-#endif
-template <typename T, int V, int kRuns>
-__global__ void __launch_bounds__(kThreads, kRuns == 1 ? 4 : 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+// computed once.  A unit is kAccesses accesses - kRuns = 2: the pairs of a run of V elements
+// with another one, kRuns = 1: V / 2 pairs of neighbours - as far apart as there are units, or
+// as many runs of V elements that are copied.  Heads of odd sizes take narrow accesses, several
+// a thread: what counts is how many bytes are in flight.  The loads of kHeads heads come before
+// their stores.
+template <typename T, int V, int kRuns, int kAccesses, int kHeads>
+__global__ void __launch_bounds__(kThreads, kRuns == 1 && sizeof(T) == 2 ? 4 : 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int kPairs = V * kRuns / 2;
-  constexpr int kHeads = HEADS;
   launch_dependents();
   grid_dependency_wait();
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -111,66 +108,87 @@ __global__ void __launch_bounds__(kThreads, kRuns == 1 ? 4 : 1) rotary_kernel(co
     at = token % a.tokens;
   }
   const bool turns = unit < a.turning;
-  float c[kPairs], s[kPairs];
+  // the unit's first access of its part of a head, the part's units and accesses
+  const int first = turns ? unit : unit - a.turning, units = turns ? a.turning : a.units - a.turning;
+  float c[kAccesses][kPairs], s[kAccesses][kPairs];
   if (turns) {
     const int64_t index = batch * a.positions_stride + at;
     const int64_t pos = a.index_bytes == 8 ? static_cast<const int64_t*>(a.positions)[index] : static_cast<const int32_t*>(a.positions)[index];
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) {
-      sine_cosine(uint32_t(uint64_t(pos) * a.phases[unit * kPairs + j] >> 32), &s[j], &c[j]);
-      c[j] *= a.scale;
-      s[j] *= a.inverse ? -a.scale : a.scale;
-    }
+    for (int m = 0; m < kAccesses; ++m)
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const int pair = min((first + m * units) * kPairs + j, a.rotary_dim / 2 - 1);
+        sine_cosine(uint32_t(uint64_t(pos) * a.phases[pair] >> 32), &s[m][j], &c[m][j]);
+        c[m][j] *= a.scale;
+        s[m][j] *= a.inverse ? -a.scale : a.scale;
+      }
   }
-  const int begin = turns ? unit * a.run_step : a.rotary_dim + (unit - a.turning) * V;
-  // kHeads heads from the one at `from`, a step apart, or as many as are left
-  auto some = [&](auto turning, auto all_there, int left, const T* from, T* to, int64_t from_step, int64_t to_step) {
+  const T *from0, *from1;
+  T *to0, *to1;
+  auto place = [&](const Tensor& t, const T*& from, T*& to) {
+    const int begin = turns ? first * a.run_step : a.rotary_dim + first * V;
+    from = static_cast<const T*>(t.x) + batch * t.x_stride[0] + at * t.x_stride[1] + begin;
+    to = static_cast<T*>(t.out) + batch * t.out_stride[0] + at * t.out_stride[1] + begin;
+  };
+  place(a.t[0], from0, to0);
+  place(a.t[1], from1, to1);
+  // kHeads heads from h on, or as many as are left
+  auto some = [&](auto turning, auto all_there, int h) {
     constexpr bool kTurn = decltype(turning)::value, kAll = decltype(all_there)::value;
     constexpr int kUsed = kTurn ? kRuns : 1;
-    alignas(32) T x[kHeads][kUsed][V];
-#pragma unroll
-    for (int k = 0; k < kHeads; ++k)
-      if (kAll || k < left) {
-#pragma unroll
-        for (int n = 0; n < kUsed; ++n) load_raw<T, V>(from + k * from_step + n * a.second, x[k][n]);
-      }
+    const int gap = units * (kTurn ? a.run_step : V);
+    alignas(32) T x[kHeads][kAccesses][kUsed][V];
+    T* to[kHeads];
+    bool there[kHeads][kAccesses];
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
-      if (!kAll && k >= left) return;
-      float f[kUsed][V];
+      const int head = h + k * a.splits, later = head - a.t[0].heads;
+      const T* from = later < 0 ? from0 + head * a.t[0].x_stride[2] : from1 + later * a.t[1].x_stride[2];
+      to[k] = later < 0 ? to0 + head * a.t[0].out_stride[2] : to1 + later * a.t[1].out_stride[2];
+      const int accesses = kTurn ? a.rotary_dim / (V * kRuns) : (later < 0 ? a.t[0].rest : a.t[1].rest) / V;
 #pragma unroll
-      for (int n = 0; n < kUsed; ++n)
+      for (int m = 0; m < kAccesses; ++m) {
+        there[k][m] = (kAll || head < a.heads) && ((kTurn && kAccesses == 1) || first + m * units < accesses);
+        if (there[k][m]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[n][j] = widen(x[k][n][j]);
-      if constexpr (kTurn) {
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          if constexpr (kRuns == 2)
-            turn(f[0][j], f[1][j], c[j], s[j]);
-          else
-            turn(f[0][2 * j], f[0][2 * j + 1], c[j], s[j]);
+          for (int n = 0; n < kUsed; ++n) load_raw<T, V>(from + m * gap + n * a.second, x[k][m][n]);
         }
       }
-#pragma unroll
-      for (int n = 0; n < kUsed; ++n) store_vec<T, V>(to + k * to_step + n * a.second, f[n]);
     }
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k)
+#pragma unroll
+      for (int m = 0; m < kAccesses; ++m) {
+        float f[kUsed][V];
+#pragma unroll
+        for (int n = 0; n < kUsed; ++n)
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[n][j] = widen(x[k][m][n][j]);
+        if constexpr (kTurn) {
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            if constexpr (kRuns == 2)
+              turn(f[0][j], f[1][j], c[m][j], s[m][j]);
+            else
+              turn(f[0][2 * j], f[0][2 * j + 1], c[m][j], s[m][j]);
+          }
+        }
+        if (there[k][m]) {
+#pragma unroll
+          for (int n = 0; n < kUsed; ++n) store_vec<T, V>(to[k] + m * gap + n * a.second, f[n]);
+        }
+      }
   };
-  auto all = [&](auto turning, const Tensor& t) {
-    const T* from = static_cast<const T*>(t.x) + batch * t.x_stride[0] + at * t.x_stride[1] + split * t.x_stride[2] + begin;
-    T* to = static_cast<T*>(t.out) + batch * t.out_stride[0] + at * t.out_stride[1] + split * t.out_stride[2] + begin;
-    const int64_t from_step = a.splits * t.x_stride[2], to_step = a.splits * t.out_stride[2];
-    int left = (t.heads - split + a.splits - 1) / a.splits;   // (split is below the heads of both tensors together)
-    for (; left >= kHeads; left -= kHeads, from += kHeads * from_step, to += kHeads * to_step)
-      some(turning, std::true_type{}, left, from, to, from_step, to_step);
-    if (left > 0) some(turning, std::false_type{}, left, from, to, from_step, to_step);
+  auto all = [&](auto turning) {
+    int h = split;
+    for (; h + (kHeads - 1) * a.splits < a.heads; h += kHeads * a.splits) some(turning, std::true_type{}, h);
+    if (h < a.heads) some(turning, std::false_type{}, h);
   };
-  if (turns) {
-    all(std::true_type{}, a.t[0]);
-    all(std::true_type{}, a.t[1]);
-  } else {
-    if (begin - a.rotary_dim < a.t[0].rest) all(std::false_type{}, a.t[0]);
-    if (begin - a.rotary_dim < a.t[1].rest) all(std::false_type{}, a.t[1]);
-  }
+  if (turns)
+    all(std::true_type{});
+  else
+    all(std::false_type{});
 }
 
 // ---- host -----------------------------------------------------------------------------
@@ -254,24 +272,42 @@ bool fits(const View& v, int elems) {
   return ok;
 }
 
+// Accesses of a thread, of V elements each, where a launch has enough threads without; and the
+// heads whose loads it has in flight.
+template <typename T>
+constexpr int accesses(int v) {
+  return v == 8 ? 1 : v == 4 ? 2 : v == 2 ? 4 : sizeof(T) == 4 ? 4 : 2;
+}
+template <typename T>
+constexpr int heads(int v, int runs, int accesses) {
+  return v * runs * accesses * int(sizeof(T)) > 64 ? 2 : 4;
+}
+
 template <typename T, int V, int kRuns>
-fsp_status launch_rotary(const RotaryArgs& a, cudaStream_t st) {
+fsp_status launch_rotary(const RotaryArgs& a, bool several, cudaStream_t st) {
+  constexpr int kMany = accesses<T>(V);
   const int64_t ctas = (a.n_threads + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX) return fail(FSP_EUNSUPPORTED, "too many tokens");
-  return launch_next(rotary_kernel<T, V, kRuns>, dim3(unsigned(ctas)), kThreads, 0, 1, a, st, "rotary kernel launch");
+  void (*kernel)(RotaryArgs) = several ? rotary_kernel<T, V, kRuns, kMany, heads<T>(V, kRuns, kMany)> : rotary_kernel<T, V, kRuns, 1, heads<T>(V, kRuns, 1)>;
+  return launch_next(kernel, dim3(unsigned(ctas)), kThreads, 0, 1, a, st, "rotary kernel launch");
 }
 
 template <typename T>
-fsp_status launch_width(const RotaryArgs& a, int v, int runs, cudaStream_t st) {
-  if (runs == 1) return v == 8 ? launch_rotary<T, 8, 1>(a, st) : launch_rotary<T, 2, 1>(a, st);
-  return v == 8 ? launch_rotary<T, 8, 2>(a, st) : v == 2 ? launch_rotary<T, 2, 2>(a, st) : launch_rotary<T, 1, 2>(a, st);
+fsp_status launch_width(const RotaryArgs& a, int v, int runs, bool several, cudaStream_t st) {
+  if (runs == 1)
+    return v == 8 ? launch_rotary<T, 8, 1>(a, several, st) : v == 4 ? launch_rotary<T, 4, 1>(a, several, st) : launch_rotary<T, 2, 1>(a, several, st);
+  return v == 8   ? launch_rotary<T, 8, 2>(a, several, st)
+         : v == 4 ? launch_rotary<T, 4, 2>(a, several, st)
+         : v == 2 ? launch_rotary<T, 2, 2>(a, several, st)
+                  : launch_rotary<T, 1, 2>(a, several, st);
 }
 
-// Threads that a launch spreads a token's heads for, where there are few tokens.
-#ifndef ENOUGH
-#define ENOUGH 1536
-#endif
-constexpr int64_t kEnoughThreads = 152 * ENOUGH;
+// A token's heads are spread over threads until a launch has this many (16 + 8 heads of 128,
+// us, with 152 x 768 and 152 x 384: 1024 tokens 7.3 and 5.9, 4096 tokens 12.2 and 13.7).
+constexpr int64_t kEnoughThreads = 152 * 384;
+// From this many threads of one access each on they take several (20000 tokens, 12 bf16 heads
+// of 146, 60 turned in pairs: 63 us with one, 38 with four).
+constexpr int64_t kSeveralThreads = 152 * 1536;
 
 fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, int64_t batch, int64_t tokens,
                   const void* positions, int32_t index_bytes, int64_t positions_stride, const uint64_t* phases,
@@ -338,7 +374,7 @@ fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, in
     for (int i = 0; i < n_views; ++i) ok = ok && fits(views[i], k) && views[i].head_dim % k == 0;
     return ok;
   };
-  const int v = fit(8) ? 8 : fit(2) ? 2 : 1;
+  const int v = fit(8) ? 8 : fit(4) ? 4 : fit(2) ? 2 : 1;
   const int runs = half || v == 1 ? 2 : 1;
   a.positions = positions;
   a.phases = phases;
@@ -346,8 +382,14 @@ fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, in
   a.tokens = tokens;
   a.scale = scale;
   a.index_bytes = index_bytes;
-  a.turning = int(rotary_dim / (v * runs));
-  a.units = a.turning + (std::max(a.t[0].rest, a.t[1].rest) + v - 1) / v;
+  auto units = [&](int per_unit) {
+    auto of = [&](int64_t elements) { return int((elements + int64_t(v) * per_unit - 1) / (int64_t(v) * per_unit)); };
+    a.turning = of(rotary_dim / runs);
+    a.units = a.turning + of(std::max(a.t[0].rest, a.t[1].rest));
+  };
+  units(1);
+  const bool several = batch * tokens * a.units >= kSeveralThreads;
+  if (several) units(dtype == FSP_DTYPE_F32 ? accesses<float>(v) : accesses<__nv_bfloat16>(v));
   a.rotary_dim = int(rotary_dim);
   a.run_step = half ? v : v * runs;
   a.second = half ? int(rotary_dim / 2) : 1;
@@ -356,7 +398,7 @@ fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, in
   a.splits = int(std::clamp<int64_t>(kEnoughThreads / alone, 1, a.heads));
   a.n_threads = alone * a.splits;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == FSP_DTYPE_F32 ? launch_width<float>(a, v, runs, st) : launch_width<__nv_bfloat16>(a, v, runs, st);
+  return dtype == FSP_DTYPE_F32 ? launch_width<float>(a, v, runs, several, st) : launch_width<__nv_bfloat16>(a, v, runs, several, st);
 }
 
 }  // namespace
