@@ -22,7 +22,7 @@ EXPORTS = ("fsp_adamw_list_create", "fsp_adamw_list_info", "fsp_adamw_list_destr
            "fsp_layer_norm_backward", "fsp_dropout", "fsp_rotary_phases", "fsp_rotary")
 
 
-class _RotaryTensor(ctypes.Structure):
+class _RotaryTensor(ctypes.Structure):   # ten words of 64 bits (Rotary passes them as such)
     _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
                 ("x_strides", ctypes.c_int64 * 3), ("out_strides", ctypes.c_int64 * 3)]
 
@@ -55,7 +55,7 @@ def bind(L) -> None:
                                     i32, vp, size, vp],
         "fsp_dropout": [vp, i32, i64, i64, i64, ctypes.c_double, ctypes.c_uint64, i64, vp, vp, i32, i64, vp, i32, i64, vp],
         "fsp_rotary_phases": [P(ctypes.c_double), i64, P(ctypes.c_uint64)],
-        "fsp_rotary": [P(_RotaryTensor), i32, i32, i64, i64, vp, i32, i64, vp, i64, i32, f32, i32, vp],
+        "fsp_rotary": [vp, i32, i32, i64, i64, vp, i32, i64, vp, i64, i32, f32, i32, vp],
     }.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -557,12 +557,24 @@ def _param(x, dim: int, what: str, device: int) -> int:
     return code
 
 
-def _pair(x, y, what: str, dim: int, device: int):
+def _rows_of(x, what: str):
+    """(rows, columns, row stride) of a tensor as rows of its last dimension (a number: of one)."""
+    shape = x.shape
+    dim = shape[-1] if shape else 1
+    if dim and x.is_contiguous():
+        return x.numel() // dim, dim, dim
+    rows, stride = _flat(x, dim, what)
+    return rows, dim, stride
+
+
+def _pair(x, y, what, dim: int, device: int):
     """The one dtype code of two parameters, each of which may be None."""
-    codes = [_param(t, dim, name, device) for t, name in zip((x, y), what.split()) if t is not None]
-    if len(set(codes)) > 1:
-        raise TypeError(f"{what.replace(' ', ' and ')} must have the same dtype")
-    return codes[0] if codes else 0
+    first, second = what
+    a = None if x is None else _param(x, dim, first, device)
+    b = None if y is None else _param(y, dim, second, device)
+    if a is not None and b is not None and a != b:
+        raise TypeError(f"{first} and {second} must have the same dtype")
+    return a if a is not None else b if b is not None else 0
 
 
 def _like(out, x, what: str, dtype):
@@ -589,23 +601,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True
     reads.  Nothing is recorded for autograd."""
     here = _current()
     code = _dtype(x, "x", here)
-    dim = x.shape[-1] if x.dim() else 0
-    rows, stride = _flat(x, dim, "x")
-    param = _pair(weight, bias, "weight bias", dim, here)
+    rows, dim, stride = _rows_of(x, "x")
+    param = _pair(weight, bias, ("weight", "bias"), dim, here)
     if out is None:
         out = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
         out_stride = max(1, dim)
     else:
         _like(out, x, "out", out_dtype)
-        out_stride = _flat(out, dim, "out")[1]
+        out_stride = _rows_of(out, "out")[2]
     if stats is True:
         stats = _empty((*x.shape[:-1], 2), _torch.float32, x.device, stream)
-    elif stats is False:
-        stats = None
+        stats_ptr = stats.data_ptr()
+    elif stats is None or stats is False:
+        stats = stats_ptr = None
+    else:
+        stats_ptr = _stats(stats, x, here)
     status = _lib.fsp_layer_norm(x.data_ptr(), code, rows, dim, stride, None if weight is None else weight.data_ptr(),
                                  None if bias is None else bias.data_ptr(), param, eps, 1 if center else 0,
                                  out.data_ptr(), _dtype(out, "out", here), out_stride,
-                                 None if stats is None else _stats(stats, x, here), _handle(stream, here))
+                                 stats_ptr, _handle(stream, here))
     if status:
         _fsp._check(status, "fsp_layer_norm")
     return out if stats is None else (out, stats)
@@ -630,14 +644,13 @@ def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, gr
     ``layer_norm_backward_workspace_bytes`` bytes (None: allocated here)."""
     here = _current()
     code, dy_code = _dtype(x, "x", here), _dtype(grad_out, "grad_out", here)
-    dim = x.shape[-1] if x.dim() else 0
-    rows, stride = _flat(x, dim, "x")
+    rows, dim, stride = _rows_of(x, "x")
     if grad_out.shape != x.shape:
         raise ValueError("grad_out must have x's shape")
-    dy_stride = _flat(grad_out, dim, "grad_out")[1]
+    dy_stride = _rows_of(grad_out, "grad_out")[2]
     stats_ptr = _stats(stats, x, here)
     w_code = 0 if weight is None else _param(weight, dim, "weight", here)
-    grad_code = _pair(grad_weight, grad_bias, "grad_weight grad_bias", dim, here)
+    grad_code = _pair(grad_weight, grad_bias, ("grad_weight", "grad_bias"), dim, here)
     columns = grad_weight is not None or grad_bias is not None
     if not need_grad_x and (add is not None or out is not None):
         raise ValueError("add and out need need_grad_x")
@@ -645,7 +658,7 @@ def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, gr
     if add is not None:
         _on(here, add, "add")
         _like(add, x, "add", x.dtype)
-        add_stride = _flat(add, dim, "add")[1]
+        add_stride = _rows_of(add, "add")[2]
     if not need_grad_x:
         out = None
         if not columns:
@@ -655,7 +668,7 @@ def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, gr
     else:
         _on(here, out, "out")
         _like(out, x, "out", x.dtype)
-        dx_stride = _flat(out, dim, "out")[1]
+        dx_stride = _rows_of(out, "out")[2]
     if not columns:
         workspace = None
     elif workspace is not None:
@@ -687,8 +700,7 @@ def dropout(x, p: float, seed: int, call=0, residual=None, out=None, out_dtype=N
     any two calls of a run should differ in one of them."""
     here = _current()
     code = _dtype(x, "x", here)
-    dim = x.shape[-1] if x.dim() else 1
-    rows, stride = _flat(x, dim, "x") if x.dim() else (1, 1)
+    rows, dim, stride = _rows_of(x, "x")
     call_ptr = None
     if not isinstance(call, int):
         if call.dtype != _torch.int64 or call.numel() != 1:
@@ -699,13 +711,13 @@ def dropout(x, p: float, seed: int, call=0, residual=None, out=None, out_dtype=N
     if residual is not None:
         r_code = _dtype(residual, "residual", here)
         _like(residual, x, "residual", None)
-        r_stride = _flat(residual, dim, "residual")[1] if x.dim() else 1
+        r_stride = _rows_of(residual, "residual")[2]
     if out is None:
         out = _empty(x.shape, out_dtype or (x if residual is None else residual).dtype, x.device, stream)
         out_stride = max(1, dim)
     else:
         _like(out, x, "out", out_dtype)
-        out_stride = _flat(out, dim, "out")[1] if x.dim() else 1
+        out_stride = _rows_of(out, "out")[2]
     status = _lib.fsp_dropout(x.data_ptr(), code, rows, dim, stride, p, seed & 0xFFFFFFFFFFFFFFFF, call, call_ptr,
                               None if residual is None else residual.data_ptr(), r_code, r_stride, out.data_ptr(),
                               _dtype(out, "out", here), out_stride, _handle(stream, here))
@@ -778,58 +790,73 @@ class Rotary:
     def _run(self, x, positions, out, inverse: int, stream):
         here = _current()
         pair = isinstance(x, (tuple, list))
-        xs = tuple(x) if pair else (x,)
-        if not 1 <= len(xs) <= 2:
+        xs = x if pair else (x,)
+        n = len(xs)
+        if not 1 <= n <= 2:
             raise ValueError("one tensor or a pair is rotated by a call")
-        outs = (None,) * len(xs) if out is None else tuple(out) if pair else (out,)
-        if len(outs) != len(xs):
+        outs = (None,) * n if out is None else out if pair else (out,)
+        if len(outs) != n:
             raise ValueError("out must be as many tensors")
-        code = _dtype(xs[0], "x", here)
-        shape = xs[0].shape[:-2]
-        if xs[0].dim() not in (3, 4):
+        lead = xs[0].shape[:-2]
+        dims, dtype = len(lead), xs[0].dtype
+        if not 1 <= dims <= 2:
             raise ValueError("x must have 3 or 4 dimensions")
-        batch, tokens = (1, *shape) if len(shape) == 1 else shape
+        batch, tokens = lead if dims == 2 else (1, lead[0])
+        words, got = [], []
+        for x_i, o in zip(xs, outs):
+            shape = x_i.shape
+            if shape[:-2] != lead:
+                raise ValueError("the tensors must have the same batch and tokens")
+            code = _dtype(x_i, "x", here)
+            if x_i.dtype != dtype:
+                raise TypeError("the tensors must have the same dtype")
+            heads, head_dim = shape[-2:]
+            strides = _head_strides(x_i, "x")
+            if o is None:
+                o = _empty(shape, dtype, x_i.device, stream)
+                token = heads * head_dim
+                out_strides = (tokens * token, token, head_dim)
+            else:
+                if o.shape != shape or o.dtype != dtype:
+                    raise ValueError("out has another shape or dtype")
+                if o.get_device() != here:
+                    _on(here, o, "out")
+                out_strides = _head_strides(o, "out")
+            words += (x_i.data_ptr(), o.data_ptr(), heads, head_dim, *strides, *out_strides)
+            got.append(o)
         if positions.get_device() != here:
             _on(here, positions, "positions")
         index = _INDEX.get(positions.dtype)
         if index is None:
             raise TypeError(f"positions: unsupported dtype {positions.dtype}")
-        if tuple(positions.shape) == tuple(shape):
+        if positions.shape == lead:
             positions_stride = tokens
-        elif tuple(positions.shape) == (tokens,):
+        elif positions.shape == (tokens,):
             positions_stride = 0
         else:
-            raise ValueError(f"positions must have shape {tuple(shape)} or {(tokens,)}")
+            raise ValueError(f"positions must have shape {tuple(lead)} or {(tokens,)}")
         if not positions.is_contiguous():
             raise ValueError("positions must be contiguous")
-        if self.phases.get_device() != here:
-            _on(here, self.phases, "the frequencies")
-        tensors = (_RotaryTensor * len(xs))()
-        got = []
-        for t, x_i, o in zip(tensors, xs, outs):
-            if x_i.shape[:-2] != shape or x_i.dim() != len(shape) + 2:
-                raise ValueError("the tensors must have the same batch and tokens")
-            if x_i.dtype != xs[0].dtype:
-                raise TypeError("the tensors must have the same dtype")
-            if o is None:
-                o = _empty(x_i.shape, x_i.dtype, x_i.device, stream)
-            elif o.shape != x_i.shape or o.dtype != x_i.dtype:
-                raise ValueError("out has another shape or dtype")
-            for what, y, strides in (("x", x_i, t.x_strides), ("out", o, t.out_strides)):
-                if y.get_device() != here:
-                    _on(here, y, what)
-                s = y.stride()
-                if s[-1] != 1 and y.shape[-1] > 1:
-                    raise ValueError(f"{what}: the elements of a head must be adjacent")
-                strides[:] = (0, *s[:2]) if len(s) == 3 else s[:3]
-            t.x, t.out, t.heads, t.head_dim = x_i.data_ptr(), o.data_ptr(), x_i.shape[-2], x_i.shape[-1]
-            got.append(o)
-        status = _lib.fsp_rotary(tensors, len(xs), code, batch, tokens, positions.data_ptr(), index, positions_stride,
-                                 self.phases.data_ptr(), self.dim, 0 if self.layout == "half" else 1, self.scale, inverse,
+        phases = self.phases
+        if phases.get_device() != here:
+            _on(here, phases, "the frequencies")
+        status = _lib.fsp_rotary(_WORDS[n](*words), n, code, batch, tokens, positions.data_ptr(), index, positions_stride,
+                                 phases.data_ptr(), self.dim, 0 if self.layout == "half" else 1, self.scale, inverse,
                                  _handle(stream, here))
         if status:
             _fsp._check(status, "fsp_rotary")
         return tuple(got) if pair else got[0]
+
+
+_WORDS = (None, ctypes.c_int64 * 10, ctypes.c_int64 * 20)   # of one fsp_rotary_tensor, of two
+
+
+def _head_strides(x, what: str):
+    """Strides of the batches, tokens and heads of a tensor whose heads' elements are adjacent."""
+    strides = x.stride()
+    if strides[-1] != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{what}: the elements of a head must be adjacent")
+    return strides[:3] if len(strides) == 4 else (0, *strides[:2])
 
 
 def _frequencies(dim: int, base: float, scaling, factor: float, length, turns):
