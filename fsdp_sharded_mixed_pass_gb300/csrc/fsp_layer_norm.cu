@@ -329,26 +329,36 @@ struct Columns {
           for (int k = 0; k < kBytes; k += 16) copy_async(dst + n * T * kBytes + k, src + n * T * kBytes + k, there);
         }
     } else if (row < rows) {
-      const uintptr_t begin = reinterpret_cast<uintptr_t>(address(s, row)), base = begin & ~uintptr_t(15);
-      const int bytes = (int(begin - base) + dim * kSize + 15) & ~15;
-      const uintptr_t lowest = reinterpret_cast<uintptr_t>(s.p), highest = reinterpret_cast<uintptr_t>(address(s, rows - 1)) + dim * kSize;
-      if (base >= lowest && base + bytes <= highest) {
-        for (int k = t * 16; k < bytes; k += T * 16) copy_async(smem_at(stage) + k, reinterpret_cast<const void*>(base + k), true);
+      const char* begin = address(s, row);
+      const int before = int(reinterpret_cast<uintptr_t>(begin) & 15), bytes = (before + dim * kSize + 15) & ~15;
+      const char* src = begin - before + t * 16;
+      const uint32_t dst = smem_at(stage) + t * 16;
+      if (inside(s, row, rows)) {
+#pragma unroll
+        for (int k = 0; k < kGroup; k += T * 16)
+          if (k + t * 16 < bytes) copy_async(dst + k, src + k, true);
       } else {
-        for (uintptr_t p = base + t * 16; p < base + bytes; p += T * 16) {
+        const char *lowest = static_cast<const char*>(s.p), *highest = address(s, rows - 1) + dim * kSize;
+        for (int k = t * 16; k < bytes; k += T * 16) {
+          const char* p = begin - before + k;
           if (p >= lowest && p + 16 <= highest) {
-            copy_async(smem_at(stage) + uint32_t(p - base), reinterpret_cast<const void*>(p), true);
+            copy_async(smem_at(stage) + k, p, true);
           } else {
-            for (uintptr_t q = p < lowest ? lowest : p; q < p + 16 && q < highest; q += kSize)
-              *reinterpret_cast<Y*>(stage + (q - base)) = *reinterpret_cast<const Y*>(q);
+            for (const char* q = p < lowest ? lowest : p; q < p + 16 && q < highest; q += kSize)
+              *reinterpret_cast<Y*>(stage + k + (q - p)) = *reinterpret_cast<const Y*>(q);
           }
         }
       }
     }
   }
+  // Whether the 16-byte pieces that cover a row lie within the matrix for certain.
+  static __device__ __forceinline__ bool inside(Stream s, uint32_t row, uint32_t rows) {
+    const uint32_t margin = s.stride * kSize >= 16 ? 1 : 16;   // rows of 16 bytes
+    return row >= margin && row + margin < rows;
+  }
   // Bytes of a stage before a row's first.
   static __device__ __forceinline__ int skip(Stream s, uint32_t row) {
-    return kShift ? int(reinterpret_cast<uintptr_t>(address(s, row)) & 15) : 0;
+    return kShift ? int((uint32_t(reinterpret_cast<uintptr_t>(s.p)) + row * uint32_t(s.stride) * kSize) & 15u) : 0;
   }
   static __device__ __forceinline__ float2 pair_of(uint32_t w) {   // bf16
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -436,10 +446,12 @@ __device__ __forceinline__ void write_row(O* out, int dim, bool there, char* sta
     group_sync<T>();
     char* base = reinterpret_cast<char*>(out) - ahead;
     const int whole = ahead > 0 ? 16 : 0;   // the first whole piece
-    for (int k = whole + t * 16; k + 16 <= end; k += T * 16)
-      __stcs(reinterpret_cast<uint4*>(base + k), *reinterpret_cast<const uint4*>(staging + k));
-    const int head = ahead + t * kSize, tail = max(whole, end & ~15) + t * kSize;   // elements before and after them
-    if (t < 16 / kSize) {
+#pragma unroll
+    for (int k = 0; k < T * E * kSize + 16; k += T * 16)
+      if (k + t * 16 >= whole && k + t * 16 + 16 <= end)
+        __stcs(reinterpret_cast<uint4*>(base + t * 16 + k), *reinterpret_cast<const uint4*>(staging + t * 16 + k));
+    if (t < 16 / kSize) {   // elements before and after them
+      const int head = ahead + t * kSize, tail = max(whole, end & ~15) + t * kSize;
       if (head < min(whole, end)) *reinterpret_cast<O*>(base + head) = *reinterpret_cast<const O*>(staging + head);
       if (tail < end) *reinterpret_cast<O*>(base + tail) = *reinterpret_cast<const O*>(staging + tail);
     }
@@ -808,8 +820,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_columns_kernel(const __g
   void* out = blockIdx.y == 0 ? a.grad_weight : a.grad_bias;
   if (!out) return;
   const int64_t col = int64_t(blockIdx.x) * 32 + lane;
-  float sum = 0.f;
+  float sum = 0.f, old = 0.f;
   if (col < a.dim) {
+    if (warp == 0 && a.accumulate) old = load_any(out, a.grad_param_f32, col);
 #pragma unroll
     for (int k = 0; k < (kParts + kJoinWarps - 1) / kJoinWarps; ++k) {
       const int p = warp + k * kJoinWarps;
@@ -822,7 +835,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_columns_kernel(const __g
   sum = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) sum += share[w][lane];
-  if (a.accumulate) sum += load_any(out, a.grad_param_f32, col);
+  sum += old;
   store_any<1>(out, a.grad_param_f32, col, &sum);
 }
 

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import fsp as _fsp
 from .optim import _on_stream
@@ -848,7 +849,7 @@ class Rotary:
         return tuple(got) if pair else got[0]
 
 
-_WORDS = (None, ctypes.c_int64 * 10, ctypes.c_int64 * 20)   # of one fsp_rotary_tensor, of two
+_WORDS = (None, struct.Struct("=10q").pack, struct.Struct("=20q").pack)   # one fsp_rotary_tensor, two
 
 
 def _head_strides(x, what: str):
