@@ -50,6 +50,22 @@ def test_dropout(rows, dim, pad, shift, x_t, res_t, out_t):
         assert intact() and ok() and fsp.device_error() == 0
 
 
+@pytest.mark.parametrize("rows,dim,pad,shift,res_t,out_t", [(8193, 1024, 0, 0, "bf16", "bf16"), (8200, 1032, 8, 8, "f32", "f32"), (9001, 1001, 0, 0, "bf16", "f32"),
+                                                            (8400, 1001, 3, 1, "f32", "bf16"), (4100, 2056, 16, 0, "", "bf16")])
+def test_many_elements(rows, dim, pad, shift, res_t, out_t):
+    """From 2^23 elements on a thread takes several blocks of the generator: the same results as call by call on parts."""
+    n = rows * (dim + pad) + shift
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    new = lambda t: torch.randn(n, generator=g, device="cuda").to(DT[t])[shift:].view(rows, dim + pad)[:, :dim]  # noqa: E731
+    x, h, y = new("bf16"), new(res_t) if res_t else None, new(out_t)
+    fsp.dropout(x, 0.1, SEED, CALL, residual=h, out=y)
+    keep = torch.from_numpy(R.random16(rows * dim, SEED, CALL) >= 6554).cuda().view(rows, dim)
+    want = torch.where(keep, x.double() * (65536 / (65536 - 6554)), 0.0) + (0 if h is None else h.double())
+    tol = 2 * R.U * (x.double() * 1.2).abs() + R.U * want.abs()
+    assert bool(((y - want).abs() <= tol + (2.0 ** -8 * (want.abs() + tol) if out_t == "bf16" else 0)).all())
+    assert fsp.device_error() == 0
+
+
 def test_the_mask_is_a_function_of_seed_call_and_index():
     ones = torch.ones(7, 1000, device="cuda")
     mask = lambda x, *a: fsp.dropout(x, 0.5, *a) != 0  # noqa: E731

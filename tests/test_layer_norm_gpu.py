@@ -92,6 +92,40 @@ def test_backward(rows, dim, pad, shift, x_t, dy_t, par_t):
         assert off_by(only, want[0], tol[0], x_t) == 0
 
 
+# enough elements for the kernel that streams rows: every width it tells apart, rows with gaps, off alignment, of a few
+# elements, and counts of rows that leave groups of threads without one
+MANY = [(300001, 3, 0, 0), (100003, 8, 0, 0), (120001, 7, 1, 1), (47001, 17, 0, 0), (20011, 40, 8, 8), (6301, 128, 0, 0), (6200, 129, 0, 1), (3301, 256, 16, 0),
+        (2999, 263, 0, 0), (1601, 520, 8, 0), (1555, 517, 3, 1), (801, 1001, 0, 1), (790, 1024, 0, 2), (401, 2040, 0, 0), (391, 2047, 2, 0), (200, 4099, 0, 0),
+        (193, 4096, 8, 8), (101, 8191, 1, 0), (97, 8192, 0, 0), (53, 16383, 0, 1), (49, 16384, 0, 0)]
+
+
+@pytest.mark.parametrize("x_t,out_t,par_t", TYPES)
+@pytest.mark.parametrize("rows,dim,pad,shift", MANY)
+def test_many_rows(rows, dim, pad, shift, x_t, out_t, par_t):
+    rng = np.random.default_rng(rows + dim)
+    x, _ = matrix(rows, dim, x_t, pad, shift, _inputs(rows, dim, rng))
+    w, b = _vector(rng, dim, 1, 0.3, par_t), _vector(rng, dim, 0, 0.3, par_t)
+    for center, bias in ((True, b), (False, None)):
+        y, intact = matrix(rows, dim, out_t, pad, shift)
+        _, stats = fsp.layer_norm(x, w, bias, eps=EPS, center=center, out=y, stats=True)
+        want, tol = R.norm(values(x), values(w), 0.0 if bias is None else values(bias), EPS, center)
+        assert off_by(y, want[0], tol[0], out_t) == 0
+        st = values(stats)
+        assert off_by(st[:, 0], want[1], tol[1], "f32") == 0 and off_by(st[:, 1], want[2], tol[2], "f32") == 0
+        assert intact()
+    # in place, and the gradients (of the last statistics) into the place of grad_out
+    if x_t == out_t:
+        z, intact = matrix(rows, dim, x_t, pad, shift)
+        z.copy_(x)
+        assert torch.equal(fsp.layer_norm(z, w, eps=EPS, center=False, out=z), y) and intact()
+    dy, intact = matrix(rows, dim, x_t, pad, shift, rng.normal(0, 1, (rows, dim)))
+    want, tol = R.norm_gradients(values(x), st[:, 0], st[:, 1], values(dy), values(w), 0.0, False)
+    dw, db = (torch.empty(dim, device="cuda") for _ in range(2))
+    fsp.layer_norm_backward(x, stats, dy, w, center=False, grad_weight=dw, grad_bias=db, out=dy)
+    assert off_by(dy, want[0], tol[0], x_t) == 0 and off_by(dw, want[1], tol[1], "f32") == 0 and off_by(db, want[2], tol[2], "f32") == 0
+    assert intact() and fsp.device_error() == 0
+
+
 @pytest.mark.parametrize("rows,dim,x_t", [(4099, 1024, "bf16"), (2500, 1001, "f32"), (40000, 128, "bf16"), (1999, 2048, "bf16"),
                                           (70001, 40, "f32"), (650, 8192, "bf16"), (20000, 17, "bf16"), (310, 16384, "f32")])
 def test_long_batches(rows, dim, x_t):

@@ -61,6 +61,42 @@ def test_rotation(tokens, heads, head_dim, dim, layout, dtype):
     assert fsp.device_error() == 0
 
 
+# enough tokens for threads that take several heads and several narrow accesses; batches, one tensor or two
+@pytest.mark.parametrize("dtype,layout,batch,tokens,heads,kv,head_dim,dim", [
+    ("bf16", "half", 2, 1601, 11, 3, 90, 90), ("f32", "half", 1, 3001, 9, 2, 192, 118), ("bf16", "interleaved", 1, 4003, 7, 5, 146, 60),
+    ("f32", "interleaved", 3, 2001, 5, 1, 84, 20), ("bf16", "half", 1, 30011, 5, 0, 128, 128), ("bf16", "interleaved", 2, 12007, 1, 1, 72, 8),
+    ("f32", "half", 1, 40001, 1, 0, 20, 12), ("bf16", "half", 1, 5003, 6, 6, 100, 40), ("f32", "interleaved", 1, 9001, 2, 3, 34, 34)])
+def test_many_tokens(dtype, layout, batch, tokens, heads, kv, head_dim, dim):
+    """Against 64 bits on the device, out of a projection's rows into tensors of their own."""
+    rope = fsp.Rotary(dim, layout=layout, scaling="ntk", factor=8.0)
+    qkv = torch.randn(batch, tokens, heads + 2 * kv, head_dim, device="cuda").to(DT[dtype])
+    q, k = qkv[:, :, :heads], qkv[:, :, heads:heads + kv]
+    pos = torch.randint(0, 100000, (batch, tokens), device="cuda")
+    turn = pos[:, :, None, None].double() * torch.tensor(rope.frequencies, dtype=torch.float64, device="cuda")
+    got = rope.forward((q, k), pos), rope.backward((q, k), pos)
+    for x, fwd, bwd in ((q, got[0][0], got[1][0]), (k, got[0][1], got[1][1])):
+        for y, sign in ((fwd, 1), (bwd, -1)):
+            a, b = (x[..., :dim // 2], x[..., dim // 2:dim]) if layout == "half" else (x[..., 0:dim:2], x[..., 1:dim:2])
+            a, b, c, s = a.double(), b.double(), turn.cos(), sign * turn.sin()
+            u, v = (y[..., :dim // 2], y[..., dim // 2:dim]) if layout == "half" else (y[..., 0:dim:2], y[..., 1:dim:2])
+            # the angle at 100000 in doubles: 2^-52 of 10^5, far below
+            tol = R.ROTARY_TOL * (a.abs() + b.abs())
+            for out, want in ((u, a * c - b * s), (v, b * c + a * s)):
+                assert bool(((out - want).abs() <= tol + (2.0 ** -8 * (want.abs() + tol) if dtype == "bf16" else 0)).all())
+            assert torch.equal(y[..., dim:], x[..., dim:])
+    buf = qkv.clone()
+    bq, bk = buf[:, :, :heads], buf[:, :, heads:heads + kv]
+    rope.forward((bq, bk), pos, out=(bq, bk))
+    assert torch.equal(bq, got[0][0]) and torch.equal(bk, got[0][1]) and torch.equal(buf[:, :, heads + kv:], qkv[:, :, heads + kv:])
+    # one tensor in place, the other not: only the other's rest is copied
+    if kv:
+        buf = qkv.clone()
+        out = torch.full((batch, tokens, kv, head_dim), float("nan"), device="cuda", dtype=DT[dtype])
+        rope.forward((buf[:, :, :heads], k), pos, out=(buf[:, :, :heads], out))
+        assert torch.equal(buf[:, :, :heads], got[0][0]) and torch.equal(out, got[0][1])
+    assert fsp.device_error() == 0
+
+
 def test_position_zero_and_far_positions():
     x = torch.randn(4, 2, 64, device="cuda")
     rope = fsp.Rotary(64)
