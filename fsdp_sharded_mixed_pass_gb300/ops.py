@@ -7,6 +7,7 @@ current device, where every tensor of a call has to be.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 
@@ -550,14 +551,6 @@ class Fp8Linear:
 
 # ---- layer norm ------------------------------------------------------------------------
 
-def _param(x, dim: int, what: str, device: int) -> int:
-    """The library's code of a parameter's dtype, a vector of ``dim`` adjacent elements."""
-    code = _dtype(x, what, device)
-    if tuple(x.shape) != (dim,) or (dim > 1 and x.stride(0) != 1):
-        raise ValueError(f"{what} must be {dim} adjacent elements")
-    return code
-
-
 def _rows_of(x, what: str):
     """(rows, columns, row stride) of a tensor as rows of its last dimension (a number: of one)."""
     shape = x.shape
@@ -568,26 +561,34 @@ def _rows_of(x, what: str):
     return rows, dim, stride
 
 
-def _pair(x, y, what, dim: int, device: int):
+def _row_stride(x, like, dim: int, what: str, dtype=None) -> int:
+    """The row stride of a tensor (of ``dtype``, where one is given) that has the shape of ``like``."""
+    if x.shape != like.shape or (dtype is not None and x.dtype != dtype):
+        raise ValueError(f"{what} has another shape{'' if dtype is None else ' or dtype'}")
+    return dim if dim and x.is_contiguous() else _flat(x, dim, what)[1] if x.shape else 1
+
+
+def _param(x, dim: int, what: str, device: int) -> int:
+    """The library's code of a parameter's dtype, a vector of ``dim`` adjacent elements."""
+    code = _dtype(x, what, device)
+    if x.shape != (dim,) or not x.is_contiguous():
+        raise ValueError(f"{what} must be {dim} adjacent elements")
+    return code
+
+
+def _two_params(x, y, names, dim: int, device: int):
     """The one dtype code of two parameters, each of which may be None."""
-    first, second = what
-    a = None if x is None else _param(x, dim, first, device)
-    b = None if y is None else _param(y, dim, second, device)
-    if a is not None and b is not None and a != b:
-        raise TypeError(f"{first} and {second} must have the same dtype")
-    return a if a is not None else b if b is not None else 0
+    a = None if x is None else _param(x, dim, names[0], device)
+    b = a if y is None else _param(y, dim, names[1], device)
+    if a is not None and a != b:
+        raise TypeError(f"{names[0]} and {names[1]} must have the same dtype")
+    return b or 0
 
 
-def _like(out, x, what: str, dtype):
-    """Checks a buffer given for a result of x's shape."""
-    if out.shape != x.shape or (dtype is not None and out.dtype != dtype):
-        raise ValueError(f"{what} has another shape or dtype")
-
-
-def _stats(stats, x, device: int):
-    """Checks the (mean, 1 / deviation) pairs of x's rows."""
-    if _dtype(stats, "stats", device) != 0 or tuple(stats.shape) != (*x.shape[:-1], 2) or not stats.is_contiguous():
-        raise ValueError(f"stats must be contiguous fp32 of shape {(*x.shape[:-1], 2)}")
+def _stats(stats, rows: int, device: int):
+    """The address of the (mean, 1 / deviation) pairs of ``rows`` rows."""
+    if _dtype(stats, "stats", device) != 0 or stats.shape[-1:] != (2,) or stats.numel() != 2 * rows or not stats.is_contiguous():
+        raise ValueError(f"stats must be contiguous fp32 pairs of {rows} rows")
     return stats.data_ptr()
 
 
@@ -603,29 +604,28 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True
     here = _current()
     code = _dtype(x, "x", here)
     rows, dim, stride = _rows_of(x, "x")
-    param = _pair(weight, bias, ("weight", "bias"), dim, here)
+    param = _two_params(weight, bias, ("weight", "bias"), dim, here)
     if out is None:
         out = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
-        out_stride = max(1, dim)
+        out_stride = dim or 1
     else:
-        _like(out, x, "out", out_dtype)
-        out_stride = _rows_of(out, "out")[2]
+        out_stride = _row_stride(out, x, dim, "out", out_dtype)
     if stats is True:
         stats = _empty((*x.shape[:-1], 2), _torch.float32, x.device, stream)
         stats_ptr = stats.data_ptr()
     elif stats is None or stats is False:
         stats = stats_ptr = None
     else:
-        stats_ptr = _stats(stats, x, here)
+        stats_ptr = _stats(stats, rows, here)
     status = _lib.fsp_layer_norm(x.data_ptr(), code, rows, dim, stride, None if weight is None else weight.data_ptr(),
                                  None if bias is None else bias.data_ptr(), param, eps, 1 if center else 0,
-                                 out.data_ptr(), _dtype(out, "out", here), out_stride,
-                                 stats_ptr, _handle(stream, here))
+                                 out.data_ptr(), _dtype(out, "out", here), out_stride, stats_ptr, _handle(stream, here))
     if status:
         _fsp._check(status, "fsp_layer_norm")
     return out if stats is None else (out, stats)
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_backward_workspace_bytes(rows: int, dim: int) -> int:
     """Device workspace bytes ``layer_norm_backward`` needs for the parameters' gradients."""
     out = ctypes.c_size_t(0)
@@ -646,42 +646,46 @@ def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, gr
     here = _current()
     code, dy_code = _dtype(x, "x", here), _dtype(grad_out, "grad_out", here)
     rows, dim, stride = _rows_of(x, "x")
-    if grad_out.shape != x.shape:
-        raise ValueError("grad_out must have x's shape")
-    dy_stride = _rows_of(grad_out, "grad_out")[2]
-    stats_ptr = _stats(stats, x, here)
-    w_code = 0 if weight is None else _param(weight, dim, "weight", here)
-    grad_code = _pair(grad_weight, grad_bias, ("grad_weight", "grad_bias"), dim, here)
+    dy_stride = _row_stride(grad_out, x, dim, "grad_out")
+    stats_ptr = _stats(stats, rows, here)
+    weight_ptr = add_ptr = out_ptr = dw_ptr = db_ptr = work_ptr = None
+    w_code = work_bytes = 0
+    if weight is not None:
+        w_code, weight_ptr = _param(weight, dim, "weight", here), weight.data_ptr()
+    grad_code = _two_params(grad_weight, grad_bias, ("grad_weight", "grad_bias"), dim, here)
+    if grad_weight is not None:
+        dw_ptr = grad_weight.data_ptr()
+    if grad_bias is not None:
+        db_ptr = grad_bias.data_ptr()
     columns = grad_weight is not None or grad_bias is not None
-    if not need_grad_x and (add is not None or out is not None):
-        raise ValueError("add and out need need_grad_x")
-    add_stride = dx_stride = max(1, dim)
-    if add is not None:
-        _on(here, add, "add")
-        _like(add, x, "add", x.dtype)
-        add_stride = _rows_of(add, "add")[2]
+    add_stride = dx_stride = dim or 1
     if not need_grad_x:
-        out = None
+        if add is not None or out is not None:
+            raise ValueError("add and out need need_grad_x")
         if not columns:
             return None
-    elif out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream)
     else:
-        _on(here, out, "out")
-        _like(out, x, "out", x.dtype)
-        dx_stride = _rows_of(out, "out")[2]
-    if not columns:
-        workspace = None
-    elif workspace is not None:
-        _on(here, workspace, "workspace")
-    else:
-        workspace = _empty(layer_norm_backward_workspace_bytes(rows, dim), _torch.uint8, x.device, stream)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        if add is not None:
+            _on(here, add, "add")
+            add_stride, add_ptr = _row_stride(add, x, dim, "add", x.dtype), add.data_ptr()
+        if out is None:
+            out = _empty(x.shape, x.dtype, x.device, stream)
+        else:
+            _on(here, out, "out")
+            dx_stride = _row_stride(out, x, dim, "out", x.dtype)
+        out_ptr = out.data_ptr()
+    if columns:
+        if workspace is None:
+            work_bytes = layer_norm_backward_workspace_bytes(rows, dim)
+            workspace = _empty(work_bytes, _torch.uint8, x.device, stream)
+        else:
+            _on(here, workspace, "workspace")
+            work_bytes = workspace.numel() * workspace.element_size()
+        work_ptr = workspace.data_ptr()
     status = _lib.fsp_layer_norm_backward(
         x.data_ptr(), code, rows, dim, stride, stats_ptr, 1 if center else 0, grad_out.data_ptr(), dy_code, dy_stride,
-        ptr(weight), w_code, ptr(add), add_stride, ptr(out), dx_stride, ptr(grad_weight), ptr(grad_bias), grad_code,
-        1 if accumulate else 0, ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _handle(stream, here))
+        weight_ptr, w_code, add_ptr, add_stride, out_ptr, dx_stride, dw_ptr, db_ptr, grad_code, 1 if accumulate else 0,
+        work_ptr, work_bytes, _handle(stream, here))
     if status:
         _fsp._check(status, "fsp_layer_norm_backward")
     return out
@@ -711,14 +715,12 @@ def dropout(x, p: float, seed: int, call=0, residual=None, out=None, out_dtype=N
     r_code, r_stride = 0, stride
     if residual is not None:
         r_code = _dtype(residual, "residual", here)
-        _like(residual, x, "residual", None)
-        r_stride = _rows_of(residual, "residual")[2]
+        r_stride = _row_stride(residual, x, dim, "residual")
     if out is None:
         out = _empty(x.shape, out_dtype or (x if residual is None else residual).dtype, x.device, stream)
-        out_stride = max(1, dim)
+        out_stride = dim or 1
     else:
-        _like(out, x, "out", out_dtype)
-        out_stride = _rows_of(out, "out")[2]
+        out_stride = _row_stride(out, x, dim, "out", out_dtype)
     status = _lib.fsp_dropout(x.data_ptr(), code, rows, dim, stride, p, seed & 0xFFFFFFFFFFFFFFFF, call, call_ptr,
                               None if residual is None else residual.data_ptr(), r_code, r_stride, out.data_ptr(),
                               _dtype(out, "out", here), out_stride, _handle(stream, here))
