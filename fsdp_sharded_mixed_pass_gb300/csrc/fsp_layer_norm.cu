@@ -249,7 +249,7 @@ struct Held {
   static constexpr bool kShift = V < 4;
   static constexpr int N = kShift ? E / 2 : E / V;        // accesses, or pairs
   static constexpr int W = kShift ? 2 : V;                // elements of one
-  [[maybe_unused]] static constexpr int kStep = V == 1 ? T : 1;            // between the two columns of a pair
+  enum { kStep = V == 1 ? T : 1 };            // between the two columns of a pair
   static __device__ __forceinline__ int thread() { return threadIdx.x % T; }
   static __device__ __forceinline__ int column(int n) { return V == 1 ? 2 * n * T + thread() : (n * T + thread()) * W; }
   // Zeros for what lies past the row's end.
