@@ -292,7 +292,7 @@ struct Columns {
   using H = Held<V, T, E>;
   static constexpr bool kShift = H::kShift;
   static constexpr int kSize = int(sizeof(Y)), kBytes = kSize * V;
-  static constexpr int kGroup = T * E * kSize + (kShift ? 32 : 0);   // of a group; kShift: and what surrounds a row
+  static constexpr int kGroup = T * E * kSize + (kShift ? 16 : 0);   // of a group; kShift: and what surrounds a row
   static constexpr int kStage = kRingThreads / T * kGroup;
   static_assert(kGroup % 16 == 0 && (kShift || kBytes % 16 == 0));
 
@@ -379,6 +379,23 @@ struct Columns {
         f[2 * k + 1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
       }
     }
+  }
+  // kShift: pair n of this thread's columns, zeros past the row's end.
+  static __device__ __forceinline__ float2 read_pair(char* stage, int skip, int dim, int n) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(group(stage) + (skip & ~3));
+    float2 f;
+    if constexpr (kSize == 4) {
+      from += H::column(n);
+      f = make_float2(__uint_as_float(from[0]), __uint_as_float(from[H::kStep]));
+    } else {
+      from += n * T + H::thread();
+      f = skip & 2 ? make_float2(__uint_as_float(from[0] & 0xffff0000u), __uint_as_float(from[1] << 16)) : pair_of(from[0]);
+    }
+    if ((n + 1) * T * 2 > dim) {   // (not the whole group)
+      if (H::column(n) >= dim) f.x = 0.f;
+      if (H::column(n) + H::kStep >= dim) f.y = 0.f;
+    }
+    return f;
   }
   // All of this thread's columns, zeros past the row's end.
   static __device__ __forceinline__ void read_row(char* stage, int skip, int dim, float2 (&f)[E / 2]) {
@@ -532,7 +549,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
 // All gradients in one pass over x and dy.  A thread adds its columns' terms of dw and db in
 // registers; the CTA's groups are joined in shared memory at the end, so that a launch leaves
 // one pair of partial sums per CTA.  kKeep: h and g stay in registers from the sums to dx
-// (E = 16; kShift: dx then takes x's place in the stage); otherwise they are read again.
+// (E = 16; kShift: dx then takes x's place in the stage); otherwise they are read again (20000
+// odd bf16 rows of 1001: 35 us with 16 columns a thread, 49 with 32 that are read again).
 template <typename X, typename G, int V, int T, int E, int kStages>
 __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid_constant__ GradArgs a) {
   constexpr int kGroups = kRingThreads / T;
@@ -540,7 +558,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
   using H = Held<V, T, E>;
   using CX = Columns<X, V, T, E>;
   using CG = Columns<G, V, T, E>;
-  static_assert(kKeep || !H::kShift);
   constexpr int kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][2];
@@ -576,7 +593,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     copies_wait<kStages - 1>();
     if constexpr (H::kShift) group_sync<T>();
     const int end = there ? dim : 0;   // kShift: nothing of what an earlier row left
-    float2 h[(kKeep ? E : V) / 2], g[(kKeep ? E : V) / 2], sg = both(0.f), sgh = both(0.f);
+    const int skip_dy = CG::skip(dy, at.row), skip_x = CX::skip(x, at.row), skip_add = CX::skip(add, at.row);
+    float2 h[(kKeep ? E : H::W) / 2], g[(kKeep ? E : H::W) / 2], sg = both(0.f), sgh = both(0.f);
     auto normalise = [&](float2& x) { x = __fmul2_rn(__fadd2_rn(x, both(-st.x)), both(st.y)); };
     auto add_terms = [&](int e, float2& g, float2 h) {   // pair e; g becomes dy w
       dw[e] = __ffma2_rn(g, h, dw[e]);
@@ -585,9 +603,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
       sg = __fadd2_rn(sg, g);
       sgh = __ffma2_rn(g, h, sgh);
     };
+    auto read = [&](int n) {   // (not kKeep) access n of dy and h
+      if constexpr (H::kShift) {
+        g[0] = CG::read_pair(stage, skip_dy, end, n);
+        h[0] = CX::read_pair(stage + CG::kStage, skip_x, end, n);
+      } else {
+        CG::read(stage, n, g);
+        CX::read(stage + CG::kStage, n, h);
+      }
+#pragma unroll
+      for (int i = 0; i < H::W / 2; ++i) normalise(h[i]);
+    };
     if constexpr (kKeep) {
-      CG::read_row(stage, CG::skip(dy, at.row), end, g);
-      CX::read_row(stage + CG::kStage, CX::skip(x, at.row), end, h);
+      CG::read_row(stage, skip_dy, end, g);
+      CX::read_row(stage + CG::kStage, skip_x, end, h);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
         normalise(h[e]);
@@ -596,44 +625,38 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     } else {
 #pragma unroll
       for (int n = 0; n < H::N; ++n) {
-        CG::read(stage, n, g);
-        CX::read(stage + CG::kStage, n, h);
+        read(n);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          normalise(h[i]);
-          add_terms(n * V / 2 + i, g[i], h[i]);
-        }
+        for (int i = 0; i < H::W / 2; ++i) add_terms(n * H::W / 2 + i, g[i], h[i]);
       }
     }
     if (a.grad_x) {
       float s[2] = {sum_of(sg), sum_of(sgh)};
       group_sum<T>(s, share, which);
       const float2 mean_g = both(a.center ? -s[0] / count : 0.f), mean_gh = both(-s[1] / count), r = both(st.y);
-      float2 plus[H::kShift ? E / 2 : 1];
-      if constexpr (H::kShift) {
+      float2 plus[H::kShift && kKeep ? E / 2 : 1];
+      if constexpr (H::kShift && kKeep) {
         if (a.add) {
-          CX::read_row(stage + CG::kStage + CX::kStage, CX::skip(add, at.row), end, plus);
+          CX::read_row(stage + CG::kStage + CX::kStage, skip_add, end, plus);
         } else {
 #pragma unroll
           for (int i = 0; i < E / 2; ++i) plus[i] = both(0.f);
         }
       }
       auto result = [&](int n, float2* f) {
-        if constexpr (H::kShift) {
+        if constexpr (H::kShift && kKeep) {
           f[0] = plus[n];
+        } else if constexpr (H::kShift) {
+          f[0] = a.add ? CX::read_pair(stage + CG::kStage + CX::kStage, skip_add, end, n) : both(0.f);
         } else {
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) f[i] = both(0.f);
           if (a.add) CX::read(stage + CG::kStage + CX::kStage, n, f);
         }
         if constexpr (!kKeep) {
-          CG::read(stage, n, g);
-          CX::read(stage + CG::kStage, n, h);
+          read(n);
 #pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            normalise(h[i]);
-            g[i] = __fmul2_rn(g[i], w[n * V / 2 + i]);
-          }
+          for (int i = 0; i < H::W / 2; ++i) g[i] = __fmul2_rn(g[i], w[n * H::W / 2 + i]);
         }
 #pragma unroll
         for (int i = 0; i < H::W / 2; ++i) {
@@ -641,8 +664,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
           f[i] = __ffma2_rn(r, __ffma2_rn(h[k], mean_gh, __fadd2_rn(g[k], mean_g)), f[i]);
         }
       };
-      write_row<X, V, T, E>(static_cast<X*>(a.grad_x) + (there ? at.row : 0) * a.grad_x_stride, dim, there, CX::group(stage + CG::kStage),
-                            result);
+      char* staging = kKeep ? CX::group(stage + CG::kStage) : ring + kStages * kStage + threadIdx.x / T * (T * E * int(sizeof(X)) + 16);
+      write_row<X, V, T, E>(static_cast<X*>(a.grad_x) + (there ? at.row : 0) * a.grad_x_stride, dim, there, staging, result);
     }
     if constexpr (H::kShift) group_sync<T>();   // all have read the stage
     copy_row(stage, at.row + kStages * at.step);
@@ -747,6 +770,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_grad_kernel(const __grid_co
       if (a.weight) g[j] *= load_any(a.weight, a.weight_f32, c + j);
     }
   };
+#pragma unroll 4
   for (int64_t c = first; c < a.dim; c += step) {
     load(c);
     float t = 0.f, u = 0.f;
@@ -760,6 +784,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_grad_kernel(const __grid_co
   }
   cta_sum<2>(s, share);
   const float mean_g = a.center ? s[0] / float(a.dim) : 0.f, mean_gh = s[1] / float(a.dim);
+#pragma unroll 2
   for (int64_t c = first; c < a.dim; c += step) {
     load(c);
     float add[V] = {};
@@ -772,6 +797,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_grad_kernel(const __grid_co
 
 // The weight's and the bias's gradient: part p of the rows, 32 x V columns a CTA.
 constexpr int kColumnWarps = 8;
+constexpr int64_t kPartRows = 64;   // rows of a part, while there are few: parts are written and read again
 
 template <typename X, typename G, int V>
 __global__ void __launch_bounds__(kColumnWarps * 32) column_sums_kernel(const __grid_constant__ GradArgs a) {
@@ -866,7 +892,7 @@ fsp_status launch_few(const NormArgs& a, cudaStream_t st) {
 }
 
 // Most shared memory that a ring takes.
-constexpr int kRingBytes = 224 << 10;
+constexpr int kRingBytes = 226 << 10;
 
 template <typename X, bool kShift, int T, int E>
 fsp_status launch_ring(const NormArgs& a, cudaStream_t st) {
@@ -948,7 +974,8 @@ fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
   constexpr bool kWide = sizeof(X) + sizeof(G) == 8;
   constexpr int V = kShift ? (kWide ? 1 : 2) : kWide ? 4 : 8, kGroups = kRingThreads / T;
   constexpr int kStage = 2 * Columns<X, V, T, E>::kStage + Columns<G, V, T, E>::kStage;
-  constexpr int kStages = std::min(4, kRingBytes / kStage), kSmem = kStages * kStage;
+  constexpr int kStaging = kShift && E > 16 ? kGroups * (T * E * int(sizeof(X)) + 16) : 0;
+  constexpr int kStages = std::min(4, (kRingBytes - kStaging) / kStage), kSmem = kStages * kStage + kStaging;
   void (*kernel)(GradArgs) = grad_ring_kernel<X, G, V, T, E, kStages>;
   fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
@@ -958,8 +985,9 @@ fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
 }
 
 template <typename X, typename G, int V>
-fsp_status launch_wide_grad(const GradArgs& a, cudaStream_t st) {
+fsp_status launch_wide_grad(GradArgs a, cudaStream_t st) {
   fsp_status s = FSP_OK;
+  a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kPartRows - 1) / kPartRows));
   if (a.grad_weight || a.grad_bias) {   // (first: grad_x may take the place of x or grad_out)
     const dim3 grid(unsigned((a.dim + 32 * V - 1) / (32 * V)), unsigned(a.n_parts));
     if (a.rows > 0)
@@ -979,7 +1007,9 @@ fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
   if (a.dim <= 2048) return launch_ring_grad<X, G, V == 1, 128, 16>(a, st);
   if (a.dim <= 4096) return launch_ring_grad<X, G, V == 1, 256, 16>(a, st);
   if (a.dim <= 8192) return launch_ring_grad<X, G, V == 1, 512, 16>(a, st);
-  if (V > 1 && a.dim <= 16384) return launch_ring_grad<X, G, false, 512, 32>(a, st);
+  // (odd rows of fp32: 32 columns a thread leave no room for a row of results beside one of each input)
+  if constexpr (V > 1 || sizeof(X) + sizeof(G) == 4)
+    if (a.dim <= 16384) return launch_ring_grad<X, G, V == 1, 512, 32>(a, st);
   return launch_wide_grad<X, G, V>(a, st);
 }
 
