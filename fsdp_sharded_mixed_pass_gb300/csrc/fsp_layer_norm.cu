@@ -164,16 +164,24 @@ __global__ void __launch_bounds__(T > 128 ? T : 128) norm_kernel(const __grid_co
 // group's part of a ring of stages in shared memory (cp.async): the copies of kStages - 1
 // rows are in flight while a row is reduced, without registers for them.
 //
-// Rows that begin and end at multiples of 16 bytes: a thread copies what it reads itself, so
-// that the ring needs no barriers.  Others (kShift): the group copies the 16-byte pieces that
-// cover the row, and a thread reads pairs of elements from wherever they begin; a row of
-// results is laid down in shared memory likewise and leaves in 16-byte pieces.  A piece that
-// reaches past a matrix's first or last byte is filled with the elements that are the matrix's.
+// Rows whose accesses of eight elements begin at multiples of their size (kWhole), and others of
+// an even count of bf16 elements or of fp32 ones, in pieces of four or eight bytes (kPart): a
+// thread copies what it reads itself, so that the ring needs no barriers.  Otherwise (kShift) the
+// group copies the 16-byte pieces that cover the row, and a thread reads pairs of elements from
+// wherever they begin; a row of results is laid down in shared memory likewise and leaves in
+// 16-byte pieces.  A piece that reaches past a matrix's first or last byte is filled with the
+// elements that are the matrix's.  (Measured, kPart and kShift, us: forward 20000 x 700 bf16 16.2
+// and 18.6, but 4099 x 1001 fp32 to bf16 9.5 and 8.4, so the forward pass of fp32 takes kShift;
+// gradients of 20000 x 700 bf16 29.4 and 33.8.)
 
 constexpr int kRingThreads = 512;
 
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {   // 16 bytes, or zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+template <int kPiece>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {   // 4, 8 or 16 bytes, or zeros
+  if constexpr (kPiece == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kPiece), "r"(there ? kPiece : 0) : "memory");
 }
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -240,15 +248,18 @@ struct Stream {
   int64_t stride;
 };
 
-// Which columns a thread of a group of T holds, as E / 2 pairs.  Rows at multiples of 16 bytes:
-// accesses n of V elements, from column (n T + t) V on (V = 4 or 8).  kShift: pair i is columns
-// 2 (i T + t) and the next (V = 2), or 2 i T + t and T further (V = 1, fp32 alone), so that a
-// warp reads words of shared memory side by side.
+// How the rows of a call lie: kWhole, kPart or kShift, above.
+enum Rows { kWhole, kPart, kShift };
+
+// Which columns a thread of a group of T holds, as E / 2 pairs.  kWhole: accesses n of V
+// elements, from column (n T + t) V on (V = 4 or 8).  Otherwise pair i is columns 2 (i T + t)
+// and the next (V = 2), or 2 i T + t and T further (V = 1, fp32 alone), so that a warp reads
+// words of shared memory side by side.
 template <int V, int T, int E>
 struct Held {
-  static constexpr bool kShift = V < 4;
-  static constexpr int N = kShift ? E / 2 : E / V;        // accesses, or pairs
-  static constexpr int W = kShift ? 2 : V;                // elements of one
+  static constexpr bool kPairs = V < 4;
+  static constexpr int N = kPairs ? E / 2 : E / V;        // accesses, or pairs
+  static constexpr int W = kPairs ? 2 : V;                // elements of one
   enum { kStep = V == 1 ? T : 1 };            // between the two columns of a pair
   static __device__ __forceinline__ int thread() { return threadIdx.x % T; }
   static __device__ __forceinline__ int column(int n) { return V == 1 ? 2 * n * T + thread() : (n * T + thread()) * W; }
@@ -273,7 +284,7 @@ struct Held {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = column(n);
-      if constexpr (kShift) {
+      if constexpr (kPairs) {
         if (c < dim) f[n].x = load_any(p, f32, c);
         if (c + kStep < dim) f[n].y = load_any(p, f32, c + kStep);
       } else if (c < dim) {
@@ -287,14 +298,13 @@ struct Held {
 };
 
 // Rows of Y in a stage of the ring.
-template <typename Y, int V, int T, int E>
+template <typename Y, int V, int T, int E, Rows R>
 struct Columns {
   using H = Held<V, T, E>;
-  static constexpr bool kShift = H::kShift;
   static constexpr int kSize = int(sizeof(Y)), kBytes = kSize * V;
-  static constexpr int kGroup = T * E * kSize + (kShift ? 16 : 0);   // of a group; kShift: and what surrounds a row
+  static constexpr int kGroup = T * E * kSize + (R == kShift ? 16 : 0);   // of a group; kShift: and what surrounds a row
   static constexpr int kStage = kRingThreads / T * kGroup;
-  static_assert(kGroup % 16 == 0 && (kShift || kBytes % 16 == 0));
+  static_assert(kGroup % 16 == 0 && (R != kWhole || kBytes % 16 == 0) && (R == kWhole) == (V >= 4));
 
   static __device__ __forceinline__ char* group(char* stage) { return stage + threadIdx.x / T * kGroup; }
   static __device__ __forceinline__ const char* address(Stream s, uint32_t row) {
@@ -302,31 +312,40 @@ struct Columns {
   }
   // Zeros for the columns past a row's end, which no copy writes.
   static __device__ __forceinline__ void clear(char* stage, int dim) {
-    if constexpr (!kShift) {
-      const int t = H::thread();
-      stage = group(stage) + t * kBytes;
+    const int t = H::thread();
+    stage = group(stage);
+    if constexpr (R == kWhole) {
 #pragma unroll
       for (int n = 0; n < H::N; ++n)
         if (n * T * V >= dim - t * V) {
 #pragma unroll
-          for (int k = 0; k < kBytes; k += 16) *reinterpret_cast<uint4*>(stage + n * T * kBytes + k) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < kBytes; k += 16) *reinterpret_cast<uint4*>(stage + (n * T + t) * kBytes + k) = make_uint4(0, 0, 0, 0);
         }
+    } else if constexpr (R == kPart) {
+#pragma unroll
+      for (int n = 0; n < H::N; ++n) {
+        Y* at = reinterpret_cast<Y*>(stage) + H::column(n);
+        if (H::column(n) >= dim) at[0] = narrow<Y>(0.f);
+        if (H::column(n) + H::kStep >= dim) at[H::kStep] = narrow<Y>(0.f);
+      }
     }
   }
   // Starts the copies of a row; past the last, zeros where other groups of the warp go on (T < 32).
   static __device__ __forceinline__ void copy(char* stage, Stream s, uint32_t row, uint32_t rows, int dim) {
     const int t = H::thread();
     stage = group(stage);
-    if constexpr (!kShift) {
+    if constexpr (R != kShift) {
       const bool there = row < rows;
       if (T >= 32 && !there) return;
+      // (V = 1: two columns a pair, each a copy)
+      constexpr int kCopies = R == kPart && V == 1 ? 2 * H::N : H::N, kPiece = kBytes < 16 ? kBytes : 16;
       const char* src = address(s, there ? row : 0) + t * kBytes;
       const uint32_t dst = smem_at(stage) + t * kBytes;
 #pragma unroll
-      for (int n = 0; n < H::N; ++n)
+      for (int n = 0; n < kCopies; ++n)
         if (n * T * V < dim - t * V) {
 #pragma unroll
-          for (int k = 0; k < kBytes; k += 16) copy_async(dst + n * T * kBytes + k, src + n * T * kBytes + k, there);
+          for (int k = 0; k < kBytes; k += kPiece) copy_async<kPiece>(dst + n * T * kBytes + k, src + n * T * kBytes + k, there);
         }
     } else if (row < rows) {
       const char* begin = address(s, row);
@@ -336,13 +355,13 @@ struct Columns {
       if (inside(s, row, rows)) {
 #pragma unroll
         for (int k = 0; k < kGroup; k += T * 16)
-          if (k + t * 16 < bytes) copy_async(dst + k, src + k, true);
+          if (k + t * 16 < bytes) copy_async<16>(dst + k, src + k, true);
       } else {
         const char *lowest = static_cast<const char*>(s.p), *highest = address(s, rows - 1) + dim * kSize;
         for (int k = t * 16; k < bytes; k += T * 16) {
           const char* p = begin - before + k;
           if (p >= lowest && p + 16 <= highest) {
-            copy_async(smem_at(stage) + k, p, true);
+            copy_async<16>(smem_at(stage) + k, p, true);
           } else {
             for (const char* q = p < lowest ? lowest : p; q < p + 16 && q < highest; q += kSize)
               *reinterpret_cast<Y*>(stage + k + (q - p)) = *reinterpret_cast<const Y*>(q);
@@ -358,7 +377,7 @@ struct Columns {
   }
   // Bytes of a stage before a row's first.
   static __device__ __forceinline__ int skip(Stream s, uint32_t row) {
-    return kShift ? int((uint32_t(reinterpret_cast<uintptr_t>(s.p)) + row * uint32_t(s.stride) * kSize) & 15u) : 0;
+    return R == kShift ? int((uint32_t(reinterpret_cast<uintptr_t>(s.p)) + row * uint32_t(s.stride) * kSize) & 15u) : 0;
   }
   static __device__ __forceinline__ float2 pair_of(uint32_t w) {   // bf16
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -380,7 +399,7 @@ struct Columns {
       }
     }
   }
-  // kShift: pair n of this thread's columns, zeros past the row's end.
+  // Pair n of this thread's columns (not kWhole), zeros past the row's end.
   static __device__ __forceinline__ float2 read_pair(char* stage, int skip, int dim, int n) {
     const uint32_t* from = reinterpret_cast<const uint32_t*>(group(stage) + (skip & ~3));
     float2 f;
@@ -391,7 +410,7 @@ struct Columns {
       from += n * T + H::thread();
       f = skip & 2 ? make_float2(__uint_as_float(from[0] & 0xffff0000u), __uint_as_float(from[1] << 16)) : pair_of(from[0]);
     }
-    if ((n + 1) * T * 2 > dim) {   // (not the whole group)
+    if (R == kShift && (n + 1) * T * 2 > dim) {   // (not the whole group)
       if (H::column(n) >= dim) f.x = 0.f;
       if (H::column(n) + H::kStep >= dim) f.y = 0.f;
     }
@@ -399,7 +418,7 @@ struct Columns {
   }
   // All of this thread's columns, zeros past the row's end.
   static __device__ __forceinline__ void read_row(char* stage, int skip, int dim, float2 (&f)[E / 2]) {
-    if constexpr (!kShift) {
+    if constexpr (R == kWhole) {
 #pragma unroll
       for (int n = 0; n < H::N; ++n) read(stage, n, f + n * V / 2);
     } else {
@@ -410,7 +429,7 @@ struct Columns {
         for (int n = 0; n < H::N; ++n) f[n] = make_float2(__uint_as_float(from[2 * n * T]), __uint_as_float(from[2 * n * T + H::kStep]));
       } else {
         from += H::thread();
-        if (skip & 2) {   // (the same for the whole group) pairs across two words
+        if (R == kShift && skip & 2) {   // (the same for the whole group) pairs across two words
 #pragma unroll
           for (int n = 0; n < H::N; ++n)
             f[n] = make_float2(__uint_as_float(from[n * T] & 0xffff0000u), __uint_as_float(from[n * T + 1] << 16));
@@ -419,7 +438,7 @@ struct Columns {
           for (int n = 0; n < H::N; ++n) f[n] = pair_of(from[n * T]);
         }
       }
-      H::mask(dim, f);
+      if constexpr (R == kShift) H::mask(dim, f);
     }
   }
 };
@@ -427,17 +446,23 @@ struct Columns {
 // A row of results: result(n, f) gives access (or pair) n of a thread.  kShift: by way of
 // `staging`, 16 bytes more than the group's E * T elements in shared memory, which the barriers
 // of the sums before it have left free.  there: whether the group has a row.
-template <typename O, int V, int T, int E, typename Result>
+template <typename O, int V, int T, int E, Rows R, typename Result>
 __device__ __forceinline__ void write_row(O* out, int dim, bool there, char* staging, Result result) {
   using H = Held<V, T, E>;
   const int t = H::thread();
-  if constexpr (!H::kShift) {
+  if constexpr (R != kShift) {
     if (!there) return;
 #pragma unroll
     for (int n = 0; n < H::N; ++n) {
-      float2 f[V / 2];
+      float2 f[H::W / 2];
       result(n, f);
-      if (H::column(n) < dim) store_vec<O, V>(out + H::column(n), reinterpret_cast<const float*>(f));
+      const int c = H::column(n);
+      if constexpr (V == 1) {
+        if (c < dim) store_vec<O, 1>(out + c, &f->x);
+        if (c + T < dim) store_vec<O, 1>(out + c + T, &f->y);
+      } else if (c < dim) {
+        store_vec<O, V>(out + c, reinterpret_cast<const float*>(f));
+      }
     }
   } else {
     // laid down as far from a multiple of 16 bytes as it is in memory, so that whole pieces leave
@@ -475,9 +500,9 @@ __device__ __forceinline__ void write_row(O* out, int dim, bool there, char* sta
   }
 }
 
-template <typename X, int V, int T, int E, int kStages>
+template <typename X, int V, int T, int E, int kStages, Rows R>
 __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid_constant__ NormArgs a) {
-  using C = Columns<X, V, T, E>;
+  using C = Columns<X, V, T, E, R>;
   using H = Held<V, T, E>;
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][1];
@@ -502,7 +527,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
     char* stage = ring + slot * C::kStage;
     slot = slot + 1 == kStages ? 0 : slot + 1;
     copies_wait<kStages - 1>();
-    if constexpr (H::kShift) group_sync<T>();
+    if constexpr (R == kShift) group_sync<T>();
     float2 f[E / 2], part[2] = {};
     float m = 0.f, s[1];
     C::read_row(stage, C::skip(x, at.row), dim, f);
@@ -536,7 +561,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
     auto write = [&](auto* out) {
       using O = std::remove_pointer_t<decltype(out)>;
       char* staging = ring + kStages * C::kStage + threadIdx.x / T * (T * E * int(sizeof(O)) + 16);
-      write_row<O, V, T, E>(out + (there ? at.row : 0) * a.out_stride, dim, there, staging, result);
+      write_row<O, V, T, E, R>(out + (there ? at.row : 0) * a.out_stride, dim, there, staging, result);
     };
     if (a.out_f32)
       write(static_cast<float*>(a.out));
@@ -551,13 +576,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
 // one pair of partial sums per CTA.  kKeep: h and g stay in registers from the sums to dx
 // (E = 16; kShift: dx then takes x's place in the stage); otherwise they are read again (20000
 // odd bf16 rows of 1001: 35 us with 16 columns a thread, 49 with 32 that are read again).
-template <typename X, typename G, int V, int T, int E, int kStages>
+template <typename X, typename G, int V, int T, int E, int kStages, Rows R>
 __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid_constant__ GradArgs a) {
   constexpr int kGroups = kRingThreads / T;
   constexpr bool kKeep = E <= 16;
   using H = Held<V, T, E>;
-  using CX = Columns<X, V, T, E>;
-  using CG = Columns<G, V, T, E>;
+  using CX = Columns<X, V, T, E, R>;
+  using CG = Columns<G, V, T, E, R>;
   constexpr int kStage = 2 * CX::kStage + CG::kStage;   // dy, x, add
   extern __shared__ __align__(16) char ring[];
   __shared__ float share[2][kRingThreads / 32][2];
@@ -591,7 +616,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     const float2 st = there ? next : make_float2(0.f, 0.f);
     if (at.row + at.step < rows) next = a.stats[at.row + at.step];
     copies_wait<kStages - 1>();
-    if constexpr (H::kShift) group_sync<T>();
+    if constexpr (R == kShift) group_sync<T>();
     const int end = there ? dim : 0;   // kShift: nothing of what an earlier row left
     const int skip_dy = CG::skip(dy, at.row), skip_x = CX::skip(x, at.row), skip_add = CX::skip(add, at.row);
     float2 h[(kKeep ? E : H::W) / 2], g[(kKeep ? E : H::W) / 2], sg = both(0.f), sgh = both(0.f);
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
       sgh = __ffma2_rn(g, h, sgh);
     };
     auto read = [&](int n) {   // (not kKeep) access n of dy and h
-      if constexpr (H::kShift) {
+      if constexpr (H::kPairs) {
         g[0] = CG::read_pair(stage, skip_dy, end, n);
         h[0] = CX::read_pair(stage + CG::kStage, skip_x, end, n);
       } else {
@@ -634,8 +659,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
       float s[2] = {sum_of(sg), sum_of(sgh)};
       group_sum<T>(s, share, which);
       const float2 mean_g = both(a.center ? -s[0] / count : 0.f), mean_gh = both(-s[1] / count), r = both(st.y);
-      float2 plus[H::kShift && kKeep ? E / 2 : 1];
-      if constexpr (H::kShift && kKeep) {
+      float2 plus[H::kPairs && kKeep ? E / 2 : 1];
+      if constexpr (H::kPairs && kKeep) {
         if (a.add) {
           CX::read_row(stage + CG::kStage + CX::kStage, skip_add, end, plus);
         } else {
@@ -644,9 +669,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
         }
       }
       auto result = [&](int n, float2* f) {
-        if constexpr (H::kShift && kKeep) {
+        if constexpr (H::kPairs && kKeep) {
           f[0] = plus[n];
-        } else if constexpr (H::kShift) {
+        } else if constexpr (H::kPairs) {
           f[0] = a.add ? CX::read_pair(stage + CG::kStage + CX::kStage, skip_add, end, n) : both(0.f);
         } else {
 #pragma unroll
@@ -665,9 +690,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
         }
       };
       char* staging = kKeep ? CX::group(stage + CG::kStage) : ring + kStages * kStage + threadIdx.x / T * (T * E * int(sizeof(X)) + 16);
-      write_row<X, V, T, E>(static_cast<X*>(a.grad_x) + (there ? at.row : 0) * a.grad_x_stride, dim, there, staging, result);
+      write_row<X, V, T, E, R>(static_cast<X*>(a.grad_x) + (there ? at.row : 0) * a.grad_x_stride, dim, there, staging, result);
     }
-    if constexpr (H::kShift) group_sync<T>();   // all have read the stage
+    if constexpr (R == kShift) group_sync<T>();   // all have read the stage
     copy_row(stage, at.row + kStages * at.step);
   }
   copies_wait<0>();
@@ -684,7 +709,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     float* to = joined + group * kCols;
 #pragma unroll
     for (int n = 0; n < H::N; ++n) {
-      if constexpr (H::kShift) {
+      if constexpr (H::kPairs) {
         to[H::column(n)] = y[n].x;
         to[H::column(n) + H::kStep] = y[n].y;
       } else {
@@ -894,14 +919,14 @@ fsp_status launch_few(const NormArgs& a, cudaStream_t st) {
 // Most shared memory that a ring takes.
 constexpr int kRingBytes = 226 << 10;
 
-template <typename X, bool kShift, int T, int E>
+template <typename X, Rows R, int T, int E>
 fsp_status launch_ring(const NormArgs& a, cudaStream_t st) {
-  constexpr int V = !kShift ? 16 / int(sizeof(X)) : sizeof(X) == 4 ? 1 : 2;
-  using C = Columns<X, V, T, E>;
-  constexpr int kStaging = kShift ? kRingThreads / T * (T * E * 4 + 16) : 0;
+  constexpr int V = R == kWhole ? 16 / int(sizeof(X)) : sizeof(X) == 4 ? 1 : 2;
+  using C = Columns<X, V, T, E, R>;
+  constexpr int kStaging = R == kShift ? kRingThreads / T * (T * E * 4 + 16) : 0;
   constexpr int kStages = std::min((kRingBytes - kStaging) / C::kStage, C::kStage > 48 << 10 ? 3 : C::kStage > 24 << 10 ? 4 : 6);
   constexpr int kSmem = kStages * C::kStage + kStaging;
-  void (*kernel)(NormArgs) = norm_ring_kernel<X, V, T, E, kStages>;
+  void (*kernel)(NormArgs) = norm_ring_kernel<X, V, T, E, kStages, R>;
   const fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   const int64_t ctas = std::min<int64_t>(kParts, (a.rows + kRingThreads / T - 1) / (kRingThreads / T));
@@ -913,8 +938,9 @@ fsp_status launch_ring(const NormArgs& a, cudaStream_t st) {
 // 8192 x 128 3.8 and 2.7; 64 x 8192 2.8 and 3.4, 256 x 8192 6.1 and 3.9).
 constexpr int64_t kRingElements = 3 << 18;
 
-template <typename X, int V>
+template <typename X, Rows R>
 fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
+  constexpr int V = R == kWhole ? 8 : 1;
   if (a.rows * a.dim < kRingElements) {
     if (a.dim <= 256) return launch_few<X, V, 32, 8>(a, st);
     if (a.dim <= 512) return launch_few<X, V, 64, 8>(a, st);
@@ -923,15 +949,15 @@ fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
     if (a.dim <= 4096) return launch_few<X, V, 512, 8>(a, st);
     if (a.dim <= 8192) return launch_few<X, V, 1024, 8>(a, st);
   } else {
-    if (a.dim <= 128) return launch_ring<X, V == 1, 8, 16>(a, st);
-    if (a.dim <= 256) return launch_ring<X, V == 1, 16, 16>(a, st);
-    if (a.dim <= 512) return launch_ring<X, V == 1, 32, 16>(a, st);
-    if (a.dim <= 1024) return launch_ring<X, V == 1, 32, 32>(a, st);
-    if (a.dim <= 2048) return launch_ring<X, V == 1, 64, 32>(a, st);
-    if (a.dim <= 4096) return launch_ring<X, V == 1, 128, 32>(a, st);
-    if (a.dim <= 8192) return launch_ring<X, V == 1, 256, 32>(a, st);
+    if (a.dim <= 128) return launch_ring<X, R, 8, 16>(a, st);
+    if (a.dim <= 256) return launch_ring<X, R, 16, 16>(a, st);
+    if (a.dim <= 512) return launch_ring<X, R, 32, 16>(a, st);
+    if (a.dim <= 1024) return launch_ring<X, R, 32, 32>(a, st);
+    if (a.dim <= 2048) return launch_ring<X, R, 64, 32>(a, st);
+    if (a.dim <= 4096) return launch_ring<X, R, 128, 32>(a, st);
+    if (a.dim <= 8192) return launch_ring<X, R, 256, 32>(a, st);
   }
-  if (a.dim <= 16384) return launch_ring<X, V == 1, 512, 32>(a, st);
+  if (a.dim <= 16384) return launch_ring<X, R, 512, 32>(a, st);
   return launch_next(wide_norm_kernel<X, V>, dim3(unsigned(a.rows)), kWideThreads, 0, 1, a, st, "layer norm kernel launch");
 }
 
@@ -954,11 +980,11 @@ fsp_status norm(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs
   if (s != FSP_OK) return s;
   NormArgs a{x, weight, bias, out, reinterpret_cast<float2*>(stats), rows, dim, xs, os, eps, center != 0, pd == FSP_DTYPE_F32, od == FSP_DTYPE_F32};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(out, os, od, 8) && (!weight || rows_fit(weight, 0, pd, 8)) &&
-                   (!bias || rows_fit(bias, 0, pd, 8));
+  auto fit = [&](int v) { return dim % v == 0 && rows_fit(x, xs, xd, v) && rows_fit(out, os, od, v); };
+  const bool whole = fit(8) && (!weight || rows_fit(weight, 0, pd, 8)) && (!bias || rows_fit(bias, 0, pd, 8));
   using B = __nv_bfloat16;
-  if (xd == FSP_DTYPE_F32) return vec ? launch_norm<float, 8>(a, st) : launch_norm<float, 1>(a, st);
-  return vec ? launch_norm<B, 8>(a, st) : launch_norm<B, 1>(a, st);
+  if (xd == FSP_DTYPE_F32) return whole ? launch_norm<float, kWhole>(a, st) : launch_norm<float, kShift>(a, st);
+  return whole ? launch_norm<B, kWhole>(a, st) : fit(2) ? launch_norm<B, kPart>(a, st) : launch_norm<B, kShift>(a, st);
 }
 
 int64_t parts_of(int64_t rows) { return std::min<int64_t>(kParts, rows); }
@@ -969,14 +995,14 @@ fsp_status launch_join(const GradArgs& a, cudaStream_t st) {
                      "layer norm gradient (join) kernel launch");
 }
 
-template <typename X, typename G, bool kShift, int T, int E>
+template <typename X, typename G, Rows R, int T, int E>
 fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
   constexpr bool kWide = sizeof(X) + sizeof(G) == 8;
-  constexpr int V = kShift ? (kWide ? 1 : 2) : kWide ? 4 : 8, kGroups = kRingThreads / T;
-  constexpr int kStage = 2 * Columns<X, V, T, E>::kStage + Columns<G, V, T, E>::kStage;
-  constexpr int kStaging = kShift && E > 16 ? kGroups * (T * E * int(sizeof(X)) + 16) : 0;
+  constexpr int V = R == kWhole ? (kWide ? 4 : 8) : kWide ? 1 : 2, kGroups = kRingThreads / T;
+  constexpr int kStage = 2 * Columns<X, V, T, E, R>::kStage + Columns<G, V, T, E, R>::kStage;
+  constexpr int kStaging = R == kShift && E > 16 ? kGroups * (T * E * int(sizeof(X)) + 16) : 0;
   constexpr int kStages = std::min(4, (kRingBytes - kStaging) / kStage), kSmem = kStages * kStage + kStaging;
-  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, V, T, E, kStages>;
+  void (*kernel)(GradArgs) = grad_ring_kernel<X, G, V, T, E, kStages, R>;
   fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
@@ -998,24 +1024,26 @@ fsp_status launch_wide_grad(GradArgs a, cudaStream_t st) {
   return launch_next(wide_grad_kernel<X, G, V>, dim3(unsigned(a.rows)), kWideThreads, 0, 1, a, st, "layer norm gradient kernel launch");
 }
 
-template <typename X, typename G, int V>
+template <typename X, typename G, Rows R>
 fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
-  if (a.dim <= 128) return launch_ring_grad<X, G, V == 1, 8, 16>(a, st);
-  if (a.dim <= 256) return launch_ring_grad<X, G, V == 1, 16, 16>(a, st);
-  if (a.dim <= 512) return launch_ring_grad<X, G, V == 1, 32, 16>(a, st);
-  if (a.dim <= 1024) return launch_ring_grad<X, G, V == 1, 64, 16>(a, st);
-  if (a.dim <= 2048) return launch_ring_grad<X, G, V == 1, 128, 16>(a, st);
-  if (a.dim <= 4096) return launch_ring_grad<X, G, V == 1, 256, 16>(a, st);
-  if (a.dim <= 8192) return launch_ring_grad<X, G, V == 1, 512, 16>(a, st);
-  // (odd rows of fp32: 32 columns a thread leave no room for a row of results beside one of each input)
-  if constexpr (V > 1 || sizeof(X) + sizeof(G) == 4)
-    if (a.dim <= 16384) return launch_ring_grad<X, G, V == 1, 512, 32>(a, st);
-  return launch_wide_grad<X, G, V>(a, st);
+  if (a.dim <= 128) return launch_ring_grad<X, G, R, 8, 16>(a, st);
+  if (a.dim <= 256) return launch_ring_grad<X, G, R, 16, 16>(a, st);
+  if (a.dim <= 512) return launch_ring_grad<X, G, R, 32, 16>(a, st);
+  if (a.dim <= 1024) return launch_ring_grad<X, G, R, 64, 16>(a, st);
+  if (a.dim <= 2048) return launch_ring_grad<X, G, R, 128, 16>(a, st);
+  if (a.dim <= 4096) return launch_ring_grad<X, G, R, 256, 16>(a, st);
+  if (a.dim <= 8192) return launch_ring_grad<X, G, R, 512, 16>(a, st);
+  // (odd rows of fp32 beside bf16: 32 columns a thread leave no room for a row of results beside one of each input)
+  if constexpr (R != kShift || sizeof(X) + sizeof(G) == 4)
+    if (a.dim <= 16384) return launch_ring_grad<X, G, R, 512, 32>(a, st);
+  return launch_wide_grad<X, G, R == kWhole ? 8 : 1>(a, st);
 }
 
 template <typename X, typename G>
-fsp_status launch_grad_v(const GradArgs& a, bool vec, cudaStream_t st) {
-  return vec ? launch_grad<X, G, 8>(a, st) : launch_grad<X, G, 1>(a, st);
+fsp_status launch_grad(const GradArgs& a, Rows rows, cudaStream_t st) {
+  if (rows == kWhole) return launch_grad<X, G, kWhole>(a, st);
+  if constexpr (sizeof(X) + sizeof(G) == 8) return launch_grad<X, G, kPart>(a, st);   // (elements of four bytes)
+  else return rows == kPart ? launch_grad<X, G, kPart>(a, st) : launch_grad<X, G, kShift>(a, st);
 }
 
 fsp_status backward(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs, const float* stats, int32_t center,
@@ -1075,12 +1103,14 @@ fsp_status backward(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_
   a.grad_param_f32 = pd == FSP_DTYPE_F32;
   a.accumulate = accumulate != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = dim % 8 == 0 && rows_fit(x, xs, xd, 8) && rows_fit(grad, gs, gd, 8) && (!add || rows_fit(add, as, xd, 8)) &&
-                   (!grad_x || rows_fit(grad_x, ds, xd, 8)) && (!weight || rows_fit(weight, 0, wd, 8));
+  auto fit = [&](int v) {
+    return dim % v == 0 && rows_fit(x, xs, xd, v) && rows_fit(grad, gs, gd, v) && (!add || rows_fit(add, as, xd, v)) &&
+           (!grad_x || rows_fit(grad_x, ds, xd, v));
+  };
+  const Rows lie = fit(8) && (!weight || rows_fit(weight, 0, wd, 8)) ? kWhole : fit(2) ? kPart : kShift;
   using B = __nv_bfloat16;
-  if (xd == FSP_DTYPE_F32)
-    return gd == FSP_DTYPE_F32 ? launch_grad_v<float, float>(a, vec, st) : launch_grad_v<float, B>(a, vec, st);
-  return gd == FSP_DTYPE_F32 ? launch_grad_v<B, float>(a, vec, st) : launch_grad_v<B, B>(a, vec, st);
+  if (xd == FSP_DTYPE_F32) return gd == FSP_DTYPE_F32 ? launch_grad<float, float>(a, lie, st) : launch_grad<float, B>(a, lie, st);
+  return gd == FSP_DTYPE_F32 ? launch_grad<B, float>(a, lie, st) : launch_grad<B, B>(a, lie, st);
 }
 
 }  // namespace
