@@ -7,8 +7,9 @@
 // by the seed, its counter (i / 8, call).  The mask is a function of (seed, call, i) and is
 // never stored: the gradient is the same function of dy, without the residual.
 //
-// Bound: HBM.  Sixteen bits an element, so that ten rounds (a block of four words) serve
-// eight elements.
+// Bound: HBM (2^26 bf16 elements onto a residual 57 us, 1.03 of the measured copy; without one 44
+// us, 0.90, where issue slots count too).  Sixteen bits an element, so that ten rounds (a block of
+// four words) serve eight elements; with 32 the generator alone would take as long as the memory.
 #include <type_traits>
 
 #include "fsp_rows.cuh"

@@ -5,9 +5,10 @@
 //
 // the gradient is the same with the angle negated.
 //
-// Bound: HBM.  A frequency is held in units of 2^-64 turn per position, so t f_j modulo a
-// turn is one 64-bit product that wraps: as exact at position 2^31 as at position 1, without
-// arithmetic in 64-bit floating point.
+// Bound: HBM (131072 tokens of 12 bf16 heads of 64 61 us, 0.97 of the measured copy; 16384 of 24
+// heads of 128 within a projection's rows 34 us, 0.87).  A frequency is held in units of 2^-64
+// turn per position, so t f_j modulo a turn is one 64-bit product that wraps: as exact at position
+// 2^31 as at position 1, without arithmetic in 64-bit floating point.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
