@@ -14,7 +14,9 @@
 //     residual's 81 us, 0.97; 131072 x 128 12 and 22 us; odd rows 20000 x 1001 20 and 35 us, bound by
 //     their instructions);
 //   longer rows: a CTA per row, which reads it three times.
-// All sums are fp32; no sum's order depends on timing.
+// All sums are fp32; no sum's order depends on timing.  In the ring a mean is a product with
+// 1 / dim and r is rsqrtf's (two roundings, and at most two steps of 2^-23: divisions and a root
+// cost a short row a tenth of its instructions).
 #include <algorithm>
 #include <type_traits>
 
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
   float2 w[E / 2], b[E / 2];
   H::load(a.weight, a.param_f32, dim, 1.f, w);
   H::load(a.bias, a.param_f32, dim, 0.f, b);
-  const float count = float(dim);
+  const float share_of = 1.f / float(dim);
   int slot = 0;
   for (int which = 0; at.first < rows; at.next(), which ^= 1) {
     char* stage = ring + slot * C::kStage;
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
       for (int i = 0; i < E / 2; ++i) part[i & 1] = __fadd2_rn(part[i & 1], f[i]);
       s[0] = sum_of(__fadd2_rn(part[0], part[1]));
       group_sum<T>(s, share, 0);
-      m = s[0] / count;
+      m = s[0] * share_of;
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) f[i] = __fadd2_rn(f[i], both(-m));
       H::mask(dim, f);
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
     group_sum<T>(s, share, a.center ? 1 : which);
     C::copy(stage, x, at.row + kStages * at.step, rows, dim);   // (all that was read has entered the sum)
     copies_issued();
-    const float r = 1.f / sqrtf(s[0] / count + a.eps);
+    const float r = rsqrtf(s[0] * share_of + a.eps);
     const bool there = at.row < rows;
     if (a.stats && H::thread() == 0 && there) a.stats[at.row] = make_float2(m, r);
     auto result = [&](int n, float2* y) {
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
   }
   float2 w[E / 2], dw[E / 2] = {}, db[E / 2] = {};
   H::load(a.weight, a.weight_f32, dim, 1.f, w);
-  const float count = float(dim);
+  const float share_of = 1.f / float(dim);
   float2 next = at.row < rows ? a.stats[at.row] : make_float2(0.f, 0.f);
   int slot = 0;
   for (int which = 0; at.first < rows; at.next(), which ^= 1) {
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     if (a.grad_x) {
       float s[2] = {sum_of(sg), sum_of(sgh)};
       group_sum<T>(s, share, which);
-      const float2 mean_g = both(a.center ? -s[0] / count : 0.f), mean_gh = both(-s[1] / count), r = both(st.y);
+      const float2 mean_g = both(a.center ? -s[0] * share_of : 0.f), mean_gh = both(-s[1] * share_of), r = both(st.y);
       float2 plus[H::kPairs && kKeep ? E / 2 : 1];
       if constexpr (H::kPairs && kKeep) {
         if (a.add) {

@@ -22,13 +22,13 @@ def norm(x, w, b, eps, center):
     r = 1 / np.sqrt(var + eps)
     h = c * r
     y = h * w + b
-    # the mean: a term goes through `depth` additions, then the division
+    # the mean: a term goes through `depth` additions, then the division, or 1 / n and a product
     em = (depth(n) + 2) * U * np.abs(x).mean(1, keepdims=True) if center else 0 * m
     ec = em + U * np.abs(c)
     # the variance: its terms' own error, the additions, the division, eps
     ev = (2 * np.abs(c) * ec + ec * ec).mean(1, keepdims=True) + (depth(n) + 4) * U * (var + eps)
     with np.errstate(divide="ignore", invalid="ignore"):
-        er = 0.5 * ev / (var + eps - np.minimum(ev, 0.5 * (var + eps))) + 4 * U   # relative; root, division
+        er = 0.5 * ev / (var + eps - np.minimum(ev, 0.5 * (var + eps))) + 4 * U   # relative; root and division, or a root of two steps of 2^-23
     eh = ec * r * (1 + er) + np.abs(h) * (er + 2 * U)
     ey = np.abs(w) * eh + U * (np.abs(y) + np.abs(h * w) * 0) + 2 * U * np.abs(h * w)
     return (y, m[:, 0], r[:, 0]), (ey, em[:, 0] + U * np.abs(m[:, 0]), (er * r)[:, 0])
