@@ -11,7 +11,7 @@
 //   many rows of up to 16384 elements: a CTA per SM that stays, rows ahead in a ring in shared
 //     memory, the gradients of all three in one pass and a join of one pair of partial sums per
 //     CTA (32768 x 2048 bf16: forward 46 us, 0.87 of the measured copy, gradients with the
-//     residual's 81 us, 0.97; 131072 x 128 12 and 22 us; odd rows 20000 x 1001 20 and 35 us, bound by
+//     residual's 82 us, 0.97; 131072 x 128 12 and 21 us; odd rows 20000 x 1001 20 and 35 us, bound by
 //     their instructions);
 //   longer rows: a CTA per row, which reads it three times.
 // All sums are fp32; no sum's order depends on timing.  In the ring a mean is a product with
@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(T > 128 ? T : 128) norm_kernel(const __grid_co
 // group copies the 16-byte pieces that cover the row, and a thread reads pairs of elements from
 // wherever they begin; a row of results is laid down in shared memory likewise and leaves in
 // 16-byte pieces.  A piece that reaches past a matrix's first or last byte is filled with the
-// elements that are the matrix's.  (Measured, kPart and kShift, us: forward 20000 x 700 bf16 16.2
-// and 18.6, but 4099 x 1001 fp32 to bf16 9.5 and 8.4, so the forward pass of fp32 takes kShift;
-// gradients of 20000 x 700 bf16 29.4 and 33.8.)
+// elements that are the matrix's.  (Measured, kPart and kShift, us: forward 20000 x 700 bf16 15.8
+// and 17.9, but 4099 x 1001 fp32 to bf16 9.4 and 8.1, so the forward pass of fp32 takes kShift;
+// gradients of 20000 x 700 bf16 23.3 and 33.5.)
 
 constexpr int kRingThreads = 512;
 
@@ -961,6 +961,7 @@ fsp_status launch_norm(const NormArgs& a, cudaStream_t st) {
     if (a.dim <= 4096) return launch_few<X, V, 512, 8>(a, st);
     if (a.dim <= 8192) return launch_few<X, V, 1024, 8>(a, st);
   } else {
+    if (a.dim <= 64) return launch_ring<X, R, 8, 8>(a, st);
     if (a.dim <= 128) return launch_ring<X, R, 8, 16>(a, st);
     if (a.dim <= 256) return launch_ring<X, R, 16, 16>(a, st);
     if (a.dim <= 512) return launch_ring<X, R, 32, 16>(a, st);
@@ -1038,6 +1039,7 @@ fsp_status launch_wide_grad(GradArgs a, cudaStream_t st) {
 
 template <typename X, typename G, Rows R>
 fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
+  if (a.dim <= 64) return launch_ring_grad<X, G, R, 8, 8>(a, st);
   if (a.dim <= 128) return launch_ring_grad<X, G, R, 8, 16>(a, st);
   if (a.dim <= 256) return launch_ring_grad<X, G, R, 16, 16>(a, st);
   if (a.dim <= 512) return launch_ring_grad<X, G, R, 32, 16>(a, st);

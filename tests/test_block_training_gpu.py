@@ -108,6 +108,45 @@ def test_a_captured_step_replays():
     assert fsp.device_error() == 0
 
 
+def test_calls_that_follow_one_another_at_once():
+    """Each call starts while the one before it ends: a chain of calls in place gives what waiting after each gives."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rope = fsp.Rotary(64)
+
+    def chain(wait):
+        done = torch.cuda.synchronize if wait else lambda: None
+        h = torch.randn(3000, 512, generator=gen.manual_seed(1), device="cuda")
+        w, dw = torch.rand(512, generator=gen, device="cuda") + 0.5, torch.zeros(512, device="cuda")
+        pos = torch.arange(3000, device="cuda")
+        grad = torch.ones(3000, 512, device="cuda")
+        for k in range(6):
+            n, stats = fsp.layer_norm(h, w, stats=True)
+            done()
+            rope.forward(n.view(3000, 8, 64), pos, out=n.view(3000, 8, 64))
+            done()
+            fsp.dropout(n, 0.3, 5, k, residual=h, out=h)
+            done()
+            fsp.layer_norm_backward(n, stats, grad, w, grad_weight=dw, accumulate=True, add=h, out=grad)
+            done()
+            fsp.layer_norm(grad, out=grad)
+            done()
+        return h, grad, dw
+
+    want = chain(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+    # the same on two streams side by side
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(chain(False))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    assert fsp.device_error() == 0
+
+
 def test_it_runs():
     from block_training import train
     losses = train(steps=4, batch=4, length=16, vocab=100)

@@ -97,7 +97,8 @@ def test_backward(rows, dim, pad, shift, x_t, dy_t, par_t):
 MANY = [(300001, 3, 0, 0), (100003, 8, 0, 0), (120001, 7, 1, 1), (47001, 17, 0, 0), (20011, 40, 8, 8), (6301, 128, 0, 0), (6200, 129, 0, 1), (3301, 256, 16, 0),
         (2999, 263, 0, 0), (1601, 520, 8, 0), (1555, 517, 3, 1), (801, 1001, 0, 1), (790, 1024, 0, 2), (401, 2040, 0, 0), (391, 2047, 2, 0), (200, 4099, 0, 0),
         (193, 4096, 8, 8), (101, 8191, 1, 0), (97, 8192, 0, 0), (53, 16383, 0, 1), (49, 16384, 0, 0),
-        (51, 16382, 2, 2), (90, 10000, 2, 4), (1500, 1002, 0, 0), (2000, 700, 4, 2), (50003, 30, 2, 0), (9001, 182, 0, 2)]
+        (51, 16382, 2, 2), (90, 10000, 2, 4), (1500, 1002, 0, 0), (2000, 700, 4, 2), (50003, 30, 2, 0), (9001, 182, 0, 2), (13001, 64, 0, 0),
+        (12500, 65, 0, 0), (30001, 32, 0, 0)]
 
 
 @pytest.mark.parametrize("x_t,out_t,par_t", TYPES)
