@@ -711,14 +711,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
   if (!a.grad_weight && !a.grad_bias) return;
   __syncthreads();
   constexpr int kCols = T * E;
-  float* joined = reinterpret_cast<float*>(ring);   // [kGroups][kCols], of dw and then of db
-  static_assert(kGroups * kCols * 4 <= kStages * kStage);
-  const int group = threadIdx.x / T;
+  float* joined = reinterpret_cast<float*>(ring);   // [2][kGroups][kCols], of dw and db
+  static_assert(2 * kGroups * kCols * 4 <= kStages * kStage);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (!(which ? a.grad_bias : a.grad_weight)) continue;
     const float2* y = which ? db : dw;
-    float* to = joined + group * kCols;
+    float* to = joined + (which * kGroups + threadIdx.x / T) * kCols;
 #pragma unroll
     for (int n = 0; n < H::N; ++n) {
       if constexpr (H::kPairs) {
@@ -730,14 +729,25 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
           *reinterpret_cast<float4*>(&to[H::column(n) + 2 * i]) = make_float4(y[n * V / 2 + i].x, y[n * V / 2 + i].y, y[n * V / 2 + i + 1].x, y[n * V / 2 + i + 1].y);
       }
     }
-    __syncthreads();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    void* out = which ? a.grad_bias : a.grad_weight;
+    if (!out) continue;
+    const float* from = joined + which * kGroups * kCols;
+    float* part = a.parts + (int64_t(blockIdx.x) * 2 + which) * dim;
     for (int c = threadIdx.x; c < kCols && c < dim; c += kRingThreads) {
       float v = 0.f;
 #pragma unroll 8
-      for (int k = 0; k < kGroups; ++k) v += joined[k * kCols + c];
-      a.parts[(int64_t(blockIdx.x) * 2 + which) * a.dim + c] = v;
+      for (int k = 0; k < kGroups; ++k) v += from[k * kCols + c];
+      if (gridDim.x > 1) {
+        part[c] = v;
+      } else {   // nothing to add these to: no second launch
+        if (a.accumulate) v += load_any(out, a.grad_param_f32, c);
+        store_any<1>(out, a.grad_param_f32, c, &v);
+      }
     }
-    __syncthreads();
   }
 }
 
@@ -1020,7 +1030,7 @@ fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
   if (s != FSP_OK) return s;
   a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
   if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kRingThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
-  return s == FSP_OK && (a.grad_weight || a.grad_bias) ? launch_join(a, st) : s;
+  return s == FSP_OK && (a.grad_weight || a.grad_bias) && a.n_parts != 1 ? launch_join(a, st) : s;   // (one CTA joins by itself)
 }
 
 template <typename X, typename G, int V>
