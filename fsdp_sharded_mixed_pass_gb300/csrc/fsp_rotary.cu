@@ -161,12 +161,12 @@ __global__ void __launch_bounds__(kThreads, kRuns == 1 && sizeof(T) == 2 ? 4 : 1
     for (int k = 0; k < kHeads; ++k)
 #pragma unroll
       for (int m = 0; m < kAccesses; ++m) {
-        float f[kUsed][V];
-#pragma unroll
-        for (int n = 0; n < kUsed; ++n)
-#pragma unroll
-          for (int j = 0; j < V; ++j) f[n][j] = widen(x[k][m][n][j]);
         if constexpr (kTurn) {
+          float f[kRuns][V];
+#pragma unroll
+          for (int n = 0; n < kRuns; ++n)
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[n][j] = widen(x[k][m][n][j]);
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) {
             if constexpr (kRuns == 2)
@@ -174,10 +174,12 @@ __global__ void __launch_bounds__(kThreads, kRuns == 1 && sizeof(T) == 2 ? 4 : 1
             else
               turn(f[0][2 * j], f[0][2 * j + 1], c[m][j], s[m][j]);
           }
-        }
-        if (there[k][m]) {
+          if (there[k][m]) {
 #pragma unroll
-          for (int n = 0; n < kUsed; ++n) store_vec<T, V>(to[k] + m * gap + n * a.second, f[n]);
+            for (int n = 0; n < kRuns; ++n) store_vec<T, V>(to[k] + m * gap + n * a.second, f[n]);
+          }
+        } else if (there[k][m]) {
+          store_raw<T, V>(to[k] + m * gap, x[k][m][0]);   // (the bits themselves)
         }
       }
   };

@@ -68,11 +68,8 @@ __device__ __forceinline__ void load_vec(const T* p, float* f) {
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float* f) {
+__device__ __forceinline__ void store_raw(T* p, const T* t) {
   constexpr int kBytes = int(sizeof(T)) * V;
-  alignas(32) T t[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) t[j] = narrow<T>(f[j]);
   const uint32_t* w = reinterpret_cast<const uint32_t*>(t);
   if constexpr (V == 1) {
     p[0] = t[0];
@@ -88,6 +85,13 @@ __device__ __forceinline__ void store_vec(T* p, const float* f) {
     static_assert(kBytes == 4);
     __stcs(reinterpret_cast<uint32_t*>(p), *w);
   }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float* f) {
+  alignas(32) T t[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) t[j] = narrow<T>(f[j]);
+  store_raw<T, V>(p, t);
 }
 
 // ---- host ----------------------------------------------------------------------------

@@ -156,6 +156,16 @@ def test_the_gradient_undoes_and_matches_differences():
     assert float((y - x).abs().max()) <= 2 * R.ROTARY_TOL * 2 * float(x.abs().max()) * 2
 
 
+@pytest.mark.parametrize("dtype,bits", [(torch.bfloat16, torch.int16), (torch.float32, torch.int32)])
+@pytest.mark.parametrize("head_dim,dim", [(64, 32), (36, 10), (66, 34)])
+def test_what_is_not_rotated_keeps_its_bits(dtype, bits, head_dim, dim):
+    raw = torch.arange(50 * 3 * head_dim, device="cuda") * 40503
+    x = raw.to(bits).view(dtype).view(50, 3, head_dim)   # NaNs of all kinds among them
+    for layout in ("half", "interleaved"):
+        y = fsp.Rotary(dim, layout=layout).forward(x, torch.arange(50, device="cuda"))
+        assert torch.equal(y.view(bits)[..., dim:], x.view(bits)[..., dim:])
+
+
 def test_empties_streams_and_graphs():
     rope = fsp.Rotary(16)
     x, pos = torch.randn(6, 3, 16, device="cuda"), torch.arange(6, device="cuda")
