@@ -224,8 +224,8 @@ bool disjoint(const View& v, const View& w) {
   if (v.size != w.size) return false;
   for (int k = 0; k < 6; ++k) {
     const View& from = k < 3 ? v : w;
-    if (from.extent[k % 3] == 1) continue;
     const int64_t m = from.stride[k % 3];
+    if (from.extent[k % 3] == 1 || m == 0) continue;   // (0: an input that repeats a head)
     auto part = [&](const View& x) {   // elements that it covers of a period; 0: it has none
       int64_t n = x.head_dim;
       for (int d = 0; d < 3; ++d) {

@@ -116,6 +116,9 @@ def test_rotary_refusals(lib):
     # one's output within the other's input
     assert _rotary(lib, [dict(), dict(out=FAKE)]) == B.FSP_EINVAL
     assert _rotary(lib, [dict(out=FAKE, xs=(0, 192, 64), os_=(0, 192, 64)), dict(x=FAKE + 192, xs=(0, 192, 64))]) == B.FSP_EINVAL
+    # an input that repeats its heads, under the output's span
+    for xs in ((0, 128, 64), (512, 0, 64), (512, 128, 0), (0, 0, 0)):
+        assert _rotary(lib, [dict(xs=xs, os_=(1024, 256, 64), out=FAKE + 64)], batch=2) == B.FSP_EINVAL and b"overlaps" in lib.fsp_last_error()
     assert _rotary(lib, tokens=1 << 30, batch=1 << 30) == B.FSP_EUNSUPPORTED
 
 

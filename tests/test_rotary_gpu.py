@@ -166,6 +166,17 @@ def test_what_is_not_rotated_keeps_its_bits(dtype, bits, head_dim, dim):
         assert torch.equal(y.view(bits)[..., dim:], x.view(bits)[..., dim:])
 
 
+def test_inputs_that_repeat():
+    """Broadcast heads, tokens and batches are read as they stand."""
+    rope, pos = fsp.Rotary(32), torch.arange(6, device="cuda") * 11
+    for shape in ((1, 1, 3, 40), (2, 1, 1, 40), (1, 6, 1, 40)):
+        x = torch.randn(shape, device="cuda").expand(2, 6, 3, 40)
+        assert torch.equal(rope.forward(x, pos), rope.forward(x.contiguous(), pos))
+    buf = torch.randn(2 * 6 * 3 * 40, device="cuda")
+    with pytest.raises(fsp.FspError, match="overlaps"):
+        rope.forward(buf[:40].view(1, 1, 1, 40).expand(2, 6, 3, 40), pos, out=buf.view(2, 6, 3, 40))
+
+
 def test_empties_streams_and_graphs():
     rope = fsp.Rotary(16)
     x, pos = torch.randn(6, 3, 16, device="cuda"), torch.arange(6, device="cuda")
