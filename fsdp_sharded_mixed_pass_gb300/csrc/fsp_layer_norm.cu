@@ -1010,18 +1010,25 @@ fsp_status norm(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs
   return whole ? launch_norm<B, kWhole>(a, st) : fit(2) ? launch_norm<B, kPart>(a, st) : launch_norm<B, kShift>(a, st);
 }
 
-int64_t parts_of(int64_t rows) { return std::min<int64_t>(kParts, rows); }
-size_t workspace_of(int64_t rows, int64_t dim) { return size_t(parts_of(rows)) * 2 * size_t(dim) * 4 + 256; }   // (from a multiple of 256)
+// Up to this many rows a group one CTA takes them all, which saves the second launch (32 x 512 and
+// 16 x 1024 4.3 and 4.7 us, on two CTAs 4.8 and 5.1; four rows a group 5.7 and 6.3 for 64 and 32
+// rows, on several CTAs 4.8 and 5.0).
+constexpr int kAlone = 2;
+
+// Threads of a group for rows of up to 8192 elements (0: of more).
+constexpr int grad_threads(int64_t dim) {
+  return dim <= 128 ? 8 : dim <= 256 ? 16 : dim <= 512 ? 32 : dim <= 1024 ? 64 : dim <= 2048 ? 128 : dim <= 4096 ? 256 : dim <= 8192 ? 512 : 0;
+}
+bool alone(int64_t rows, int64_t dim) { return grad_threads(dim) && rows <= kAlone * (kRingThreads / grad_threads(dim)); }
+
+size_t workspace_of(int64_t rows, int64_t dim) {   // (from a multiple of 256)
+  return rows == 0 || alone(rows, dim) ? 0 : size_t(std::min<int64_t>(kParts, rows)) * 2 * size_t(dim) * 4 + 256;
+}
 
 fsp_status launch_join(const GradArgs& a, cudaStream_t st) {
   return launch_next(join_columns_kernel, dim3(unsigned((a.dim + 31) / 32), 2), kJoinWarps * 32, 0, 1, a, st,
                      "layer norm gradient (join) kernel launch");
 }
-
-// Up to this many rows a group one CTA takes them all, which saves the second launch (32 x 512 and
-// 16 x 1024 4.3 and 4.7 us, on two CTAs 4.8 and 5.1; four rows a group 5.7 and 6.3 for 64 and 32
-// rows, on several CTAs 4.8 and 5.0).
-constexpr int kAlone = 2;
 
 template <typename X, typename G, Rows R, int T, int E>
 fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
@@ -1034,7 +1041,7 @@ fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
   fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
-  if (a.rows > 0 && a.rows <= kAlone * kGroups) a.n_parts = 1;
+  if (a.rows > 0 && alone(a.rows, a.dim)) a.n_parts = 1;
   if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kRingThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
   return s == FSP_OK && (a.grad_weight || a.grad_bias) && a.n_parts != 1 ? launch_join(a, st) : s;   // (one CTA joins by itself)
 }
@@ -1055,14 +1062,15 @@ fsp_status launch_wide_grad(GradArgs a, cudaStream_t st) {
 
 template <typename X, typename G, Rows R>
 fsp_status launch_grad(const GradArgs& a, cudaStream_t st) {
-  if (a.dim <= 64) return launch_ring_grad<X, G, R, 8, 8>(a, st);
-  if (a.dim <= 128) return launch_ring_grad<X, G, R, 8, 16>(a, st);
-  if (a.dim <= 256) return launch_ring_grad<X, G, R, 16, 16>(a, st);
-  if (a.dim <= 512) return launch_ring_grad<X, G, R, 32, 16>(a, st);
-  if (a.dim <= 1024) return launch_ring_grad<X, G, R, 64, 16>(a, st);
-  if (a.dim <= 2048) return launch_ring_grad<X, G, R, 128, 16>(a, st);
-  if (a.dim <= 4096) return launch_ring_grad<X, G, R, 256, 16>(a, st);
-  if (a.dim <= 8192) return launch_ring_grad<X, G, R, 512, 16>(a, st);
+  switch (grad_threads(a.dim)) {
+    case 8: return a.dim <= 64 ? launch_ring_grad<X, G, R, 8, 8>(a, st) : launch_ring_grad<X, G, R, 8, 16>(a, st);
+    case 16: return launch_ring_grad<X, G, R, 16, 16>(a, st);
+    case 32: return launch_ring_grad<X, G, R, 32, 16>(a, st);
+    case 64: return launch_ring_grad<X, G, R, 64, 16>(a, st);
+    case 128: return launch_ring_grad<X, G, R, 128, 16>(a, st);
+    case 256: return launch_ring_grad<X, G, R, 256, 16>(a, st);
+    case 512: return launch_ring_grad<X, G, R, 512, 16>(a, st);
+  }
   // (odd rows of fp32 beside bf16: 32 columns a thread leave no room for a row of results beside one of each input)
   if constexpr (R != kShift || sizeof(X) + sizeof(G) == 4)
     if (a.dim <= 16384) return launch_ring_grad<X, G, R, 512, 32>(a, st);
@@ -1097,7 +1105,7 @@ fsp_status backward(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_
   if (s == FSP_OK) s = check_vector(grad_bias, dim, pd, "grad_bias");
   if (s != FSP_OK) return s;
   if (dim == 0 || (!grad_x && !columns) || (rows == 0 && (!columns || accumulate))) return FSP_OK;
-  const size_t need = columns && rows > 0 ? workspace_of(rows, dim) : 0;
+  const size_t need = columns ? workspace_of(rows, dim) : 0;
   if (need) {
     if (!workspace) return fail(FSP_EINVAL, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % 16) return fail(FSP_EINVAL, "workspace is not 16-byte aligned");
@@ -1127,7 +1135,6 @@ fsp_status backward(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_
   a.grad_stride = gs;
   a.add_stride = as;
   a.grad_x_stride = ds;
-  a.n_parts = int(parts_of(rows));
   a.center = center != 0;
   a.weight_f32 = wd == FSP_DTYPE_F32;
   a.grad_param_f32 = pd == FSP_DTYPE_F32;

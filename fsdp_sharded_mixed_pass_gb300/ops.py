@@ -587,7 +587,7 @@ def _two_params(x, y, names, dim: int, device: int):
 
 def _stats(stats, rows: int, device: int):
     """The address of the (mean, 1 / deviation) pairs of ``rows`` rows."""
-    if _dtype(stats, "stats", device) != 0 or stats.shape[-1:] != (2,) or stats.numel() != 2 * rows or not stats.is_contiguous():
+    if _dtype(stats, "stats", device) != 0 or stats.numel() != 2 * rows or stats.size(-1) != 2 or not stats.is_contiguous():
         raise ValueError(f"stats must be contiguous fp32 pairs of {rows} rows")
     return stats.data_ptr()
 
@@ -677,11 +677,13 @@ def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, gr
     if columns:
         if workspace is None:
             work_bytes = layer_norm_backward_workspace_bytes(rows, dim)
-            workspace = _empty(work_bytes, _torch.uint8, x.device, stream)
+            if work_bytes:
+                workspace = _empty(work_bytes, _torch.uint8, x.device, stream)
         else:
             _on(here, workspace, "workspace")
             work_bytes = workspace.numel() * workspace.element_size()
-        work_ptr = workspace.data_ptr()
+        if work_bytes:
+            work_ptr = workspace.data_ptr()
     status = _lib.fsp_layer_norm_backward(
         x.data_ptr(), code, rows, dim, stride, stats_ptr, 1 if center else 0, grad_out.data_ptr(), dy_code, dy_stride,
         weight_ptr, w_code, add_ptr, add_stride, out_ptr, dx_stride, dw_ptr, db_ptr, grad_code, 1 if accumulate else 0,

@@ -215,7 +215,7 @@ fsp_status fsp_layer_norm(const void* x, int32_t x_dtype, int64_t rows, int64_t 
                           void* out, int32_t out_dtype, int64_t out_stride, float* stats, void* cuda_stream);
 
 /* Device workspace, in bytes, of fsp_layer_norm_backward where it computes
- * grad_weight or grad_bias (otherwise it needs none). */
+ * grad_weight or grad_bias (otherwise it needs none; 0 for a few rows: it may be NULL). */
 fsp_status fsp_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim, size_t* bytes);
 
 /* The gradients, from the forward pass's x, stats and center.  With

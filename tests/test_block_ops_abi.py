@@ -63,8 +63,8 @@ def test_layer_norm_backward_refusals(lib):
     assert _grad(lib, rows=0, acc=1) == B.FSP_OK and _grad(lib, dim=0) == B.FSP_OK and _grad(lib, dx=None, dw=None) == B.FSP_OK
     for kw in (dict(rows=-1), dict(dim=-8), dict(xd=2), dict(gd=2), dict(xs=7), dict(gs=7), dict(x=None), dict(dy=None), dict(stats=None),
                dict(stats=FAKE + GAP + 4), dict(w=FAKE + 6 * GAP, wd=3), dict(pd=3), dict(add=FAKE + 6 * GAP, as_=7), dict(ds=7),
-               dict(add=FAKE + 6 * GAP, dx=None), dict(work=None), dict(work_bytes=255), dict(work=FAKE + 5 * GAP + 8),
-               dict(dx=FAKE + 4), dict(dx=FAKE, ds=9), dict(dw=FAKE), dict(db=FAKE + 4 * GAP + 4), dict(work=FAKE + 3 * GAP),
+               dict(add=FAKE + 6 * GAP, dx=None), dict(rows=4000, work=None), dict(rows=4000, work_bytes=255), dict(rows=4000, work=FAKE + 5 * GAP + 8),
+               dict(dx=FAKE + 4), dict(dx=FAKE, ds=9), dict(dw=FAKE), dict(db=FAKE + 4 * GAP + 4), dict(rows=4000, work=FAKE + 3 * GAP),
                dict(w=FAKE + 3 * GAP), dict(dw=FAKE + 4 * GAP + 2), dict(dx=FAKE + GAP)):
         assert _grad(lib, **kw) == B.FSP_EINVAL, kw
         assert lib.fsp_last_error()
@@ -73,6 +73,10 @@ def test_layer_norm_backward_refusals(lib):
     assert bytes_of(4, 8, None) == B.FSP_EINVAL and bytes_of(-1, 8, ctypes.byref(size)) == B.FSP_EINVAL
     assert bytes_of(4, (1 << 20) + 1, ctypes.byref(size)) == B.FSP_EUNSUPPORTED
     assert bytes_of(100000, 1024, ctypes.byref(size)) == B.FSP_OK and 1024 * 8 <= size.value <= 1024 * 8 * 1024
+    for rows, dim in ((0, 1 << 20), (1, 8192), (2, 5000), (16, 1024), (128, 3)):   # what one CTA takes
+        assert bytes_of(rows, dim, ctypes.byref(size)) == B.FSP_OK and size.value == 0
+    for rows, dim in ((1, 8193), (3, 8192), (17, 1024), (129, 3)):
+        assert bytes_of(rows, dim, ctypes.byref(size)) == B.FSP_OK and size.value >= dim * 8
 
 
 def _drop(lib, x=FAKE, xd=0, rows=4, dim=8, xs=8, p=0.5, call=None, h=None, hd=0, hs=8, out=FAKE + GAP, od=0, os_=8):

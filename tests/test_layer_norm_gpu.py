@@ -154,7 +154,7 @@ def test_long_batches(rows, dim, x_t):
         assert bool(((got - exact).abs() <= (rows + 2 * R.depth(dim) + 16) * R.U * mag).all())
     for _ in range(2):
         dw2, db2 = torch.empty(2, dim, device="cuda")
-        junk = torch.full((fsp.layer_norm_backward_workspace_bytes(rows, dim),), 0xFF, dtype=torch.uint8, device="cuda")
+        junk = torch.full((fsp.layer_norm_backward_workspace_bytes(rows, dim),), 0xFF, dtype=torch.uint8, device="cuda")   # (sums' places are written first)
         dx2 = fsp.layer_norm_backward(x, stats, dy, w, grad_weight=dw2, grad_bias=db2, add=add, workspace=junk)
         assert torch.equal(dw, dw2) and torch.equal(db, db2) and torch.equal(dx, dx2)
     assert fsp.device_error() == 0
@@ -242,6 +242,29 @@ def test_empty_batches():
     assert fsp.layer_norm_backward(x, stats, x).shape == (0, 8)
 
 
+# both sides of what one CTA takes
+@pytest.mark.parametrize("rows,dim", [(128, 40), (129, 40), (128, 100), (129, 101), (64, 256), (65, 255), (32, 512), (33, 512), (16, 1024), (17, 1001), (8, 2048),
+                                      (9, 2048), (4, 4096), (5, 4095), (2, 8192), (3, 8192), (1, 8200), (2, 16384), (1, 20000)])
+def test_gradients_of_few_rows(rows, dim):
+    rng = np.random.default_rng(rows + dim)
+    x, _ = matrix(rows, dim, "bf16", fill=_inputs(rows, dim, rng))
+    dy, _ = matrix(rows, dim, "bf16", fill=rng.normal(0, 1, (rows, dim)))
+    _, stats = fsp.layer_norm(x, stats=True)
+    st = values(stats)
+    want, tol = R.norm_gradients(values(x), st[:, 0], st[:, 1], values(dy), 1.0, 0.0, True)
+    for accumulate in (False, True):
+        dw, old = _vector(rng, dim, 0, 1, "bf16"), None
+        db = _vector(rng, dim, 0, 1, "bf16")
+        old = [values(t) if accumulate else 0.0 for t in (dw, db)]
+        need = fsp.layer_norm_backward_workspace_bytes(rows, dim)
+        work = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device="cuda") if accumulate else None
+        dx = fsp.layer_norm_backward(x, stats, dy, grad_weight=dw, grad_bias=db, accumulate=accumulate, workspace=work)
+        assert off_by(dx, want[0], tol[0], "bf16") == 0
+        for g, o, v, t in zip((dw, db), old, want[1:], tol[1:]):
+            assert off_by(g, v + o, t + R.U * (np.abs(v + o) + np.abs(v)), "bf16") == 0
+    assert fsp.device_error() == 0
+
+
 def test_offsets_past_32_bits():
     big = torch.zeros(2 ** 20 + 3, 4096, dtype=torch.bfloat16, device="cuda")   # rows 4096 apart: 2^32 elements and more
     x = big[:, :64]
@@ -303,6 +326,7 @@ def test_refusals():
     with pytest.raises(fsp.FspError, match="overlaps"):
         fsp.layer_norm_backward(x, stats, x, grad_weight=x[0])
     with pytest.raises(fsp.FspError, match="workspace"):
-        fsp.layer_norm_backward(x, stats, x, grad_weight=w, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+        many = torch.zeros(500, 16, device="cuda")
+        fsp.layer_norm_backward(many, many[:, :2].contiguous(), many, grad_weight=w, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(fsp.FspError, match="eps"):
         fsp.layer_norm(x, eps=-1.0)
