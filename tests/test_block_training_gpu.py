@@ -108,21 +108,24 @@ def test_a_captured_step_replays():
     assert fsp.device_error() == 0
 
 
-def test_calls_that_follow_one_another_at_once():
-    """Each call starts while the one before it ends: a chain of calls in place gives what waiting after each gives."""
+@pytest.mark.parametrize("width,heads,dtype", [(512, 8, torch.float32), (513, 9, torch.bfloat16), (1001, 7, torch.bfloat16), (1002, 6, torch.bfloat16),
+                                               (777, 7, torch.float32)])
+def test_calls_that_follow_one_another_at_once(width, heads, dtype):
+    """Each call starts while the one before it ends: a chain of calls in place gives what waiting after each gives.
+    (Odd rows share pieces of memory with the rows beside them, which other CTAs write.)"""
     gen = torch.Generator(device="cuda").manual_seed(9)
-    rope = fsp.Rotary(64)
+    rope = fsp.Rotary(width // heads // 2 * 2)
 
     def chain(wait):
         done = torch.cuda.synchronize if wait else lambda: None
-        h = torch.randn(3000, 512, generator=gen.manual_seed(1), device="cuda")
-        w, dw = torch.rand(512, generator=gen, device="cuda") + 0.5, torch.zeros(512, device="cuda")
+        h = torch.randn(3000, width, generator=gen.manual_seed(1), device="cuda").to(dtype)
+        w, dw = torch.rand(width, generator=gen, device="cuda") + 0.5, torch.zeros(width, device="cuda")
         pos = torch.arange(3000, device="cuda")
-        grad = torch.ones(3000, 512, device="cuda")
+        grad = torch.randn(3000, width, generator=gen, device="cuda").to(dtype)
         for k in range(6):
             n, stats = fsp.layer_norm(h, w, stats=True)
             done()
-            rope.forward(n.view(3000, 8, 64), pos, out=n.view(3000, 8, 64))
+            rope.forward(n.view(3000, heads, -1), pos, out=n.view(3000, heads, -1))
             done()
             fsp.dropout(n, 0.3, 5, k, residual=h, out=h)
             done()
