@@ -14,9 +14,8 @@
 //     residual's 82 us, 0.97; 131072 x 128 12 and 21 us; odd rows 20000 x 1001 20 and 35 us, bound by
 //     their instructions);
 //   longer rows: a CTA per row, which reads it three times.
-// All sums are fp32; no sum's order depends on timing.  In the ring a mean is a product with
-// 1 / dim and r is rsqrtf's (two roundings, and at most two steps of 2^-23: divisions and a root
-// cost a short row a tenth of its instructions).
+// All sums are fp32; no sum's order depends on timing.  In the ring r is rsqrtf's (at most two
+// steps of 2^-23: a root and a division cost a short row a tenth of its instructions).
 #include <algorithm>
 #include <type_traits>
 
@@ -236,6 +235,14 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*share)[kRingThr
 // Two elements an instruction, each rounded as its own.
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
+
+// s / n, share = 1 / n.  q = s share is off by up to 1.5 * 2^-23 of itself; what is missing, s - q n,
+// is exact in a fused product, and q plus its share is s / n within 2^-24 and, where s / n is a
+// float, that float.  (NaN of an infinite sum.)
+__device__ __forceinline__ float mean_of(float s, float n, float share) {
+  const float q = s * share;
+  return __fmaf_rn(__fmaf_rn(-q, n, s), share, q);
+}
 
 // The rows of a thread: `row` its group's, `first` that of its warp's first group (the groups
 // of a warp advance together), `step` to the next.  (Below 2^32, also those past the last.)
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
   float2 w[E / 2], b[E / 2];
   H::load(a.weight, a.param_f32, dim, 1.f, w);
   H::load(a.bias, a.param_f32, dim, 0.f, b);
-  const float share_of = 1.f / float(dim);
+  const float count = float(dim), share_of = 1.f / count;
   int slot = 0;
   for (int which = 0; at.first < rows; at.next(), which ^= 1) {
     char* stage = ring + slot * C::kStage;
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
       for (int i = 0; i < E / 2; ++i) part[i & 1] = __fadd2_rn(part[i & 1], f[i]);
       s[0] = sum_of(__fadd2_rn(part[0], part[1]));
       group_sum<T>(s, share, 0);
-      m = s[0] * share_of;
+      m = mean_of(s[0], count, share_of);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) f[i] = __fadd2_rn(f[i], both(-m));
       H::mask(dim, f);
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
   }
   float2 w[E / 2], dw[E / 2] = {}, db[E / 2] = {};
   H::load(a.weight, a.weight_f32, dim, 1.f, w);
-  const float share_of = 1.f / float(dim);
+  const float count = float(dim), share_of = 1.f / count;
   float2 next = at.row < rows ? a.stats[at.row] : make_float2(0.f, 0.f);
   int slot = 0;
   for (int which = 0; at.first < rows; at.next(), which ^= 1) {
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     if (a.grad_x) {
       float s[2] = {sum_of(sg), sum_of(sgh)};
       group_sum<T>(s, share, which);
-      const float2 mean_g = both(a.center ? -s[0] * share_of : 0.f), mean_gh = both(-s[1] * share_of), r = both(st.y);
+      const float2 mean_g = both(a.center ? -mean_of(s[0], count, share_of) : 0.f), mean_gh = both(-mean_of(s[1], count, share_of)), r = both(st.y);
       float2 plus[H::kPairs && kKeep ? E / 2 : 1];
       if constexpr (H::kPairs && kKeep) {
         if (a.add) {

@@ -1,0 +1,44 @@
+"""What the norm's arithmetic has to get right beyond the rounding of ordinary values: rows of one value."""
+import numpy as np
+import pytest
+import torch
+
+import fsdp_sharded_mixed_pass_gb300 as fsp
+
+import block_reference as R
+from block_cases import DT, matrix, off_by, values
+from gpu_cases import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ensure_built()
+
+
+# rows, dim, pad: few rows and many, lengths that have no exact reciprocal, even, odd, with gaps
+ONE_VALUE = [(3, 6, 0), (300, 1000, 0), (4096, 1000, 0), (4096, 1001, 0), (1200, 700, 4), (40000, 30, 2), (30011, 33, 0), (100, 9999, 0), (100, 10000, 0),
+             (60, 16381, 1), (3, 20000, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim,pad", ONE_VALUE)
+def test_rows_of_one_value(rows, dim, pad, dtype):
+    """Values of eight significant bits: every partial sum of up to 2^16 of them is a float, and so is the mean:
+    nothing is left of the row."""
+    for value in (99840.0, -40960.0, 0.30078125, 3.5):
+        x, _ = matrix(rows, dim, dtype, pad, fill=np.full((rows, dim), value))
+        y, stats = fsp.layer_norm(x, stats=True)
+        assert float(y.abs().max()) == 0 and bool((stats[:, 0] == value).all())
+        dy, _ = matrix(rows, dim, dtype, pad, fill=np.random.default_rng(rows).normal(0, 1, (rows, dim)))
+        dw = torch.empty(dim, device="cuda")
+        dx = fsp.layer_norm_backward(x, stats, dy, grad_weight=dw)
+        st = values(stats)
+        want, tol = R.norm_gradients(values(x), st[:, 0], st[:, 1], values(dy), 1.0, 0.0, True)
+        assert off_by(dx, want[0], tol[0], dtype) == 0 and float(dw.abs().max()) == 0
+        dy.fill_(value)   # and nothing of a gradient of one value
+        assert float(fsp.layer_norm_backward(x, stats, dy).abs().max()) == 0
+    assert fsp.device_error() == 0
