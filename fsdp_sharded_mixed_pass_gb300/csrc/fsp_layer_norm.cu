@@ -238,10 +238,10 @@ __device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
 
 // s / n, share = 1 / n.  q = s share is off by up to 1.5 * 2^-23 of itself; what is missing, s - q n,
 // is exact in a fused product, and q plus its share is s / n within 2^-24 and, where s / n is a
-// float, that float.  (NaN of an infinite sum.)
+// float, that float.  (An infinite sum has an infinite mean, and nothing that is missing.)
 __device__ __forceinline__ float mean_of(float s, float n, float share) {
-  const float q = s * share;
-  return __fmaf_rn(__fmaf_rn(-q, n, s), share, q);
+  const float q = s * share, mean = __fmaf_rn(__fmaf_rn(-q, n, s), share, q);
+  return fabsf(q) <= 3.4e38f ? mean : q;
 }
 
 // The rows of a thread: `row` its group's, `first` that of its warp's first group (the groups

@@ -42,3 +42,19 @@ def test_rows_of_one_value(rows, dim, pad, dtype):
         dy.fill_(value)   # and nothing of a gradient of one value
         assert float(fsp.layer_norm_backward(x, stats, dy).abs().max()) == 0
     assert fsp.device_error() == 0
+
+
+@pytest.mark.parametrize("rows,dim", [(5, 100), (9000, 100), (4096, 1001), (60, 16000), (3, 20000)])
+def test_infinite_sums(rows, dim):
+    """An infinity among a row's gradients, at h = 1: both means are infinite, and so is the gradient of every other element;
+    a row whose sum of finite values leaves fp32's range has infinite statistics.  The rows beside them are as they were."""
+    x, dy = torch.randn(2, rows, dim, device="cuda")
+    _, stats = fsp.layer_norm(x, stats=True)
+    clean = fsp.layer_norm_backward(x, stats, dy)
+    dy[1, 7], x[1], stats[1] = float("inf"), 1, torch.tensor([0.0, 1.0], device="cuda")
+    got = fsp.layer_norm_backward(x, stats, dy)
+    assert bool(got[1, 7].isnan()) and bool((got[1, 8:] == -float("inf")).all()) and bool((got[1, :7] == -float("inf")).all())
+    assert torch.equal(got[2:], clean[2:]) and torch.equal(got[0], clean[0])
+    x[2] = 3e38
+    y, stats = fsp.layer_norm(x, stats=True)
+    assert bool(y[2].isnan().all()) and stats[2].tolist() == [float("inf"), 0.0] and bool(y[3:].isfinite().all())
