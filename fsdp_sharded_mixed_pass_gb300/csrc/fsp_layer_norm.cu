@@ -14,8 +14,9 @@
 //     residual's 82 us, 0.97; 131072 x 128 12 and 21 us; odd rows 20000 x 1001 20 and 35 us, bound by
 //     their instructions);
 //   longer rows: a CTA per row, which reads it three times.
-// All sums are fp32; no sum's order depends on timing.  In the ring r is rsqrtf's (at most two
-// steps of 2^-23: a root and a division cost a short row a tenth of its instructions).
+// All sums are fp32; no sum's order depends on timing.  In the ring a mean is a corrected product
+// with 1 / dim and r a corrected rsqrtf (divisions and a root cost a short row a tenth of its
+// instructions).
 #include <algorithm>
 #include <type_traits>
 
@@ -238,10 +239,16 @@ __device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
 
 // s / n, share = 1 / n.  q = s share is off by up to 1.5 * 2^-23 of itself; what is missing, s - q n,
 // is exact in a fused product, and q plus its share is s / n within 2^-24 and, where s / n is a
-// float, that float.  (An infinite sum has an infinite mean, and nothing that is missing.)
+// float, that float.  (An infinite sum has an infinite mean: fminf takes the other for NaN.)
 __device__ __forceinline__ float mean_of(float s, float n, float share) {
-  const float q = s * share, mean = __fmaf_rn(__fmaf_rn(-q, n, s), share, q);
-  return fabsf(q) <= 3.4e38f ? mean : q;
+  const float q = s * share;
+  return __fmaf_rn(fminf(__fmaf_rn(-q, n, s), 3.4e38f), share, q);
+}
+// 1 / sqrt(v) of v >= 0: rsqrtf, up to two steps of 2^-23 off, and a step of Newton's method on
+// 1 / r^2 = v, after which the roundings are left (1.5 * 2^-24; likewise for zeros and infinities).
+__device__ __forceinline__ float root_of(float v) {
+  const float r = rsqrtf(v);
+  return __fmaf_rn(0.5f * r, fminf(__fmaf_rn(-v * r, r, 1.f), 1.f), r);
 }
 
 // The rows of a thread: `row` its group's, `first` that of its warp's first group (the groups
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
     group_sum<T>(s, share, a.center ? 1 : which);
     C::copy(stage, x, at.row + kStages * at.step, rows, dim);   // (all that was read has entered the sum)
     copies_issued();
-    const float r = rsqrtf(s[0] * share_of + a.eps);
+    const float r = root_of(s[0] * share_of + a.eps);
     const bool there = at.row < rows;
     if (a.stats && H::thread() == 0 && there) a.stats[at.row] = make_float2(m, r);
     auto result = [&](int n, float2* y) {

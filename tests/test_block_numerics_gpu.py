@@ -58,3 +58,17 @@ def test_infinite_sums(rows, dim):
     x[2] = 3e38
     y, stats = fsp.layer_norm(x, stats=True)
     assert bool(y[2].isnan().all()) and stats[2].tolist() == [float("inf"), 0.0] and bool(y[3:].isfinite().all())
+
+
+@pytest.mark.parametrize("rows,dim", [(300, 64), (40000, 64), (20000, 128), (20000, 1024)])
+def test_inverse_deviations(rows, dim):
+    """Rows of +-a, a of seven bits: the squares, their sums (at most 2^24) and the division by 2^k are exact, so the
+    variance is, and eps's sum is rounded once.  Then r's own roundings: 1.5 * 2^-24 of a step of Newton's method after
+    the terms of its square (2^-46), or half of 2^-24 of a root and a division's."""
+    rng = np.random.default_rng(dim)
+    a = np.ldexp(rng.integers(64, 128, rows), rng.integers(-9, 3, rows)).astype(np.float32)
+    x = torch.from_numpy((a[:, None] * np.where(rng.random((rows, dim)) < 0.5, -1, 1)).astype(np.float32)).cuda()
+    for eps in (0.0, 1e-5, 2.0 ** -12, 0.3, 3e-3, 0.011):
+        _, stats = fsp.layer_norm(x, eps=eps, center=False, stats=True)
+        r = 1 / np.sqrt((a * a + np.float32(eps)).astype(np.float64))
+        assert (np.abs(values(stats[:, 1]) - r) <= 1.51 * R.U * r).all() and float(stats[:, 0].abs().max()) == 0
