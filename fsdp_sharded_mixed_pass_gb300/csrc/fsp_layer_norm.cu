@@ -599,7 +599,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
 
 // All gradients in one pass over x and dy.  A thread adds its columns' terms of dw and db in
 // registers; the CTA's groups are joined in shared memory at the end, so that a launch leaves
-// one pair of partial sums per CTA.  kKeep: h and g stay in registers from the sums to dx
+// one pair of partial sums per CTA.  What is multiplied is d = x - m, and r joins dy for dw and
+// the row's sum for mean(g h): past a row's end, where dy is 0 and d is -m, h = d r may be infinite
+// and 0 h not a number.  kKeep: d and g stay in registers from the sums to dx
 // (E = 16; kShift: dx then takes x's place in the stage); otherwise they are read again (20000
 // odd bf16 rows of 1001: 35 us with 16 columns a thread, 49 with 32 that are read again).
 template <typename X, typename G, int V, int T, int E, int kStages, Rows R>
@@ -645,46 +647,47 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     if constexpr (R == kShift) group_sync<T>();
     const int end = there ? dim : 0;   // kShift: nothing of what an earlier row left
     const int skip_dy = CG::skip(dy, at.row), skip_x = CX::skip(x, at.row), skip_add = CX::skip(add, at.row);
-    float2 h[(kKeep ? E : H::W) / 2], g[(kKeep ? E : H::W) / 2], sg = both(0.f), sgh = both(0.f);
-    auto normalise = [&](float2& x) { x = __fmul2_rn(__fadd2_rn(x, both(-st.x)), both(st.y)); };
-    auto add_terms = [&](int e, float2& g, float2 h) {   // pair e; g becomes dy w
-      dw[e] = __ffma2_rn(g, h, dw[e]);
+    float2 d[(kKeep ? E : H::W) / 2], g[(kKeep ? E : H::W) / 2], sg = both(0.f), sgd = both(0.f);
+    auto centre = [&](float2& x) { x = __fadd2_rn(x, both(-st.x)); };
+    auto add_terms = [&](int e, float2& g, float2 d) {   // pair e; g becomes dy w
+      dw[e] = __ffma2_rn(__fmul2_rn(g, both(st.y)), d, dw[e]);
       db[e] = __fadd2_rn(db[e], g);
       g = __fmul2_rn(g, w[e]);
       sg = __fadd2_rn(sg, g);
-      sgh = __ffma2_rn(g, h, sgh);
+      sgd = __ffma2_rn(g, d, sgd);
     };
-    auto read = [&](int n) {   // (not kKeep) access n of dy and h
+    auto read = [&](int n) {   // (not kKeep) access n of dy and d
       if constexpr (H::kPairs) {
         g[0] = CG::read_pair(stage, skip_dy, end, n);
-        h[0] = CX::read_pair(stage + CG::kStage, skip_x, end, n);
+        d[0] = CX::read_pair(stage + CG::kStage, skip_x, end, n);
       } else {
         CG::read(stage, n, g);
-        CX::read(stage + CG::kStage, n, h);
+        CX::read(stage + CG::kStage, n, d);
       }
 #pragma unroll
-      for (int i = 0; i < H::W / 2; ++i) normalise(h[i]);
+      for (int i = 0; i < H::W / 2; ++i) centre(d[i]);
     };
     if constexpr (kKeep) {
       CG::read_row(stage, skip_dy, end, g);
-      CX::read_row(stage + CG::kStage, skip_x, end, h);
+      CX::read_row(stage + CG::kStage, skip_x, end, d);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        normalise(h[e]);
-        add_terms(e, g[e], h[e]);
+        centre(d[e]);
+        add_terms(e, g[e], d[e]);
       }
     } else {
 #pragma unroll
       for (int n = 0; n < H::N; ++n) {
         read(n);
 #pragma unroll
-        for (int i = 0; i < H::W / 2; ++i) add_terms(n * H::W / 2 + i, g[i], h[i]);
+        for (int i = 0; i < H::W / 2; ++i) add_terms(n * H::W / 2 + i, g[i], d[i]);
       }
     }
     if (a.grad_x) {
-      float s[2] = {sum_of(sg), sum_of(sgh)};
+      float s[2] = {sum_of(sg), sum_of(sgd)};
       group_sum<T>(s, share, which);
-      const float2 mean_g = both(a.center ? -mean_of(s[0], count, share_of) : 0.f), mean_gh = both(-mean_of(s[1], count, share_of)), r = both(st.y);
+      const float2 mean_g = both(a.center ? -mean_of(s[0], count, share_of) : 0.f), r = both(st.y);
+      const float2 of_d = both(-(mean_of(s[1], count, share_of) * st.y) * st.y);   // h mean(g h) = d times this
       float2 plus[H::kPairs && kKeep ? E / 2 : 1];
       if constexpr (H::kPairs && kKeep) {
         if (a.add) {
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < H::W / 2; ++i) {
           const int k = kKeep ? n * H::W / 2 + i : i;
-          f[i] = __ffma2_rn(r, __ffma2_rn(h[k], mean_gh, __fadd2_rn(g[k], mean_g)), f[i]);
+          f[i] = __ffma2_rn(r, __ffma2_rn(d[k], of_d, __fadd2_rn(g[k], mean_g)), f[i]);
         }
       };
       char* staging = kKeep ? CX::group(stage + CG::kStage) : ring + kStages * kStage + threadIdx.x / T * (T * E * int(sizeof(X)) + 16);

@@ -72,3 +72,23 @@ def test_inverse_deviations(rows, dim):
         _, stats = fsp.layer_norm(x, eps=eps, center=False, stats=True)
         r = 1 / np.sqrt((a * a + np.float32(eps)).astype(np.float64))
         assert (np.abs(values(stats[:, 1]) - r) <= 1.51 * R.U * r).all() and float(stats[:, 0].abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim,pad,shift", [(4, 6, 0, 0), (5, 8, 0, 0), (7, 33, 0, 1), (130, 40, 0, 0), (300, 200, 0, 0), (300, 201, 3, 0), (9, 1000, 0, 0), (5, 2049, 0, 0),
+                                                (3, 9000, 0, 0), (3, 9002, 2, 2), (3, 9001, 0, 1), (4, 128, 0, 0), (2, 20000, 0, 0)])
+def test_means_far_from_the_rows_spread(rows, dim, pad, shift, dtype):
+    """Rows of 2^112 whose inverse deviation is 2^20: m r is out of fp32's range, x - m is not.  (Sums of 2^112 up to
+    2^15 times are floats.)"""
+    x, _ = matrix(rows, dim, dtype, pad, shift, np.full((rows, dim), 2.0 ** 112))
+    dy, _ = matrix(rows, dim, dtype, pad, shift, np.random.default_rng(dim).normal(0, 1, (rows, dim)))
+    for center in (True, False):
+        y, stats = fsp.layer_norm(x, eps=2.0 ** -40, center=center, stats=True)
+        if not center:   # its variance is out of range: statistics as if there were none
+            stats = torch.tensor([2.0 ** 112, 2.0 ** 20], device="cuda").repeat(rows, 1)
+        assert bool((stats == torch.tensor([2.0 ** 112, 2.0 ** 20], device="cuda")).all())
+        dw, db = torch.empty(2, dim, device="cuda")
+        dx = fsp.layer_norm_backward(x, stats, dy, center=center, grad_weight=dw, grad_bias=db)
+        want, tol = R.norm_gradients(values(x), values(stats[:, 0]), values(stats[:, 1]), values(dy), 1.0, 0.0, center)
+        assert off_by(dx, want[0], tol[0], dtype) == 0 and float(dw.abs().max()) == 0 and off_by(db, want[2], tol[2], "f32") == 0
+    assert fsp.device_error() == 0
