@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_ring_kernel(const __grid
     for (int i = 0; i < E / 2; ++i) part[i & 1] = __ffma2_rn(f[i], f[i], part[i & 1]);
     s[0] = sum_of(__fadd2_rn(part[0], part[1]));
     group_sum<T>(s, share, a.center ? 1 : which);
-    C::copy(stage, x, at.row + kStages * at.step, rows, dim);   // (all that was read has entered the sum)
+    if constexpr (R == kShift && T <= 32) __syncwarp();   // (of larger groups the sum's barrier: all have read the stage)
+    C::copy(stage, x, at.row + kStages * at.step, rows, dim);
     copies_issued();
     const float r = root_of(s[0] * share_of + a.eps);
     const bool there = at.row < rows;
@@ -686,6 +687,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) grad_ring_kernel(const __grid
     if (a.grad_x) {
       float s[2] = {sum_of(sg), sum_of(sgd)};
       group_sum<T>(s, share, which);
+      if constexpr (R == kShift && kKeep && T <= 32) __syncwarp();   // dx takes the place of x, which all have read
       const float2 mean_g = both(a.center ? -mean_of(s[0], count, share_of) : 0.f), r = both(st.y);
       const float2 of_d = both(-(mean_of(s[1], count, share_of) * st.y) * st.y);   // h mean(g h) = d times this
       float2 plus[H::kPairs && kKeep ? E / 2 : 1];
