@@ -1060,7 +1060,7 @@ fsp_status launch_ring_grad(GradArgs a, cudaStream_t st) {
   fsp_status s = allow_kernel(reinterpret_cast<const void*>(kernel), kSmem);
   if (s != FSP_OK) return s;
   a.n_parts = int(std::min<int64_t>(kParts, (a.rows + kGroups - 1) / kGroups));
-  if (a.rows > 0 && alone(a.rows, a.dim)) a.n_parts = 1;
+  if (a.rows > 0 && (a.grad_weight || a.grad_bias) && alone(a.rows, a.dim)) a.n_parts = 1;
   if (a.rows > 0) s = launch_next(kernel, dim3(unsigned(a.n_parts)), kRingThreads, kSmem, 1, a, st, "layer norm gradient kernel launch");
   return s == FSP_OK && (a.grad_weight || a.grad_bias) && a.n_parts != 1 ? launch_join(a, st) : s;   // (one CTA joins by itself)
 }
