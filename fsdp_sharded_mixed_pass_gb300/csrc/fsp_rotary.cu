@@ -7,8 +7,9 @@
 //
 // Bound: HBM (131072 tokens of 12 bf16 heads of 64 61 us, 0.97 of the measured copy; 16384 of 24
 // heads of 128 within a projection's rows 34 us, 0.87).  A frequency is held in units of 2^-64
-// turn per position, so t f_j modulo a turn is one 64-bit product that wraps: as exact at position
-// 2^31 as at position 1, without arithmetic in 64-bit floating point.
+// turn per position, rounded once, so t f_j modulo a turn is one 64-bit product that wraps, off by at
+// most |t| 2^-65 turn (2^-34 at position 2^31, where a 32-bit angle's last place is 2^-32), without
+// arithmetic in 64-bit floating point.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -49,7 +50,7 @@ struct RotaryArgs {
 
 // Sine and cosine of an angle in units of 2^-32 turn.  The nearest quarter is taken off in
 // whole numbers; what is left, r in [-pi/4, pi/4], goes through the Taylor series up to r^9 / 9!
-// and r^10 / 10! (what follows is below 2^-29 and 2^-32 of the result).
+// and r^10 / 10! (what follows is below 2^-28 and 2^-32 of the result).
 __device__ __forceinline__ void sine_cosine(uint32_t angle, float* sine, float* cosine) {
   const uint32_t quarter = (angle + 0x20000000u) >> 30;
   const float r = float(int32_t(angle - (quarter << 30))) * 1.46291807926715968e-9f;   // pi / 2^31
@@ -408,16 +409,40 @@ fsp_status rotary(const fsp_rotary_tensor* tensors, int32_t n, int32_t dtype, in
 }  // namespace
 }  // namespace fsp
 
+namespace fsp {
+namespace {
+
+// f / (2 pi) in units of 2^-64 turn, without whole turns, rounded to the nearest (and off by 2^-11 of a
+// unit at most before that).  |f| = M 2^e with M of 53 bits below 2^64: M times the bits of 1 / (2 pi) from
+// weight 2^-(e + 1) on, the first 64 of which count units and the next 64 parts of one; what is above them
+// gives whole turns.
+uint64_t phase_of(double f) {
+  // 1 / (2 pi), 192 bits after the point (pi by Machin's formula in whole numbers)
+  constexpr uint64_t kPerRadian[4] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull, 0};
+  auto bits = [&](int from) -> uint64_t {   // 64 of them
+    if (from <= -64) return 0;
+    if (from < 0) return kPerRadian[0] >> -from;
+    const int i = from / 64, k = from % 64;
+    return k ? kPerRadian[i] << k | kPerRadian[i + 1] >> (64 - k) : kPerRadian[i];
+  };
+  int e;
+  const uint64_t m = uint64_t(std::ldexp(std::frexp(std::fabs(f), &e), 53));
+  e -= 53;   // at most 11
+  const unsigned __int128 parts = static_cast<unsigned __int128>(m) * bits(e + 64) + (uint64_t(1) << 63);
+  const uint64_t phase = m * bits(e) + uint64_t(parts >> 64);
+  return f < 0 ? 0 - phase : phase;
+}
+
+}  // namespace
+}  // namespace fsp
+
 extern "C" fsp_status fsp_rotary_phases(const double* frequencies, int64_t n, uint64_t* phases) {
   return fsp::guard([&]() -> fsp_status {
     fsp::clear_error();
     if (n < 0 || (n > 0 && (!frequencies || !phases))) return fsp::fail(FSP_EINVAL, "n is negative or a pointer NULL");
     for (int64_t j = 0; j < n; ++j) {
-      if (!std::isfinite(frequencies[j])) return fsp::fail(FSP_EINVAL, "a frequency is not finite");
-      // turns per position, without the whole ones
-      const double turns = std::fmod(frequencies[j] / 6.283185307179586476925, 1.0);
-      const uint64_t part = uint64_t(std::ldexp(std::fabs(turns), 64));
-      phases[j] = turns < 0 ? 0 - part : part;
+      if (!(std::fabs(frequencies[j]) < 18446744073709551616.0)) return fsp::fail(FSP_EINVAL, "a frequency is not finite, or 2^64 or above");
+      phases[j] = fsp::phase_of(frequencies[j]);
     }
     return FSP_OK;
   });

@@ -274,14 +274,15 @@ typedef struct {
   int64_t out_strides[3];  /* every element has a place of its own */
 } fsp_rotary_tensor;
 
-/* Host: n frequencies (radians per position, finite) in units of 2^-64 turn per
- * position, without whole turns - what fsp_rotary reads on the device. */
+/* Host: n frequencies (radians per position, magnitudes below 2^64) in units of 2^-64
+ * turn per position, without whole turns, rounded to the nearest - what fsp_rotary reads
+ * on the device. */
 fsp_status fsp_rotary_phases(const double* frequencies, int64_t n, uint64_t* phases);
 
 /* Turns pair j = 0 ... rotary_dim / 2 - 1 of every head, (a, b), by the angle of its
  * token's position t: out = scale (a cos - b sin, b cos + a sin)(t f_j); elements
- * past rotary_dim are copied.  t f_j is exact modulo a turn for any int64 t; sine,
- * cosine and products in fp32, rounded once.  inverse: by the negated angle, which
+ * past rotary_dim are copied.  t times the phase is exact modulo a turn for any int64 t, so
+ * t f_j is off by at most |t| 2^-65 turn; sine, cosine and products in fp32, rounded once.  inverse: by the negated angle, which
  * is the gradient.
  *   tensors: n (1 or 2: queries and keys in one launch) of `dtype`.
  *   positions: int32 (index_bytes 4) or int64 (8), batch b's tokens from
