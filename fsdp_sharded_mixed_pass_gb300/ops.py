@@ -701,7 +701,7 @@ def dropout(x, p: float, seed: int, call=0, residual=None, out=None, out_dtype=N
     once to ``out_dtype`` (default: the residual's, or x's).  ``out`` may be ``x`` or
     ``residual``.
 
-    Which elements go is a function of ``seed`` (64 bits), ``call`` (an int, or a device
+    Which elements go is a function of ``seed`` (64 bits), ``call`` (an int of 64 bits, or a device
     int64 tensor of one element: the form to capture in a CUDA graph) and the element's
     index, so no mask is stored: ``dropout_backward`` takes the same seed and call, and
     any two calls of a run should differ in one of them."""
@@ -709,7 +709,10 @@ def dropout(x, p: float, seed: int, call=0, residual=None, out=None, out_dtype=N
     code = _dtype(x, "x", here)
     rows, dim, stride = _rows_of(x, "x")
     call_ptr = None
-    if not isinstance(call, int):
+    if isinstance(call, int):
+        if not -1 << 63 <= call < 1 << 63:
+            raise ValueError("call must be within 64 bits")   # (another call's masks otherwise)
+    else:
         if call.dtype != _torch.int64 or call.numel() != 1:
             raise ValueError("call must be an int or one int64 element")
         _on(here, call, "call")
