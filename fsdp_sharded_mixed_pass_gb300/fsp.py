@@ -482,6 +482,8 @@ def sharded_step_host(plan: Plan, host_grads, master, exp_avg, exp_avg_sq, host_
     fp32 state on the device; ``workspace`` is a device tensor of at least
     ``host_step_workspace_bytes`` bytes.  Asynchronous on ``stream``."""
     args = _step_args(plan, host_grads, master, exp_avg, exp_avg_sq, host_params, hparams, step, grad_dtype)
+    if not isinstance(workspace, int) and not workspace.is_contiguous():   # (an expanded tensor has more elements than memory)
+        raise ValueError("workspace must be contiguous")
     nbytes = workspace.numel() * workspace.element_size() if not isinstance(workspace, int) else 0
     _check(lib().fsp_sharded_step_host(*args, ctypes.c_void_p(_ptr(workspace)), nbytes, int(chunk_elems),
                                        ctypes.c_void_p(_stream_handle(stream))), "fsp_sharded_step_host")

@@ -156,6 +156,16 @@ def _tokens(tokens, device: int) -> int:
     return size
 
 
+def _workspace_bytes(workspace, device: int) -> int:
+    """Bytes of a workspace tensor on ``device``; they must be its own, one after the other
+    (an expanded tensor has more elements than memory)."""
+    if workspace.get_device() != device:
+        _on(device, workspace, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _empty(shape, dtype, device, stream):
     """A buffer whose memory is handed out (and later taken back) in the order
     of the stream the call runs on."""
@@ -370,15 +380,14 @@ def embedding_backward(tokens, grad_out, grad_weight, scale: float = 1.0, paddin
     if padding_idx is not None and not 0 <= padding_idx < vocab:
         raise ValueError("padding_idx is not a row of grad_weight")
     grad_code, code = _dtype(grad_out, "grad_out", here), _dtype(grad_weight, "grad_weight", here)
-    if workspace is not None:
-        _on(here, workspace, "workspace")
-    else:
+    if workspace is None:
         workspace = _empty(embedding_backward_workspace_bytes(vocab, dim, n), _torch.uint8, grad_weight.device, stream)
+    work_bytes = _workspace_bytes(workspace, here)
     status = _lib.fsp_embedding_backward(
         tokens.data_ptr(), size, n, grad_out.data_ptr(), grad_code, dim, grad_stride,
         grad_weight.data_ptr(), code, vocab, stride, scale,
         -1 if padding_idx is None else padding_idx, 1 if accumulate else 0, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _handle(stream, here))
+        work_bytes, _handle(stream, here))
     if status:
         _fsp._check(status, "fsp_embedding_backward")
     return grad_weight
@@ -680,8 +689,7 @@ def layer_norm_backward(x, stats, grad_out, weight=None, center: bool = True, gr
             if work_bytes:
                 workspace = _empty(work_bytes, _torch.uint8, x.device, stream)
         else:
-            _on(here, workspace, "workspace")
-            work_bytes = workspace.numel() * workspace.element_size()
+            work_bytes = _workspace_bytes(workspace, here)
         if work_bytes:
             work_ptr = workspace.data_ptr()
     status = _lib.fsp_layer_norm_backward(
