@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(T > 128 ? T : 128) norm_kernel(const __grid_co
 // group copies the 16-byte pieces that cover the row, and a thread reads pairs of elements from
 // wherever they begin; a row of results is laid down in shared memory likewise and leaves in
 // 16-byte pieces.  A piece that reaches past a matrix's first or last byte is filled with the
-// elements that are the matrix's.  (Measured, kPart and kShift, us: forward 20000 x 700 bf16 15.8
+// elements that are the matrix's.  (Measured, kPart and kShift, us: forward 20000 x 700 bf16 15.9
 // and 17.9, but 4099 x 1001 fp32 to bf16 9.4 and 8.1, so the forward pass of fp32 takes kShift;
-// gradients of 20000 x 700 bf16 23.3 and 33.5.)
+// gradients of 20000 x 700 bf16 23.8 and 33.5.)
 
 constexpr int kRingThreads = 512;
 
@@ -237,7 +237,7 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*share)[kRingThr
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
 
-// s / n, share = 1 / n.  q = s share is off by up to 1.5 * 2^-23 of itself; what is missing, s - q n,
+// s / n, share = 1 / n.  q = s share is off by up to 2^-23 of itself; what is missing, s - q n,
 // is exact in a fused product, and q plus its share is s / n within 2^-24 and, where s / n is a
 // float, that float.  (An infinite sum has an infinite mean: fminf takes the other for NaN.)
 __device__ __forceinline__ float mean_of(float s, float n, float share) {
@@ -1029,9 +1029,10 @@ fsp_status norm(const void* x, int32_t xd, int64_t rows, int64_t dim, int64_t xs
   return whole ? launch_norm<B, kWhole>(a, st) : fit(2) ? launch_norm<B, kPart>(a, st) : launch_norm<B, kShift>(a, st);
 }
 
-// Up to this many rows a group one CTA takes them all, which saves the second launch (32 x 512 and
-// 16 x 1024 4.3 and 4.7 us, on two CTAs 4.8 and 5.1; four rows a group 5.7 and 6.3 for 64 and 32
-// rows, on several CTAs 4.8 and 5.0).
+// Where the parameters' gradients are wanted, one CTA takes up to this many rows a group, which
+// saves the second launch (32 x 512 and 16 x 1024 4.3 and 4.7 us, on two CTAs 4.8 and 5.1; four
+// rows a group 5.7 and 6.3 for 64 and 32 rows, on several CTAs 4.8 and 5.0).  The gradient of x
+// alone has no second launch to save (32 x 512 3.1 us on one CTA, 2.3 on two).
 constexpr int kAlone = 2;
 
 // Threads of a group for rows of up to 8192 elements (0: of more).

@@ -81,8 +81,10 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // with another one, kRuns = 1: V / 2 pairs of neighbours - as far apart as there are units, or
 // as many runs of V elements that are copied.  Heads of odd sizes take narrow accesses, several
 // a thread: what counts is how many bytes are in flight.  The loads of kHeads heads come before
-// their stores.  (Four CTAs per SM for bf16 neighbours 61 us, unbounded 64, 131072 x 12 heads of
-// 64; three for halves 40 us, two, as their registers allow, 34, 16384 x 24 heads of 128.)
+// their stores.  (Measured at accesses of eight elements: four CTAs per SM for bf16 neighbours 61 us,
+// unbounded 64, 131072 x 12 heads of 64; three for halves 40 us, two, as their registers allow, 34,
+// 16384 x 24 heads of 128.  Narrower neighbours have the bound without a measurement; those of four
+// elements, two accesses a thread, spill 18 bytes for it.)
 template <typename T, int V, int kRuns, int kAccesses, int kHeads>
 __global__ void __launch_bounds__(kThreads, kRuns == 1 && sizeof(T) == 2 ? 4 : 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int kPairs = V * kRuns / 2;
@@ -308,7 +310,8 @@ fsp_status launch_width(const RotaryArgs& a, int v, int runs, bool several, cuda
 }
 
 // A token's heads are spread over threads until a launch has this many (16 + 8 heads of 128,
-// us, with 152 x 768 and 152 x 384: 1024 tokens 7.3 and 5.9, 4096 tokens 12.2 and 13.7).
+// us, with 152 x 768 and 152 x 384: 1024 tokens 7.3 and 5.9, 4096 tokens 12.2 and 13.5: one number,
+// which costs some thousands of tokens what it gains a thousand).
 constexpr int64_t kEnoughThreads = 152 * 384;
 // From this many threads of one access each on they take several (20000 tokens, 12 bf16 heads
 // of 146, 60 turned in pairs: 63 us with one, 38 with four).

@@ -203,7 +203,9 @@ fsp_status fsp_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int
 
 /* Each row of x: m its mean (center 0: m = 0, the norm by the root mean square),
  * r = 1 / sqrt(mean (x - m)^2 + eps), out = (x - m) r weight + bias; computed in
- * fp32 from the row's values, rounded once.
+ * fp32 from the row's values, rounded once.  Sums are added in an order that the sizes,
+ * types and alignment alone decide: a row's last bits may differ between calls of few
+ * rows and of many.
  *   x: rows x dim of x_dtype, rows x_stride (>= dim) elements apart; out likewise
  *            (out may be x itself: same pointer, type and stride).
  *   weight, bias: dim elements of param_dtype; NULL: ones, zeros.

@@ -6,7 +6,9 @@ U = 2.0 ** -24   # half a step of fp32, relative
 
 
 def depth(n):
-    """Most additions that a term of a row's sum goes through: at least 16 threads share a row."""
+    """Most additions that a term of a row's sum goes through.  Rows of up to 128 elements: at most 16 of a
+    thread's own and four steps of its group; longer ones are shared by at least 16 threads, whose sums are joined in
+    16 steps or, from 4097 elements on (256 and more of the first term), 5 among lanes and 16 or 32 warps."""
     return -(-n // 16) + 16
 
 
